@@ -7,6 +7,9 @@ package loads nothing; the first call loads libnq.so and fails loudly if it
 is missing.
 """
 from ._binding import (  # noqa: F401
+    KVCache,
+    KVSequences,
+    MoERouter,
     NQ_ROW_INDEPENDENT_ROWS,
     NQError,
     library_path,
@@ -23,6 +26,12 @@ from ._binding import (  # noqa: F401
     nq_gather_qmm_row_exact,
     nq_gather_qmm_lhs,
     nq_gather_qmm_workspace_bytes,
+    nq_kv_append,
+    nq_kv_attention,
+    nq_kv_attention_workspace_bytes,
+    nq_kv_read,
+    nq_moe_route,
+    nq_moe_route_grad,
     nq_qmm,
     nq_qmm_batched,
     nq_qmm_grad_scales_biases,

@@ -18,6 +18,10 @@ NQ_ROUTE_GEMV, NQ_ROUTE_TILED = 1, 2
 NQ_MXFP4, NQ_MXFP8, NQ_NVFP4 = 1, 2, 3
 # floating-point mode -> (C enum, bits per code, group size)
 FP_MODES = {"mxfp4": (NQ_MXFP4, 4, 32), "mxfp8": (NQ_MXFP8, 8, 32), "nvfp4": (NQ_NVFP4, 4, 16)}
+NQ_KV_INT8, NQ_KV_FP8 = 1, 2
+KV_FORMATS = {"int8": NQ_KV_INT8, "fp8": NQ_KV_FP8}
+NQ_MOE_SOFTMAX, NQ_MOE_SIGMOID = 1, 2
+MOE_SCORES = {"softmax": NQ_MOE_SOFTMAX, "sigmoid": NQ_MOE_SIGMOID}
 
 _lib = None
 
@@ -84,13 +88,19 @@ _SIGNATURES = {
                          _SZ, _P],
     "nq_fp_qmm_notrans_workspace_bytes": [_I64, _I64, _I64, _I32, _I32, _I32],
     "nq_fp_qmm_notrans": [_P, _I32, _I64, _I64, _P, _P, _P, _I64, _I32, _I32, _P, _P, _SZ, _P],
+    "nq_kv_append": [_P, _P, _P, _I64, _P, _I64, _I32, _P],
+    "nq_kv_read": [_P, _P, _P, _P, _I32, _P],
+    "nq_kv_attention_workspace_bytes": [_P, _P, _I32, _I32],
+    "nq_kv_attention": [_P, _P, _P, _I32, _I64, _I32, ctypes.c_float, _I32, _I64, _P, _P, _P, _SZ, _P],
+    "nq_moe_route": [_P, _P, _I32, _I64, _I64, _P, _P, _P, _P],
+    "nq_moe_route_grad": [_P, _P, _I32, _I64, _I64, _P, _P, _P, _P],
     "nq_status_string": [_I32],
     "nq_last_error": [],
     "nq_version": [],
 }
 _RESTYPES = {"nq_qmm_workspace_bytes": _SZ, "nq_gather_qmm_workspace_bytes": _SZ,
              "nq_qmm_notrans_workspace_bytes": _SZ, "nq_fp_gather_qmm_workspace_bytes": _SZ,
-             "nq_fp_qmm_notrans_workspace_bytes": _SZ,
+             "nq_fp_qmm_notrans_workspace_bytes": _SZ, "nq_kv_attention_workspace_bytes": _SZ,
              "nq_status_string": ctypes.c_char_p, "nq_last_error": ctypes.c_char_p,
              "nq_version": ctypes.c_char_p}
 
@@ -591,3 +601,264 @@ def nq_fp_qmm_notrans(x, codes, scales, mode, global_scale=None, row_exact=False
                                  _stream(stream)))
     return y
 
+
+# ---------------------------------------------------------------- key/value cache in 8 bits
+class _KVCacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", _P), ("v_codes", _P), ("k_scales", _P), ("v_scales", _P), ("blocks", _I64),
+                ("kv_heads", _I32), ("head_dim", _I32), ("block_tokens", _I32), ("format", _I32)]
+
+
+class _KVSeqsStruct(ctypes.Structure):
+    _fields_ = [("row_start", _P), ("lengths", _P), ("block_table", _P), ("batch", _I64), ("max_blocks", _I64),
+                ("table_stride", _I64), ("rows", _I64)]
+
+
+class _MoERouterStruct(ctypes.Structure):
+    _fields_ = [("experts", _I32), ("score", _I32), ("groups", _I32), ("top_groups", _I32), ("group_best", _I32),
+                ("top_k", _I32), ("renormalise", _I32), ("scale", ctypes.c_float)]
+
+
+class KVCache:
+    """A paged key/value cache in 8 bits (nq_kv_cache): k_codes [blocks,
+    kv_heads, block_tokens, head_dim] and v_codes [blocks, kv_heads, head_dim,
+    block_tokens] uint8, k_scales and v_scales [blocks, kv_heads] float32;
+    format "int8" or "fp8".  The constructor allocates the arrays (contents
+    undefined until written); wrap() takes existing ones."""
+
+    def __init__(self, blocks, kv_heads, block_tokens, head_dim, format="int8", device="cuda"):
+        torch = _torch()
+        u8 = {"dtype": torch.uint8, "device": device}
+        f32 = {"dtype": torch.float32, "device": device}
+        self._bind(torch.empty((blocks, kv_heads, block_tokens, head_dim), **u8),
+                   torch.empty((blocks, kv_heads), **f32),
+                   torch.empty((blocks, kv_heads, head_dim, block_tokens), **u8),
+                   torch.empty((blocks, kv_heads), **f32), format)
+
+    @classmethod
+    def wrap(cls, k_codes, k_scales, v_codes, v_scales, format):
+        self = cls.__new__(cls)
+        self._bind(k_codes, k_scales, v_codes, v_scales, format)
+        return self
+
+    def _bind(self, k_codes, k_scales, v_codes, v_scales, format):
+        torch = _torch()
+        if format not in KV_FORMATS:
+            raise ValueError(f"unknown cache format {format!r} (one of {sorted(KV_FORMATS)})")
+        for name, t, dt in (("k_codes", k_codes, torch.uint8), ("v_codes", v_codes, torch.uint8),
+                            ("k_scales", k_scales, torch.float32), ("v_scales", v_scales, torch.float32)):
+            _contig(name, t)
+            if t.dtype != dt:
+                raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+        blocks, kv_heads, block_tokens, head_dim = k_codes.shape
+        if tuple(v_codes.shape) != (blocks, kv_heads, head_dim, block_tokens) or \
+                tuple(k_scales.shape) != (blocks, kv_heads) or tuple(v_scales.shape) != (blocks, kv_heads):
+            raise ValueError("codes and scales do not describe one cache")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.blocks, self.kv_heads, self.block_tokens, self.head_dim = blocks, kv_heads, block_tokens, head_dim
+        self.format = format
+        self._struct = _KVCacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                                      v_scales.data_ptr(), blocks, kv_heads, head_dim, block_tokens,
+                                      KV_FORMATS[format])
+        self._ref = ctypes.byref(self._struct)
+
+
+class KVSequences:
+    """The sequences of a call (nq_kv_seqs): row_start [batch + 1], lengths
+    [batch] and block_table [batch, max_blocks] int32 on the GPU, rows the
+    number of rows of the call's arrays.  Row i of sequence b is token
+    lengths[b] - row_start[b + 1] + i.  The tensors may be updated in place
+    between calls."""
+
+    def __init__(self, row_start, lengths, block_table, rows):
+        torch = _torch()
+        for name, t in (("row_start", row_start), ("lengths", lengths)):
+            _contig(name, t)
+        for name, t in (("row_start", row_start), ("lengths", lengths), ("block_table", block_table)):
+            if t.dtype != torch.int32 or not t.is_cuda:
+                raise TypeError(f"{name} must be an int32 GPU tensor")
+        batch = lengths.numel()
+        if row_start.numel() != batch + 1 or block_table.dim() != 2 or block_table.shape[0] != batch:
+            raise ValueError("row_start, lengths and block_table do not describe one batch")
+        max_blocks = block_table.shape[1]
+        if max_blocks > 1 and block_table.stride(1) != 1:
+            raise ValueError("the rows of block_table must be contiguous")
+        stride = block_table.stride(0) if batch > 1 else max_blocks
+        self.row_start, self.lengths, self.block_table, self.rows = row_start, lengths, block_table, rows
+        self.batch = batch
+        self._struct = _KVSeqsStruct(row_start.data_ptr(), lengths.data_ptr(), block_table.data_ptr(), batch,
+                                     max_blocks, stride, rows)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _row_stride(name, t, rows, heads, dim):
+    """The row stride of a [rows, heads, dim] tensor whose rows are dense."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.shape != (rows, heads, dim):
+        raise ValueError(f"{name} must have shape {(rows, heads, dim)}, got {tuple(t.shape)}")
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != dim):
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return s[0] if rows > 1 else heads * dim
+
+
+def nq_kv_append(cache, seqs, k, v, stream=None):
+    """Writes the keys and values of seqs' rows, k and v [rows, kv_heads,
+    head_dim] (f32 or bf16, any row stride of whole 16 bytes), into cache."""
+    lib = _lib or load_library()
+    ldk = _row_stride("k", k, seqs.rows, cache.kv_heads, cache.head_dim)
+    ldv = _row_stride("v", v, seqs.rows, cache.kv_heads, cache.head_dim)
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must have the same dtype")
+    status = lib.nq_kv_append(cache._ref, seqs._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, _dt(k), _stream(stream))
+    if status:
+        _check(status)
+
+
+def nq_kv_read(cache, seqs, out_dtype=None, k=None, v=None, stream=None):
+    """The tokens of seqs' rows -> (k, v) [rows, kv_heads, head_dim] in
+    out_dtype (default bf16)."""
+    torch = _torch()
+    lib = _lib or load_library()
+    shape = (seqs.rows, cache.kv_heads, cache.head_dim)
+    dt = out_dtype or torch.bfloat16
+    if k is None:
+        k = _empty(stream, shape, dt, cache.k_codes.device)
+    if v is None:
+        v = _empty(stream, shape, dt, cache.k_codes.device)
+    for name, t in (("k", k), ("v", v)):
+        _contig(name, t)
+        if tuple(t.shape) != shape or t.dtype != k.dtype:
+            raise ValueError(f"{name} must have shape {shape} and the other output's dtype")
+    status = lib.nq_kv_read(cache._ref, seqs._ref, k.data_ptr(), v.data_ptr(), _dt(k), _stream(stream))
+    if status:
+        _check(status)
+    return k, v
+
+
+def nq_kv_attention_workspace_bytes(cache, seqs, q_heads, x_dtype):
+    torch = _torch()
+    xd = NQ_F32 if x_dtype == torch.float32 else NQ_BF16
+    return load_library().nq_kv_attention_workspace_bytes(cache._ref, seqs._ref, q_heads, xd)
+
+
+def nq_kv_attention(cache, seqs, q, scale=None, causal=True, window=0, out=None, lse=None, workspace=None,
+                    stream=None):
+    """Attention of q [rows, q_heads, head_dim] (f32 or bf16, any row stride of
+    whole 16 bytes) over cache -> out, dense, in q's dtype.  scale: factor of
+    the scores (default head_dim ** -0.5); window > 0: only the last `window`
+    tokens of a row (with causal); lse: an optional [rows, q_heads] float32
+    tensor for the log-sum-exp of the scores.  The workspace is allocated here
+    when not given."""
+    torch = _torch()
+    lib = _lib or load_library()
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, q_heads, head_dim]")
+    heads = q.shape[1]
+    ldq = _row_stride("q", q, seqs.rows, heads, cache.head_dim)
+    dt = _dt(q)
+    if out is None:
+        out = _empty(stream, q.shape, q.dtype, q.device)
+    else:
+        _contig("out", out)
+        if out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must have q's shape and dtype")
+    if lse is not None:
+        _contig("lse", lse)
+        if tuple(lse.shape) != (seqs.rows, heads) or lse.dtype != torch.float32:
+            raise ValueError("lse must be float32 [rows, q_heads]")
+    if workspace is None:
+        ws_bytes = lib.nq_kv_attention_workspace_bytes(cache._ref, seqs._ref, heads, dt)
+        if ws_bytes:
+            workspace = _empty(stream, ws_bytes, torch.uint8, q.device)
+    else:
+        _contig("workspace", workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    status = lib.nq_kv_attention(cache._ref, seqs._ref, q.data_ptr(), dt, ldq, heads,
+                                 cache.head_dim ** -0.5 if scale is None else scale, int(bool(causal)), window,
+                                 out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                 None if workspace is None else workspace.data_ptr(), ws_bytes, _stream(stream))
+    if status:
+        _check(status)
+    return out
+
+
+# ---------------------------------------------------------------- expert routing
+class MoERouter:
+    """How tokens choose experts (nq_moe_router): the top_k largest of score
+    "softmax" or "sigmoid" (plus a bias), from the top_groups best of `groups`
+    groups of neighbouring experts -- a group's score is its largest key
+    (group_best 1) or the sum of its two largest (2); weights divided by their
+    sum when renormalise, times scale."""
+
+    def __init__(self, experts, top_k, score="softmax", groups=1, top_groups=None, group_best=1, renormalise=False,
+                 scale=1.0):
+        if score not in MOE_SCORES:
+            raise ValueError(f"unknown score {score!r} (one of {sorted(MOE_SCORES)})")
+        self.experts, self.top_k, self.score, self.groups = experts, top_k, score, groups
+        self.top_groups = groups if top_groups is None else top_groups
+        self.group_best, self.renormalise, self.scale = group_best, bool(renormalise), scale
+        self._struct = _MoERouterStruct(experts, MOE_SCORES[score], groups, self.top_groups, group_best, top_k,
+                                        int(self.renormalise), scale)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _logits(router, logits):
+    if not logits.is_cuda:
+        raise ValueError("logits must be a GPU tensor")
+    if logits.dim() != 2 or logits.shape[1] != router.experts or (router.experts > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [tokens, experts] with contiguous rows")
+    return logits.shape[0], logits.stride(0) if logits.shape[0] > 1 else router.experts
+
+
+def nq_moe_route(router, logits, bias=None, ids=None, weights=None, stream=None):
+    """logits [tokens, experts] (f32 or bf16, any row stride), bias [experts]
+    float32 or None -> (ids [tokens, top_k] uint32-as-int32, weights [tokens,
+    top_k] float32), the largest key first."""
+    torch = _torch()
+    lib = _lib or load_library()
+    tokens, ld = _logits(router, logits)
+    shape = (tokens, router.top_k)
+    if bias is not None:
+        _contig("bias", bias)
+        if bias.dtype != torch.float32 or bias.numel() != router.experts:
+            raise ValueError("bias must be float32 [experts]")
+    if ids is None:
+        ids = _empty(stream, shape, torch.int32, logits.device)
+    if weights is None:
+        weights = _empty(stream, shape, torch.float32, logits.device)
+    for name, t, dt in (("ids", ids, torch.int32), ("weights", weights, torch.float32)):
+        _contig(name, t)
+        if t.shape != shape or t.dtype != dt:
+            raise ValueError(f"{name} must be {dt} {shape}")
+    status = lib.nq_moe_route(router._ref, logits.data_ptr(), _dt(logits), tokens, ld,
+                              None if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+                              _stream(stream))
+    if status:
+        _check(status)
+    return ids, weights
+
+
+def nq_moe_route_grad(router, logits, ids, dweights, dlogits=None, stream=None):
+    """The logits' gradient of sum(dweights * weights): ids from nq_moe_route,
+    dweights [tokens, top_k] float32 -> dlogits [tokens, experts], dense, in
+    the logits' dtype."""
+    torch = _torch()
+    lib = _lib or load_library()
+    tokens, ld = _logits(router, logits)
+    shape = (tokens, router.top_k)
+    for name, t, dt in (("ids", ids, torch.int32), ("dweights", dweights, torch.float32)):
+        _contig(name, t)
+        if t.shape != shape or t.dtype != dt:
+            raise ValueError(f"{name} must be {dt} {shape}")
+    if dlogits is None:
+        dlogits = _empty(stream, (tokens, router.experts), logits.dtype, logits.device)
+    else:
+        _contig("dlogits", dlogits)
+        if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
+            raise ValueError("dlogits must have the logits' shape and dtype")
+    status = lib.nq_moe_route_grad(router._ref, logits.data_ptr(), _dt(logits), tokens, ld, ids.data_ptr(),
+                                   dweights.data_ptr(), dlogits.data_ptr(), _stream(stream))
+    if status:
+        _check(status)
+    return dlogits

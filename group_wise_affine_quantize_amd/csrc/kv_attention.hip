@@ -1,0 +1,593 @@
+// Attention over the 8-bit key/value cache (contract in include/nq.h).
+//
+// Mathematics.  For a query row q and the visible tokens t of its sequence,
+//   z_t = scale * q . k_t,   out = sum_t e^(z_t) v_t / sum_t e^(z_t),
+// with k_t = sk_t * ck_t and v_t = sv_t * cv_t (block scales times codes).  In
+// one pass over the tokens, in base 2 and with the value scale drawn into
+// the exponent:
+//   x_t = log2(e) * scale * sk_t * (q . ck_t) + log2(sv_t),
+//   p_t = 2^(x_t - M + 14),  M the running maximum of x_t,
+//   O = sum_t p_t cv_t,      L = sum_t p_t / sv_t,      out = O / L.
+// Drawing sv into x makes p_t the whole weight of a code row, so that the
+// second product runs on bare codes, and 2^14 is the most that any p_t is, so
+// that p_t fits fp16: with 11 bits for weights within 2^-28 of the largest,
+// and a floor 2^-38 of it.  (bf16 would keep 8 bits, which shows in a bf16
+// result.)  Codes are exact in fp16.  A query row is taken times a power of
+// two that brings its largest element to [2^14, 2^15); a bf16 element then is
+// exact in fp16 down to 2^-28 of the largest.  fp32 rows and weights are the
+// sum of two fp16 numbers (22 bits) and take two matrix products each.  Sums,
+// maxima and the states M, L, O are fp32.
+//
+// Matrix products: S^T = K q^T and O^T = V^T P^T on 16x16x32 fp16 MFMA with
+// the tokens in the rows of the first product.  Lane l (r = l % 16, g = l / 16)
+// holds column (query row) r and, after the first product, tokens 16 g + 4 n +
+// i of the 64-token tile (n the MFMA, i the register): the order in which K's
+// rows are fed is free, and this one leaves each lane 16 neighbouring tokens,
+// which are exactly the operand of the second product (16 bytes of a V^T row
+// per lane).  No value moves between lanes but the running maximum.
+#include "nq_kv_device.h"
+
+namespace nqk {
+
+namespace {
+
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float float4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kTile = 64;        // tokens per tile
+constexpr int kWaves = 4;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
+constexpr float kPScale = 14.0f;  // log2 of the largest weight
+// What stands for the scale of an all-zero block of values.  Any would do for
+// its zero codes; a small one keeps its tokens, however large their scores,
+// from raising M over the tokens that do add to O, and 2^80 of them still
+// count in L.
+constexpr float kZeroBlockScale = 0x1p-80f;
+constexpr float kNegInf = -__builtin_inff();
+
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float fast_log2(float x) { return __builtin_amdgcn_logf(x); }
+
+// Eight codes (two words) -> eight fp16 values, exactly.
+template <int FMT> __device__ __forceinline__ half8_t codes_to_half(uint32_t w0, uint32_t w1)
+{
+    uint32_t p[4];
+    if constexpr (FMT == KV_INT8) {
+        // 0x6400 | c is fp16 1024 + c; less 1152 it is c - 128
+        p[0] = __builtin_amdgcn_perm(0x64646464u, w0, 0x04010400u);
+        p[1] = __builtin_amdgcn_perm(0x64646464u, w0, 0x04030402u);
+        p[2] = __builtin_amdgcn_perm(0x64646464u, w1, 0x04010400u);
+        p[3] = __builtin_amdgcn_perm(0x64646464u, w1, 0x04030402u);
+        const half2_t off = {(_Float16)1152.0f, (_Float16)1152.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const half2_t h = __builtin_bit_cast(half2_t, p[i]) - off;
+            p[i] = __builtin_bit_cast(uint32_t, h);
+        }
+    } else {
+        p[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w0, 1.0f, false));
+        p[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w0, 1.0f, true));
+        p[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w1, 1.0f, false));
+        p[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w1, 1.0f, true));
+    }
+    const uint4_t v = {p[0], p[1], p[2], p[3]};
+    return __builtin_bit_cast(half8_t, v);
+}
+
+// Parts of fp32 numbers in fp16: one for bf16 queries, two for fp32 ones.
+template <typename T> struct Parts { static constexpr int n = 2; };
+template <> struct Parts<bf16_bits> { static constexpr int n = 1; };
+
+template <int NP> __device__ __forceinline__ void split_half(const float *v, half8_t *h)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const _Float16 a = (_Float16)v[i];
+        h[0][i] = a;
+        if constexpr (NP == 2) h[1][i] = (_Float16)(v[i] - (float)a);
+    }
+}
+
+__device__ __forceinline__ float4_t mfma(half8_t a, half8_t b, float4_t c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+struct AttnArgs {
+    KvAttnLaunch a;
+    float *part_o;      // [workers * 2][16 * CT][D]
+    float *part_ml;     // [workers * 2][16 * CT][2]
+    int workers;        // workgroups of the streaming kernel
+    int group;          // query heads per key/value head
+};
+
+// The streaming kernel's work is a flat list of tiles: for each sequence with
+// rows, for each key/value head, for each tile of `cols` query rows (a row is
+// a token and one of the head's queries), the 64-token tiles of the tokens
+// that the sequence's rows can see.
+struct StreamSeq {
+    KvSeq q;
+    int64_t lo, hi;     // tokens that some row sees (hi <= lo: none)
+    int64_t t0, nt;     // first tile, tiles (at least one)
+    int64_t ct;         // column tiles
+    int64_t work;       // ct * kv_heads * nt
+};
+
+__device__ __forceinline__ StreamSeq stream_seq(const AttnArgs &A, int b, int cols)
+{
+    const KvAttnLaunch &a = A.a;
+    StreamSeq s;
+    s.q = kv_seq(a.s, b);
+    const int64_t cap = a.s.max_blocks << a.c.block_shift;
+    s.hi = s.q.len < cap ? s.q.len : cap;
+    s.lo = 0;
+    if (a.window > 0) {
+        s.lo = s.q.first - a.window + 1;
+        if (s.lo < 0) s.lo = 0;
+    }
+    s.t0 = s.lo >> 6;
+    s.nt = s.hi > s.lo ? ((s.hi + 63) >> 6) - s.t0 : 1;
+    s.ct = (s.q.n * A.group + cols - 1) / cols;
+    s.work = s.ct * s.nt * a.c.kv_heads;
+    return s;
+}
+
+__device__ __forceinline__ int64_t stream_total(const AttnArgs &A, int cols)
+{
+    const int lane = (int)(threadIdx.x & 63u);
+    int64_t t = 0;
+    for (int b = lane; b < A.a.s.batch; b += 64) t += stream_seq(A, b, cols).work;
+    return __shfl(wave_scan(t, lane), 63);
+}
+
+__device__ __forceinline__ int64_t stream_share(const AttnArgs &A, int64_t total)
+{
+    // at least two tiles for each wave, so that short contexts do not fall
+    // into parts that cost more to join than to read
+    const int64_t share = (total + A.workers - 1) / A.workers;
+    return share < 2 * kWaves ? 2 * kWaves : share;
+}
+
+// Where a query column stands: its row of the call, head, and the tokens that
+// it sees, [lo, hi).
+struct Column {
+    int64_t row;        // -1: no such column
+    int head;
+    int64_t lo, hi;
+};
+
+__device__ __forceinline__ Column column(const AttnArgs &A, const StreamSeq &s, int64_t idx, int kv_head)
+{
+    const KvAttnLaunch &a = A.a;
+    Column c;
+    c.row = -1, c.head = 0, c.lo = 0, c.hi = 0;
+    if (idx < s.q.n * A.group) {
+        const int64_t i = idx / A.group;
+        c.row = s.q.r0 + i;
+        c.head = kv_head * A.group + (int)(idx - i * A.group);
+        const int64_t pos = s.q.first + i;
+        c.hi = s.hi;
+        if (a.causal && pos + 1 < c.hi) c.hi = pos + 1;
+        if (a.window > 0 && pos - a.window + 1 > 0) c.lo = pos - a.window + 1;
+    }
+    return c;
+}
+
+template <typename T> __device__ __forceinline__ void load_f32x8(const T *p, float *v);
+template <> __device__ __forceinline__ void load_f32x8<float>(const float *p, float *v)
+{
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+template <> __device__ __forceinline__ void load_f32x8<bf16_bits>(const bf16_bits *p, float *v)
+{
+    const uint4 d = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+template <typename T> __device__ __forceinline__ void store_f32x4(T *p, const float *v);
+template <> __device__ __forceinline__ void store_f32x4<float>(float *p, const float *v)
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <> __device__ __forceinline__ void store_f32x4<bf16_bits>(bf16_bits *p, const float *v)
+{
+    uint2 w;
+    w.x = f32_to_bf16(v[0]) | f32_to_bf16(v[1]) << 16;
+    w.y = f32_to_bf16(v[2]) | f32_to_bf16(v[3]) << 16;
+    *reinterpret_cast<uint2 *>(p) = w;
+}
+
+// A row's power of two: f * 2^k has its largest element in [2^14, 2^15).
+// Returns 2^k; *back is 2^-k.
+__device__ __forceinline__ float row_scale(float largest, float *back)
+{
+    int e = (int)(__float_as_uint(largest) >> 23) & 255;   // biased exponent
+    e = e < 27 ? 27 : (e > 254 ? 254 : e);                 // both powers stay normal
+    *back = __uint_as_float((uint32_t)(e - 14) << 23);
+    return __uint_as_float((uint32_t)(254 + 14 - e) << 23);
+}
+
+__device__ __forceinline__ float group_max(float v, int lane)   // over the four lanes of a column
+{
+    v = fmaxf(v, xor_lane<16>(v, lane));
+    return fmaxf(v, xor_lane<32>(v, lane));
+}
+__device__ __forceinline__ float group_sum(float v, int lane)
+{
+    v += xor_lane<16>(v, lane);
+    return v + xor_lane<32>(v, lane);
+}
+
+// The state of CT column tiles in one wave's registers.
+template <int D, int CT, int NP> struct State {
+    half8_t q[CT][D / 32][NP];
+    float c[CT];                 // log2(e) * scale / row power of two
+    float m[CT], l[CT];
+    float4_t o[CT][D / 16];
+};
+
+template <int D, int CT, int FMT, typename T>
+__global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
+{
+    constexpr int NP = Parts<T>::n, COLS = 16 * CT, KS = D / 32, DT = D / 16;
+    constexpr int LDO = D + 4;
+    __shared__ float sh_m[kWaves][COLS], sh_l[kWaves][COLS];
+    __shared__ float sh_o[2][COLS][LDO];
+    const KvAttnLaunch &a = A.a;
+    const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4, gk = r >> 2;
+    const int sh = a.c.block_shift, bmask = (1 << sh) - 1;
+
+    const int64_t total = stream_total(A, COLS), share = stream_share(A, total);
+    int64_t at = (int64_t)blockIdx.x * share;
+    const int64_t end = at + share < total ? at + share : total;
+    if (at >= end) return;
+    int64_t inside;
+    int b = kv_locate(a.s.batch, at, [&](int i) -> int64_t { return stream_seq(A, i, COLS).work; }, &inside);
+    if (b < 0) return;
+    b = __builtin_amdgcn_readfirstlane(b);
+    StreamSeq s = stream_seq(A, b, COLS);
+
+    while (at < end) {
+        while (inside >= s.work) {      // the next sequence with work
+            inside -= s.work;
+            if (++b >= a.s.batch) return;
+            s = stream_seq(A, b, COLS);
+        }
+        const int64_t seg = inside / s.nt, tile0 = inside - seg * s.nt;
+        const int head = (int)(seg / s.ct);
+        const int64_t ctile = seg - (int64_t)head * s.ct;
+        const int64_t tiles = s.nt - tile0 < end - at ? s.nt - tile0 : end - at;
+        const bool whole = tile0 == 0 && tiles == s.nt;
+
+        State<D, CT, NP> st;
+        int64_t seg_lo = INT64_MAX, seg_hi = 0, all_lo = 0, all_hi = INT64_MAX;
+        int64_t col_lo[CT], col_hi[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            const Column c = column(A, s, ctile * COLS + 16 * ct + r, head);
+            col_lo[ct] = c.lo, col_hi[ct] = c.hi;
+            float f[KS][8], top = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                if (c.row >= 0)
+                    load_f32x8<T>(static_cast<const T *>(a.q) + c.row * a.ldq + (int64_t)c.head * D + 64 * (ks >> 1) +
+                                      16 * g + 8 * (ks & 1), f[ks]);
+                else
+                    for (int i = 0; i < 8; ++i) f[ks][i] = 0.0f;
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[ks][i]));
+            }
+            float back;
+            const float up = row_scale(group_max(top, lane), &back);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                for (int i = 0; i < 8; ++i) f[ks][i] *= up;
+                split_half<NP>(f[ks], st.q[ct][ks]);
+            }
+            st.c[ct] = a.scale * kLog2e * back;
+            st.m[ct] = kNegInf;
+            st.l[ct] = 0.0f;
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) st.o[ct][dt] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        // tokens that some column sees, and tokens that every column sees
+        {
+            const int64_t n = s.q.n * A.group;
+            const Column first = column(A, s, ctile * COLS, head);
+            const int64_t li = ctile * COLS + COLS - 1 < n - 1 ? ctile * COLS + COLS - 1 : n - 1;
+            const Column last = column(A, s, li, head);
+            seg_lo = first.lo, seg_hi = last.hi, all_lo = last.lo, all_hi = first.hi;
+        }
+
+        for (int64_t ti = tile0 + wave; ti < tile0 + tiles; ti += kWaves) {
+            const int64_t base = (s.t0 + ti) << 6;
+            // block of this lane's key rows, and of its value and score tokens
+            const int64_t pk = base + 16 * gk, pv = base + 16 * g;
+            int64_t idk = -1, idv = -1;
+            if (pk < seg_hi && pk + 16 > seg_lo) idk = kv_block(a.s, a.c.blocks, b, pk >> sh);
+            if (pv < seg_hi && pv + 16 > seg_lo) idv = kv_block(a.s, a.c.blocks, b, pv >> sh);
+            const bool has = idv >= 0;
+            const bool masked = base < all_lo || base + kTile > all_hi || __any(!has);
+            idk = idk < 0 ? 0 : idk;
+            const int64_t idv0 = has ? idv : 0;
+            const uint8_t *kp = a.c.k_codes + (((idk * a.c.kv_heads + head) << sh) + (pk & bmask) + (r & 3)) * D + 16 * g;
+            const uint8_t *vp = a.c.v_codes + (((idv0 * a.c.kv_heads + head) * D + r) << sh) + (pv & bmask);
+            uint4 kw[4][D / 64], vw[DT];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) kw[n][j] = *reinterpret_cast<const uint4 *>(kp + 4 * n * D + 64 * j);
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) vw[dt] = *reinterpret_cast<const uint4 *>(vp + ((int64_t)(16 * dt) << sh));
+            float sk = 0.0f, sv = 1.0f;
+            if (has) {
+                sk = a.c.k_scales[idv * a.c.kv_heads + head];
+                sv = a.c.v_scales[idv * a.c.kv_heads + head];
+                if (sv == 0.0f) sv = kZeroBlockScale;
+            }
+            if (masked) {
+                // codes of tokens that no column sees are whatever memory
+                // holds, an E4M3 NaN for instance: make them zero codes
+                uint32_t keep[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    keep[w] = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int64_t t = pv + 4 * w + e;
+                        if (has && t >= seg_lo && t < seg_hi) keep[w] |= 255u << (8 * e);
+                    }
+                }
+                constexpr uint32_t z = KvFmt<FMT>::zero4;
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) {
+                    vw[dt].x = (vw[dt].x & keep[0]) | (z & ~keep[0]);
+                    vw[dt].y = (vw[dt].y & keep[1]) | (z & ~keep[1]);
+                    vw[dt].z = (vw[dt].z & keep[2]) | (z & ~keep[2]);
+                    vw[dt].w = (vw[dt].w & keep[3]) | (z & ~keep[3]);
+                }
+            }
+
+            float4_t S[CT][4];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) S[ct][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) {
+                    const half8_t k0 = codes_to_half<FMT>(kw[n][j].x, kw[n][j].y);
+                    const half8_t k1 = codes_to_half<FMT>(kw[n][j].z, kw[n][j].w);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) {
+                            S[ct][n] = mfma(k0, st.q[ct][2 * j][p], S[ct][n]);
+                            S[ct][n] = mfma(k1, st.q[ct][2 * j + 1][p], S[ct][n]);
+                        }
+                }
+            const float lsv = fast_log2(sv), isv = 1.0f / sv;
+            half8_t P[CT][2][NP];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const float f = st.c[ct] * sk;
+                float x[16], mx = kNegInf;
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v = S[ct][n][i];
+                        v = fmaf(v, f, lsv);
+                        if (masked) {
+                            const int64_t t = pv + 4 * n + i;
+                            if (!has || t < col_lo[ct] || t >= col_hi[ct]) v = kNegInf;
+                        }
+                        x[4 * n + i] = v;
+                        mx = fmaxf(mx, v);
+                    }
+                const float mnew = fmaxf(st.m[ct], group_max(mx, lane));
+                const float mref = mnew == kNegInf ? 0.0f : mnew;   // no token yet: every weight is 2^-inf
+                const float alpha = fast_exp2(st.m[ct] - mref);
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    x[i] = fast_exp2(x[i] - mref + kPScale);
+                    sum += x[i];
+                }
+                st.m[ct] = mnew;
+                st.l[ct] = fmaf(st.l[ct], alpha, sum * isv);
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) st.o[ct][dt] *= alpha;
+                split_half<NP>(x, P[ct][0]);
+                split_half<NP>(x + 8, P[ct][1]);
+            }
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) {
+                const half8_t v0 = codes_to_half<FMT>(vw[dt].x, vw[dt].y);
+                const half8_t v1 = codes_to_half<FMT>(vw[dt].z, vw[dt].w);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
+                        st.o[ct][dt] = mfma(v0, P[ct][0][p], st.o[ct][dt]);
+                        st.o[ct][dt] = mfma(v1, P[ct][1][p], st.o[ct][dt]);
+                    }
+            }
+        }
+
+        // join the four waves: maxima first, then two rounds of pairwise sums
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            st.l[ct] = group_sum(st.l[ct], lane);
+            if (g == 0) sh_m[wave][16 * ct + r] = st.m[ct];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            const int col = 16 * ct + r;
+            float m = sh_m[0][col];
+            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh_m[w][col]);
+            const float f = m == kNegInf ? 0.0f : fast_exp2(st.m[ct] - m);
+            st.m[ct] = m;
+            st.l[ct] *= f;
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) st.o[ct][dt] *= f;
+            if (g == 0) sh_l[wave][col] = st.l[ct];
+        }
+        for (int step = 2; step >= 1; step >>= 1) {
+            if (wave >= step && wave < 2 * step)
+                for (int ct = 0; ct < CT; ++ct)
+                    for (int dt = 0; dt < DT; ++dt)
+                        *reinterpret_cast<float4_t *>(&sh_o[wave - step][16 * ct + r][16 * dt + 4 * g]) = st.o[ct][dt];
+            __syncthreads();
+            if (wave < step)
+                for (int ct = 0; ct < CT; ++ct)
+                    for (int dt = 0; dt < DT; ++dt)
+                        st.o[ct][dt] += *reinterpret_cast<float4_t *>(&sh_o[wave][16 * ct + r][16 * dt + 4 * g]);
+            __syncthreads();
+        }
+        if (wave == 0) {
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (tile0 == 0 ? 1 : 0);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const int col = 16 * ct + r;
+                const float l = sh_l[0][col] + sh_l[1][col] + sh_l[2][col] + sh_l[3][col];
+                const Column c = column(A, s, ctile * COLS + col, head);
+                if (c.row < 0) continue;
+                if (whole) {
+                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                    T *out = static_cast<T *>(a.out) + (c.row * a.q_heads + c.head) * D;
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt) {
+                        float v[4];
+                        for (int i = 0; i < 4; ++i) v[i] = st.o[ct][dt][i] * inv;
+                        store_f32x4<T>(out + 16 * dt + 4 * g, v);
+                    }
+                    if (a.lse && g == 0)
+                        a.lse[c.row * a.q_heads + c.head] = l > 0.0f ? (st.m[ct] - kPScale + fast_log2(l)) * kLn2 : kNegInf;
+                } else {
+                    float *po = A.part_o + (slot * COLS + col) * D;
+                    float *pm = A.part_ml + (slot * COLS + col) * 2;
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt)
+                        *reinterpret_cast<float4_t *>(po + 16 * dt + 4 * g) = st.o[ct][dt];
+                    if (g == 0) pm[0] = st.m[ct], pm[1] = l;
+                }
+            }
+        }
+        __syncthreads();
+        at += tiles;
+        inside += tiles;
+    }
+}
+
+// Joins the parts of the segments that several workgroups shared, in the
+// order of the tokens.  Workgroup j looks at the border between workers j and
+// j + 1; the one at the first border inside a segment joins it.
+template <int D, int CT, typename T>
+__global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs A)
+{
+    constexpr int COLS = 16 * CT;
+    const KvAttnLaunch &a = A.a;
+    const int64_t total = stream_total(A, COLS), share = stream_share(A, total);
+    const int64_t border = ((int64_t)blockIdx.x + 1) * share;
+    if (border >= total) return;
+    int64_t inside;
+    const int b = kv_locate(a.s.batch, border, [&](int i) -> int64_t { return stream_seq(A, i, COLS).work; }, &inside);
+    if (b < 0) return;
+    const StreamSeq s = stream_seq(A, b, COLS);
+    const int64_t seg = inside / s.nt, tile = inside - seg * s.nt;
+    if (tile == 0 || tile > share) return;     // between segments, or not the first border inside
+    const int head = (int)(seg / s.ct);
+    const int64_t ctile = seg - (int64_t)head * s.ct;
+    const int64_t w0 = blockIdx.x, w1 = (border - tile + s.nt - 1) / share;
+
+    for (int i = (int)threadIdx.x; i < COLS * (D / 4); i += 256) {
+        const int col = i / (D / 4), d = (i % (D / 4)) * 4;
+        const Column c = column(A, s, ctile * COLS + col, head);
+        if (c.row < 0) continue;
+        float m = kNegInf;
+        for (int64_t w = w0; w <= w1; ++w)
+            m = fmaxf(m, A.part_ml[((2 * w + (w == w0 ? 1 : 0)) * COLS + col) * 2]);
+        float l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (m != kNegInf)
+            for (int64_t w = w0; w <= w1; ++w) {
+                const int64_t at = (2 * w + (w == w0 ? 1 : 0)) * COLS + col;
+                const float f = fast_exp2(A.part_ml[2 * at] - m);
+                const float4 o = *reinterpret_cast<const float4 *>(A.part_o + at * D + d);
+                l = fmaf(f, A.part_ml[2 * at + 1], l);
+                v[0] = fmaf(f, o.x, v[0]), v[1] = fmaf(f, o.y, v[1]);
+                v[2] = fmaf(f, o.z, v[2]), v[3] = fmaf(f, o.w, v[3]);
+            }
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        for (int e = 0; e < 4; ++e) v[e] *= inv;
+        store_f32x4<T>(static_cast<T *>(a.out) + (c.row * a.q_heads + c.head) * D + d, v);
+        if (a.lse && d == 0)
+            a.lse[c.row * a.q_heads + c.head] = l > 0.0f ? (m - kPScale + fast_log2(l)) * kLn2 : kNegInf;
+    }
+}
+
+// Column tiles per wave: as many columns as one sequence's rows of a head
+// are likely to fill.
+int stream_ct(const KvAttnLaunch &a)
+{
+    const int64_t group = a.q_heads / a.c.kv_heads;
+    const int64_t per = a.s.rows > a.s.batch ? (a.s.rows + a.s.batch - 1) / a.s.batch : 1;
+    const int64_t cols = per * group;
+    return cols <= 16 || a.c.head_dim > 128 ? 1 : 2;
+}
+
+constexpr int kWorkers = 512;   // two workgroups of four waves per compute unit
+
+template <int D, int CT, int FMT, typename T> hipError_t stream_go(const AttnArgs &A, hipStream_t stream)
+{
+    kv_stream_kernel<D, CT, FMT, T><<<A.workers, 64 * kWaves, 0, stream>>>(A);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    kv_join_kernel<D, CT, T><<<A.workers - 1, 256, 0, stream>>>(A);
+    return hipGetLastError();
+}
+
+template <int D, int CT> hipError_t stream_types(const AttnArgs &A, hipStream_t stream)
+{
+    if (A.a.format == KV_INT8)
+        return A.a.x_dt == 0 ? stream_go<D, CT, KV_INT8, float>(A, stream) : stream_go<D, CT, KV_INT8, bf16_bits>(A, stream);
+    return A.a.x_dt == 0 ? stream_go<D, CT, KV_FP8, float>(A, stream) : stream_go<D, CT, KV_FP8, bf16_bits>(A, stream);
+}
+
+}  // namespace
+
+size_t kv_attn_ws_bytes(const KvAttnLaunch &a)
+{
+    const size_t cols = 16 * (size_t)stream_ct(a), slots = 2 * kWorkers;
+    return slots * cols * ((size_t)a.c.head_dim + 2) * sizeof(float);
+}
+
+hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream)
+{
+    AttnArgs A;
+    A.a = a;
+    A.workers = kWorkers;
+    A.group = a.q_heads / a.c.kv_heads;
+    const int ct = stream_ct(a);
+    A.part_o = static_cast<float *>(a.workspace);
+    A.part_ml = A.part_o + (size_t)2 * kWorkers * 16 * ct * a.c.head_dim;
+    switch (a.c.head_dim) {
+    case 64: return ct == 1 ? stream_types<64, 1>(A, stream) : stream_types<64, 2>(A, stream);
+    case 128: return ct == 1 ? stream_types<128, 1>(A, stream) : stream_types<128, 2>(A, stream);
+    case 192: return stream_types<192, 1>(A, stream);
+    default: return stream_types<256, 1>(A, stream);
+    }
+}
+
+}  // namespace nqk

@@ -11,6 +11,7 @@
 
 #include "nq.h"
 #include "nq_internal.h"
+#include "nq_kv.h"
 
 namespace {
 
@@ -363,6 +364,159 @@ nq_status check_global_scale(const char *op, int mode, const float *g)
         return fail(NQ_ERR_QUANT, "%s: a global scale is only defined for NQ_NVFP4", op);
     if (g && !aligned_to(g, 4)) return fail(NQ_ERR_ALIGN, "%s: global scales must be 4-byte aligned", op);
     return NQ_OK;
+}
+
+// ---- key/value cache and routing
+bool finite(float f) { return f - f == 0.0f; }
+
+nq_status check_kv_cache(const char *op, const nq_kv_cache *c)
+{
+    if (!c) return fail(NQ_ERR_NULL, "%s: cache is null", op);
+    if (c->format != NQ_KV_INT8 && c->format != NQ_KV_FP8)
+        return fail(NQ_ERR_QUANT, "%s: unknown cache format=%d", op, c->format);
+    if (c->block_tokens != 16 && c->block_tokens != 32 && c->block_tokens != 64 && c->block_tokens != 128)
+        return fail(NQ_ERR_QUANT, "%s: block_tokens=%d is not 16, 32, 64 or 128", op, c->block_tokens);
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 192 && c->head_dim != 256)
+        return fail(NQ_ERR_SHAPE, "%s: head_dim=%d is not 64, 128, 192 or 256", op, c->head_dim);
+    if (c->kv_heads < 1 || c->kv_heads > 65535)
+        return fail(NQ_ERR_SHAPE, "%s: kv_heads=%d is not in 1 .. 65535", op, c->kv_heads);
+    if (c->blocks < 1 || c->blocks >= kMaxDim)
+        return fail(NQ_ERR_SHAPE, "%s: blocks=%lld is not in 1 .. 2^31 - 1", op, (long long)c->blocks);
+    if (c->blocks > (kMaxElems << 6) / ((int64_t)c->kv_heads * c->head_dim * c->block_tokens))
+        return fail(NQ_ERR_SHAPE, "%s: the cache is too large", op);
+    return NQ_OK;
+}
+
+// The pointers, once the call is known to have work.
+nq_status check_kv_pointers(const char *op, const nq_kv_cache *c, const nq_kv_seqs *s)
+{
+    if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales)
+        return fail(NQ_ERR_NULL, "%s: the cache's codes and scales must be non-null", op);
+    if (!s->row_start || !s->lengths || (s->max_blocks > 0 && !s->block_table))
+        return fail(NQ_ERR_NULL, "%s: row_start, lengths and block_table must be non-null", op);
+    if (!aligned16(c->k_codes) || !aligned16(c->v_codes))
+        return fail(NQ_ERR_ALIGN, "%s: the cache's codes must be 16-byte aligned", op);
+    if (!aligned_to(c->k_scales, 4) || !aligned_to(c->v_scales, 4) || !aligned_to(s->row_start, 4) ||
+        !aligned_to(s->lengths, 4) || !aligned_to(s->block_table, 4))
+        return fail(NQ_ERR_ALIGN, "%s: scales, row_start, lengths and block_table must be 4-byte aligned", op);
+    return NQ_OK;
+}
+
+nq_status check_kv_seqs(const char *op, const nq_kv_seqs *s)
+{
+    if (!s) return fail(NQ_ERR_NULL, "%s: seqs is null", op);
+    if (s->batch < 0 || s->rows < 0 || s->max_blocks < 0)
+        return fail(NQ_ERR_SHAPE, "%s: negative size (batch=%lld, rows=%lld, max_blocks=%lld)", op,
+                    (long long)s->batch, (long long)s->rows, (long long)s->max_blocks);
+    if (s->batch > (1 << 24) || s->rows > ((int64_t)1 << 30) || s->max_blocks >= kMaxDim || s->table_stride >= kMaxDim)
+        return fail(NQ_ERR_SHAPE, "%s: size too large (batch=%lld, rows=%lld, max_blocks=%lld)", op,
+                    (long long)s->batch, (long long)s->rows, (long long)s->max_blocks);
+    if (s->table_stride < s->max_blocks)
+        return fail(NQ_ERR_SHAPE, "%s: table_stride=%lld is below max_blocks=%lld", op, (long long)s->table_stride,
+                    (long long)s->max_blocks);
+    return NQ_OK;
+}
+
+nq_status check_kv_rows(const char *op, const char *name, const void *p, int64_t ld, int64_t width, int64_t bytes)
+{
+    if (!p) return fail(NQ_ERR_NULL, "%s: %s must be non-null", op, name);
+    if (!aligned16(p)) return fail(NQ_ERR_ALIGN, "%s: %s must be 16-byte aligned", op, name);
+    if (ld < width || ld >= kMaxDim)
+        return fail(NQ_ERR_SHAPE, "%s: row stride %lld of %s is below its %lld columns or too large", op, (long long)ld,
+                    name, (long long)width);
+    if (ld * bytes % 16 != 0)
+        return fail(NQ_ERR_ALIGN, "%s: row stride %lld of %s is not a multiple of 16 bytes", op, (long long)ld, name);
+    return NQ_OK;
+}
+
+int64_t kv_code_bytes(const nq_kv_cache *c)
+{
+    return c->blocks * c->kv_heads * c->head_dim * (int64_t)c->block_tokens;
+}
+int64_t kv_scale_bytes(const nq_kv_cache *c) { return c->blocks * c->kv_heads * 4; }
+
+// Whether a span overlaps any of the cache's arrays.
+bool overlaps_cache(const nq_kv_cache *c, Span s)
+{
+    return overlap(s, Span{c->k_codes, kv_code_bytes(c)}) || overlap(s, Span{c->v_codes, kv_code_bytes(c)}) ||
+           overlap(s, Span{c->k_scales, kv_scale_bytes(c)}) || overlap(s, Span{c->v_scales, kv_scale_bytes(c)});
+}
+bool overlaps_seqs(const nq_kv_seqs *q, Span s)
+{
+    return overlap(s, Span{q->row_start, (q->batch + 1) * 4}) || overlap(s, Span{q->lengths, q->batch * 4}) ||
+           overlap(s, Span{q->block_table, ((q->batch - 1) * q->table_stride + q->max_blocks) * 4});
+}
+// The cache's own arrays must be apart, and apart from the tables.
+nq_status check_kv_apart(const char *op, const nq_kv_cache *c, const nq_kv_seqs *s)
+{
+    const Span a[4] = {{c->k_codes, kv_code_bytes(c)}, {c->v_codes, kv_code_bytes(c)},
+                       {c->k_scales, kv_scale_bytes(c)}, {c->v_scales, kv_scale_bytes(c)}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(a[i], a[j])) return fail(NQ_ERR_ALIAS, "%s: the cache's arrays overlap", op);
+        if (overlaps_seqs(s, a[i])) return fail(NQ_ERR_ALIAS, "%s: the cache overlaps seqs' arrays", op);
+    }
+    return NQ_OK;
+}
+
+nqk::KvCache kv_cache_of(const nq_kv_cache *c)
+{
+    nqk::KvCache k;
+    k.k_codes = static_cast<uint8_t *>(c->k_codes), k.v_codes = static_cast<uint8_t *>(c->v_codes);
+    k.k_scales = c->k_scales, k.v_scales = c->v_scales;
+    k.blocks = c->blocks, k.kv_heads = c->kv_heads, k.head_dim = c->head_dim;
+    k.block_shift = c->block_tokens == 16 ? 4 : c->block_tokens == 32 ? 5 : c->block_tokens == 64 ? 6 : 7;
+    return k;
+}
+
+nqk::KvSeqs kv_seqs_of(const nq_kv_seqs *s)
+{
+    nqk::KvSeqs k;
+    k.row_start = s->row_start, k.lengths = s->lengths, k.table = s->block_table;
+    k.rows = s->rows, k.max_blocks = s->max_blocks, k.ldt = s->table_stride, k.batch = (int)s->batch;
+    return k;
+}
+
+int64_t rows_span(int64_t rows, int64_t ld, int64_t width, int64_t bytes)
+{
+    return rows > 0 ? ((rows - 1) * ld + width) * bytes : 0;
+}
+
+nq_status check_router(const char *op, const nq_moe_router *r)
+{
+    if (!r) return fail(NQ_ERR_NULL, "%s: router is null", op);
+    if (r->score != NQ_MOE_SOFTMAX && r->score != NQ_MOE_SIGMOID)
+        return fail(NQ_ERR_QUANT, "%s: unknown score=%d", op, r->score);
+    if (r->experts < 1 || r->experts > 1024)
+        return fail(NQ_ERR_SHAPE, "%s: experts=%d is not in 1 .. 1024", op, r->experts);
+    if (r->groups < 1 || r->groups > 64 || r->experts % r->groups)
+        return fail(NQ_ERR_SHAPE, "%s: groups=%d is not in 1 .. 64 or does not divide experts=%d", op, r->groups, r->experts);
+    if (r->top_groups < 1 || r->top_groups > r->groups)
+        return fail(NQ_ERR_SHAPE, "%s: top_groups=%d is not in 1 .. groups=%d", op, r->top_groups, r->groups);
+    if (r->group_best < 1 || r->group_best > 2 || (r->group_best == 2 && r->groups > 1 && r->experts / r->groups < 2))
+        return fail(NQ_ERR_SHAPE, "%s: group_best=%d is not 1 or 2, or a group has fewer experts", op, r->group_best);
+    if (r->top_k < 1 || r->top_k > 32 || r->top_k > r->top_groups * (r->experts / r->groups))
+        return fail(NQ_ERR_SHAPE, "%s: top_k=%d is not in 1 .. 32 or passes the experts of the kept groups", op, r->top_k);
+    if (!finite(r->scale)) return fail(NQ_ERR_SHAPE, "%s: scale is not finite", op);
+    return NQ_OK;
+}
+
+nq_status check_moe_logits(const char *op, const nq_moe_router *r, int x_dt, int64_t tokens, int64_t ld)
+{
+    if (!dtype_ok(x_dt)) return fail(NQ_ERR_DTYPE, "%s: unknown dtype x_dt=%d", op, x_dt);
+    if (tokens < 0 || tokens > ((int64_t)1 << 30))
+        return fail(NQ_ERR_SHAPE, "%s: tokens=%lld is negative or too large", op, (long long)tokens);
+    if (ld < r->experts || ld >= kMaxDim)
+        return fail(NQ_ERR_SHAPE, "%s: row stride %lld is below experts=%d or too large", op, (long long)ld, r->experts);
+    return NQ_OK;
+}
+
+nqk::MoeRoute moe_of(const nq_moe_router *r)
+{
+    nqk::MoeRoute m;
+    m.experts = r->experts, m.score = r->score, m.groups = r->groups, m.top_groups = r->top_groups;
+    m.group_best = r->group_best, m.top_k = r->top_k, m.renormalise = r->renormalise, m.scale = r->scale;
+    return m;
 }
 
 }  // namespace
@@ -1060,6 +1214,155 @@ nq_status nq_fp_qmm_notrans(const void *x, nq_dtype x_dt, int64_t m, int64_t ni,
             return fail(NQ_ERR_ALIAS, "%s: the workspace overlaps an argument", op);
     }
     return check_launch(op, nqk::launch_fp_qmm_nt(a, stream));
+}
+
+// ---- key/value cache
+nq_status nq_kv_append(const nq_kv_cache *cache, const nq_kv_seqs *seqs, const void *k, int64_t ldk,
+                       const void *v, int64_t ldv, nq_dtype x_dt, hipStream_t stream)
+{
+    const char *op = "nq_kv_append";
+    g_last_error.clear();
+    if (!dtype_ok(x_dt)) return fail(NQ_ERR_DTYPE, "%s: unknown dtype x_dt=%d", op, (int)x_dt);
+    nq_status st;
+    if ((st = check_kv_cache(op, cache)) || (st = check_kv_seqs(op, seqs))) return st;
+    if (seqs->rows == 0 || seqs->batch == 0) return NQ_OK;
+    if ((st = check_kv_pointers(op, cache, seqs)) || (st = check_kv_apart(op, cache, seqs))) return st;
+    const int64_t width = (int64_t)cache->kv_heads * cache->head_dim, xb = dtype_bytes(x_dt);
+    if ((st = check_kv_rows(op, "k", k, ldk, width, xb)) || (st = check_kv_rows(op, "v", v, ldv, width, xb))) return st;
+    if (overlaps_cache(cache, Span{k, rows_span(seqs->rows, ldk, width, xb)}) ||
+        overlaps_cache(cache, Span{v, rows_span(seqs->rows, ldv, width, xb)}))
+        return fail(NQ_ERR_ALIAS, "%s: the cache overlaps k or v", op);
+    nqk::KvAppendLaunch a;
+    a.c = kv_cache_of(cache), a.s = kv_seqs_of(seqs);
+    a.k = k, a.v = v, a.ldk = ldk, a.ldv = ldv, a.x_dt = x_dt, a.format = cache->format;
+    return check_launch(op, nqk::launch_kv_append(a, stream));
+}
+
+nq_status nq_kv_read(const nq_kv_cache *cache, const nq_kv_seqs *seqs, void *k, void *v, nq_dtype out_dt,
+                     hipStream_t stream)
+{
+    const char *op = "nq_kv_read";
+    g_last_error.clear();
+    if (!dtype_ok(out_dt)) return fail(NQ_ERR_DTYPE, "%s: unknown dtype out_dt=%d", op, (int)out_dt);
+    nq_status st;
+    if ((st = check_kv_cache(op, cache)) || (st = check_kv_seqs(op, seqs))) return st;
+    if (seqs->rows == 0 || seqs->batch == 0) return NQ_OK;
+    if ((st = check_kv_pointers(op, cache, seqs))) return st;
+    if (!k || !v) return fail(NQ_ERR_NULL, "%s: k and v must be non-null", op);
+    if (!aligned16(k) || !aligned16(v)) return fail(NQ_ERR_ALIGN, "%s: k and v must be 16-byte aligned", op);
+    const int64_t bytes = seqs->rows * cache->kv_heads * cache->head_dim * dtype_bytes(out_dt);
+    const Span sk{k, bytes}, sv{v, bytes};
+    if (overlap(sk, sv) || overlaps_cache(cache, sk) || overlaps_cache(cache, sv) || overlaps_seqs(seqs, sk) ||
+        overlaps_seqs(seqs, sv))
+        return fail(NQ_ERR_ALIAS, "%s: an output overlaps an input or the other output", op);
+    nqk::KvReadLaunch a;
+    a.c = kv_cache_of(cache), a.s = kv_seqs_of(seqs);
+    a.k = k, a.v = v, a.out_dt = out_dt, a.format = cache->format;
+    return check_launch(op, nqk::launch_kv_read(a, stream));
+}
+
+size_t nq_kv_attention_workspace_bytes(const nq_kv_cache *cache, const nq_kv_seqs *seqs, int32_t q_heads,
+                                       nq_dtype x_dt)
+{
+    const char *op = "nq_kv_attention_workspace_bytes";
+    g_last_error.clear();
+    if (check_kv_cache(op, cache) || check_kv_seqs(op, seqs) || !dtype_ok(x_dt) || q_heads < 1 ||
+        q_heads % cache->kv_heads || seqs->rows == 0 || seqs->batch == 0)
+        return 0;
+    nqk::KvAttnLaunch a{};
+    a.c = kv_cache_of(cache), a.s = kv_seqs_of(seqs), a.q_heads = q_heads, a.x_dt = x_dt, a.format = cache->format;
+    return nqk::kv_attn_ws_bytes(a);
+}
+
+nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, const void *q, nq_dtype x_dt,
+                          int64_t ldq, int32_t q_heads, float softmax_scale, int32_t causal, int64_t window,
+                          void *out, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const char *op = "nq_kv_attention";
+    g_last_error.clear();
+    if (!dtype_ok(x_dt)) return fail(NQ_ERR_DTYPE, "%s: unknown dtype x_dt=%d", op, (int)x_dt);
+    nq_status st;
+    if ((st = check_kv_cache(op, cache)) || (st = check_kv_seqs(op, seqs))) return st;
+    if (q_heads < 1 || q_heads > 65535 || q_heads % cache->kv_heads)
+        return fail(NQ_ERR_SHAPE, "%s: q_heads=%d is not a multiple of kv_heads=%d in 1 .. 65535", op, q_heads,
+                    cache->kv_heads);
+    if (!finite(softmax_scale) || !(softmax_scale > 0.0f))
+        return fail(NQ_ERR_SHAPE, "%s: softmax_scale is not finite and positive", op);
+    if (window < 0 || (window > 0 && !causal))
+        return fail(NQ_ERR_SHAPE, "%s: window=%lld is negative, or set without causal", op, (long long)window);
+    if (seqs->rows == 0 || seqs->batch == 0) return NQ_OK;
+    if ((st = check_kv_pointers(op, cache, seqs))) return st;
+    const int64_t width = (int64_t)q_heads * cache->head_dim, xb = dtype_bytes(x_dt);
+    if ((st = check_kv_rows(op, "q", q, ldq, width, xb)) || (st = check_kv_rows(op, "out", out, width, width, xb)))
+        return st;
+    if (!aligned_to(lse, 4)) return fail(NQ_ERR_ALIGN, "%s: lse must be 4-byte aligned", op);
+    const Span so{out, seqs->rows * width * xb}, sl{lse, lse ? seqs->rows * q_heads * 4 : 0},
+        sq{q, rows_span(seqs->rows, ldq, width, xb)};
+    if (overlap(so, sq) || overlap(so, sl) || overlap(sl, sq) || overlaps_cache(cache, so) || overlaps_cache(cache, sl) ||
+        overlaps_seqs(seqs, so) || overlaps_seqs(seqs, sl))
+        return fail(NQ_ERR_ALIAS, "%s: an output overlaps an input or the other output", op);
+    nqk::KvAttnLaunch a{};
+    a.c = kv_cache_of(cache), a.s = kv_seqs_of(seqs);
+    a.q = q, a.ldq = ldq, a.out = out, a.lse = lse, a.workspace = workspace, a.q_heads = q_heads, a.x_dt = x_dt;
+    a.format = cache->format, a.causal = causal != 0, a.window = window, a.scale = softmax_scale;
+    const size_t need = nqk::kv_attn_ws_bytes(a);
+    if (need) {
+        if (!workspace || workspace_bytes < need)
+            return fail(NQ_ERR_WORKSPACE, "%s: workspace of %zu bytes needed (got %zu)", op, need,
+                        workspace ? workspace_bytes : (size_t)0);
+        if (!aligned16(workspace)) return fail(NQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", op);
+        const Span sw{workspace, (int64_t)need};
+        if (overlap(sw, so) || overlap(sw, sl) || overlap(sw, sq) || overlaps_cache(cache, sw) || overlaps_seqs(seqs, sw))
+            return fail(NQ_ERR_ALIAS, "%s: the workspace overlaps an argument", op);
+    }
+    return check_launch(op, nqk::launch_kv_attention(a, stream));
+}
+
+// ---- expert routing
+nq_status nq_moe_route(const nq_moe_router *router, const void *logits, nq_dtype x_dt, int64_t tokens,
+                       int64_t ld, const float *bias, uint32_t *ids, float *weights, hipStream_t stream)
+{
+    const char *op = "nq_moe_route";
+    g_last_error.clear();
+    nq_status st;
+    if ((st = check_router(op, router)) || (st = check_moe_logits(op, router, x_dt, tokens, ld))) return st;
+    if (tokens == 0) return NQ_OK;
+    if (!logits || !ids || !weights) return fail(NQ_ERR_NULL, "%s: logits, ids and weights must be non-null", op);
+    const int64_t xb = dtype_bytes(x_dt), out = tokens * router->top_k * 4;
+    if (!aligned_to(logits, xb) || !aligned_to(bias, 4) || !aligned_to(ids, 4) || !aligned_to(weights, 4))
+        return fail(NQ_ERR_ALIGN, "%s: an array is not aligned to its element size", op);
+    const Span si{ids, out}, sw{weights, out}, sl{logits, rows_span(tokens, ld, router->experts, xb)},
+        sb{bias, bias ? (int64_t)router->experts * 4 : 0};
+    if (overlap(si, sw) || overlap(si, sl) || overlap(si, sb) || overlap(sw, sl) || overlap(sw, sb))
+        return fail(NQ_ERR_ALIAS, "%s: an output overlaps an input or the other output", op);
+    nqk::MoeRouteLaunch a;
+    a.r = moe_of(router), a.logits = logits, a.bias = bias, a.tokens = tokens, a.ldl = ld;
+    a.ids = ids, a.weights = weights, a.x_dt = x_dt;
+    return check_launch(op, nqk::launch_moe_route(a, stream));
+}
+
+nq_status nq_moe_route_grad(const nq_moe_router *router, const void *logits, nq_dtype x_dt, int64_t tokens,
+                            int64_t ld, const uint32_t *ids, const float *dweights, void *dlogits,
+                            hipStream_t stream)
+{
+    const char *op = "nq_moe_route_grad";
+    g_last_error.clear();
+    nq_status st;
+    if ((st = check_router(op, router)) || (st = check_moe_logits(op, router, x_dt, tokens, ld))) return st;
+    if (tokens == 0) return NQ_OK;
+    if (!logits || !ids || !dweights || !dlogits)
+        return fail(NQ_ERR_NULL, "%s: logits, ids, dweights and dlogits must be non-null", op);
+    const int64_t xb = dtype_bytes(x_dt), in = tokens * router->top_k * 4;
+    if (!aligned_to(logits, xb) || !aligned_to(dlogits, xb) || !aligned_to(ids, 4) || !aligned_to(dweights, 4))
+        return fail(NQ_ERR_ALIGN, "%s: an array is not aligned to its element size", op);
+    const Span sd{dlogits, tokens * router->experts * xb};
+    if (overlap(sd, Span{logits, rows_span(tokens, ld, router->experts, xb)}) || overlap(sd, Span{ids, in}) ||
+        overlap(sd, Span{dweights, in}))
+        return fail(NQ_ERR_ALIAS, "%s: dlogits overlaps an input", op);
+    nqk::MoeGradLaunch a;
+    a.r = moe_of(router), a.logits = logits, a.ids = ids, a.dweights = dweights, a.dlogits = dlogits;
+    a.tokens = tokens, a.ldl = ld, a.x_dt = x_dt;
+    return check_launch(op, nqk::launch_moe_route_grad(a, stream));
 }
 
 const char *nq_status_string(nq_status s)

@@ -426,6 +426,143 @@ nq_status nq_fp_qmm_notrans(const void *x, nq_dtype x_dt, int64_t m, int64_t ni,
                             int32_t row_exact, void *y, void *workspace, size_t workspace_bytes,
                             hipStream_t stream);
 
+/* ---------------------------------------------------------------- key/value cache in 8 bits */
+
+/* A paged cache of attention keys and values in 8 bits, written as tokens
+ * arrive and read by attention.  Tokens lie in blocks of block_tokens (16,
+ * 32, 64 or 128) slots; every block has, for each key/value head, one fp32
+ * scale for its keys and one for its values, and a value is scale * c:
+ *   NQ_KV_INT8  c = byte - 128, -127 <= c <= 127;
+ *   NQ_KV_FP8   c = the byte as an E4M3 number (see NQ_MXFP8), |c| <= 448.
+ * Layout (dense): k_codes [blocks, kv_heads, block_tokens, head_dim] bytes;
+ * v_codes [blocks, kv_heads, head_dim, block_tokens] bytes -- values are kept
+ * transposed inside a block, the order in which the product of weights and
+ * values reads them; k_scales and v_scales [blocks, kv_heads] fp32.  head_dim
+ * is 64, 128, 192 or 256.  The arrays belong to the caller; the codes' base
+ * pointers are 16-byte aligned, the scales' 4-byte aligned.  A new cache
+ * needs no initialisation: nothing is read that was not written. */
+typedef enum { NQ_KV_INT8 = 1, NQ_KV_FP8 = 2 } nq_kv_format;
+typedef struct {
+    void *k_codes, *v_codes;
+    float *k_scales, *v_scales;
+    int64_t blocks;       /* 1 .. 2^31 - 1 */
+    int32_t kv_heads;     /* 1 .. 65535 */
+    int32_t head_dim;
+    int32_t block_tokens;
+    int32_t format;       /* nq_kv_format */
+} nq_kv_cache;
+
+/* The sequences of a call (device arrays of int32, 4-byte aligned).  The
+ * call's rows row_start[b] .. row_start[b + 1] - 1 belong to sequence b and
+ * are the LAST tokens of its lengths[b] tokens: row i is token lengths[b] -
+ * row_start[b + 1] + i.  So a serving step adds its new tokens to lengths,
+ * then calls nq_kv_append and nq_kv_attention with the same arrays.  Token t
+ * lies in slot t % block_tokens of block block_table[b * table_stride + t /
+ * block_tokens].  Sequences may have any number of rows, none included, and
+ * any length, 0 included.
+ * The contents are read on the device and cannot be checked before the call;
+ * whatever they hold, only the cache, the rows and the outputs are touched:
+ * row_start is clamped to 0 .. rows and to an order that does not fall, a
+ * negative length counts as 0, and a token whose block lies past max_blocks or whose id is
+ * not in 0 .. blocks - 1 does not exist: it is not written, reads as zeros,
+ * and is not attended to.  The same holds for a row before a sequence's first
+ * token (more rows than tokens).  Rows that no sequence has are left alone. */
+typedef struct {
+    const int32_t *row_start;    /* [batch + 1] */
+    const int32_t *lengths;      /* [batch] */
+    const int32_t *block_table;  /* [batch, table_stride], max_blocks of each row used */
+    int64_t batch;
+    int64_t max_blocks, table_stride;
+    int64_t rows;                /* rows of the call's arrays */
+} nq_kv_seqs;
+
+/* Write the rows' keys and values into the cache: k and v are [rows,
+ * kv_heads, head_dim] (x_dt) with row strides ldk and ldv in elements (at
+ * least kv_heads * head_dim, a multiple of 16 bytes, e.g. column ranges of a
+ * fused projection), 16-byte aligned.  For each block and head, with a = the
+ * largest |x| of the rows that fall into it and qmax = 127 (INT8) or 448 (FP8):
+ *   - a block whose first token is among the rows takes scale = fp32(a /
+ *     qmax), at least 2^-100, or 0 when a = 0;
+ *   - a block that holds earlier tokens of the sequence keeps its scale s if
+ *     a <= fp32(qmax * s); otherwise it takes s * 2^j, j the smallest that
+ *     brings fp32(a / fp32(qmax * s)) to at most 2^j, and the earlier codes are
+ *     rounded to it (an earlier value is then off by less than one step of the
+ *     last scale, however often the scale grew); if s = 0 or that quotient is
+ *     over 2^20, it takes a new block's scale and the earlier codes become zero;
+ *   - code = the code nearest to fp32(x * fp32(1 / scale)), ties to even,
+ *     clamped to +-qmax (zero codes for scale = 0).
+ * All in fp32, bit-exact.  Non-finite values are outside the contract.  Rows
+ * of two sequences must not fall into the same block. */
+nq_status nq_kv_append(const nq_kv_cache *cache, const nq_kv_seqs *seqs, const void *k, int64_t ldk,
+                       const void *v, int64_t ldv, nq_dtype x_dt, hipStream_t stream);
+
+/* Read the rows' tokens back: k and v [rows, kv_heads, head_dim] (dense,
+ * out_dt) = fp32(scale * c) rounded to nearest even.  With row counts equal
+ * to the lengths, whole sequences. */
+nq_status nq_kv_read(const nq_kv_cache *cache, const nq_kv_seqs *seqs, void *k, void *v, nq_dtype out_dt,
+                     hipStream_t stream);
+
+/* Workspace bytes of nq_kv_attention; a function of sizes only. */
+size_t nq_kv_attention_workspace_bytes(const nq_kv_cache *cache, const nq_kv_seqs *seqs, int32_t q_heads,
+                                       nq_dtype x_dt);
+
+/* Attention of the rows' queries over the cache.  q [rows, q_heads, head_dim]
+ * (x_dt, row stride ldq in elements, a multiple of 16 bytes, 16-byte
+ * aligned); q_heads is a multiple of kv_heads, and query head h reads
+ * key/value head h / (q_heads / kv_heads).  out [rows, q_heads, head_dim]
+ * (dense, x_dt), for the row at token p:
+ *   out = sum_t w_t v_t,  w = softmax over the visible t of scale * q . k_t,
+ * visible: the sequence's tokens t; with causal != 0 those with t <= p, and
+ * with window > 0 (causal only) those with t > p - window.  lse (null, or
+ * [rows, q_heads] fp32): log of the sum of exp(scale * q . k_t).  A row that
+ * sees nothing gives zeros, and lse -infinity.  softmax_scale must be finite
+ * and positive.  Keys, values and sums are fp32-accurate; for bf16 queries
+ * the weights of the second product keep 11 bits (fp16), for fp32 queries
+ * both products take their operands with 22 bits; weights times their values'
+ * scale lose bits from 2^-28 of a row's largest down and end at 2^-39 of it.  The workspace (16-byte
+ * aligned) is scratch of one call at a time. */
+nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, const void *q, nq_dtype x_dt,
+                          int64_t ldq, int32_t q_heads, float softmax_scale, int32_t causal, int64_t window,
+                          void *out, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------- expert routing */
+
+/* How tokens choose experts (ids that nq_gather_qmm and its kin take). */
+typedef enum { NQ_MOE_SOFTMAX = 1, NQ_MOE_SIGMOID = 2 } nq_moe_score;
+typedef struct {
+    int32_t experts;      /* 1 .. 1024 */
+    int32_t score;        /* nq_moe_score */
+    int32_t groups;       /* 1 .. 64, divides experts */
+    int32_t top_groups;   /* groups kept per token, 1 .. groups */
+    int32_t group_best;   /* a group's score: its largest key (1) or the sum of its two largest (2) */
+    int32_t top_k;        /* 1 .. 32, at most top_groups * experts / groups */
+    int32_t renormalise;  /* weights divided by their sum */
+    float scale;          /* factor of the weights, finite */
+} nq_moe_router;
+
+/* ids [tokens, top_k] uint32 and weights [tokens, top_k] fp32 of logits
+ * [tokens, experts] (x_dt, row stride ld >= experts, element aligned).  With p
+ * = softmax or sigmoid of a token's logits, an expert's key is p + bias (bias
+ * [experts] fp32, e.g. for balance), or without a bias (null) the logit itself
+ * (p has its order; the two largest of a group are summed as p).  The
+ * top_groups groups of experts / groups neighbouring experts with the largest
+ * scores stay, and of their experts the top_k largest keys are chosen, in
+ * falling order; among equals the lowest index comes first, for groups too.
+ * weights = p of the chosen experts (without the bias), divided by their sum
+ * when renormalise (0 if the sum is 0), times scale.  A NaN key sorts as
+ * -infinity; a softmax row with no logit above -infinity has p = 0.  Other
+ * non-finite logits give valid ids and unspecified weights. */
+nq_status nq_moe_route(const nq_moe_router *router, const void *logits, nq_dtype x_dt, int64_t tokens,
+                       int64_t ld, const float *bias, uint32_t *ids, float *weights, hipStream_t stream);
+
+/* Derivative of sum(dweights * weights) for the logits (the choice and the
+ * bias have none): ids as nq_moe_route gave them, dweights [tokens, top_k]
+ * fp32, dlogits [tokens, experts] (dense, x_dt).  ids must be distinct within
+ * a token; an id >= experts is skipped. */
+nq_status nq_moe_route_grad(const nq_moe_router *router, const void *logits, nq_dtype x_dt, int64_t tokens,
+                            int64_t ld, const uint32_t *ids, const float *dweights, void *dlogits,
+                            hipStream_t stream);
+
 /* ---------------------------------------------------------------- errors */
 
 /* A static description of a status code. */
