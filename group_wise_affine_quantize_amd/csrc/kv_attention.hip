@@ -38,6 +38,8 @@ typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 64;        // tokens per tile
 constexpr int kWaves = 4;
+constexpr int kWorkers = 512;    // two workgroups of four waves per compute unit
+constexpr int kJoinThreads = 512, kJoinCols = 4;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kPScale = 14.0f;  // log2 of the largest weight
@@ -102,76 +104,110 @@ struct AttnArgs {
     float *part_ml;     // [workers * 2][16 * CT][2]
     int workers;        // workgroups of the streaming kernel
     int group;          // query heads per key/value head
+    int unit_shift;     // log2 of the tiles of a unit of work
+    bool splits;        // whether a segment can have more than one unit
 };
 
-// The streaming kernel's work is a flat list of tiles: for each sequence with
-// rows, for each key/value head, for each tile of `cols` query rows (a row is
-// a token and one of the head's queries), the 64-token tiles of the tokens
-// that the sequence's rows can see.
+// The streaming kernel's work is a flat list of units (runs of 64-token
+// tiles): for each sequence with rows, for each key/value head and each tile
+// of `cols` query rows (a row is a token and one of the head's queries) -- a
+// segment -- the units of the tokens that the sequence's rows can see.  Every
+// worker takes an equal run of the list, whatever the lengths.
 struct StreamSeq {
-    KvSeq q;
-    int64_t lo, hi;     // tokens that some row sees (hi <= lo: none)
-    int64_t t0, nt;     // first tile, tiles (at least one)
-    int64_t ct;         // column tiles
-    int64_t work;       // ct * kv_heads * nt
+    int r0, n, first, len;  // rows of the call, tokens (see KvSeq)
+    int lo, hi;             // tokens that some row sees (hi <= lo: none)
+    int t0, nt;             // first tile, tiles (at least one)
+    uint32_t ct;            // column tiles
+    uint32_t units;         // per segment
+    uint32_t work;          // units of all segments
 };
 
 __device__ __forceinline__ StreamSeq stream_seq(const AttnArgs &A, int b, int cols)
 {
     const KvAttnLaunch &a = A.a;
+    const KvSeq q = kv_seq(a.s, b);
     StreamSeq s;
-    s.q = kv_seq(a.s, b);
-    const int64_t cap = a.s.max_blocks << a.c.block_shift;
-    s.hi = s.q.len < cap ? s.q.len : cap;
+    s.r0 = (int)q.r0, s.n = (int)q.n, s.first = (int)q.first, s.len = (int)q.len;
+    const int cap = (int)(a.s.max_blocks << a.c.block_shift);
+    s.hi = s.len < cap ? s.len : cap;
     s.lo = 0;
     if (a.window > 0) {
-        s.lo = s.q.first - a.window + 1;
-        if (s.lo < 0) s.lo = 0;
+        const int64_t lo = q.first - a.window + 1;
+        s.lo = lo < 0 ? 0 : (int)lo;
     }
     s.t0 = s.lo >> 6;
     s.nt = s.hi > s.lo ? ((s.hi + 63) >> 6) - s.t0 : 1;
-    s.ct = (s.q.n * A.group + cols - 1) / cols;
-    s.work = s.ct * s.nt * a.c.kv_heads;
+    s.ct = (uint32_t)(s.n * A.group + cols - 1) / (uint32_t)cols;
+    s.units = (uint32_t)(s.nt + (1 << A.unit_shift) - 1) >> A.unit_shift;
+    s.work = s.ct * s.units * (uint32_t)a.c.kv_heads;
     return s;
 }
 
-__device__ __forceinline__ int64_t stream_total(const AttnArgs &A, int cols)
+// Units per worker.  At least two tiles for each wave, so that short contexts
+// do not fall into parts that cost more to join than to read.
+__device__ __forceinline__ uint32_t share_of(const AttnArgs &A, uint32_t total)
 {
-    const int lane = (int)(threadIdx.x & 63u);
-    int64_t t = 0;
-    for (int b = lane; b < A.a.s.batch; b += 64) t += stream_seq(A, b, cols).work;
-    return __shfl(wave_scan(t, lane), 63);
+    const uint32_t share = (total + A.workers - 1) / A.workers, least = A.unit_shift ? 1 : 2 * kWaves;
+    return share < least ? least : share;
 }
 
-__device__ __forceinline__ int64_t stream_share(const AttnArgs &A, int64_t total)
+// Finds the sequence of unit `at(share)` of the list: its number (-1: past the
+// list's end), the unit's number inside it, the list's length and the share.
+template <typename At>
+__device__ __forceinline__ int stream_locate(const AttnArgs &A, int cols, At at, uint32_t *inside, uint32_t *total,
+                                             uint32_t *share)
 {
-    // at least two tiles for each wave, so that short contexts do not fall
-    // into parts that cost more to join than to read
-    const int64_t share = (total + A.workers - 1) / A.workers;
-    return share < 2 * kWaves ? 2 * kWaves : share;
+    const int batch = A.a.s.batch, lane = (int)(threadIdx.x & 63u);
+    uint32_t work = lane < batch ? stream_seq(A, lane, cols).work : 0u;
+    uint32_t upto = wave_scan32(work);
+    uint32_t sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+    *total = sum;
+    for (int b = 64 + lane; b - lane < batch; b += 64)
+        *total += (uint32_t)__builtin_amdgcn_readlane(
+            (int)wave_scan32(b < batch ? stream_seq(A, b, cols).work : 0u), 63);
+    *share = share_of(A, *total);
+    const uint32_t want = at(*share);
+    if (want >= *total) return -1;
+    uint32_t base = 0;
+    for (int b0 = 0; b0 < batch; b0 += 64) {
+        if (b0) {
+            work = b0 + lane < batch ? stream_seq(A, b0 + lane, cols).work : 0u;
+            upto = wave_scan32(work);
+            sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+        }
+        if (base + sum > want) {
+            const int l = __ffsll((unsigned long long)__ballot(base + upto > want)) - 1;
+            *inside = want - base - (uint32_t)__builtin_amdgcn_readlane((int)(upto - work), l);
+            return b0 + l;
+        }
+        base += sum;
+    }
+    return -1;
 }
 
 // Where a query column stands: its row of the call, head, and the tokens that
 // it sees, [lo, hi).
 struct Column {
-    int64_t row;        // -1: no such column
+    int row;            // -1: no such column
     int head;
-    int64_t lo, hi;
+    int lo, hi;
 };
 
-__device__ __forceinline__ Column column(const AttnArgs &A, const StreamSeq &s, int64_t idx, int kv_head)
+__device__ __forceinline__ Column column(const AttnArgs &A, const StreamSeq &s, int idx, int kv_head)
 {
     const KvAttnLaunch &a = A.a;
     Column c;
     c.row = -1, c.head = 0, c.lo = 0, c.hi = 0;
-    if (idx < s.q.n * A.group) {
-        const int64_t i = idx / A.group;
-        c.row = s.q.r0 + i;
-        c.head = kv_head * A.group + (int)(idx - i * A.group);
-        const int64_t pos = s.q.first + i;
-        c.hi = s.hi;
-        if (a.causal && pos + 1 < c.hi) c.hi = pos + 1;
-        if (a.window > 0 && pos - a.window + 1 > 0) c.lo = pos - a.window + 1;
+    if (idx < s.n * A.group) {
+        const int i = (int)((uint32_t)idx / (uint32_t)A.group);
+        c.row = s.r0 + i;
+        c.head = kv_head * A.group + (idx - i * A.group);
+        const int pos = s.first + i;
+        c.hi = a.causal && pos < s.hi ? pos + 1 : s.hi;
+        if (a.window > 0) {
+            const int64_t lo = (int64_t)pos - a.window + 1;
+            c.lo = lo < 0 ? 0 : (int)lo;
+        }
     }
     return c;
 }
@@ -231,7 +267,7 @@ __device__ __forceinline__ float group_sum(float v, int lane)
 template <int D, int CT, int NP> struct State {
     half8_t q[CT][D / 32][NP];
     float c[CT];                 // log2(e) * scale / row power of two
-    float m[CT], l[CT];
+    float m[CT], l[CT];          // m: the maximum less 14, so that weights are 2^(x - m)
     float4_t o[CT][D / 16];
 };
 
@@ -247,31 +283,28 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
     const int r = lane & 15, g = lane >> 4, gk = r >> 2;
     const int sh = a.c.block_shift, bmask = (1 << sh) - 1;
 
-    const int64_t total = stream_total(A, COLS), share = stream_share(A, total);
-    int64_t at = (int64_t)blockIdx.x * share;
-    const int64_t end = at + share < total ? at + share : total;
-    if (at >= end) return;
-    int64_t inside;
-    int b = kv_locate(a.s.batch, at, [&](int i) -> int64_t { return stream_seq(A, i, COLS).work; }, &inside);
+    uint32_t inside, total, share;
+    int b = stream_locate(A, COLS, [](uint32_t s) { return blockIdx.x * s; }, &inside, &total, &share);
     if (b < 0) return;
-    b = __builtin_amdgcn_readfirstlane(b);
+    uint32_t left = total - blockIdx.x * share < share ? total - blockIdx.x * share : share;
     StreamSeq s = stream_seq(A, b, COLS);
 
-    while (at < end) {
+    while (left > 0) {
         while (inside >= s.work) {      // the next sequence with work
             inside -= s.work;
             if (++b >= a.s.batch) return;
             s = stream_seq(A, b, COLS);
         }
-        const int64_t seg = inside / s.nt, tile0 = inside - seg * s.nt;
+        const uint32_t seg = inside / s.units, unit0 = inside - seg * s.units;
         const int head = (int)(seg / s.ct);
-        const int64_t ctile = seg - (int64_t)head * s.ct;
-        const int64_t tiles = s.nt - tile0 < end - at ? s.nt - tile0 : end - at;
-        const bool whole = tile0 == 0 && tiles == s.nt;
+        const int ctile = (int)(seg - (uint32_t)head * s.ct);
+        const uint32_t units = s.units - unit0 < left ? s.units - unit0 : left;
+        const bool whole = units == s.units;
+        const int tile0 = (int)(unit0 << A.unit_shift);
+        const int tile1 = unit0 + units == s.units ? s.nt : (int)((unit0 + units) << A.unit_shift);
 
         State<D, CT, NP> st;
-        int64_t seg_lo = INT64_MAX, seg_hi = 0, all_lo = 0, all_hi = INT64_MAX;
-        int64_t col_lo[CT], col_hi[CT];
+        int col_lo[CT], col_hi[CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
             const Column c = column(A, s, ctile * COLS + 16 * ct + r, head);
@@ -280,7 +313,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 if (c.row >= 0)
-                    load_f32x8<T>(static_cast<const T *>(a.q) + c.row * a.ldq + (int64_t)c.head * D + 64 * (ks >> 1) +
+                    load_f32x8<T>(static_cast<const T *>(a.q) + (int64_t)c.row * a.ldq + c.head * D + 64 * (ks >> 1) +
                                       16 * g + 8 * (ks & 1), f[ks]);
                 else
                     for (int i = 0; i < 8; ++i) f[ks][i] = 0.0f;
@@ -300,62 +333,58 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
             for (int dt = 0; dt < DT; ++dt) st.o[ct][dt] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
         }
         // tokens that some column sees, and tokens that every column sees
-        {
-            const int64_t n = s.q.n * A.group;
-            const Column first = column(A, s, ctile * COLS, head);
-            const int64_t li = ctile * COLS + COLS - 1 < n - 1 ? ctile * COLS + COLS - 1 : n - 1;
-            const Column last = column(A, s, li, head);
-            seg_lo = first.lo, seg_hi = last.hi, all_lo = last.lo, all_hi = first.hi;
-        }
+        const int count = s.n * A.group, last_col = (ctile + 1) * COLS < count ? (ctile + 1) * COLS - 1 : count - 1;
+        const Column c0 = column(A, s, ctile * COLS, head), c1 = column(A, s, last_col, head);
+        const int seg_lo = c0.lo, seg_hi = c1.hi, all_lo = c1.lo, all_hi = c0.hi;
 
-        for (int64_t ti = tile0 + wave; ti < tile0 + tiles; ti += kWaves) {
-            const int64_t base = (s.t0 + ti) << 6;
-            // block of this lane's key rows, and of its value and score tokens
-            const int64_t pk = base + 16 * gk, pv = base + 16 * g;
-            int64_t idk = -1, idv = -1;
-            if (pk < seg_hi && pk + 16 > seg_lo) idk = kv_block(a.s, a.c.blocks, b, pk >> sh);
-            if (pv < seg_hi && pv + 16 > seg_lo) idv = kv_block(a.s, a.c.blocks, b, pv >> sh);
-            const bool has = idv >= 0;
-            const bool masked = base < all_lo || base + kTile > all_hi || __any(!has);
-            idk = idk < 0 ? 0 : idk;
-            const int64_t idv0 = has ? idv : 0;
-            const uint8_t *kp = a.c.k_codes + (((idk * a.c.kv_heads + head) << sh) + (pk & bmask) + (r & 3)) * D + 16 * g;
-            const uint8_t *vp = a.c.v_codes + (((idv0 * a.c.kv_heads + head) * D + r) << sh) + (pv & bmask);
-            uint4 kw[4][D / 64], vw[DT];
+        // A tile's blocks: of this lane's key rows, and of its value and score
+        // tokens; -1 where no column sees the 16 tokens or no block holds them.
+        const int *table = a.s.table + (int64_t)b * a.s.ldt;
+        auto block_of = [&](int pos) -> int {
+            if (pos >= seg_hi || pos + 16 <= seg_lo) return -1;     // also keeps pos inside the table
+            const int id = table[pos >> sh];
+            return id >= 0 && id < (int)a.c.blocks ? id : -1;
+        };
+        uint4 kw[4][D / 64], vw[DT];
+        float sk, sv;
+        auto load_keys = [&](int base, int idk) {
+            const int pk = base + 16 * gk;
+            const uint8_t *kp = a.c.k_codes + (int64_t)((((int64_t)(idk < 0 ? 0 : idk) * a.c.kv_heads + head) << sh) +
+                                                        (pk & bmask) + (r & 3)) * D + 16 * g;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int j = 0; j < D / 64; ++j) kw[n][j] = *reinterpret_cast<const uint4 *>(kp + 4 * n * D + 64 * j);
+        };
+        auto load_values = [&](int base, int idv) {
+            const int pv = base + 16 * g;
+            const int64_t slab = (int64_t)(idv < 0 ? 0 : idv) * a.c.kv_heads + head;
+            const uint8_t *vp = a.c.v_codes + ((slab * D + r) << sh) + (pv & bmask);
 #pragma unroll
-            for (int dt = 0; dt < DT; ++dt) vw[dt] = *reinterpret_cast<const uint4 *>(vp + ((int64_t)(16 * dt) << sh));
-            float sk = 0.0f, sv = 1.0f;
-            if (has) {
-                sk = a.c.k_scales[idv * a.c.kv_heads + head];
-                sv = a.c.v_scales[idv * a.c.kv_heads + head];
-                if (sv == 0.0f) sv = kZeroBlockScale;
+            for (int dt = 0; dt < DT; ++dt) vw[dt] = *reinterpret_cast<const uint4 *>(vp + ((16 * dt) << sh));
+            sk = 0.0f, sv = 1.0f;
+            if (idv >= 0) sk = a.c.k_scales[slab], sv = a.c.v_scales[slab];
+        };
+
+        // The loop keeps one tile's loads in flight: keys of the next tile go
+        // out once this one's first product has read its registers, values
+        // once the second has, block ids one tile before those.
+        int ti = tile0 + wave;
+        int idk = -1, idv = -1, idk2 = -1, idv2 = -1;
+        if (ti < tile1) {
+            const int base = (s.t0 + ti) << 6;
+            idk = block_of(base + 16 * gk), idv = block_of(base + 16 * g);
+            if (ti + kWaves < tile1) {
+                const int next = (s.t0 + ti + kWaves) << 6;
+                idk2 = block_of(next + 16 * gk), idv2 = block_of(next + 16 * g);
             }
-            if (masked) {
-                // codes of tokens that no column sees are whatever memory
-                // holds, an E4M3 NaN for instance: make them zero codes
-                uint32_t keep[4];
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    keep[w] = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int64_t t = pv + 4 * w + e;
-                        if (has && t >= seg_lo && t < seg_hi) keep[w] |= 255u << (8 * e);
-                    }
-                }
-                constexpr uint32_t z = KvFmt<FMT>::zero4;
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) {
-                    vw[dt].x = (vw[dt].x & keep[0]) | (z & ~keep[0]);
-                    vw[dt].y = (vw[dt].y & keep[1]) | (z & ~keep[1]);
-                    vw[dt].z = (vw[dt].z & keep[2]) | (z & ~keep[2]);
-                    vw[dt].w = (vw[dt].w & keep[3]) | (z & ~keep[3]);
-                }
-            }
+            load_keys(base, idk);
+            load_values(base, idv);
+        }
+        for (; ti < tile1; ti += kWaves) {
+            const int base = (s.t0 + ti) << 6, pv = base + 16 * g;
+            const bool more = ti + kWaves < tile1, has = idv >= 0;
+            const bool masked = base < all_lo || base + kTile > all_hi || __any(!has);
 
             float4_t S[CT][4];
 #pragma unroll
@@ -376,7 +405,12 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
                             S[ct][n] = mfma(k1, st.q[ct][2 * j + 1][p], S[ct][n]);
                         }
                 }
-            const float lsv = fast_log2(sv), isv = 1.0f / sv;
+            const int next = (s.t0 + ti + kWaves) << 6;
+            idk = idk2;
+            if (more) load_keys(next, idk2);
+
+            const float vs = sv == 0.0f ? kZeroBlockScale : sv;
+            const float lsv = fast_log2(vs), isv = 1.0f / vs;
             half8_t P[CT][2][NP];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
@@ -385,23 +419,21 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float v = S[ct][n][i];
-                        v = fmaf(v, f, lsv);
-                        if (masked) {
-                            const int64_t t = pv + 4 * n + i;
-                            if (!has || t < col_lo[ct] || t >= col_hi[ct]) v = kNegInf;
-                        }
-                        x[4 * n + i] = v;
-                        mx = fmaxf(mx, v);
-                    }
-                const float mnew = fmaxf(st.m[ct], group_max(mx, lane));
-                const float mref = mnew == kNegInf ? 0.0f : mnew;   // no token yet: every weight is 2^-inf
+                    for (int i = 0; i < 4; ++i) x[4 * n + i] = fmaf(S[ct][n][i], f, lsv);
+                if (masked) {
+                    const int lo = has ? col_lo[ct] - pv : 16, hi = col_hi[ct] - pv;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = i < lo || i >= hi ? kNegInf : x[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[i]);
+                const float mnew = fmaxf(st.m[ct], group_max(mx, lane) - kPScale);
+                const float mref = mnew == kNegInf ? 0.0f : mnew;   // no token yet: every weight is 0
                 const float alpha = fast_exp2(st.m[ct] - mref);
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    x[i] = fast_exp2(x[i] - mref + kPScale);
+                    x[i] = fast_exp2(x[i] - mref);
                     sum += x[i];
                 }
                 st.m[ct] = mnew;
@@ -410,6 +442,24 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
                 for (int dt = 0; dt < DT; ++dt) st.o[ct][dt] *= alpha;
                 split_half<NP>(x, P[ct][0]);
                 split_half<NP>(x + 8, P[ct][1]);
+            }
+            if constexpr (FMT == KV_FP8) {
+                if (masked) {
+                    // codes of tokens that no column sees are whatever memory
+                    // holds, a NaN for instance: make them zeros
+                    const int lo = has ? seg_lo - pv : 16, hi = seg_hi - pv;
+                    uint32_t keep[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        keep[w] = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (4 * w + e >= lo && 4 * w + e < hi) keep[w] |= 255u << (8 * e);
+                    }
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt)
+                        vw[dt].x &= keep[0], vw[dt].y &= keep[1], vw[dt].z &= keep[2], vw[dt].w &= keep[3];
+                }
             }
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt) {
@@ -422,6 +472,14 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
                         st.o[ct][dt] = mfma(v0, P[ct][0][p], st.o[ct][dt]);
                         st.o[ct][dt] = mfma(v1, P[ct][1][p], st.o[ct][dt]);
                     }
+            }
+            idv = idv2;
+            if (more) {
+                load_values(next, idv2);
+                if (ti + 2 * kWaves < tile1) {
+                    const int after = (s.t0 + ti + 2 * kWaves) << 6;
+                    idk2 = block_of(after + 16 * gk), idv2 = block_of(after + 16 * g);
+                }
             }
         }
 
@@ -457,7 +515,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
             __syncthreads();
         }
         if (wave == 0) {
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (tile0 == 0 ? 1 : 0);
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 const int col = 16 * ct + r;
@@ -466,7 +524,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
                 if (c.row < 0) continue;
                 if (whole) {
                     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                    T *out = static_cast<T *>(a.out) + (c.row * a.q_heads + c.head) * D;
+                    T *out = static_cast<T *>(a.out) + ((int64_t)c.row * a.q_heads + c.head) * D;
 #pragma unroll
                     for (int dt = 0; dt < DT; ++dt) {
                         float v[4];
@@ -474,7 +532,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
                         store_f32x4<T>(out + 16 * dt + 4 * g, v);
                     }
                     if (a.lse && g == 0)
-                        a.lse[c.row * a.q_heads + c.head] = l > 0.0f ? (st.m[ct] - kPScale + fast_log2(l)) * kLn2 : kNegInf;
+                        a.lse[(int64_t)c.row * a.q_heads + c.head] = l > 0.0f ? (st.m[ct] + fast_log2(l)) * kLn2 : kNegInf;
                 } else {
                     float *po = A.part_o + (slot * COLS + col) * D;
                     float *pm = A.part_ml + (slot * COLS + col) * 2;
@@ -486,8 +544,8 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
             }
         }
         __syncthreads();
-        at += tiles;
-        inside += tiles;
+        left -= units;
+        inside += units;
     }
 }
 
@@ -495,45 +553,80 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
 // order of the tokens.  Workgroup j looks at the border between workers j and
 // j + 1; the one at the first border inside a segment joins it.
 template <int D, int CT, typename T>
-__global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs A)
+__global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 {
-    constexpr int COLS = 16 * CT;
+    constexpr int COLS = 16 * CT, QUADS = D / 4, LANES = kJoinCols * QUADS, RUNS = kJoinThreads / LANES;
+    __shared__ float sh_f[kWorkers][kJoinCols];
+    __shared__ float sh_m[kJoinCols], sh_l[kJoinCols];
+    __shared__ float4 sh_o[RUNS][LANES];
     const KvAttnLaunch &a = A.a;
-    const int64_t total = stream_total(A, COLS), share = stream_share(A, total);
-    const int64_t border = ((int64_t)blockIdx.x + 1) * share;
-    if (border >= total) return;
-    int64_t inside;
-    const int b = kv_locate(a.s.batch, border, [&](int i) -> int64_t { return stream_seq(A, i, COLS).work; }, &inside);
+    const int tid = (int)threadIdx.x;
+    uint32_t inside, total, share;
+    const int b = stream_locate(A, COLS, [](uint32_t s) { return (blockIdx.x + 1) * s; }, &inside, &total, &share);
     if (b < 0) return;
     const StreamSeq s = stream_seq(A, b, COLS);
-    const int64_t seg = inside / s.nt, tile = inside - seg * s.nt;
-    if (tile == 0 || tile > share) return;     // between segments, or not the first border inside
-    const int head = (int)(seg / s.ct);
-    const int64_t ctile = seg - (int64_t)head * s.ct;
-    const int64_t w0 = blockIdx.x, w1 = (border - tile + s.nt - 1) / share;
+    const uint32_t seg = inside / s.units, unit = inside - seg * s.units;
+    if (unit == 0 || unit > share) return;     // between segments, or not the first border inside
+    const int head = (int)(seg / s.ct), col0 = (int)blockIdx.y * kJoinCols;
+    const int idx0 = (int)(seg - (uint32_t)head * s.ct) * COLS + col0;
+    if (idx0 >= s.n * A.group) return;
+    // worker blockIdx.x has the first part, in its second slot; the others in their first
+    const int w0 = (int)blockIdx.x, parts = (int)(((blockIdx.x + 1) * share - unit + s.units - 1) / share) - w0 + 1;
+    auto slot = [&](int p) -> int64_t { return (2 * (int64_t)(w0 + p) + (p == 0 ? 1 : 0)) * COLS + col0; };
 
-    for (int i = (int)threadIdx.x; i < COLS * (D / 4); i += 256) {
-        const int col = i / (D / 4), d = (i % (D / 4)) * 4;
-        const Column c = column(A, s, ctile * COLS + col, head);
-        if (c.row < 0) continue;
+    // each part's factor: 2^(M_part - M)
+    for (int i = tid; i < parts * kJoinCols; i += kJoinThreads)
+        sh_f[i / kJoinCols][i % kJoinCols] = A.part_ml[2 * (slot(i / kJoinCols) + i % kJoinCols)];
+    __syncthreads();
+    if (tid < 64 * kJoinCols) {
+        const int c = tid >> 6, lane = tid & 63;
         float m = kNegInf;
-        for (int64_t w = w0; w <= w1; ++w)
-            m = fmaxf(m, A.part_ml[((2 * w + (w == w0 ? 1 : 0)) * COLS + col) * 2]);
-        float l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (m != kNegInf)
-            for (int64_t w = w0; w <= w1; ++w) {
-                const int64_t at = (2 * w + (w == w0 ? 1 : 0)) * COLS + col;
-                const float f = fast_exp2(A.part_ml[2 * at] - m);
-                const float4 o = *reinterpret_cast<const float4 *>(A.part_o + at * D + d);
-                l = fmaf(f, A.part_ml[2 * at + 1], l);
-                v[0] = fmaf(f, o.x, v[0]), v[1] = fmaf(f, o.y, v[1]);
-                v[2] = fmaf(f, o.z, v[2]), v[3] = fmaf(f, o.w, v[3]);
-            }
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        for (int p = lane; p < parts; p += 64) m = fmaxf(m, sh_f[p][c]);
+        m = fmaxf(m, xor_lane<1>(m, lane));
+        m = fmaxf(m, xor_lane<2>(m, lane));
+        m = fmaxf(m, xor_lane<4>(m, lane));
+        m = fmaxf(m, xor_lane<8>(m, lane));
+        m = group_max(m, lane);
+        float l = 0.0f;
+        for (int p = lane; p < parts; p += 64) {
+            const float f = m == kNegInf ? 0.0f : fast_exp2(sh_f[p][c] - m);
+            sh_f[p][c] = f;
+            l = fmaf(f, A.part_ml[2 * (slot(p) + c) + 1], l);
+        }
+        l += xor_lane<1>(l, lane);
+        l += xor_lane<2>(l, lane);
+        l += xor_lane<4>(l, lane);
+        l += xor_lane<8>(l, lane);
+        l = group_sum(l, lane);
+        if (lane == 0) sh_m[c] = m, sh_l[c] = l;
+    }
+    __syncthreads();
+
+    const int run = tid / LANES, i = tid % LANES, c = i / QUADS, d = (i % QUADS) * 4;
+    if (run < RUNS) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float *o = A.part_o + (int64_t)c * D + d;
+#pragma unroll 8
+        for (int p = run; p < parts; p += RUNS) {
+            const float f = sh_f[p][c];
+            const float4 w = *reinterpret_cast<const float4 *>(o + slot(p) * D);
+            v.x = fmaf(f, w.x, v.x), v.y = fmaf(f, w.y, v.y), v.z = fmaf(f, w.z, v.z), v.w = fmaf(f, w.w, v.w);
+        }
+        sh_o[run][i] = v;
+    }
+    __syncthreads();
+    const Column q = column(A, s, idx0 + c, head);
+    if (run == 0 && q.row >= 0) {
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < RUNS; ++k) {
+            const float4 w = sh_o[k][i];
+            v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
+        }
+        const float l = sh_l[c], inv = l > 0.0f ? 1.0f / l : 0.0f;
         for (int e = 0; e < 4; ++e) v[e] *= inv;
-        store_f32x4<T>(static_cast<T *>(a.out) + (c.row * a.q_heads + c.head) * D + d, v);
+        store_f32x4<T>(static_cast<T *>(a.out) + ((int64_t)q.row * a.q_heads + q.head) * D + d, v);
         if (a.lse && d == 0)
-            a.lse[c.row * a.q_heads + c.head] = l > 0.0f ? (m - kPScale + fast_log2(l)) * kLn2 : kNegInf;
+            a.lse[(int64_t)q.row * a.q_heads + q.head] = l > 0.0f ? (sh_m[c] + fast_log2(l)) * kLn2 : kNegInf;
     }
 }
 
@@ -547,14 +640,14 @@ int stream_ct(const KvAttnLaunch &a)
     return cols <= 16 || a.c.head_dim > 128 ? 1 : 2;
 }
 
-constexpr int kWorkers = 512;   // two workgroups of four waves per compute unit
 
 template <int D, int CT, int FMT, typename T> hipError_t stream_go(const AttnArgs &A, hipStream_t stream)
 {
     kv_stream_kernel<D, CT, FMT, T><<<A.workers, 64 * kWaves, 0, stream>>>(A);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    kv_join_kernel<D, CT, T><<<A.workers - 1, 256, 0, stream>>>(A);
+    if (!A.splits) return e;
+    kv_join_kernel<D, CT, T><<<dim3(A.workers - 1, 16 * CT / kJoinCols), kJoinThreads, 0, stream>>>(A);
     return hipGetLastError();
 }
 
@@ -580,6 +673,15 @@ hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream)
     A.workers = kWorkers;
     A.group = a.q_heads / a.c.kv_heads;
     const int ct = stream_ct(a);
+    // Units of one tile, unless the list could then pass 32 bits.  Contexts
+    // that can have no more than 16 tiles are one unit: four tiles for each
+    // wave, which take less than a second launch.
+    const int64_t tiles = ((a.s.max_blocks << a.c.block_shift) >> 6) + 1;
+    const double segments = ((double)a.s.rows * A.group / (16 * ct) + a.s.batch) * a.c.kv_heads;
+    A.unit_shift = 0;
+    while (segments * (double)((tiles >> A.unit_shift) + 1) >= 0x1p31) ++A.unit_shift;
+    if (tiles <= 16) A.unit_shift = 4;
+    A.splits = tiles > (int64_t)1 << A.unit_shift;
     A.part_o = static_cast<float *>(a.workspace);
     A.part_ml = A.part_o + (size_t)2 * kWorkers * 16 * ct * a.c.head_dim;
     switch (a.c.head_dim) {

@@ -411,6 +411,8 @@ nq_status check_kv_seqs(const char *op, const nq_kv_seqs *s)
     if (s->batch > (1 << 24) || s->rows > ((int64_t)1 << 30) || s->max_blocks >= kMaxDim || s->table_stride >= kMaxDim)
         return fail(NQ_ERR_SHAPE, "%s: size too large (batch=%lld, rows=%lld, max_blocks=%lld)", op,
                     (long long)s->batch, (long long)s->rows, (long long)s->max_blocks);
+    if (s->max_blocks * 128 > kMaxDim - 128)
+        return fail(NQ_ERR_SHAPE, "%s: max_blocks=%lld is too large", op, (long long)s->max_blocks);
     if (s->table_stride < s->max_blocks)
         return fail(NQ_ERR_SHAPE, "%s: table_stride=%lld is below max_blocks=%lld", op, (long long)s->table_stride,
                     (long long)s->max_blocks);
@@ -1286,6 +1288,8 @@ nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, cons
     if (q_heads < 1 || q_heads > 65535 || q_heads % cache->kv_heads)
         return fail(NQ_ERR_SHAPE, "%s: q_heads=%d is not a multiple of kv_heads=%d in 1 .. 65535", op, q_heads,
                     cache->kv_heads);
+    if (seqs->rows * q_heads >= kMaxDim)
+        return fail(NQ_ERR_SHAPE, "%s: rows=%lld times q_heads=%d is too large", op, (long long)seqs->rows, q_heads);
     if (!finite(softmax_scale) || !(softmax_scale > 0.0f))
         return fail(NQ_ERR_SHAPE, "%s: softmax_scale is not finite and positive", op);
     if (window < 0 || (window > 0 && !causal))
@@ -1304,7 +1308,8 @@ nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, cons
     nqk::KvAttnLaunch a{};
     a.c = kv_cache_of(cache), a.s = kv_seqs_of(seqs);
     a.q = q, a.ldq = ldq, a.out = out, a.lse = lse, a.workspace = workspace, a.q_heads = q_heads, a.x_dt = x_dt;
-    a.format = cache->format, a.causal = causal != 0, a.window = window, a.scale = softmax_scale;
+    a.format = cache->format, a.causal = causal != 0, a.scale = softmax_scale;
+    a.window = std::min<int64_t>(window, (int64_t)1 << 32);   // past every length
     const size_t need = nqk::kv_attn_ws_bytes(a);
     if (need) {
         if (!workspace || workspace_bytes < need)

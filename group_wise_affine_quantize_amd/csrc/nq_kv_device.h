@@ -117,6 +117,19 @@ __device__ __forceinline__ int64_t wave_scan(int64_t v, int lane)
     return v;
 }
 
+// The same over 32 bits, by lane shifts inside rows of 16 and row broadcasts.
+__device__ __forceinline__ uint32_t wave_scan32(uint32_t v)
+{
+    auto add = [&](int o) { v += (uint32_t)o; };
+    add(__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true));    // row_shr:1
+    add(__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true));
+    add(__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true));
+    add(__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true));
+    add(__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));   // row 0 -> 1, 2 -> 3
+    add(__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));   // rows 0, 1 -> 2, 3
+    return v;
+}
+
 // Finds, for a wave, which sequence holds item `item` when sequence b has
 // count(b) items, and the item's number in it; -1 when there is none.  Lanes
 // look at 64 sequences at a time.
