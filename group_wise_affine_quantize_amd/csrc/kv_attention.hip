@@ -25,123 +25,17 @@
 // rows are fed is free, and this one leaves each lane 16 neighbouring tokens,
 // which are exactly the operand of the second product (16 bytes of a V^T row
 // per lane).  No value moves between lanes but the running maximum.
-#include "nq_kv_device.h"
+#include <algorithm>
+
+#include "nq_kv_attn.h"
 
 namespace nqk {
 
 namespace {
 
-typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
-typedef float float4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
-
-constexpr int kTile = 64;        // tokens per tile
-constexpr int kWaves = 4;
 constexpr int kWorkers = 512;    // two workgroups of four waves per compute unit
 constexpr int kJoinThreads = 512, kJoinCols = 4;
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.693147180559945309417f;
-constexpr float kPScale = 14.0f;  // log2 of the largest weight
-// What stands for the scale of an all-zero block of values.  Any would do for
-// its zero codes; a small one keeps its tokens, however large their scores,
-// from raising M over the tokens that do add to O, and 2^80 of them still
-// count in L.
-constexpr float kZeroBlockScale = 0x1p-80f;
-constexpr float kNegInf = -__builtin_inff();
-
-__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ float fast_log2(float x) { return __builtin_amdgcn_logf(x); }
-
-// Eight codes (two words) -> eight fp16 values, exactly.
-template <int FMT> __device__ __forceinline__ half8_t codes_to_half(uint32_t w0, uint32_t w1)
-{
-    uint32_t p[4];
-    if constexpr (FMT == KV_INT8) {
-        // 0x6400 | c is fp16 1024 + c; less 1152 it is c - 128
-        p[0] = __builtin_amdgcn_perm(0x64646464u, w0, 0x04010400u);
-        p[1] = __builtin_amdgcn_perm(0x64646464u, w0, 0x04030402u);
-        p[2] = __builtin_amdgcn_perm(0x64646464u, w1, 0x04010400u);
-        p[3] = __builtin_amdgcn_perm(0x64646464u, w1, 0x04030402u);
-        const half2_t off = {(_Float16)1152.0f, (_Float16)1152.0f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const half2_t h = __builtin_bit_cast(half2_t, p[i]) - off;
-            p[i] = __builtin_bit_cast(uint32_t, h);
-        }
-    } else {
-        p[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w0, 1.0f, false));
-        p[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w0, 1.0f, true));
-        p[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w1, 1.0f, false));
-        p[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w1, 1.0f, true));
-    }
-    const uint4_t v = {p[0], p[1], p[2], p[3]};
-    return __builtin_bit_cast(half8_t, v);
-}
-
-// Parts of fp32 numbers in fp16: one for bf16 queries, two for fp32 ones.
-template <typename T> struct Parts { static constexpr int n = 2; };
-template <> struct Parts<bf16_bits> { static constexpr int n = 1; };
-
-template <int NP> __device__ __forceinline__ void split_half(const float *v, half8_t *h)
-{
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const _Float16 a = (_Float16)v[i];
-        h[0][i] = a;
-        if constexpr (NP == 2) h[1][i] = (_Float16)(v[i] - (float)a);
-    }
-}
-
-__device__ __forceinline__ float4_t mfma(half8_t a, half8_t b, float4_t c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-
-struct AttnArgs {
-    KvAttnLaunch a;
-    float *part_o;      // [workers * 2][16 * CT][D]
-    float *part_ml;     // [workers * 2][16 * CT][2]
-    int workers;        // workgroups of the streaming kernel
-    int group;          // query heads per key/value head
-    int unit_shift;     // log2 of the tiles of a unit of work
-    bool splits;        // whether a segment can have more than one unit
-};
-
-// The streaming kernel's work is a flat list of units (runs of 64-token
-// tiles): for each sequence with rows, for each key/value head and each tile
-// of `cols` query rows (a row is a token and one of the head's queries) -- a
-// segment -- the units of the tokens that the sequence's rows can see.  Every
-// worker takes an equal run of the list, whatever the lengths.
-struct StreamSeq {
-    int r0, n, first, len;  // rows of the call, tokens (see KvSeq)
-    int lo, hi;             // tokens that some row sees (hi <= lo: none)
-    int t0, nt;             // first tile, tiles (at least one)
-    uint32_t ct;            // column tiles
-    uint32_t units;         // per segment
-    uint32_t work;          // units of all segments
-};
-
-__device__ __forceinline__ StreamSeq stream_seq(const AttnArgs &A, int b, int cols)
-{
-    const KvAttnLaunch &a = A.a;
-    const KvSeq q = kv_seq(a.s, b);
-    StreamSeq s;
-    s.r0 = (int)q.r0, s.n = (int)q.n, s.first = (int)q.first, s.len = (int)q.len;
-    const int cap = (int)(a.s.max_blocks << a.c.block_shift);
-    s.hi = s.len < cap ? s.len : cap;
-    s.lo = 0;
-    if (a.window > 0) {
-        const int64_t lo = q.first - a.window + 1;
-        s.lo = lo < 0 ? 0 : (int)lo;
-    }
-    s.t0 = s.lo >> 6;
-    s.nt = s.hi > s.lo ? ((s.hi + 63) >> 6) - s.t0 : 1;
-    s.ct = (uint32_t)(s.n * A.group + cols - 1) / (uint32_t)cols;
-    s.units = (uint32_t)(s.nt + (1 << A.unit_shift) - 1) >> A.unit_shift;
-    s.work = s.ct * s.units * (uint32_t)a.c.kv_heads;
-    return s;
-}
+constexpr int kWaves = 4;
 
 // Units per worker.  At least two tiles for each wave, so that short contexts
 // do not fall into parts that cost more to join than to read.
@@ -183,84 +77,6 @@ __device__ __forceinline__ int stream_locate(const AttnArgs &A, int cols, At at,
         base += sum;
     }
     return -1;
-}
-
-// Where a query column stands: its row of the call, head, and the tokens that
-// it sees, [lo, hi).
-struct Column {
-    int row;            // -1: no such column
-    int head;
-    int lo, hi;
-};
-
-__device__ __forceinline__ Column column(const AttnArgs &A, const StreamSeq &s, int idx, int kv_head)
-{
-    const KvAttnLaunch &a = A.a;
-    Column c;
-    c.row = -1, c.head = 0, c.lo = 0, c.hi = 0;
-    if (idx < s.n * A.group) {
-        const int i = (int)((uint32_t)idx / (uint32_t)A.group);
-        c.row = s.r0 + i;
-        c.head = kv_head * A.group + (idx - i * A.group);
-        const int pos = s.first + i;
-        c.hi = a.causal && pos < s.hi ? pos + 1 : s.hi;
-        if (a.window > 0) {
-            const int64_t lo = (int64_t)pos - a.window + 1;
-            c.lo = lo < 0 ? 0 : (int)lo;
-        }
-    }
-    return c;
-}
-
-template <typename T> __device__ __forceinline__ void load_f32x8(const T *p, float *v);
-template <> __device__ __forceinline__ void load_f32x8<float>(const float *p, float *v)
-{
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-template <> __device__ __forceinline__ void load_f32x8<bf16_bits>(const bf16_bits *p, float *v)
-{
-    const uint4 d = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-
-template <typename T> __device__ __forceinline__ void store_f32x4(T *p, const float *v);
-template <> __device__ __forceinline__ void store_f32x4<float>(float *p, const float *v)
-{
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-template <> __device__ __forceinline__ void store_f32x4<bf16_bits>(bf16_bits *p, const float *v)
-{
-    uint2 w;
-    w.x = f32_to_bf16(v[0]) | f32_to_bf16(v[1]) << 16;
-    w.y = f32_to_bf16(v[2]) | f32_to_bf16(v[3]) << 16;
-    *reinterpret_cast<uint2 *>(p) = w;
-}
-
-// A row's power of two: f * 2^k has its largest element in [2^14, 2^15).
-// Returns 2^k; *back is 2^-k.
-__device__ __forceinline__ float row_scale(float largest, float *back)
-{
-    int e = (int)(__float_as_uint(largest) >> 23) & 255;   // biased exponent
-    e = e < 27 ? 27 : (e > 254 ? 254 : e);                 // both powers stay normal
-    *back = __uint_as_float((uint32_t)(e - 14) << 23);
-    return __uint_as_float((uint32_t)(254 + 14 - e) << 23);
-}
-
-__device__ __forceinline__ float group_max(float v, int lane)   // over the four lanes of a column
-{
-    v = fmaxf(v, xor_lane<16>(v, lane));
-    return fmaxf(v, xor_lane<32>(v, lane));
-}
-__device__ __forceinline__ float group_sum(float v, int lane)
-{
-    v += xor_lane<16>(v, lane);
-    return v + xor_lane<32>(v, lane);
 }
 
 // The state of CT column tiles in one wave's registers.
@@ -630,16 +446,54 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
     }
 }
 
-// Column tiles per wave: as many columns as one sequence's rows of a head
-// are likely to fill.
-int stream_ct(const KvAttnLaunch &a)
-{
-    const int64_t group = a.q_heads / a.c.kv_heads;
-    const int64_t per = a.s.rows > a.s.batch ? (a.s.rows + a.s.batch - 1) / a.s.batch : 1;
-    const int64_t cols = per * group;
-    return cols <= 16 || a.c.head_dim > 128 ? 1 : 2;
-}
+// The kernels a call takes, and their workspace: functions of sizes only.
+//
+// Sequences with up to kFew query columns per head go through the streaming
+// kernel, which splits long contexts evenly; longer ones through the tile
+// kernel, whose operands serve more columns.  Which of them a batch holds is
+// only known on the device: both are launched, unless one sequence has all
+// rows or there are at most two rows per sequence (then all of them are
+// streamed).
+constexpr int kFew = 64;
 
+struct Route {
+    bool stream, tile;
+    int ct;             // 16-column blocks per wave of the streaming kernel
+    int few;
+    unsigned tile_bound;
+    int tile_splits;
+    size_t stream_floats, tile_floats;  // parts of O in the workspace
+    size_t stream_cols, tile_cols;      // columns that these stand for
+};
+
+Route route_of(const KvAttnLaunch &a)
+{
+    Route r;
+    const int64_t group = a.q_heads / a.c.kv_heads, cols = a.s.rows * group, D = a.c.head_dim;
+    if (a.s.batch == 1) r.stream = cols <= kFew, r.tile = !r.stream, r.few = kFew;
+    else if (cols <= kFew || a.s.rows <= 2 * (int64_t)a.s.batch) r.stream = true, r.tile = false, r.few = INT32_MAX;
+    else r.stream = r.tile = true, r.few = kFew;
+    const int64_t per = std::max<int64_t>(1, (a.s.rows + a.s.batch - 1) / a.s.batch) * group;
+    r.ct = per <= 16 || D > 128 ? 1 : 2;
+    r.stream_cols = r.stream ? (size_t)2 * kWorkers * 16 * r.ct : 0;
+    r.stream_floats = r.stream_cols * D;
+    r.tile_bound = 0, r.tile_splits = 1, r.tile_cols = 0, r.tile_floats = 0;
+    if (r.tile) {
+        const int64_t M = prefill_columns(a);
+        const int64_t bound = std::min<int64_t>(cols / M + a.s.batch, cols);
+        r.tile_bound = (unsigned)bound;
+        // too few workgroups for 256 compute units: tokens are split, at least
+        // eight tiles to a part
+        const int64_t segments = bound * a.c.kv_heads, tiles = ((a.s.max_blocks << a.c.block_shift) >> 6) + 1;
+        if (segments < 192)
+            r.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>(512 / segments, tiles / 8));
+        if (r.tile_splits > 1) {
+            r.tile_cols = (size_t)(segments * r.tile_splits * M);
+            r.tile_floats = r.tile_cols * D;
+        }
+    }
+    return r;
+}
 
 template <int D, int CT, int FMT, typename T> hipError_t stream_go(const AttnArgs &A, hipStream_t stream)
 {
@@ -662,31 +516,39 @@ template <int D, int CT> hipError_t stream_types(const AttnArgs &A, hipStream_t 
 
 size_t kv_attn_ws_bytes(const KvAttnLaunch &a)
 {
-    const size_t cols = 16 * (size_t)stream_ct(a), slots = 2 * kWorkers;
-    return slots * cols * ((size_t)a.c.head_dim + 2) * sizeof(float);
+    // the two kernels run one after the other: they share the workspace
+    const Route r = route_of(a);
+    return std::max(r.stream_floats + 2 * r.stream_cols, r.tile_floats + 2 * r.tile_cols) * sizeof(float);
 }
 
 hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream)
 {
+    const Route r = route_of(a);
     AttnArgs A;
     A.a = a;
     A.workers = kWorkers;
     A.group = a.q_heads / a.c.kv_heads;
-    const int ct = stream_ct(a);
+    A.few = r.few, A.tile_bound = r.tile_bound, A.tile_splits = r.tile_splits;
+    A.unit_shift = 0, A.splits = false;
+    A.part_o = static_cast<float *>(a.workspace);
+    if (r.tile) {
+        A.part_ml = A.part_o + r.tile_floats;
+        const hipError_t e = launch_kv_prefill(A, stream);
+        if (e != hipSuccess || !r.stream) return e;
+    }
     // Units of one tile, unless the list could then pass 32 bits.  Contexts
     // that can have no more than 16 tiles are one unit: four tiles for each
     // wave, which take less than a second launch.
     const int64_t tiles = ((a.s.max_blocks << a.c.block_shift) >> 6) + 1;
-    const double segments = ((double)a.s.rows * A.group / (16 * ct) + a.s.batch) * a.c.kv_heads;
-    A.unit_shift = 0;
+    const double segments = ((double)a.s.rows * A.group / (16 * r.ct) + a.s.batch) * a.c.kv_heads;
     while (segments * (double)((tiles >> A.unit_shift) + 1) >= 0x1p31) ++A.unit_shift;
     if (tiles <= 16) A.unit_shift = 4;
     A.splits = tiles > (int64_t)1 << A.unit_shift;
-    A.part_o = static_cast<float *>(a.workspace);
-    A.part_ml = A.part_o + (size_t)2 * kWorkers * 16 * ct * a.c.head_dim;
+    A.part_ml = A.part_o + r.stream_floats;
+    const bool one = r.ct == 1;
     switch (a.c.head_dim) {
-    case 64: return ct == 1 ? stream_types<64, 1>(A, stream) : stream_types<64, 2>(A, stream);
-    case 128: return ct == 1 ? stream_types<128, 1>(A, stream) : stream_types<128, 2>(A, stream);
+    case 64: return one ? stream_types<64, 1>(A, stream) : stream_types<64, 2>(A, stream);
+    case 128: return one ? stream_types<128, 1>(A, stream) : stream_types<128, 2>(A, stream);
     case 192: return stream_types<192, 1>(A, stream);
     default: return stream_types<256, 1>(A, stream);
     }
