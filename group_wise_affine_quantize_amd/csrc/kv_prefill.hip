@@ -18,7 +18,14 @@
 //
 // The reference R of the weights 2^(x - R) only moves when a column's maximum
 // passes it by kSlack: a move costs a pass over O, and weights may reach
-// 2^(14 + kSlack) in fp16.
+// 2^(kTop + kSlack) in fp16.
+//
+// 3 prompts of 2530 to 4096 tokens, 32 heads of 128 over 8 int8 key/value heads: 380 us, 737 TFLOP/s
+// of the visible products, where a large fp16 library product reaches 1131.
+// A tile takes about 4450 cycles at the 1.97 GHz that the card keeps up:
+// about 330 vector instructions for each of the two waves of a SIMD and 2048
+// cycles of MFMA per SIMD, overlapped as far as the two waves' phases differ.  The LDS (256 bytes
+// a cycle with the keys above) is a quarter used.
 #include "nq_kv_attn.h"
 #include "nq_tiles.h"
 
@@ -28,7 +35,8 @@ namespace {
 
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
-constexpr float kSlack = 1.5f;
+// Weights are at most 2^12 where R is set, and 2^15.5 before it moves again.
+constexpr float kTop = 12.0f, kSlack = 3.5f;
 
 template <int D> struct Shape {
     static constexpr int W = D <= 128 ? 8 : 4;      // waves
@@ -43,6 +51,14 @@ __device__ __forceinline__ float16_t mfma32(half8_t a, half8_t b, float16_t c)
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
+// A row's 16-byte chunks are placed at their number xored with a key, so that
+// sixteen neighbouring rows' chunks of one number -- what a phase of a 16-byte
+// read takes -- lie in different quarters of the 64 banks.
+template <int CHUNKS> __device__ __forceinline__ int key_of(int row)
+{
+    return CHUNKS % 16 == 0 ? row & 15 : (row >> 1) & 7;
+}
+
 // The column tiles of a sequence here.
 template <int M> __device__ __forceinline__ uint32_t tile_count(const AttnArgs &A, int b)
 {
@@ -51,24 +67,38 @@ template <int M> __device__ __forceinline__ uint32_t tile_count(const AttnArgs &
     return cols > A.few ? (uint32_t)(cols + M - 1) / M : 0u;
 }
 
-// Finds column tile `rank` counted from the end of the list (the last tiles of
-// a causal sequence see the most tokens, and start first).
+// The workgroups start with the column tiles of the highest number (of all
+// sequences), which see the most tokens of a causal prompt: the last ones to
+// start are short.  Finds the sequence and number of tile `rank` in that
+// order; -1 past the last.
 template <int M> __device__ __forceinline__ int tile_locate(const AttnArgs &A, uint32_t rank, uint32_t *ctile)
 {
     const int batch = A.a.s.batch, lane = (int)(threadIdx.x & 63u);
-    uint32_t base = 0;
-    for (int b0 = 0; b0 < batch; b0 += 64) {
-        const int b = batch - 1 - b0 - lane;
-        const uint32_t c = b >= 0 ? tile_count<M>(A, b) : 0u;
-        const uint32_t upto = wave_scan32(c);
-        const uint32_t sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
-        if (base + sum > rank) {
-            const int l = __ffsll((unsigned long long)__ballot(base + upto > rank)) - 1;
-            // tiles of this sequence after the wanted one
-            *ctile = (uint32_t)__builtin_amdgcn_readlane((int)upto, l) + base - rank - 1;
-            return batch - 1 - b0 - l;
+    const uint32_t mine = lane < batch ? tile_count<M>(A, lane) : 0u;     // of the first 64 sequences
+    auto count = [&](int b) { return b < 64 ? mine : (b < batch ? tile_count<M>(A, b) : 0u); };
+    // tiles numbered c or more
+    auto from = [&](uint32_t c) -> uint32_t {
+        uint32_t sum = 0;
+        for (int b0 = 0; b0 < batch; b0 += 64) {
+            const uint32_t n = count(b0 + lane);
+            sum += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan32(n > c ? n - c : 0u), 63);
         }
-        base += sum;
+        return sum;
+    };
+    if (from(0) <= rank) return -1;
+    uint32_t lo = 0, hi = A.tile_bound;     // from(lo) > rank >= from(hi)
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (from(mid) > rank) lo = mid;
+        else hi = mid;
+    }
+    *ctile = lo;
+    uint32_t left = rank - from(lo + 1);    // which of the sequences with more than lo tiles
+    for (int b0 = 0; b0 < batch; b0 += 64) {
+        const uint32_t upto = wave_scan32(count(b0 + lane) > lo ? 1u : 0u);
+        const uint32_t sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+        if (sum > left) return b0 + __ffsll((unsigned long long)__ballot(upto > left)) - 1;
+        left -= sum;
     }
     return -1;
 }
@@ -79,9 +109,7 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
     constexpr int NP = Parts<T>::n, M = Shape<D>::M, THREADS = Shape<D>::THREADS, PIECES = Shape<D>::PIECES;
     constexpr int LD = Shape<D>::LD, KS = D / 16, DT = D / 32;
     constexpr int KC = D / 8;       // 16-byte chunks of a key row in LDS
-    // keys [64 rows][D], values [D][64 tokens], fp16, 16-byte chunks xored with
-    // the row's low bits: the eight lanes that a phase of a 16-byte read serves
-    // then cover all banks
+    // keys [64 rows][D], values [D][64 tokens], fp16, chunks placed by key_of
     __shared__ uint4 sh_k[2][kTile * KC];
     __shared__ uint4 sh_v[2][D * 8];
     __shared__ float4 sh_s[2][4];   // of each 16 tokens: key scale, log2 and reciprocal of the value scale, whether any is there
@@ -107,33 +135,17 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
     const int t_begin = first_tile + (int)((int64_t)tiles * split / A.tile_splits);
     const int t_end = first_tile + (int)((int64_t)tiles * (split + 1) / A.tile_splits);
 
-    // queries
-    half8_t q[KS][NP];
+    // the query rows are on their way while the first tile is asked for
     const int wcol = col0 + wave * 32;          // the wave's first column
     const Column mine = column(A, s, wcol + r, head);
-    float cf = 1.0f, ref = kNegInf, l = 0.0f;
+    constexpr int RAW = 8 * (int)sizeof(T) / 16;
+    uint4 raw[KS][RAW];
     {
-        const bool is = mine.row >= 0;
-        const T *src = static_cast<const T *>(a.q) + (int64_t)(is ? mine.row : 0) * a.ldq + mine.head * D + 8 * h;
-        // twice over the row (it stays in the cache): its maximum, then its parts
-        float top = 0.0f;
+        const T *src = static_cast<const T *>(a.q) + (int64_t)(mine.row < 0 ? 0 : mine.row) * a.ldq + mine.head * D + 8 * h;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            float f[8];
-            load_f32x8<T>(src + 16 * ks, f);
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
-        }
-        top = fmaxf(top, xor_lane<32>(top, lane));
-        float back;
-        const float up = row_scale(top, &back);
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            float f[8];
-            load_f32x8<T>(src + 16 * ks, f);
-            for (int i = 0; i < 8; ++i) f[i] = is ? f[i] * up : 0.0f;
-            split_half<NP>(f, q[ks]);
-        }
-        if (is) cf = a.scale * kLog2e * back;
+            for (int i = 0; i < RAW; ++i) raw[ks][i] = reinterpret_cast<const uint4 *>(src + 16 * ks)[i];
     }
     float16_t o[DT];
 #pragma unroll
@@ -147,52 +159,51 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
 
     // Staging: this thread's 16-byte pieces of a tile's keys and values.  Block
     // ids are read a tile ahead of the codes, those a tile ahead of their
-    // conversion.
+    // conversion.  A tile starts at a multiple of 64 tokens, so a piece's place
+    // inside its block is the tile's plus the thread's own.
     const int *table = a.s.table + (int64_t)b * a.s.ldt;
     const int j_lo = seg_lo >> sh, j_hi = (seg_hi - 1) >> sh;      // table entries that may be read
-    auto entry_of = [&](int pos) -> int {
-        const int j = pos >> sh;
-        return table[j < j_lo ? j_lo : (j > j_hi ? j_hi : j)];
-    };
-    // -1 where no column sees the 16 tokens from pos, or no block holds them
-    auto block_of = [&](int pos, int entry) -> int {
-        return pos < seg_hi && pos + 16 > seg_lo && (unsigned)entry < (unsigned)a.c.blocks ? entry : -1;
-    };
+    auto entry_of = [&](int j) -> int { return table[j < j_lo ? j_lo : (j > j_hi ? j_hi : j)]; };
     const int tg = tid & 3;
+    const uint32_t stride = (uint32_t)heads * (uint32_t)(D << sh);  // bytes of a block's keys (and values)
+    const uint8_t *kp[LD], *vp = a.c.v_codes + (int64_t)head * (D << sh) + ((tid >> 2) << sh) + ((16 * tg) & bmask);
+    int kj[LD];
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+        const int piece = tid + i * THREADS, tok = piece / (D / 16), c16 = piece % (D / 16);
+        kp[i] = a.c.k_codes + (int64_t)head * (D << sh) + (tok & bmask) * D + 16 * c16;
+        kj[i] = tok >> sh;
+    }
+    const int vj = (16 * tg) >> sh;
     uint4 kw[LD], vw[LD];
-    int kid[LD], vid, vnow = -1;
+    int kid[LD], vid;
+    bool has = false;       // whether a column sees some of the 16 tokens, and a block holds them
     float sk = 1.0f, sv = 1.0f;
     auto load_ids = [&](int t) {
+        const int j = (t << 6) >> sh;
 #pragma unroll
-        for (int i = 0; i < LD; ++i) {
-            const int piece = tid + i * THREADS;
-            if (PIECES % THREADS == 0 || piece < PIECES) kid[i] = entry_of((t << 6) + piece / (D / 16));
-        }
-        vid = entry_of((t << 6) + 16 * tg);
+        for (int i = 0; i < LD; ++i)
+            if (PIECES % THREADS == 0 || tid + i * THREADS < PIECES) kid[i] = entry_of(j + kj[i]);
+        vid = entry_of(j + vj);
     };
     auto load = [&](int t) {
-        const int base = t << 6;
+        const int at = (t << 6) & bmask, pos = (t << 6) + 16 * tg;
+        const bool there = (uint32_t)vid < (uint32_t)a.c.blocks;
+        const uint32_t id = there ? (uint32_t)vid : 0u;
+        has = there && pos < seg_hi && pos + 16 > seg_lo;
 #pragma unroll
-        for (int i = 0; i < LD; ++i) {
-            const int piece = tid + i * THREADS, pos = base + piece / (D / 16), c16 = piece % (D / 16);
-            if (PIECES % THREADS == 0 || piece < PIECES) {
-                const int id = block_of(pos & ~15, kid[i]);
-                kw[i] = *reinterpret_cast<const uint4 *>(
-                    a.c.k_codes + ((((int64_t)(id < 0 ? 0 : id) * a.c.kv_heads + head) << sh) + (pos & bmask)) * D + 16 * c16);
+        for (int i = 0; i < LD; ++i)
+            if (PIECES % THREADS == 0 || tid + i * THREADS < PIECES) {
+                const uint32_t k = (uint32_t)kid[i] < (uint32_t)a.c.blocks ? (uint32_t)kid[i] : 0u;
+                kw[i] = *reinterpret_cast<const uint4 *>(kp[i] + (uint64_t)k * stride + at * D);
             }
-        }
-        const int pos = base + 16 * tg;
-        vnow = block_of(pos, vid);
-        const int64_t slab = (int64_t)(vnow < 0 ? 0 : vnow) * a.c.kv_heads + head;
 #pragma unroll
-        for (int i = 0; i < LD; ++i) {
-            const int piece = tid + i * THREADS;
-            if (PIECES % THREADS == 0 || piece < PIECES)
-                vw[i] = *reinterpret_cast<const uint4 *>(a.c.v_codes + ((slab * D + (piece >> 2)) << sh) + (pos & bmask));
-        }
+        for (int i = 0; i < LD; ++i)
+            if (PIECES % THREADS == 0 || tid + i * THREADS < PIECES)
+                vw[i] = *reinterpret_cast<const uint4 *>(vp + (uint64_t)id * stride + (at + ((i * (THREADS / 4)) << sh)));
         if (wave == 0) {        // lanes 0 to 3 use them
-            sk = a.c.k_scales[slab];
-            sv = a.c.v_scales[slab];
+            sk = a.c.k_scales[(int64_t)id * heads + head];
+            sv = a.c.v_scales[(int64_t)id * heads + head];
         }
     };
     auto stage = [&](int t, int buf) {
@@ -200,7 +211,7 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
         for (int i = 0; i < LD; ++i) {
             const int piece = tid + i * THREADS, tok = piece / (D / 16), c16 = piece % (D / 16);
             if (PIECES % THREADS == 0 || piece < PIECES) {
-                const int u = tok & 31, row = (tok & 32) + 8 * ((u >> 2) & 3) + 4 * (u >> 4) + (u & 3), key = row & 7;
+                const int u = tok & 31, row = (tok & 32) + 8 * ((u >> 2) & 3) + 4 * (u >> 4) + (u & 3), key = key_of<KC>(row);
                 const half8_t x = codes_to_half<FMT>(kw[i].x, kw[i].y), y = codes_to_half<FMT>(kw[i].z, kw[i].w);
                 sh_k[buf][row * KC + ((2 * c16) ^ key)] = __builtin_bit_cast(uint4, x);
                 sh_k[buf][row * KC + ((2 * c16 + 1) ^ key)] = __builtin_bit_cast(uint4, y);
@@ -210,8 +221,8 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
         if constexpr (FMT == KV_FP8) {
             // codes of tokens that no column sees are whatever memory holds, a
             // NaN for instance: make them zeros
-            if (vnow < 0 || pos < seg_lo || pos + 16 > seg_hi) {
-                const int lo = vnow < 0 ? 16 : seg_lo - pos, hi = seg_hi - pos;
+            if (!has || pos < seg_lo || pos + 16 > seg_hi) {
+                const int lo = !has ? 16 : seg_lo - pos, hi = seg_hi - pos;
                 uint32_t keep[4];
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
@@ -229,14 +240,13 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
             const int piece = tid + i * THREADS, d = piece >> 2;
             if (PIECES % THREADS == 0 || piece < PIECES) {
                 const half8_t x = codes_to_half<FMT>(vw[i].x, vw[i].y), y = codes_to_half<FMT>(vw[i].z, vw[i].w);
-                sh_v[buf][d * 8 + ((2 * tg) ^ (d & 7))] = __builtin_bit_cast(uint4, x);
-                sh_v[buf][d * 8 + ((2 * tg + 1) ^ (d & 7))] = __builtin_bit_cast(uint4, y);
+                sh_v[buf][d * 8 + ((2 * tg) ^ key_of<8>(d))] = __builtin_bit_cast(uint4, x);
+                sh_v[buf][d * 8 + ((2 * tg + 1) ^ key_of<8>(d))] = __builtin_bit_cast(uint4, y);
             }
         }
         if (tid < 4) {
             // all-zero keys (or none): any scale will do for scores of zero, and one
             // keeps the factor of the scores above zero
-            const bool has = vnow >= 0;
             const float k = !has || sk == 0.0f ? 1.0f : sk, v = !has ? 1.0f : (sv == 0.0f ? kZeroBlockScale : sv);
             sh_s[buf][tid] = make_float4(k, fast_log2(v), 1.0f / v, has ? 1.0f : 0.0f);
         }
@@ -247,14 +257,51 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
         load_ids(t_begin);
         load(t_begin);
         load_ids(t_begin < t_last ? t_begin + 1 : t_last);
+    }
+    half8_t q[KS][NP];
+    float cf = 1.0f, ref = kNegInf, l = 0.0f;
+    {
+        float top = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            float f[8];
+            unpack_f32x8<T>(raw[ks], f);
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+        }
+        top = fmaxf(top, xor_lane<32>(top, lane));
+        float back;
+        const float up = row_scale(top, &back);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            float f[8];
+            unpack_f32x8<T>(raw[ks], f);
+            for (int i = 0; i < 8; ++i) f[i] = mine.row >= 0 ? f[i] * up : 0.0f;
+            split_half<NP>(f, q[ks]);
+        }
+        if (mine.row >= 0) cf = a.scale * kLog2e * back;
+    }
+    if (t_begin < t_end) {
         stage(t_begin, 0);
         load(t_begin < t_last ? t_begin + 1 : t_last);
         load_ids(t_begin + 2 < t_last ? t_begin + 2 : t_last);
     }
+    // The next tile goes into the other buffer, whose readers passed the last
+    // barrier; then the loads of the one after.  The second four waves do
+    // this first in a step and the others last: of the two waves of a SIMD,
+    // one then is a phase behind the other, and they want the vector unit and
+    // the matrix cores by turns.
+    auto stage_next = [&](int t, int buf) {
+        if (t >= t_last) return;
+        stage(t + 1, buf ^ 1);
+        load(t + 2 < t_last ? t + 2 : t_last);
+        load_ids(t + 3 < t_last ? t + 3 : t_last);
+    };
+    const bool late = wave >= 4;
     lds_barrier();
     for (int t = t_begin; t < t_end; ++t) {
         const int buf = (t - t_begin) & 1, base = t << 6;
         const bool busy = base < any_hi && base + kTile > any_lo;
+        if (late) stage_next(t, buf);
         float16_t S[2];
         if (busy) {
 #pragma unroll
@@ -264,17 +311,10 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const half8_t k = __builtin_bit_cast(half8_t, sh_k[buf][(32 * u + r) * KC + ((2 * ks + h) ^ (r & 7))]);
+                    const half8_t k = __builtin_bit_cast(half8_t, sh_k[buf][(32 * u + r) * KC + ((2 * ks + h) ^ key_of<KC>(r))]);
 #pragma unroll
                     for (int p = 0; p < NP; ++p) S[u] = mfma32(k, q[ks][p], S[u]);
                 }
-        }
-        // the next tile into the other buffer, whose readers passed the last
-        // barrier, while the matrix cores work; then the loads of the one after
-        if (t < t_last) {
-            stage(t + 1, buf ^ 1);
-            load(t + 2 < t_last ? t + 2 : t_last);
-            load_ids(t + 3 < t_last ? t + 3 : t_last);
         }
         if (busy) {
             const float4 s0 = sh_s[buf][h], s1 = sh_s[buf][2 + h];
@@ -294,7 +334,7 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
 #pragma unroll
             for (int i = 1; i < 16; ++i) m0 = fmaxf(m0, S[0][i]), m1 = fmaxf(m1, S[1][i]);
             float m = fmaxf(fmaf(m0, f0, s0.y), fmaf(m1, f1, s1.y));
-            m = fmaxf(m, xor_lane<32>(m, lane)) - kPScale;
+            m = fmaxf(m, xor_lane<32>(m, lane)) - kTop;
             if (__any(m > ref + kSlack)) {
                 const float next = m > ref + kSlack ? m : ref;
                 const float alpha = next == kNegInf ? 0.0f : fast_exp2(ref - next);
@@ -323,12 +363,13 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
 #pragma unroll
                     for (int dt = 0; dt < DT; ++dt) {
                         const half8_t v = __builtin_bit_cast(
-                            half8_t, sh_v[buf][(32 * dt + r) * 8 + ((4 * u + 2 * h + e) ^ (r & 7))]);
+                            half8_t, sh_v[buf][(32 * dt + r) * 8 + ((4 * u + 2 * h + e) ^ key_of<8>(r))]);
 #pragma unroll
                         for (int p = 0; p < NP; ++p) o[dt] = mfma32(v, P[e][p], o[dt]);
                     }
             }
         }
+        if (!late) stage_next(t, buf);
         lds_barrier();
     }
 

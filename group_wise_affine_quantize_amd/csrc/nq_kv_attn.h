@@ -147,21 +147,29 @@ __device__ __forceinline__ Column column(const AttnArgs &A, const StreamSeq &s, 
     return c;
 }
 
-template <typename T> __device__ __forceinline__ void load_f32x8(const T *p, float *v);
-template <> __device__ __forceinline__ void load_f32x8<float>(const float *p, float *v)
+// Eight neighbouring elements, from the 16-byte words that hold them.
+template <typename T> __device__ __forceinline__ void unpack_f32x8(const uint4 *w, float *v);
+template <> __device__ __forceinline__ void unpack_f32x8<float>(const uint4 *w, float *v)
 {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
 }
-template <> __device__ __forceinline__ void load_f32x8<bf16_bits>(const bf16_bits *p, float *v)
+template <> __device__ __forceinline__ void unpack_f32x8<bf16_bits>(const uint4 *w, float *v)
 {
-    const uint4 d = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+    const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
+}
+template <typename T> __device__ __forceinline__ void load_f32x8(const T *p, float *v)
+{
+    uint4 w[8 * sizeof(T) / 16];
+#pragma unroll
+    for (int i = 0; i < (int)(8 * sizeof(T) / 16); ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    unpack_f32x8<T>(w, v);
 }
 
 template <typename T> __device__ __forceinline__ void store_f32x4(T *p, const float *v);
@@ -171,9 +179,12 @@ template <> __device__ __forceinline__ void store_f32x4<float>(float *p, const f
 }
 template <> __device__ __forceinline__ void store_f32x4<bf16_bits>(bf16_bits *p, const float *v)
 {
+    // the hardware's conversion: nearest, ties to even, NaN stays one
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    const bf2 a = {(__bf16)v[0], (__bf16)v[1]}, b = {(__bf16)v[2], (__bf16)v[3]};
     uint2 w;
-    w.x = f32_to_bf16(v[0]) | f32_to_bf16(v[1]) << 16;
-    w.y = f32_to_bf16(v[2]) | f32_to_bf16(v[3]) << 16;
+    w.x = __builtin_bit_cast(uint32_t, a);
+    w.y = __builtin_bit_cast(uint32_t, b);
     *reinterpret_cast<uint2 *>(p) = w;
 }
 

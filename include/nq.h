@@ -519,7 +519,7 @@ size_t nq_kv_attention_workspace_bytes(const nq_kv_cache *cache, const nq_kv_seq
  * and positive.  Keys, values and sums are fp32-accurate; for bf16 queries
  * the weights of the second product keep 11 bits (fp16), for fp32 queries
  * both products take their operands with 22 bits; weights times their values'
- * scale lose bits from 2^-28 of a row's largest down and end at 2^-39 of it.  The workspace (16-byte
+ * scale lose bits from 2^-26 of a row's largest down and end at 2^-37 of it.  The workspace (16-byte
  * aligned) is scratch of one call at a time. */
 nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, const void *q, nq_dtype x_dt,
                           int64_t ldq, int32_t q_heads, float softmax_scale, int32_t causal, int64_t window,

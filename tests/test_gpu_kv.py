@@ -182,7 +182,7 @@ def check_attention(p, start, lengths, table, q, how, scale=None, lse=True):
     # roundings, relative: the scores' sums (dim terms) and exponents (24 bits
     # of log2 e * |z|, twice), the weights (2^-12 as fp16, 2^-22 as two of
     # them) and sums over the tokens; for fp32 the query's 22 bits.  And, as the
-    # contract states, weights times value scales end 2^-39 below the largest
+    # kernels state, weights times value scales end about 2^-39 below the largest
     wide = q.dtype == torch.float32
     z = (want["reach"] + 20)[..., None]
     weight = 2 * ((dim + 8) * 2.0 ** -24 + 2.0 ** -22) * z + (2.0 ** -21 if wide else 2.0 ** -11)
