@@ -603,6 +603,18 @@ def nq_fp_qmm_notrans(x, codes, scales, mode, global_scale=None, row_exact=False
 
 
 # ---------------------------------------------------------------- key/value cache in 8 bits
+# These calls are made once or twice per layer and serving step, where a
+# microsecond on the host counts: outputs made here are not checked again, and
+# the stream's handle is taken without making a Stream object.
+def _raw_stream(stream=None):
+    """The handle of `stream`, or of the current stream of the current device."""
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+
+
 class _KVCacheStruct(ctypes.Structure):
     _fields_ = [("k_codes", _P), ("v_codes", _P), ("k_scales", _P), ("v_scales", _P), ("blocks", _I64),
                 ("kv_heads", _I32), ("head_dim", _I32), ("block_tokens", _I32), ("format", _I32)]
@@ -710,7 +722,7 @@ def nq_kv_append(cache, seqs, k, v, stream=None):
     ldv = _row_stride("v", v, seqs.rows, cache.kv_heads, cache.head_dim)
     if k.dtype != v.dtype:
         raise TypeError("k and v must have the same dtype")
-    status = lib.nq_kv_append(cache._ref, seqs._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, _dt(k), _stream(stream))
+    status = lib.nq_kv_append(cache._ref, seqs._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, _dt(k), _raw_stream(stream))
     if status:
         _check(status)
 
@@ -722,15 +734,19 @@ def nq_kv_read(cache, seqs, out_dtype=None, k=None, v=None, stream=None):
     lib = _lib or load_library()
     shape = (seqs.rows, cache.kv_heads, cache.head_dim)
     dt = out_dtype or torch.bfloat16
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _contig(name, t)
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+            dt = t.dtype
     if k is None:
         k = _empty(stream, shape, dt, cache.k_codes.device)
     if v is None:
         v = _empty(stream, shape, dt, cache.k_codes.device)
-    for name, t in (("k", k), ("v", v)):
-        _contig(name, t)
-        if tuple(t.shape) != shape or t.dtype != k.dtype:
-            raise ValueError(f"{name} must have shape {shape} and the other output's dtype")
-    status = lib.nq_kv_read(cache._ref, seqs._ref, k.data_ptr(), v.data_ptr(), _dt(k), _stream(stream))
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must have the same dtype")
+    status = lib.nq_kv_read(cache._ref, seqs._ref, k.data_ptr(), v.data_ptr(), _dt(k), _raw_stream(stream))
     if status:
         _check(status)
     return k, v
@@ -777,7 +793,7 @@ def nq_kv_attention(cache, seqs, q, scale=None, causal=True, window=0, out=None,
     status = lib.nq_kv_attention(cache._ref, seqs._ref, q.data_ptr(), dt, ldq, heads,
                                  cache.head_dim ** -0.5 if scale is None else scale, int(bool(causal)), window,
                                  out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                 None if workspace is None else workspace.data_ptr(), ws_bytes, _stream(stream))
+                                 None if workspace is None else workspace.data_ptr(), ws_bytes, _raw_stream(stream))
     if status:
         _check(status)
     return out
@@ -823,17 +839,18 @@ def nq_moe_route(router, logits, bias=None, ids=None, weights=None, stream=None)
         _contig("bias", bias)
         if bias.dtype != torch.float32 or bias.numel() != router.experts:
             raise ValueError("bias must be float32 [experts]")
+    for name, t, dt in (("ids", ids, torch.int32), ("weights", weights, torch.float32)):
+        if t is not None:
+            _contig(name, t)
+            if t.shape != shape or t.dtype != dt:
+                raise ValueError(f"{name} must be {dt} {shape}")
     if ids is None:
         ids = _empty(stream, shape, torch.int32, logits.device)
     if weights is None:
         weights = _empty(stream, shape, torch.float32, logits.device)
-    for name, t, dt in (("ids", ids, torch.int32), ("weights", weights, torch.float32)):
-        _contig(name, t)
-        if t.shape != shape or t.dtype != dt:
-            raise ValueError(f"{name} must be {dt} {shape}")
     status = lib.nq_moe_route(router._ref, logits.data_ptr(), _dt(logits), tokens, ld,
                               None if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(),
-                              _stream(stream))
+                              _raw_stream(stream))
     if status:
         _check(status)
     return ids, weights
@@ -858,7 +875,7 @@ def nq_moe_route_grad(router, logits, ids, dweights, dlogits=None, stream=None):
         if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
             raise ValueError("dlogits must have the logits' shape and dtype")
     status = lib.nq_moe_route_grad(router._ref, logits.data_ptr(), _dt(logits), tokens, ld, ids.data_ptr(),
-                                   dweights.data_ptr(), dlogits.data_ptr(), _stream(stream))
+                                   dweights.data_ptr(), dlogits.data_ptr(), _raw_stream(stream))
     if status:
         _check(status)
     return dlogits

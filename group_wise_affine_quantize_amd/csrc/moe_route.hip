@@ -14,9 +14,19 @@
 //   softmax: dx_j = p_j (d_j - sum_k d_k p_k), d_j = 0 where not chosen
 //   (renormalised, the sum is zero).
 //
-// A token's logits lie in the registers of LPT = 16 or 64 lanes, so that a
-// wave routes four tokens of up to 256 experts at once and the rounds of the
-// choice need no memory.
+// A token's logits lie in the registers of LPT = 16 or 64 lanes, EPL
+// neighbouring ones in each, so that a wave routes four tokens of up to 256
+// experts at once.
+//
+// The choice of up to kShort experts: every expert is one 64-bit number, its
+// ordered key above its falling index, so that numbers are distinct and the
+// largest is the one to choose, ties included.  As the bits of a denormal
+// double they order under v_max_f64 / v_min_f64: a compare-exchange is two
+// instructions.  Each lane sorts its own and keeps the best eight; lists of
+// two lanes merge by max(a[i], b[7 - i]) -- a bitonic sequence of the best
+// eight -- and three rounds of exchanges, and after log2(LPT) merges every
+// lane holds the token's eight in order.  More than kShort are chosen one by one,
+// a maximum over the token's lanes each.
 #include "nq_kv_device.h"
 
 namespace nqk {
@@ -25,6 +35,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxGroups = 64;
+constexpr int kShort = 8;       // experts per token up to which the choice is by sorting
 constexpr float kNegInf = -__builtin_inff();
 
 // Order-preserving map to unsigned; 0 is below every number's image.
@@ -93,11 +104,29 @@ __device__ __forceinline__ void load_logits(const T *row, int e0, int experts, b
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) x[j] = e0 + j < experts ? Elt<T>::load(row, e0 + j) : kNegInf;
+        for (int j = 0; j < EPL; ++j) {
+            const float t = Elt<T>::load(row, e0 + j < experts ? e0 + j : experts - 1);
+            x[j] = e0 + j < experts ? t : kNegInf;
+        }
     }
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// e^x to about 1.5 ulp: x log2(e) in two parts, the low one to first order.
+__device__ __forceinline__ float exp_of(float x)
+{
+    constexpr float L = 1.44269502162933349609f, Llo = 1.92596299112661746887e-8f;   // log2(e)
+    x = fminf(fmaxf(x, -150.0f), 88.0f);    // 0 from below on; no infinities, whose differences are none
+    const float t = x * L, r = fmaf(x, Llo, fmaf(x, L, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e * r, 0.693147180559945309417f, e);
+}
+
+__device__ __forceinline__ float sigmoid(float x)
+{
+    const float d = 1.0f + exp_of(-x);
+    const float y = __builtin_amdgcn_rcpf(d);
+    return x < -87.0f ? 0.0f : fmaf(fmaf(-d, y, 1.0f), y, y);   // below fp32's normal numbers: 0
+}
 
 // p of a token's logits; for softmax *top and *inv are the maximum and the
 // reciprocal-free divisor that any single logit's p can be taken with.
@@ -118,7 +147,7 @@ __device__ __forceinline__ void scores(int kind, const float *x, int lane, float
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        p[j] = expf(x[j] - ref);
+        p[j] = exp_of(x[j] - ref);
         s += p[j];
     }
     s = token_sum<LPT>(s, lane);
@@ -128,8 +157,111 @@ __device__ __forceinline__ void scores(int kind, const float *x, int lane, float
     *top = ref, *sum = s;
 }
 
-template <typename T, int LPT, int EPL>
-__global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeRouteLaunch a, int wide)
+// ---- the choice by sorting
+__device__ __forceinline__ double wide_key(uint32_t key, int e)
+{
+    const uint64_t v = (uint64_t)key << 10 | (uint64_t)(1023 - e);
+    return __longlong_as_double((long long)(key ? v : 0));
+}
+__device__ __forceinline__ void exchange(double &hi, double &lo)
+{
+    const double a = hi, b = lo;
+    hi = __builtin_fmax(a, b), lo = __builtin_fmin(a, b);
+}
+// Eight numbers that fall and then rise (or any rotation of that) into falling order.
+__device__ __forceinline__ void sort_bitonic8(double *v)
+{
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & d)) exchange(v[i], v[i + d]);
+}
+__device__ __forceinline__ void sort8(double *v)      // Batcher's odd-even merge sort, 19 exchanges
+{
+    exchange(v[0], v[1]), exchange(v[2], v[3]), exchange(v[4], v[5]), exchange(v[6], v[7]);
+    exchange(v[0], v[2]), exchange(v[1], v[3]), exchange(v[4], v[6]), exchange(v[5], v[7]);
+    exchange(v[1], v[2]), exchange(v[5], v[6]);
+    exchange(v[0], v[4]), exchange(v[1], v[5]), exchange(v[2], v[6]), exchange(v[3], v[7]);
+    exchange(v[2], v[4]), exchange(v[3], v[5]);
+    exchange(v[1], v[2]), exchange(v[3], v[4]), exchange(v[5], v[6]);
+}
+// A lane's number from the row of 16 turned by TURN lanes.
+template <int TURN> __device__ __forceinline__ uint64_t turned(uint64_t v)
+{
+    constexpr int row_ror = 0x120 + TURN;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)v, row_ror, 0xF, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(v >> 32), row_ror, 0xF, 0xF, true);
+    return (uint64_t)hi << 32 | lo;
+}
+// v[0 .. 7] and the same of another lane (o) -> the best eight of both.
+__device__ __forceinline__ void merge8(double *v, const double *o)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_fmax(v[i], o[i]);
+    sort_bitonic8(v);
+}
+// With the lane TURN places back in the row: turns by 1, 2, 4 and 8 in turn
+// give every lane the best of all 16, each counted once.
+template <int TURN> __device__ __forceinline__ void merge_turned(double *v)
+{
+    double o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        o[i] = __longlong_as_double((long long)turned<TURN>((uint64_t)__double_as_longlong(v[7 - i])));
+    merge8(v, o);
+}
+template <int OFF> __device__ __forceinline__ void merge_rows(double *v, int lane)      // OFF = 16, 32
+{
+    double o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint64_t u = (uint64_t)__double_as_longlong(v[7 - i]);
+        const uint32_t lo = __float_as_uint(xor_lane<OFF>(__uint_as_float((uint32_t)u), lane));
+        const uint32_t hi = __float_as_uint(xor_lane<OFF>(__uint_as_float((uint32_t)(u >> 32)), lane));
+        o[i] = __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+    }
+    merge8(v, o);
+}
+
+// Lanes among the 15 others of a row of 16 whose number is larger.
+template <int TURN> __device__ __forceinline__ int better_lanes(uint64_t mine)
+{
+    if constexpr (TURN == 16) return 0;
+    else {
+        return (turned<TURN>(mine) > mine) + better_lanes<TURN + 1>(mine);
+    }
+}
+
+// A token's groups when each is a power of two of lanes (LPT = 16): the best
+// one or two values of a lane and of its group's lanes, then the group's rank
+// among the others by turning the 16 lanes past each other.  Returns whether
+// the lane's group stays.
+template <int EPL>
+__device__ __forceinline__ bool group_stays(const MoeRoute &r, const float *v, int lanes_per_group, int tl, int lane)
+{
+    float b1 = kNegInf, b2 = kNegInf;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        b2 = fmaxf(b2, fminf(b1, fmaxf(v[j], kNegInf)));
+        b1 = fmaxf(b1, v[j]);
+    }
+    auto join = [&](float o1, float o2) {
+        b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+        b1 = fmaxf(b1, o1);
+    };
+    if (lanes_per_group > 1) join(xor_lane<1>(b1, lane), xor_lane<1>(b2, lane));
+    if (lanes_per_group > 2) join(xor_lane<2>(b1, lane), xor_lane<2>(b2, lane));
+    if (lanes_per_group > 4) join(xor_lane<4>(b1, lane), xor_lane<4>(b2, lane));
+    if (lanes_per_group > 8) join(xor_lane<8>(b1, lane), xor_lane<8>(b2, lane));
+    const int group = tl / lanes_per_group;
+    const uint32_t score = group < r.groups ? ordered(r.group_best == 2 ? b1 + b2 : b1) : 0u;
+    const uint64_t mine = (uint64_t)score << 32 | (uint32_t)(63 - group);
+    return better_lanes<1>(mine) < r.top_groups * lanes_per_group;
+}
+
+template <typename T, int LPT, int EPL, bool SORT>
+__global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeRouteLaunch a, int wide, int lanes_per_group)
 {
     constexpr int TOK = kThreads / LPT;
     __shared__ float sh_key[TOK][LPT * EPL];
@@ -142,17 +274,31 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeRouteLaunch a, i
     const T *row = static_cast<const T *>(a.logits) + (live ? token : a.tokens - 1) * a.ldl;
     const int e0 = tl * EPL;
 
-    float x[EPL], p[EPL], top, sum;
+    float x[EPL], p[EPL], top = 0.0f, sum = 1.0f;
     load_logits<T, EPL>(row, e0, r.experts, wide != 0, x);
-    scores<LPT, EPL>(r.score, x, lane, p, &top, &sum);
+    const bool summed = r.groups > 1 && r.group_best == 2;
+    // a sigmoid's scores are wanted for every expert only where keys are made of them
+    if (r.score == MOE_SOFTMAX || a.bias || summed || !SORT) scores<LPT, EPL>(r.score, x, lane, p, &top, &sum);
+    float bias[EPL];
+    if (a.bias)
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) bias[j] = a.bias[e0 + j < r.experts ? e0 + j : r.experts - 1];
     uint32_t key[EPL];
+    float v[EPL];           // what a group's score is made of
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        const float k = a.bias ? (e0 + j < r.experts ? p[j] + a.bias[e0 + j] : 0.0f) : x[j];
-        key[j] = e0 + j < r.experts ? ordered(k) : 0u;
-        if (r.groups > 1) sh_key[slot][e0 + j] = !a.bias && r.group_best == 2 ? p[j] : k;
+        const bool is = e0 + j < r.experts;
+        const float k = a.bias ? p[j] + bias[j] : x[j];
+        key[j] = is ? ordered(k) : 0u;
+        v[j] = is ? (!a.bias && summed ? p[j] : k) : kNegInf;
     }
-    if (r.groups > 1) {
+    if (LPT == 16 && lanes_per_group > 0) {
+        if (!group_stays<EPL>(r, v, lanes_per_group, tl, lane))
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) key[j] = 0u;
+    } else if (r.groups > 1) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) sh_key[slot][e0 + j] = v[j];
         const int size = r.experts / r.groups;
         __syncthreads();
         for (int g = tl; g < r.groups; g += LPT) {
@@ -184,6 +330,43 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeRouteLaunch a, i
         }
     }
 
+    if constexpr (SORT) {
+        double best[EPL];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) best[j] = wide_key(key[j], e0 + j);
+        sort8(best);
+        if constexpr (EPL == 16) {
+            sort8(best + 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) best[i] = __builtin_fmax(best[i], best[15 - i]);
+            sort_bitonic8(best);
+        }
+        merge_turned<1>(best);
+        merge_turned<2>(best);
+        merge_turned<4>(best);
+        merge_turned<8>(best);
+        if constexpr (LPT == 64) {
+            merge_rows<16>(best, lane);
+            merge_rows<32>(best, lane);
+        }
+        uint32_t low = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) low = tl == i ? (uint32_t)__double_as_longlong(best[i]) : low;
+        const int found = 1023 - (int)(low & 1023u), id = found < r.experts ? found : r.experts - 1;
+        const bool mine = tl < r.top_k;
+        float w = 0.0f;
+        if (mine) {             // its logit again: it is in the cache
+            const float x1 = Elt<T>::load(row, id);
+            w = r.score == MOE_SIGMOID ? sigmoid(x1) : exp_of(x1 - top) / sum;
+        }
+        const float total = token_sum<LPT>(w, lane);
+        if (live && mine) {
+            if (r.renormalise) w = total > 0.0f ? w / total : 0.0f;
+            a.ids[token * r.top_k + tl] = (uint32_t)id;
+            a.weights[token * r.top_k + tl] = w * r.scale;
+        }
+        return;
+    }
     float mine[2] = {0.0f, 0.0f}, total = 0.0f;
     for (int k = 0; k < r.top_k; ++k) {
         uint32_t best = 0u;
@@ -249,7 +432,7 @@ __global__ __launch_bounds__(kThreads) void moe_grad_kernel(MoeGradLaunch a, int
         pk[i] = 0.0f, qk[i] = 0.0f, d[i] = 0.0f;
         if (id[i] < (uint32_t)r.experts) {
             const float v = Elt<T>::load(row, id[i]);
-            pk[i] = soft ? expf(v - top) / sum : sigmoid(v);
+            pk[i] = soft ? exp_of(v - top) / sum : sigmoid(v);
             qk[i] = sigmoid(-v);                          // 1 - p of a sigmoid, without cancellation
             d[i] = a.dweights[t * r.top_k + k] * r.scale;
         }
@@ -291,7 +474,19 @@ template <typename L> unsigned grid_of(const L &a, int lpt)
 
 template <typename T, int LPT, int EPL> void go(const MoeRouteLaunch &a, int wide, hipStream_t s)
 {
-    moe_route_kernel<T, LPT, EPL><<<grid_of(a, LPT), kThreads, 0, s>>>(a, wide);
+    // lanes of a group, where that is a power of two of 16 lanes; 0: through LDS
+    int lanes = 0;
+    const int size = a.r.experts / a.r.groups;
+    if (LPT == 16 && a.r.groups > 1 && size % EPL == 0) {
+        lanes = size / EPL;
+        if (lanes & (lanes - 1) || lanes > 16) lanes = 0;
+    }
+    // Lists of eight are worth their merges where a lane has that many experts
+    // (16384 tokens of 256 experts, top 8 of 4 of 8 groups: 13.5 us sorted, 25 one by one; 32768 of 64, top 6:
+    // 10.1 and 9.3).
+    constexpr bool sorts = EPL >= 8;
+    if (sorts && a.r.top_k <= kShort) moe_route_kernel<T, LPT, EPL, sorts><<<grid_of(a, LPT), kThreads, 0, s>>>(a, wide, lanes);
+    else moe_route_kernel<T, LPT, EPL, false><<<grid_of(a, LPT), kThreads, 0, s>>>(a, wide, lanes);
 }
 template <typename T, int LPT, int EPL> void go(const MoeGradLaunch &a, int wide, hipStream_t s)
 {
