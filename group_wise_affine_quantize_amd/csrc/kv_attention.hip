@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kWorkers = 512;    // two workgroups of four waves per compute unit
 constexpr int kJoinThreads = 512, kJoinCols = 4;
+constexpr float kSlack = 1.5f;   // weights stay below 2^15.5, within fp16
 constexpr int kWaves = 4;
 
 // Units per worker.  At least two tiles for each wave, so that short contexts
@@ -79,23 +80,27 @@ __device__ __forceinline__ int stream_locate(const AttnArgs &A, int cols, At at,
     return -1;
 }
 
-// The state of CT column tiles in one wave's registers.
-template <int D, int CT, int NP> struct State {
-    half8_t q[CT][D / 32][NP];
-    float c[CT];                 // log2(e) * scale / row power of two
-    float m[CT], l[CT];          // m: the maximum less 14, so that weights are 2^(x - m)
-    float4_t o[CT][D / 16];
+// The state of a wave's 16 columns.
+template <int D, int NP> struct State {
+    half8_t q[D / 32][NP];
+    float c;                     // log2(e) * scale / row power of two
+    float m, l;                  // m: the reference, 14 below the maximum when set; weights are 2^(x - m)
+    float4_t o[D / 16];
 };
 
-template <int D, int CT, int FMT, typename T>
-__global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
+// CG groups of 16 columns; the waves of a group share its tiles.  A group's
+// waves load the tiles of the other groups' waves too, out of the L1: two
+// blocks of columns in one wave's registers would leave one wave per SIMD.
+template <int D, int CG, int FMT, typename T>
+__global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kernel(AttnArgs A)
 {
-    constexpr int NP = Parts<T>::n, COLS = 16 * CT, KS = D / 32, DT = D / 16;
+    constexpr int NP = Parts<T>::n, COLS = 16 * CG, KS = D / 32, DT = D / 16, TL = kWaves / CG;
     constexpr int LDO = D + 4;
-    __shared__ float sh_m[kWaves][COLS], sh_l[kWaves][COLS];
-    __shared__ float sh_o[2][COLS][LDO];
+    __shared__ float sh_m[TL][COLS], sh_l[TL][COLS];
+    __shared__ float sh_o[TL > 1 ? TL / 2 : 1][COLS][LDO];
     const KvAttnLaunch &a = A.a;
     const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
+    const int cg = wave % CG, turn = wave / CG;     // the wave's columns, its turn at their tiles
     const int r = lane & 15, g = lane >> 4, gk = r >> 2;
     const int sh = a.c.block_shift, bmask = (1 << sh) - 1;
 
@@ -119,12 +124,11 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
         const int tile0 = (int)(unit0 << A.unit_shift);
         const int tile1 = unit0 + units == s.units ? s.nt : (int)((unit0 + units) << A.unit_shift);
 
-        State<D, CT, NP> st;
-        int col_lo[CT], col_hi[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            const Column c = column(A, s, ctile * COLS + 16 * ct + r, head);
-            col_lo[ct] = c.lo, col_hi[ct] = c.hi;
+        State<D, NP> st;
+        int col_lo, col_hi;
+        {
+            const Column c = column(A, s, ctile * COLS + 16 * cg + r, head);
+            col_lo = c.lo, col_hi = c.hi;
             float f[KS][8], top = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
@@ -140,13 +144,13 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 for (int i = 0; i < 8; ++i) f[ks][i] *= up;
-                split_half<NP>(f[ks], st.q[ct][ks]);
+                split_half<NP>(f[ks], st.q[ks]);
             }
-            st.c[ct] = a.scale * kLog2e * back;
-            st.m[ct] = kNegInf;
-            st.l[ct] = 0.0f;
+            st.c = a.scale * kLog2e * back;
+            st.m = kNegInf;
+            st.l = 0.0f;
 #pragma unroll
-            for (int dt = 0; dt < DT; ++dt) st.o[ct][dt] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int dt = 0; dt < DT; ++dt) st.o[dt] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
         }
         // tokens that some column sees, and tokens that every column sees
         const int count = s.n * A.group, last_col = (ctile + 1) * COLS < count ? (ctile + 1) * COLS - 1 : count - 1;
@@ -185,28 +189,35 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
         // The loop keeps one tile's loads in flight: keys of the next tile go
         // out once this one's first product has read its registers, values
         // once the second has, block ids one tile before those.
-        int ti = tile0 + wave;
+        // Waves take tiles by turns; of blocks of 128 tokens, whose value rows
+        // are two tiles long, both tiles, so that a wave uses whole lines.
+        const int pair = sh == 7;
+        auto after_of = [&](int t) {
+            if (!pair) return t + TL;
+            return ((s.t0 + t) & 1) ? t + 2 * TL - 1 : t + 1;
+        };
+        int ti = tile0 + turn;
+        if (pair) ti = turn ? ((s.t0 + tile0) & ~1) + 2 * turn - s.t0 : tile0;
         int idk = -1, idv = -1, idk2 = -1, idv2 = -1;
         if (ti < tile1) {
             const int base = (s.t0 + ti) << 6;
             idk = block_of(base + 16 * gk), idv = block_of(base + 16 * g);
-            if (ti + kWaves < tile1) {
-                const int next = (s.t0 + ti + kWaves) << 6;
+            if (after_of(ti) < tile1) {
+                const int next = (s.t0 + after_of(ti)) << 6;
                 idk2 = block_of(next + 16 * gk), idv2 = block_of(next + 16 * g);
             }
             load_keys(base, idk);
             load_values(base, idv);
         }
-        for (; ti < tile1; ti += kWaves) {
+        for (; ti < tile1; ti = after_of(ti)) {
             const int base = (s.t0 + ti) << 6, pv = base + 16 * g;
-            const bool more = ti + kWaves < tile1, has = idv >= 0;
+            const int tn = after_of(ti);
+            const bool more = tn < tile1, has = idv >= 0;
             const bool masked = base < all_lo || base + kTile > all_hi || __any(!has);
 
-            float4_t S[CT][4];
+            float4_t S[4];
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int n = 0; n < 4; ++n) S[ct][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int n = 0; n < 4; ++n) S[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -214,50 +225,52 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
                     const half8_t k0 = codes_to_half<FMT>(kw[n][j].x, kw[n][j].y);
                     const half8_t k1 = codes_to_half<FMT>(kw[n][j].z, kw[n][j].w);
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
                         for (int p = 0; p < NP; ++p) {
-                            S[ct][n] = mfma(k0, st.q[ct][2 * j][p], S[ct][n]);
-                            S[ct][n] = mfma(k1, st.q[ct][2 * j + 1][p], S[ct][n]);
+                            S[n] = mfma(k0, st.q[2 * j][p], S[n]);
+                            S[n] = mfma(k1, st.q[2 * j + 1][p], S[n]);
                         }
                 }
-            const int next = (s.t0 + ti + kWaves) << 6;
+            const int next = (s.t0 + tn) << 6;
             idk = idk2;
             if (more) load_keys(next, idk2);
 
             const float vs = sv == 0.0f ? kZeroBlockScale : sv;
             const float lsv = fast_log2(vs), isv = 1.0f / vs;
-            half8_t P[CT][2][NP];
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const float f = st.c[ct] * sk;
+            half8_t P[2][NP];
+            {
+                const float f = st.c * sk;
                 float x[16], mx = kNegInf;
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[4 * n + i] = fmaf(S[ct][n][i], f, lsv);
+                    for (int i = 0; i < 4; ++i) x[4 * n + i] = fmaf(S[n][i], f, lsv);
                 if (masked) {
-                    const int lo = has ? col_lo[ct] - pv : 16, hi = col_hi[ct] - pv;
+                    const int lo = has ? col_lo - pv : 16, hi = col_hi - pv;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] = i < lo || i >= hi ? kNegInf : x[i];
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[i]);
-                const float mnew = fmaxf(st.m[ct], group_max(mx, lane) - kPScale);
-                const float mref = mnew == kNegInf ? 0.0f : mnew;   // no token yet: every weight is 0
-                const float alpha = fast_exp2(st.m[ct] - mref);
+                // the reference moves, and O with it, when a maximum passes it by kSlack
+                const float over = group_max(mx, lane) - kPScale;
+                if (__any(over > st.m + kSlack)) {
+                    const float next = over > st.m + kSlack ? over : st.m;
+                    const float alpha = next == kNegInf ? 0.0f : fast_exp2(st.m - next);
+                    st.m = next;
+                    st.l *= alpha;
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt) st.o[dt] *= alpha;
+                }
+                const float mref = st.m == kNegInf ? 0.0f : st.m;   // no token yet: every weight is 0
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     x[i] = fast_exp2(x[i] - mref);
                     sum += x[i];
                 }
-                st.m[ct] = mnew;
-                st.l[ct] = fmaf(st.l[ct], alpha, sum * isv);
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) st.o[ct][dt] *= alpha;
-                split_half<NP>(x, P[ct][0]);
-                split_half<NP>(x + 8, P[ct][1]);
+                st.l = fmaf(sum, isv, st.l);
+                split_half<NP>(x, P[0]);
+                split_half<NP>(x + 8, P[1]);
             }
             if constexpr (FMT == KV_FP8) {
                 if (masked) {
@@ -282,81 +295,69 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
                 const half8_t v0 = codes_to_half<FMT>(vw[dt].x, vw[dt].y);
                 const half8_t v1 = codes_to_half<FMT>(vw[dt].z, vw[dt].w);
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
                     for (int p = 0; p < NP; ++p) {
-                        st.o[ct][dt] = mfma(v0, P[ct][0][p], st.o[ct][dt]);
-                        st.o[ct][dt] = mfma(v1, P[ct][1][p], st.o[ct][dt]);
+                        st.o[dt] = mfma(v0, P[0][p], st.o[dt]);
+                        st.o[dt] = mfma(v1, P[1][p], st.o[dt]);
                     }
             }
             idv = idv2;
             if (more) {
                 load_values(next, idv2);
-                if (ti + 2 * kWaves < tile1) {
-                    const int after = (s.t0 + ti + 2 * kWaves) << 6;
+                if (after_of(tn) < tile1) {
+                    const int after = (s.t0 + after_of(tn)) << 6;
                     idk2 = block_of(after + 16 * gk), idv2 = block_of(after + 16 * g);
                 }
             }
         }
 
-        // join the four waves: maxima first, then two rounds of pairwise sums
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            st.l[ct] = group_sum(st.l[ct], lane);
-            if (g == 0) sh_m[wave][16 * ct + r] = st.m[ct];
-        }
+        // join the waves of a column group: references first, then sums by halves
+        st.l = group_sum(st.l, lane);
+        const int col = 16 * cg + r;
+        if (g == 0) sh_m[turn][col] = st.m;
         __syncthreads();
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            const int col = 16 * ct + r;
+        {
             float m = sh_m[0][col];
-            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh_m[w][col]);
-            const float f = m == kNegInf ? 0.0f : fast_exp2(st.m[ct] - m);
-            st.m[ct] = m;
-            st.l[ct] *= f;
+            for (int w = 1; w < TL; ++w) m = fmaxf(m, sh_m[w][col]);
+            const float f = m == kNegInf ? 0.0f : fast_exp2(st.m - m);
+            st.m = m;
+            st.l *= f;
 #pragma unroll
-            for (int dt = 0; dt < DT; ++dt) st.o[ct][dt] *= f;
-            if (g == 0) sh_l[wave][col] = st.l[ct];
+            for (int dt = 0; dt < DT; ++dt) st.o[dt] *= f;
+            if (g == 0) sh_l[turn][col] = st.l;
         }
-        for (int step = 2; step >= 1; step >>= 1) {
-            if (wave >= step && wave < 2 * step)
-                for (int ct = 0; ct < CT; ++ct)
-                    for (int dt = 0; dt < DT; ++dt)
-                        *reinterpret_cast<float4_t *>(&sh_o[wave - step][16 * ct + r][16 * dt + 4 * g]) = st.o[ct][dt];
+        if (TL == 1) __syncthreads();
+        for (int step = TL / 2; step >= 1; step >>= 1) {
+            if (turn >= step && turn < 2 * step)
+                for (int dt = 0; dt < DT; ++dt)
+                    *reinterpret_cast<float4_t *>(&sh_o[turn - step][col][16 * dt + 4 * g]) = st.o[dt];
             __syncthreads();
-            if (wave < step)
-                for (int ct = 0; ct < CT; ++ct)
-                    for (int dt = 0; dt < DT; ++dt)
-                        st.o[ct][dt] += *reinterpret_cast<float4_t *>(&sh_o[wave][16 * ct + r][16 * dt + 4 * g]);
+            if (turn < step)
+                for (int dt = 0; dt < DT; ++dt)
+                    st.o[dt] += *reinterpret_cast<float4_t *>(&sh_o[turn][col][16 * dt + 4 * g]);
             __syncthreads();
         }
-        if (wave == 0) {
+        const Column c = column(A, s, ctile * COLS + col, head);
+        if (turn == 0 && c.row >= 0) {
             const int64_t slot = 2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0);
+            float l = sh_l[0][col];
+            for (int w = 1; w < TL; ++w) l += sh_l[w][col];
+            if (whole) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                T *out = static_cast<T *>(a.out) + ((int64_t)c.row * a.q_heads + c.head) * D;
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const int col = 16 * ct + r;
-                const float l = sh_l[0][col] + sh_l[1][col] + sh_l[2][col] + sh_l[3][col];
-                const Column c = column(A, s, ctile * COLS + col, head);
-                if (c.row < 0) continue;
-                if (whole) {
-                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                    T *out = static_cast<T *>(a.out) + ((int64_t)c.row * a.q_heads + c.head) * D;
-#pragma unroll
-                    for (int dt = 0; dt < DT; ++dt) {
-                        float v[4];
-                        for (int i = 0; i < 4; ++i) v[i] = st.o[ct][dt][i] * inv;
-                        store_f32x4<T>(out + 16 * dt + 4 * g, v);
-                    }
-                    if (a.lse && g == 0)
-                        a.lse[(int64_t)c.row * a.q_heads + c.head] = l > 0.0f ? (st.m[ct] + fast_log2(l)) * kLn2 : kNegInf;
-                } else {
-                    float *po = A.part_o + (slot * COLS + col) * D;
-                    float *pm = A.part_ml + (slot * COLS + col) * 2;
-#pragma unroll
-                    for (int dt = 0; dt < DT; ++dt)
-                        *reinterpret_cast<float4_t *>(po + 16 * dt + 4 * g) = st.o[ct][dt];
-                    if (g == 0) pm[0] = st.m[ct], pm[1] = l;
+                for (int dt = 0; dt < DT; ++dt) {
+                    float v[4];
+                    for (int i = 0; i < 4; ++i) v[i] = st.o[dt][i] * inv;
+                    store_f32x4<T>(out + 16 * dt + 4 * g, v);
                 }
+                if (a.lse && g == 0)
+                    a.lse[(int64_t)c.row * a.q_heads + c.head] = l > 0.0f ? (st.m + fast_log2(l)) * kLn2 : kNegInf;
+            } else {
+                float *po = A.part_o + (slot * COLS + col) * D;
+                float *pm = A.part_ml + (slot * COLS + col) * 2;
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) *reinterpret_cast<float4_t *>(po + 16 * dt + 4 * g) = st.o[dt];
+                if (g == 0) pm[0] = st.m, pm[1] = l;
             }
         }
         __syncthreads();
@@ -368,10 +369,10 @@ __global__ __launch_bounds__(64 * kWaves) void kv_stream_kernel(AttnArgs A)
 // Joins the parts of the segments that several workgroups shared, in the
 // order of the tokens.  Workgroup j looks at the border between workers j and
 // j + 1; the one at the first border inside a segment joins it.
-template <int D, int CT, typename T>
+template <int D, int CG, typename T>
 __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 {
-    constexpr int COLS = 16 * CT, QUADS = D / 4, LANES = kJoinCols * QUADS, RUNS = kJoinThreads / LANES;
+    constexpr int COLS = 16 * CG, QUADS = D / 4, LANES = kJoinCols * QUADS, RUNS = kJoinThreads / LANES;
     __shared__ float sh_f[kWorkers][kJoinCols];
     __shared__ float sh_m[kJoinCols], sh_l[kJoinCols];
     __shared__ float4 sh_o[RUNS][LANES];
@@ -458,7 +459,7 @@ constexpr int kFew = 64;
 
 struct Route {
     bool stream, tile;
-    int ct;             // 16-column blocks per wave of the streaming kernel
+    int ct;             // 16-column groups of the streaming kernel
     int few;
     unsigned tile_bound;
     int tile_splits;
@@ -474,7 +475,7 @@ Route route_of(const KvAttnLaunch &a)
     else if (cols <= kFew || a.s.rows <= 2 * (int64_t)a.s.batch) r.stream = true, r.tile = false, r.few = INT32_MAX;
     else r.stream = r.tile = true, r.few = kFew;
     const int64_t per = std::max<int64_t>(1, (a.s.rows + a.s.batch - 1) / a.s.batch) * group;
-    r.ct = per <= 16 || D > 128 ? 1 : 2;
+    r.ct = per <= 16 ? 1 : per <= 32 ? 2 : 4;
     r.stream_cols = r.stream ? (size_t)2 * kWorkers * 16 * r.ct : 0;
     r.stream_floats = r.stream_cols * D;
     r.tile_bound = 0, r.tile_splits = 1, r.tile_cols = 0, r.tile_floats = 0;
@@ -495,21 +496,26 @@ Route route_of(const KvAttnLaunch &a)
     return r;
 }
 
-template <int D, int CT, int FMT, typename T> hipError_t stream_go(const AttnArgs &A, hipStream_t stream)
+template <int D, int CG, int FMT, typename T> hipError_t stream_go(const AttnArgs &A, hipStream_t stream)
 {
-    kv_stream_kernel<D, CT, FMT, T><<<A.workers, 64 * kWaves, 0, stream>>>(A);
+    kv_stream_kernel<D, CG, FMT, T><<<A.workers, 64 * kWaves, 0, stream>>>(A);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (!A.splits) return e;
-    kv_join_kernel<D, CT, T><<<dim3(A.workers - 1, 16 * CT / kJoinCols), kJoinThreads, 0, stream>>>(A);
+    kv_join_kernel<D, CG, T><<<dim3(A.workers - 1, 16 * CG / kJoinCols), kJoinThreads, 0, stream>>>(A);
     return hipGetLastError();
 }
 
-template <int D, int CT> hipError_t stream_types(const AttnArgs &A, hipStream_t stream)
+template <int D, int CG> hipError_t stream_types(const AttnArgs &A, hipStream_t stream)
 {
     if (A.a.format == KV_INT8)
-        return A.a.x_dt == 0 ? stream_go<D, CT, KV_INT8, float>(A, stream) : stream_go<D, CT, KV_INT8, bf16_bits>(A, stream);
-    return A.a.x_dt == 0 ? stream_go<D, CT, KV_FP8, float>(A, stream) : stream_go<D, CT, KV_FP8, bf16_bits>(A, stream);
+        return A.a.x_dt == 0 ? stream_go<D, CG, KV_INT8, float>(A, stream) : stream_go<D, CG, KV_INT8, bf16_bits>(A, stream);
+    return A.a.x_dt == 0 ? stream_go<D, CG, KV_FP8, float>(A, stream) : stream_go<D, CG, KV_FP8, bf16_bits>(A, stream);
+}
+
+template <int D> hipError_t stream_groups(const AttnArgs &A, int groups, hipStream_t stream)
+{
+    return groups == 1 ? stream_types<D, 1>(A, stream) : groups == 2 ? stream_types<D, 2>(A, stream) : stream_types<D, 4>(A, stream);
 }
 
 }  // namespace
@@ -545,12 +551,11 @@ hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream)
     if (tiles <= 16) A.unit_shift = 4;
     A.splits = tiles > (int64_t)1 << A.unit_shift;
     A.part_ml = A.part_o + r.stream_floats;
-    const bool one = r.ct == 1;
     switch (a.c.head_dim) {
-    case 64: return one ? stream_types<64, 1>(A, stream) : stream_types<64, 2>(A, stream);
-    case 128: return one ? stream_types<128, 1>(A, stream) : stream_types<128, 2>(A, stream);
-    case 192: return stream_types<192, 1>(A, stream);
-    default: return stream_types<256, 1>(A, stream);
+    case 64: return stream_groups<64>(A, r.ct, stream);
+    case 128: return stream_groups<128>(A, r.ct, stream);
+    case 192: return stream_groups<192>(A, r.ct, stream);
+    default: return stream_groups<256>(A, r.ct, stream);
     }
 }
 

@@ -73,8 +73,8 @@ __device__ __forceinline__ float4_t mfma(half8_t a, half8_t b, float4_t c)
 
 struct AttnArgs {
     KvAttnLaunch a;
-    float *part_o;      // [workers * 2][16 * CT][D]
-    float *part_ml;     // [workers * 2][16 * CT][2]
+    float *part_o;      // [workers * 2][columns][D]
+    float *part_ml;     // [workers * 2][columns][2]
     int workers;        // workgroups of the streaming kernel
     int group;          // query heads per key/value head
     int unit_shift;     // log2 of the tiles of a unit of work
