@@ -369,6 +369,11 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
 // Joins the parts of the segments that several workgroups shared, in the
 // order of the tokens.  Workgroup j looks at the border between workers j and
 // j + 1; the one at the first border inside a segment joins it.
+// Workgroups per border: one for every kJoinCols columns, but with four column
+// groups, whose parts are few, one for every 16 (most borders have nothing to
+// join, and each workgroup has to find that out).
+constexpr int join_blocks(int groups) { return groups == 4 ? 4 : 16 * groups / kJoinCols; }
+
 template <int D, int CG, typename T>
 __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 {
@@ -384,11 +389,13 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
     const StreamSeq s = stream_seq(A, b, COLS);
     const uint32_t seg = inside / s.units, unit = inside - seg * s.units;
     if (unit == 0 || unit > share) return;     // between segments, or not the first border inside
-    const int head = (int)(seg / s.ct), col0 = (int)blockIdx.y * kJoinCols;
-    const int idx0 = (int)(seg - (uint32_t)head * s.ct) * COLS + col0;
-    if (idx0 >= s.n * A.group) return;
+    const int head = (int)(seg / s.ct);
     // worker blockIdx.x has the first part, in its second slot; the others in their first
     const int w0 = (int)blockIdx.x, parts = (int)(((blockIdx.x + 1) * share - unit + s.units - 1) / share) - w0 + 1;
+    for (int turn = 0; turn < COLS / (kJoinCols * join_blocks(CG)); ++turn) {
+    const int col0 = ((int)blockIdx.y + turn * join_blocks(CG)) * kJoinCols;
+    const int idx0 = (int)(seg - (uint32_t)head * s.ct) * COLS + col0;
+    if (idx0 >= s.n * A.group) return;
     auto slot = [&](int p) -> int64_t { return (2 * (int64_t)(w0 + p) + (p == 0 ? 1 : 0)) * COLS + col0; };
 
     // each part's factor: 2^(M_part - M)
@@ -444,6 +451,8 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
         store_f32x4<T>(static_cast<T *>(a.out) + ((int64_t)q.row * a.q_heads + q.head) * D + d, v);
         if (a.lse && d == 0)
             a.lse[(int64_t)q.row * a.q_heads + q.head] = l > 0.0f ? (sh_m[c] + fast_log2(l)) * kLn2 : kNegInf;
+    }
+    __syncthreads();
     }
 }
 
@@ -502,7 +511,7 @@ template <int D, int CG, int FMT, typename T> hipError_t stream_go(const AttnArg
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (!A.splits) return e;
-    kv_join_kernel<D, CG, T><<<dim3(A.workers - 1, 16 * CG / kJoinCols), kJoinThreads, 0, stream>>>(A);
+    kv_join_kernel<D, CG, T><<<dim3(A.workers - 1, join_blocks(CG)), kJoinThreads, 0, stream>>>(A);
     return hipGetLastError();
 }
 

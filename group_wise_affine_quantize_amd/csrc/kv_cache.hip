@@ -14,6 +14,8 @@
 // One workgroup takes one block of one head, keys or values (the two have
 // their own scales), so the scale is a workgroup's reduction and no two
 // workgroups share a byte.
+#include <type_traits>
+
 #include "nq_kv_device.h"
 
 namespace nqk {
@@ -52,17 +54,6 @@ template <int FMT> __device__ __forceinline__ float grown_scale(float s, float a
     return s * __uint_as_float((uint32_t)(127 + j) << 23);
 }
 
-// Two neighbouring elements as fp32.
-template <typename T> __device__ __forceinline__ float2 load2(const T *p);
-template <> __device__ __forceinline__ float2 load2<float>(const float *p)
-{
-    return *reinterpret_cast<const float2 *>(p);
-}
-template <> __device__ __forceinline__ float2 load2<bf16_bits>(const bf16_bits *p)
-{
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
 // Four neighbouring elements as fp32.
 template <typename T> __device__ __forceinline__ float4 load4(const T *p);
 template <> __device__ __forceinline__ float4 load4<float>(const float *p)
@@ -75,6 +66,13 @@ template <> __device__ __forceinline__ float4 load4<bf16_bits>(const bf16_bits *
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                        __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
 }
+// The hardware's bf16 conversion: nearest, ties to even, NaN stays one.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    const bf2 v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
 template <typename T> __device__ __forceinline__ void store4(T *p, const float *v);
 template <> __device__ __forceinline__ void store4<float>(float *p, const float *v)
 {
@@ -82,19 +80,18 @@ template <> __device__ __forceinline__ void store4<float>(float *p, const float 
 }
 template <> __device__ __forceinline__ void store4<bf16_bits>(bf16_bits *p, const float *v)
 {
-    uint2 w;
-    w.x = f32_to_bf16(v[0]) | f32_to_bf16(v[1]) << 16;
-    w.y = f32_to_bf16(v[2]) | f32_to_bf16(v[3]) << 16;
-    *reinterpret_cast<uint2 *>(p) = w;
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
-template <typename T> __device__ __forceinline__ void store2(T *p, float a, float b);
-template <> __device__ __forceinline__ void store2<float>(float *p, float a, float b)
+template <typename T> __device__ __forceinline__ void store8(T *p, const float *v);
+template <> __device__ __forceinline__ void store8<float>(float *p, const float *v)
 {
-    *reinterpret_cast<float2 *>(p) = make_float2(a, b);
+    store4<float>(p, v);
+    store4<float>(p + 4, v + 4);
 }
-template <> __device__ __forceinline__ void store2<bf16_bits>(bf16_bits *p, float a, float b)
+template <> __device__ __forceinline__ void store8<bf16_bits>(bf16_bits *p, const float *v)
 {
-    *reinterpret_cast<uint32_t *>(p) = f32_to_bf16(a) | f32_to_bf16(b) << 16;
+    *reinterpret_cast<uint4 *>(p) =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
 // One block of one head that a call's rows touch.
@@ -124,26 +121,35 @@ __device__ __forceinline__ bool find_item(const KvSeqs &s, const KvCache &c, int
     return true;
 }
 
-template <int FMT, typename T>
+// Keys: a thread takes 8 columns of a slot.  Values: kCols columns of kSlots
+// neighbouring slots, which it transposes in registers, so that rows are read
+// along their columns and codes written along the slots.
+constexpr int kCols = 4, kSlots = 8;
+
+// The rows are read twice, for the scale and for the codes; the second time
+// they come from the cache.
+template <int D, int FMT, typename T>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendLaunch a)
 {
     __shared__ float red[4];
     Item it;
     if (!find_item(a.s, a.c, blockIdx.x, &it) || it.id < 0) return;
-    const int D = a.c.head_dim, sh = a.c.block_shift, B = 1 << sh, tid = (int)threadIdx.x;
+    const int sh = a.c.block_shift, tid = (int)threadIdx.x;
     const int64_t head = blockIdx.y, slab = it.id * a.c.kv_heads + head;
     const bool is_v = blockIdx.z != 0;
     const int64_t ld = is_v ? a.ldv : a.ldk;
     const T *x = static_cast<const T *>(is_v ? a.v : a.k) + it.row * ld + head * D;
     uint8_t *codes = (is_v ? a.c.v_codes : a.c.k_codes) + slab * ((int64_t)D << sh);
     float *scale = (is_v ? a.c.v_scales : a.c.k_scales) + slab;
-    const int count = it.hi - it.lo, quads = D >> 2;
+    const int count = it.hi - it.lo;
 
     float m = 0.0f;
-    for (int i = tid; i < count * quads; i += kThreads) {
-        const int t = i / quads, d = (i - t * quads) * 4;
-        const float4 v = load4<T>(x + (int64_t)(it.lo + t) * ld + d);
+    for (int i = tid; i < count * (D / 8); i += kThreads) {
+        const int t = i / (D / 8), d = (i % (D / 8)) * 8;
+        const T *p = x + (int64_t)(it.lo + t) * ld + d;
+        const float4 v = load4<T>(p), w = load4<T>(p + 4);
         m = fmaxf(m, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(w.x), fabsf(w.y)), fmaxf(fabsf(w.z), fabsf(w.w))));
     }
     const float held = it.lo > 0 ? *scale : 0.0f;   // read before thread 0 stores it below
     m = block_max(m, red);
@@ -155,94 +161,94 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendLaunch a)
 
     if (!is_v) {
         if (shrink != 1.0f)
-            for (int i = tid; i < it.lo * quads; i += kThreads) {
+            for (int i = tid; i < it.lo * (D / 4); i += kThreads) {
                 uint32_t *w = reinterpret_cast<uint32_t *>(codes) + i;
                 float v[4];
                 kv_values4<FMT>(*w, v);
                 for (int e = 0; e < 4; ++e) v[e] *= shrink;
                 *w = kv_codes4<FMT>(v);
             }
-        for (int i = tid; i < count * quads; i += kThreads) {
-            const int t = it.lo + i / quads, d = (i % quads) * 4;
-            const float4 f = load4<T>(x + (int64_t)t * ld + d);
-            const float v[4] = {f.x * inv, f.y * inv, f.z * inv, f.w * inv};
-            *reinterpret_cast<uint32_t *>(codes + (int64_t)t * D + d) = kv_codes4<FMT>(v);
+        for (int i = tid; i < count * (D / 8); i += kThreads) {
+            const int t = it.lo + i / (D / 8), d = (i % (D / 8)) * 8;
+            const T *p = x + (int64_t)t * ld + d;
+            const float4 f = load4<T>(p), h = load4<T>(p + 4);
+            const float v[8] = {f.x * inv, f.y * inv, f.z * inv, f.w * inv, h.x * inv, h.y * inv, h.z * inv, h.w * inv};
+            *reinterpret_cast<uint2 *>(codes + (int64_t)t * D + d) = make_uint2(kv_codes4<FMT>(v), kv_codes4<FMT>(v + 4));
         }
-    } else {
-        if (shrink != 1.0f)
-            for (int i = tid; i < D * it.lo; i += kThreads) {
-                uint8_t *p = codes + ((int64_t)(i / it.lo) << sh) + i % it.lo;
-                *p = kv_code<FMT>(kv_value<FMT>(*p) * shrink);
-            }
-        // a thread transposes 2 columns of 16 slots: loads run along the
-        // columns, stores along the slots
-        const int pairs = D >> 1;
-        for (int i = tid; i < pairs * (B >> 4); i += kThreads) {
-            const int d = (i % pairs) * 2, t0 = (i / pairs) * 16;
-            if (t0 + 16 <= it.lo || t0 >= it.hi) continue;
-            float f[2][16];
+        return;
+    }
+    if (shrink != 1.0f)
+        for (int i = tid; i < D * it.lo; i += kThreads) {
+            uint8_t *p = codes + ((int64_t)(i / it.lo) << sh) + i % it.lo;
+            *p = kv_code<FMT>(kv_value<FMT>(*p) * shrink);
+        }
+    const int first = it.lo & ~(kSlots - 1), runs = (it.hi - first + kSlots - 1) / kSlots;
+    for (int i = tid; i < (D / kCols) * runs; i += kThreads) {
+        const int d = (i % (D / kCols)) * kCols, t0 = first + (i / (D / kCols)) * kSlots;
+        float f[kCols][kSlots];
 #pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                float2 g = make_float2(0.0f, 0.0f);
-                if (t0 + t >= it.lo && t0 + t < it.hi) g = load2<T>(x + (int64_t)(t0 + t) * ld + d);
-                f[0][t] = g.x * inv, f[1][t] = g.y * inv;
-            }
+        for (int t = 0; t < kSlots; ++t) {
+            float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (t0 + t >= it.lo && t0 + t < it.hi) g = load4<T>(x + (int64_t)(t0 + t) * ld + d);
+            f[0][t] = g.x * inv, f[1][t] = g.y * inv, f[2][t] = g.z * inv, f[3][t] = g.w * inv;
+        }
+        const bool full = t0 >= it.lo && t0 + kSlots <= it.hi;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uint32_t w[4];
+        for (int e = 0; e < kCols; ++e) {
+            const uint32_t w[2] = {kv_codes4<FMT>(f[e]), kv_codes4<FMT>(f[e] + 4)};
+            uint8_t *p = codes + ((int64_t)(d + e) << sh) + t0;
+            if (full) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+            else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) w[q] = kv_codes4<FMT>(f[e] + 4 * q);
-                uint8_t *p = codes + ((int64_t)(d + e) << sh) + t0;
-                if (t0 >= it.lo && t0 + 16 <= it.hi) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-                else {
-#pragma unroll
-                    for (int t = 0; t < 16; ++t)
-                        if (t0 + t >= it.lo && t0 + t < it.hi) p[t] = (uint8_t)(w[t >> 2] >> (8 * (t & 3)));
-                }
+                for (int t = 0; t < kSlots; ++t)
+                    if (t0 + t >= it.lo && t0 + t < it.hi) p[t] = (uint8_t)(w[t >> 2] >> (8 * (t & 3)));
             }
         }
     }
 }
 
-template <int FMT, typename T>
+template <int D, int FMT, typename T>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadLaunch a)
 {
     Item it;
     if (!find_item(a.s, a.c, blockIdx.x, &it)) return;
-    const int D = a.c.head_dim, sh = a.c.block_shift, B = 1 << sh, tid = (int)threadIdx.x;
+    const int sh = a.c.block_shift, tid = (int)threadIdx.x;
     const int64_t head = blockIdx.y, ld = (int64_t)a.c.kv_heads * D;
     const bool is_v = blockIdx.z != 0, absent = it.id < 0;
     const int64_t slab = (absent ? 0 : it.id) * a.c.kv_heads + head;
     T *y = static_cast<T *>(is_v ? a.v : a.k) + it.row * ld + head * D;
     const uint8_t *codes = (is_v ? a.c.v_codes : a.c.k_codes) + slab * ((int64_t)D << sh);
     const float s = absent ? 0.0f : (is_v ? a.c.v_scales : a.c.k_scales)[slab];
-    const int count = it.hi - it.lo, quads = D >> 2;
+    const int count = it.hi - it.lo;
     if (!is_v || absent) {
-        for (int i = tid; i < count * quads; i += kThreads) {
-            const int t = it.lo + i / quads, d = (i % quads) * 4;
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (!absent) kv_values4<FMT>(*reinterpret_cast<const uint32_t *>(codes + (int64_t)t * D + d), v);
-            for (int e = 0; e < 4; ++e) v[e] *= s;
-            store4<T>(y + (int64_t)t * ld + d, v);
-        }
-    } else {
-        const int pairs = D >> 1;
-        for (int i = tid; i < pairs * (B >> 4); i += kThreads) {
-            const int d = (i % pairs) * 2, t0 = (i / pairs) * 16;
-            if (t0 + 16 <= it.lo || t0 >= it.hi) continue;
-            float f[2][16];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(codes + ((int64_t)(d + e) << sh) + t0);
-                kv_values4<FMT>(w.x, f[e]);
-                kv_values4<FMT>(w.y, f[e] + 4);
-                kv_values4<FMT>(w.z, f[e] + 8);
-                kv_values4<FMT>(w.w, f[e] + 12);
+#pragma unroll 4
+        for (int i = tid; i < count * (D / 8); i += kThreads) {
+            const int t = it.lo + i / (D / 8), d = (i % (D / 8)) * 8;
+            float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+            if (!absent) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(codes + (int64_t)t * D + d);
+                kv_values4<FMT>(w.x, v);
+                kv_values4<FMT>(w.y, v + 4);
             }
+            for (int e = 0; e < 8; ++e) v[e] *= s;
+            store8<T>(y + (int64_t)t * ld + d, v);
+        }
+        return;
+    }
+    const int first = it.lo & ~(kSlots - 1), runs = (it.hi - first + kSlots - 1) / kSlots;
+    for (int i = tid; i < (D / kCols) * runs; i += kThreads) {
+        const int d = (i % (D / kCols)) * kCols, t0 = first + (i / (D / kCols)) * kSlots;
+        float f[kCols][kSlots];
 #pragma unroll
-            for (int t = 0; t < 16; ++t)
-                if (t0 + t >= it.lo && t0 + t < it.hi)
-                    store2<T>(y + (int64_t)(t0 + t) * ld + d, f[0][t] * s, f[1][t] * s);
+        for (int e = 0; e < kCols; ++e) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(codes + ((int64_t)(d + e) << sh) + t0);
+            kv_values4<FMT>(w.x, f[e]);
+            kv_values4<FMT>(w.y, f[e] + 4);
+        }
+#pragma unroll
+        for (int t = 0; t < kSlots; ++t) {
+            const float v[4] = {f[0][t] * s, f[1][t] * s, f[2][t] * s, f[3][t] * s};
+            if (t0 + t >= it.lo && t0 + t < it.hi) store4<T>(y + (int64_t)(t0 + t) * ld + d, v);
         }
     }
 }
@@ -255,31 +261,47 @@ int64_t max_items(const KvSeqs &s, const KvCache &c)
     return s.rows < some ? s.rows : some;
 }
 
+template <typename Go> void by_head_dim(int head_dim, Go go)
+{
+    switch (head_dim) {
+    case 64: go(std::integral_constant<int, 64>()); break;
+    case 128: go(std::integral_constant<int, 128>()); break;
+    case 192: go(std::integral_constant<int, 192>()); break;
+    default: go(std::integral_constant<int, 256>()); break;
+    }
+}
+
 }  // namespace
 
 hipError_t launch_kv_append(const KvAppendLaunch &a, hipStream_t stream)
 {
     const dim3 grid((unsigned)max_items(a.s, a.c), (unsigned)a.c.kv_heads, 2);
-    if (a.format == KV_INT8) {
-        if (a.x_dt == 0) kv_append_kernel<KV_INT8, float><<<grid, kThreads, 0, stream>>>(a);
-        else kv_append_kernel<KV_INT8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
-    } else {
-        if (a.x_dt == 0) kv_append_kernel<KV_FP8, float><<<grid, kThreads, 0, stream>>>(a);
-        else kv_append_kernel<KV_FP8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
-    }
+    by_head_dim(a.c.head_dim, [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        if (a.format == KV_INT8) {
+            if (a.x_dt == 0) kv_append_kernel<D, KV_INT8, float><<<grid, kThreads, 0, stream>>>(a);
+            else kv_append_kernel<D, KV_INT8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
+        } else {
+            if (a.x_dt == 0) kv_append_kernel<D, KV_FP8, float><<<grid, kThreads, 0, stream>>>(a);
+            else kv_append_kernel<D, KV_FP8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
+        }
+    });
     return hipGetLastError();
 }
 
 hipError_t launch_kv_read(const KvReadLaunch &a, hipStream_t stream)
 {
     const dim3 grid((unsigned)max_items(a.s, a.c), (unsigned)a.c.kv_heads, 2);
-    if (a.format == KV_INT8) {
-        if (a.out_dt == 0) kv_read_kernel<KV_INT8, float><<<grid, kThreads, 0, stream>>>(a);
-        else kv_read_kernel<KV_INT8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
-    } else {
-        if (a.out_dt == 0) kv_read_kernel<KV_FP8, float><<<grid, kThreads, 0, stream>>>(a);
-        else kv_read_kernel<KV_FP8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
-    }
+    by_head_dim(a.c.head_dim, [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        if (a.format == KV_INT8) {
+            if (a.out_dt == 0) kv_read_kernel<D, KV_INT8, float><<<grid, kThreads, 0, stream>>>(a);
+            else kv_read_kernel<D, KV_INT8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
+        } else {
+            if (a.out_dt == 0) kv_read_kernel<D, KV_FP8, float><<<grid, kThreads, 0, stream>>>(a);
+            else kv_read_kernel<D, KV_FP8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
+        }
+    });
     return hipGetLastError();
 }
 

@@ -421,9 +421,12 @@ template <int D, typename T> __global__ __launch_bounds__(256) void kv_tile_join
         return ((int64_t)(blockIdx.x / heads * (uint32_t)A.tile_splits + p) * heads + head) * M + col;
     };
     float m = kNegInf;
+#pragma unroll 8
     for (int p = 0; p < A.tile_splits; ++p) m = fmaxf(m, A.part_ml[2 * at(p)]);
     float l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int p = 0; p < A.tile_splits && m != kNegInf; ++p) {
+    const int parts = m == kNegInf ? 0 : A.tile_splits;
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) {
         const float f = fast_exp2(A.part_ml[2 * at(p)] - m);
         const float4 o = *reinterpret_cast<const float4 *>(A.part_o + at(p) * D + d);
         l = fmaf(f, A.part_ml[2 * at(p) + 1], l);
