@@ -465,6 +465,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 // rows or there are at most two rows per sequence (then all of them are
 // streamed).
 constexpr int kFew = 64;
+constexpr int kPartTiles = 5;
 
 struct Route {
     bool stream, tile;
@@ -493,10 +494,12 @@ Route route_of(const KvAttnLaunch &a)
         const int64_t bound = std::min<int64_t>(cols / M + a.s.batch, cols);
         r.tile_bound = (unsigned)bound;
         // too few workgroups for 256 compute units: tokens are split, at least
-        // eight tiles to a part
-        const int64_t segments = bound * a.c.kv_heads, tiles = ((a.s.max_blocks << a.c.block_shift) >> 6) + 1;
+        // kPartTiles tiles that a column tile can see to a part
+        const int64_t segments = bound * a.c.kv_heads;
+        int64_t tiles = ((a.s.max_blocks << a.c.block_shift) >> 6) + 1;
+        if (a.window > 0) tiles = std::min<int64_t>(tiles, ((a.window + M / group) >> 6) + 2);
         if (segments < 192)
-            r.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>(512 / segments, tiles / 8));
+            r.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>(512 / segments, tiles / kPartTiles));
         if (r.tile_splits > 1) {
             r.tile_cols = (size_t)(segments * r.tile_splits * M);
             r.tile_floats = r.tile_cols * D;
