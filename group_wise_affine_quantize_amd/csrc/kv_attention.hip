@@ -6,17 +6,19 @@
 // one pass over the tokens, in base 2 and with the value scale drawn into
 // the exponent:
 //   x_t = log2(e) * scale * sk_t * (q . ck_t) + log2(sv_t),
-//   p_t = 2^(x_t - M + 14),  M the running maximum of x_t,
+//   p_t = 2^(x_t - R),
 //   O = sum_t p_t cv_t,      L = sum_t p_t / sv_t,      out = O / L.
-// Drawing sv into x makes p_t the whole weight of a code row, so that the
-// second product runs on bare codes, and 2^14 is the most that any p_t is, so
-// that p_t fits fp16: with 11 bits for weights within 2^-28 of the largest,
-// and a floor 2^-38 of it.  (bf16 would keep 8 bits, which shows in a bf16
+// R, a column's reference, is set 14 below the maximum of x_t and moves (O and
+// L are scaled) when a later maximum passes R + 14 by more than kSlack; the
+// largest p_t lies in [2^14, 2^15.5).  Drawing sv into x makes p_t the whole
+// weight of a code row, so that the second product runs on bare codes, and
+// p_t fits fp16: 11 bits for weights within 2^-28 of the largest, a floor
+// about 2^-39 below it.  (bf16 would keep 8 bits, which shows in a bf16
 // result.)  Codes are exact in fp16.  A query row is taken times a power of
 // two that brings its largest element to [2^14, 2^15); a bf16 element then is
 // exact in fp16 down to 2^-28 of the largest.  fp32 rows and weights are the
 // sum of two fp16 numbers (22 bits) and take two matrix products each.  Sums,
-// maxima and the states M, L, O are fp32.
+// references and the states O and L are fp32.
 //
 // Matrix products: S^T = K q^T and O^T = V^T P^T on 16x16x32 fp16 MFMA with
 // the tokens in the rows of the first product.  Lane l (r = l % 16, g = l / 16)
@@ -25,6 +27,13 @@
 // rows are fed is free, and this one leaves each lane 16 neighbouring tokens,
 // which are exactly the operand of the second product (16 bytes of a V^T row
 // per lane).  No value moves between lanes but the running maximum.
+//
+// What bounds it: reading the codes.  64 sequences of 1k to 8k tokens, 8 heads of
+// 128 in int8: 620 MB in 123 us, 5.0 TB/s (a 1 GiB copy moves 5.1), with two
+// workgroups of four waves per compute unit, each wave with a tile of 16 KB on
+// the way.  With more than 16 query columns two or four waves read the same tile, and
+// less is on the way: 8 draft tokens over 131k tokens, 264 MB in 82 us.  One token at
+// 333 is latency: 9.3 us.
 #include <algorithm>
 
 #include "nq_kv_attn.h"
@@ -366,14 +375,16 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
     }
 }
 
-// Joins the parts of the segments that several workgroups shared, in the
-// order of the tokens.  Workgroup j looks at the border between workers j and
-// j + 1; the one at the first border inside a segment joins it.
 // Workgroups per border: one for every kJoinCols columns, but with four column
 // groups, whose parts are few, one for every 16 (most borders have nothing to
 // join, and each workgroup has to find that out).
 constexpr int join_blocks(int groups) { return groups == 4 ? 4 : 16 * groups / kJoinCols; }
 
+// Joins the parts of the segments that several workgroups shared, in the
+// order of the tokens.  Workgroup j looks at the border between workers j and
+// j + 1; the one at the first border inside a segment joins it.  Two runs of
+// threads or more take turns at the parts (7 us for 64 sequences of 8 heads, 13
+// us where 8 segments of 32 columns have 64 parts each).
 template <int D, int CG, typename T>
 __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 {
@@ -393,66 +404,66 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
     // worker blockIdx.x has the first part, in its second slot; the others in their first
     const int w0 = (int)blockIdx.x, parts = (int)(((blockIdx.x + 1) * share - unit + s.units - 1) / share) - w0 + 1;
     for (int turn = 0; turn < COLS / (kJoinCols * join_blocks(CG)); ++turn) {
-    const int col0 = ((int)blockIdx.y + turn * join_blocks(CG)) * kJoinCols;
-    const int idx0 = (int)(seg - (uint32_t)head * s.ct) * COLS + col0;
-    if (idx0 >= s.n * A.group) return;
-    auto slot = [&](int p) -> int64_t { return (2 * (int64_t)(w0 + p) + (p == 0 ? 1 : 0)) * COLS + col0; };
+        const int col0 = ((int)blockIdx.y + turn * join_blocks(CG)) * kJoinCols;
+        const int idx0 = (int)(seg - (uint32_t)head * s.ct) * COLS + col0;
+        if (idx0 >= s.n * A.group) return;
+        auto slot = [&](int p) -> int64_t { return (2 * (int64_t)(w0 + p) + (p == 0 ? 1 : 0)) * COLS + col0; };
 
-    // each part's factor: 2^(M_part - M)
-    for (int i = tid; i < parts * kJoinCols; i += kJoinThreads)
-        sh_f[i / kJoinCols][i % kJoinCols] = A.part_ml[2 * (slot(i / kJoinCols) + i % kJoinCols)];
-    __syncthreads();
-    if (tid < 64 * kJoinCols) {
-        const int c = tid >> 6, lane = tid & 63;
-        float m = kNegInf;
-        for (int p = lane; p < parts; p += 64) m = fmaxf(m, sh_f[p][c]);
-        m = fmaxf(m, xor_lane<1>(m, lane));
-        m = fmaxf(m, xor_lane<2>(m, lane));
-        m = fmaxf(m, xor_lane<4>(m, lane));
-        m = fmaxf(m, xor_lane<8>(m, lane));
-        m = group_max(m, lane);
-        float l = 0.0f;
-        for (int p = lane; p < parts; p += 64) {
-            const float f = m == kNegInf ? 0.0f : fast_exp2(sh_f[p][c] - m);
-            sh_f[p][c] = f;
-            l = fmaf(f, A.part_ml[2 * (slot(p) + c) + 1], l);
+        // each part's factor: 2^(M_part - M)
+        for (int i = tid; i < parts * kJoinCols; i += kJoinThreads)
+            sh_f[i / kJoinCols][i % kJoinCols] = A.part_ml[2 * (slot(i / kJoinCols) + i % kJoinCols)];
+        __syncthreads();
+        if (tid < 64 * kJoinCols) {
+            const int c = tid >> 6, lane = tid & 63;
+            float m = kNegInf;
+            for (int p = lane; p < parts; p += 64) m = fmaxf(m, sh_f[p][c]);
+            m = fmaxf(m, xor_lane<1>(m, lane));
+            m = fmaxf(m, xor_lane<2>(m, lane));
+            m = fmaxf(m, xor_lane<4>(m, lane));
+            m = fmaxf(m, xor_lane<8>(m, lane));
+            m = group_max(m, lane);
+            float l = 0.0f;
+            for (int p = lane; p < parts; p += 64) {
+                const float f = m == kNegInf ? 0.0f : fast_exp2(sh_f[p][c] - m);
+                sh_f[p][c] = f;
+                l = fmaf(f, A.part_ml[2 * (slot(p) + c) + 1], l);
+            }
+            l += xor_lane<1>(l, lane);
+            l += xor_lane<2>(l, lane);
+            l += xor_lane<4>(l, lane);
+            l += xor_lane<8>(l, lane);
+            l = group_sum(l, lane);
+            if (lane == 0) sh_m[c] = m, sh_l[c] = l;
         }
-        l += xor_lane<1>(l, lane);
-        l += xor_lane<2>(l, lane);
-        l += xor_lane<4>(l, lane);
-        l += xor_lane<8>(l, lane);
-        l = group_sum(l, lane);
-        if (lane == 0) sh_m[c] = m, sh_l[c] = l;
-    }
-    __syncthreads();
+        __syncthreads();
 
-    const int run = tid / LANES, i = tid % LANES, c = i / QUADS, d = (i % QUADS) * 4;
-    if (run < RUNS) {
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float *o = A.part_o + (int64_t)c * D + d;
+        const int run = tid / LANES, i = tid % LANES, c = i / QUADS, d = (i % QUADS) * 4;
+        if (run < RUNS) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float *o = A.part_o + (int64_t)c * D + d;
 #pragma unroll 8
-        for (int p = run; p < parts; p += RUNS) {
-            const float f = sh_f[p][c];
-            const float4 w = *reinterpret_cast<const float4 *>(o + slot(p) * D);
-            v.x = fmaf(f, w.x, v.x), v.y = fmaf(f, w.y, v.y), v.z = fmaf(f, w.z, v.z), v.w = fmaf(f, w.w, v.w);
+            for (int p = run; p < parts; p += RUNS) {
+                const float f = sh_f[p][c];
+                const float4 w = *reinterpret_cast<const float4 *>(o + slot(p) * D);
+                v.x = fmaf(f, w.x, v.x), v.y = fmaf(f, w.y, v.y), v.z = fmaf(f, w.z, v.z), v.w = fmaf(f, w.w, v.w);
+            }
+            sh_o[run][i] = v;
         }
-        sh_o[run][i] = v;
-    }
-    __syncthreads();
-    const Column q = column(A, s, idx0 + c, head);
-    if (run == 0 && q.row >= 0) {
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k = 0; k < RUNS; ++k) {
-            const float4 w = sh_o[k][i];
-            v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
+        __syncthreads();
+        const Column q = column(A, s, idx0 + c, head);
+        if (run == 0 && q.row >= 0) {
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k = 0; k < RUNS; ++k) {
+                const float4 w = sh_o[k][i];
+                v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
+            }
+            const float l = sh_l[c], inv = l > 0.0f ? 1.0f / l : 0.0f;
+            for (int e = 0; e < 4; ++e) v[e] *= inv;
+            store_f32x4<T>(static_cast<T *>(a.out) + ((int64_t)q.row * a.q_heads + q.head) * D + d, v);
+            if (a.lse && d == 0)
+                a.lse[(int64_t)q.row * a.q_heads + q.head] = l > 0.0f ? (sh_m[c] + fast_log2(l)) * kLn2 : kNegInf;
         }
-        const float l = sh_l[c], inv = l > 0.0f ? 1.0f / l : 0.0f;
-        for (int e = 0; e < 4; ++e) v[e] *= inv;
-        store_f32x4<T>(static_cast<T *>(a.out) + ((int64_t)q.row * a.q_heads + q.head) * D + d, v);
-        if (a.lse && d == 0)
-            a.lse[(int64_t)q.row * a.q_heads + q.head] = l > 0.0f ? (sh_m[c] + fast_log2(l)) * kLn2 : kNegInf;
-    }
-    __syncthreads();
+        __syncthreads();
     }
 }
 
@@ -465,6 +476,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 // rows or there are at most two rows per sequence (then all of them are
 // streamed).
 constexpr int kFew = 64;
+// Tiles per part: a window of 2048 in fp32, 3 x 8 column tiles: 27 + 7 us at 5, 31 + 6 at 8.
 constexpr int kPartTiles = 5;
 
 struct Route {

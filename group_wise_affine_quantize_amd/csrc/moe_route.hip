@@ -16,7 +16,9 @@
 //
 // A token's logits lie in the registers of LPT = 16 or 64 lanes, EPL
 // neighbouring ones in each, so that a wave routes four tokens of up to 256
-// experts at once.
+// experts at once.  Bound by the vector unit: 16384 tokens of 256 experts in
+// fp32 (top 8 of 4 of 8 groups, sigmoid and bias, 17.8 MB) take 13.5 us, of
+// which the logits' bytes would need 3.5.
 //
 // The choice of up to kShort experts: every expert is one 64-bit number, its
 // ordered key above its falling index, so that numbers are distinct and the
@@ -86,6 +88,9 @@ template <int LPT> __device__ __forceinline__ uint32_t token_umax(uint32_t v, in
     return v;
 }
 
+// A NaN logit counts as -inf.
+__device__ __forceinline__ float numbered(float x) { return fmaxf(x, kNegInf); }
+
 // EPL neighbouring logits as fp32, -inf past `experts`.
 template <typename T, int EPL>
 __device__ __forceinline__ void load_logits(const T *row, int e0, int experts, bool wide, float *x)
@@ -99,14 +104,14 @@ __device__ __forceinline__ void load_logits(const T *row, int e0, int experts, b
 #pragma unroll
             for (int j = 0; j < per; ++j) {
                 const T t = v[j];
-                x[i + j] = Elt<T>::load(&t, 0);
+                x[i + j] = numbered(Elt<T>::load(&t, 0));
             }
         }
     } else {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const float t = Elt<T>::load(row, e0 + j < experts ? e0 + j : experts - 1);
-            x[j] = e0 + j < experts ? t : kNegInf;
+            x[j] = e0 + j < experts ? numbered(t) : kNegInf;
         }
     }
 }
@@ -128,8 +133,8 @@ __device__ __forceinline__ float sigmoid(float x)
     return x < -87.0f ? 0.0f : fmaf(fmaf(-d, y, 1.0f), y, y);   // below fp32's normal numbers: 0
 }
 
-// p of a token's logits; for softmax *top and *inv are the maximum and the
-// reciprocal-free divisor that any single logit's p can be taken with.
+// p of a token's logits; *top and *sum are a softmax's maximum and divisor,
+// from which any single logit's p can be taken.
 template <int LPT, int EPL>
 __device__ __forceinline__ void scores(int kind, const float *x, int lane, float *p, float *top, float *sum)
 {
@@ -356,7 +361,7 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeRouteLaunch a, i
         const bool mine = tl < r.top_k;
         float w = 0.0f;
         if (mine) {             // its logit again: it is in the cache
-            const float x1 = Elt<T>::load(row, id);
+            const float x1 = numbered(Elt<T>::load(row, id));
             w = r.score == MOE_SIGMOID ? sigmoid(x1) : exp_of(x1 - top) / sum;
         }
         const float total = token_sum<LPT>(w, lane);
@@ -431,7 +436,7 @@ __global__ __launch_bounds__(kThreads) void moe_grad_kernel(MoeGradLaunch a, int
         id[i] = k < r.top_k ? a.ids[t * r.top_k + k] : ~0u;
         pk[i] = 0.0f, qk[i] = 0.0f, d[i] = 0.0f;
         if (id[i] < (uint32_t)r.experts) {
-            const float v = Elt<T>::load(row, id[i]);
+            const float v = numbered(Elt<T>::load(row, id[i]));
             pk[i] = soft ? exp_of(v - top) / sum : sigmoid(v);
             qk[i] = sigmoid(-v);                          // 1 - p of a sigmoid, without cancellation
             d[i] = a.dweights[t * r.top_k + k] * r.scale;

@@ -1288,7 +1288,7 @@ nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, cons
     if (q_heads < 1 || q_heads > 65535 || q_heads % cache->kv_heads)
         return fail(NQ_ERR_SHAPE, "%s: q_heads=%d is not a multiple of kv_heads=%d in 1 .. 65535", op, q_heads,
                     cache->kv_heads);
-    if (seqs->rows * q_heads >= kMaxDim)
+    if (seqs->rows * q_heads >= kMaxDim / 2)
         return fail(NQ_ERR_SHAPE, "%s: rows=%lld times q_heads=%d is too large", op, (long long)seqs->rows, q_heads);
     if (!finite(softmax_scale) || !(softmax_scale > 0.0f))
         return fail(NQ_ERR_SHAPE, "%s: softmax_scale is not finite and positive", op);

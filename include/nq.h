@@ -462,11 +462,12 @@ typedef struct {
  * any length, 0 included.
  * The contents are read on the device and cannot be checked before the call;
  * whatever they hold, only the cache, the rows and the outputs are touched:
- * row_start is clamped to 0 .. rows and to an order that does not fall, a
- * negative length counts as 0, and a token whose block lies past max_blocks or whose id is
+ * row_start is clamped to 0 .. rows, a sequence whose row_start[b + 1] lies below row_start[b] has no
+ * rows, a negative length counts as 0, and a token whose block lies past max_blocks or whose id is
  * not in 0 .. blocks - 1 does not exist: it is not written, reads as zeros,
  * and is not attended to.  The same holds for a row before a sequence's first
- * token (more rows than tokens).  Rows that no sequence has are left alone. */
+ * token (more rows than tokens).  Rows that no sequence has are left alone;
+ * where sequences share rows, either may give a row its result, or none. */
 typedef struct {
     const int32_t *row_start;    /* [batch + 1] */
     const int32_t *lengths;      /* [batch] */
@@ -549,9 +550,10 @@ typedef struct {
  * scores stay, and of their experts the top_k largest keys are chosen, in
  * falling order; among equals the lowest index comes first, for groups too.
  * weights = p of the chosen experts (without the bias), divided by their sum
- * when renormalise (0 if the sum is 0), times scale.  A NaN key sorts as
- * -infinity; a softmax row with no logit above -infinity has p = 0.  Other
- * non-finite logits give valid ids and unspecified weights. */
+ * when renormalise (0 if the sum is 0), times scale.  A NaN logit counts as
+ * -infinity, a NaN key too; a softmax row with no logit above -infinity has p
+ * = 0.  Logits of +infinity give valid ids and unspecified weights.  Scores
+ * below fp32's normal numbers may count as 0. */
 nq_status nq_moe_route(const nq_moe_router *router, const void *logits, nq_dtype x_dt, int64_t tokens,
                        int64_t ld, const float *bias, uint32_t *ids, float *weights, hipStream_t stream);
 

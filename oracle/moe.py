@@ -2,8 +2,14 @@
 import numpy as np
 
 
-def scores(x, kind):
+def numbers(x):
+    """The logits, NaN as -inf."""
     x = np.asarray(x, np.float64)
+    return np.where(np.isnan(x), -np.inf, x)
+
+
+def scores(x, kind):
+    x = numbers(x)
     with np.errstate(over="ignore", invalid="ignore"):
         if kind == "sigmoid":
             return 1 / (1 + np.exp(-x))
@@ -16,7 +22,7 @@ def scores(x, kind):
 def route(x, kind, top_k, bias=None, groups=1, top_groups=1, group_best=1, renormalise=False, scale=1.0):
     """x [tokens, experts] -> ids [tokens, top_k], weights float64."""
     p = scores(x, kind)
-    key = np.asarray(x, np.float64) if bias is None else p + bias
+    key = numbers(x) if bias is None else p + bias
     summed = p if bias is None else key
     ids = np.empty((len(x), top_k), np.int64)
     for t in range(len(x)):

@@ -249,6 +249,20 @@ def test_attention_matches_the_reference(n, lengths, heads, kv, dim, block, fmt,
     check_attention(p, start, lengths, table, q.contiguous(), how, scale=0.3, lse=False)
 
 
+def test_attention_of_prompts_among_single_tokens():
+    """Sequences for the tile kernel and for the streaming one in one batch,
+    long contexts split between workgroups, more of them than a wave has lanes."""
+    rng = np.random.default_rng(3)
+    lengths = [int(rng.integers(1, 40)) for _ in range(70)] + [1500, 700, 90]
+    n = [1] * 40 + [0] * 20 + [3] * 10 + [1, 200, 90]
+    lengths = [max(a, b) for a, b in zip(n, lengths)]
+    p, table = filled(26, "int8", 32, 64, 1, lengths)
+    start = np.concatenate([[0], np.cumsum(n)])
+    for dtype in ("bf16", "f32"):
+        check_attention(p, start, lengths, table, rows(8, sum(n), 2, 64, dtype), {})
+    check_attention(p, start, lengths, table, rows(8, sum(n), 2, 64, "bf16"), {"window": 300})
+
+
 def test_attention_over_many_sequences():
     """More sequences than a wave has lanes, uneven, with gaps."""
     rng = np.random.default_rng(7)

@@ -164,3 +164,24 @@ def test_gradient_skips_ids_past_the_experts():
     dw[:, 1] = 0
     dw[0, 2] = 0
     assert bits_equal(got, B.nq_moe_route_grad(router, x, ids, dw))
+
+
+@pytest.mark.parametrize("experts,top_k,options", [(20, 3, {}), (200, 8, {}), (200, 9, {}),
+                                                   (256, 8, {"groups": 8, "top_groups": 2, "group_best": 2})])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_nan_logits_and_biases_count_as_minus_infinity(experts, top_k, options, score):
+    """Also where keys are scores plus a bias."""
+    x = logits_of(7, 12, experts, "f32")
+    x[:, ::3] = float("nan")
+    x[3, 1::3] = float("-inf")
+    bias = torch.arange(experts, device="cuda").float() % 7 / 64
+    options = {"groups": 1, "top_groups": 1, "group_best": 1, **options}
+    router = B.MoERouter(experts, top_k, score=score, **options)
+    for b in (None, bias):
+        ids, w = B.nq_moe_route(router, x, bias=b)
+        want, ww = M.route(x.double().cpu().numpy(), score, top_k, None if b is None else f64(b), **options)
+        assert np.array_equal(ids.cpu().numpy(), want)
+        assert np.all(np.abs(f64(w) - ww) <= (experts + top_k + 16) * 2.0 ** -24 * np.abs(ww))
+    bias[5] = float("nan")
+    ids, _ = B.nq_moe_route(router, torch.zeros_like(x), bias=bias)
+    assert not (ids == 5).any()
