@@ -476,11 +476,14 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 // rows or there are at most two rows per sequence (then all of them are
 // streamed).
 constexpr int kFew = 64;
+constexpr int kWholeShift = 4, kWholeTiles = 1 << kWholeShift;
 // Tiles per part: a window of 2048 in fp32, 3 x 8 column tiles: 27 + 7 us at 5, 31 + 6 at 8.
 constexpr int kPartTiles = 5;
 
 struct Route {
     bool stream, tile;
+    bool whole;         // the streaming kernel splits no segment
+    int64_t tiles;      // of a context, at most
     int ct;             // 16-column groups of the streaming kernel
     int few;
     unsigned tile_bound;
@@ -498,7 +501,11 @@ Route route_of(const KvAttnLaunch &a)
     else r.stream = r.tile = true, r.few = kFew;
     const int64_t per = std::max<int64_t>(1, (a.s.rows + a.s.batch - 1) / a.s.batch) * group;
     r.ct = per <= 16 ? 1 : per <= 32 ? 2 : 4;
-    r.stream_cols = r.stream ? (size_t)2 * kWorkers * 16 * r.ct : 0;
+    // Contexts that can have no more than 16 tiles are one unit: four tiles for
+    // each wave, which take less than a second launch, and no parts.
+    r.tiles = ((a.s.max_blocks << a.c.block_shift) >> 6) + 1;
+    r.whole = r.tiles <= kWholeTiles;
+    r.stream_cols = r.stream && !r.whole ? (size_t)2 * kWorkers * 16 * r.ct : 0;
     r.stream_floats = r.stream_cols * D;
     r.tile_bound = 0, r.tile_splits = 1, r.tile_cols = 0, r.tile_floats = 0;
     if (r.tile) {
@@ -508,7 +515,7 @@ Route route_of(const KvAttnLaunch &a)
         // too few workgroups for 256 compute units: tokens are split, at least
         // kPartTiles tiles that a column tile can see to a part
         const int64_t segments = bound * a.c.kv_heads;
-        int64_t tiles = ((a.s.max_blocks << a.c.block_shift) >> 6) + 1;
+        int64_t tiles = r.tiles;
         if (a.window > 0) tiles = std::min<int64_t>(tiles, ((a.window + M / group) >> 6) + 2);
         if (segments < 192)
             r.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>(512 / segments, tiles / kPartTiles));
@@ -566,14 +573,11 @@ hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream)
         const hipError_t e = launch_kv_prefill(A, stream);
         if (e != hipSuccess || !r.stream) return e;
     }
-    // Units of one tile, unless the list could then pass 32 bits.  Contexts
-    // that can have no more than 16 tiles are one unit: four tiles for each
-    // wave, which take less than a second launch.
-    const int64_t tiles = ((a.s.max_blocks << a.c.block_shift) >> 6) + 1;
+    // Units of one tile, unless the list could then pass 32 bits.
     const double segments = ((double)a.s.rows * A.group / (16 * r.ct) + a.s.batch) * a.c.kv_heads;
-    while (segments * (double)((tiles >> A.unit_shift) + 1) >= 0x1p31) ++A.unit_shift;
-    if (tiles <= 16) A.unit_shift = 4;
-    A.splits = tiles > (int64_t)1 << A.unit_shift;
+    while (segments * (double)((r.tiles >> A.unit_shift) + 1) >= 0x1p31) ++A.unit_shift;
+    if (r.whole) A.unit_shift = kWholeShift;
+    A.splits = r.tiles > (int64_t)1 << A.unit_shift;
     A.part_ml = A.part_o + r.stream_floats;
     switch (a.c.head_dim) {
     case 64: return stream_groups<64>(A, r.ct, stream);

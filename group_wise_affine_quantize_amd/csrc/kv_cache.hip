@@ -144,6 +144,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendLaunch a)
     const int count = it.hi - it.lo;
 
     float m = 0.0f;
+#pragma unroll 4
     for (int i = tid; i < count * (D / 8); i += kThreads) {
         const int t = i / (D / 8), d = (i % (D / 8)) * 8;
         const T *p = x + (int64_t)(it.lo + t) * ld + d;
@@ -168,6 +169,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendLaunch a)
                 for (int e = 0; e < 4; ++e) v[e] *= shrink;
                 *w = kv_codes4<FMT>(v);
             }
+#pragma unroll 4
         for (int i = tid; i < count * (D / 8); i += kThreads) {
             const int t = it.lo + i / (D / 8), d = (i % (D / 8)) * 8;
             const T *p = x + (int64_t)t * ld + d;

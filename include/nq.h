@@ -503,7 +503,8 @@ nq_status nq_kv_append(const nq_kv_cache *cache, const nq_kv_seqs *seqs, const v
 nq_status nq_kv_read(const nq_kv_cache *cache, const nq_kv_seqs *seqs, void *k, void *v, nq_dtype out_dt,
                      hipStream_t stream);
 
-/* Workspace bytes of nq_kv_attention; a function of sizes only. */
+/* Workspace bytes of nq_kv_attention; a function of sizes only (0 where no
+ * context can be split between workgroups). */
 size_t nq_kv_attention_workspace_bytes(const nq_kv_cache *cache, const nq_kv_seqs *seqs, int32_t q_heads,
                                        nq_dtype x_dt);
 

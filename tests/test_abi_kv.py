@@ -109,6 +109,9 @@ def test_attention_arguments(lib):
     assert attend(lib, c, s, lse=AT["lse"] + 2) == ALIGN
     assert attend(lib, c, s, out=AT["q"]) == ALIAS and attend(lib, c, s, lse=AT["out"]) == ALIAS
     assert attend(lib, c, s, out=AT["k_codes"]) == ALIAS
+    # contexts of up to 16 tiles of 64 tokens are not split: no workspace
+    assert lib.nq_kv_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(s), 8, 1) == 0
+    s = seqs(max_blocks=100, table_stride=100)
     need = lib.nq_kv_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(s), 8, 1)
     assert need > 0
     assert attend(lib, c, s, ws=None) == WORKSPACE and attend(lib, c, s, ws_bytes=need - 1) == WORKSPACE
