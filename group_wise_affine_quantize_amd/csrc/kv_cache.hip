@@ -10,7 +10,13 @@
 // step of the last scale (each rounding adds half a step, and the steps at
 // least double), where growing to a / qmax each time would let it drift.
 //
-// Both are bound by memory: a token of a head is read once and written once.
+// Both are bound by memory: a token of a head is read and written once (by the
+// write its row is read twice, for the scale and for the codes, the second
+// time from the cache: 77 MB fetched for 59).  14.3k tokens of 8 heads of 128,
+// bf16 to E4M3: 88 MB in 25 to 28 us; 107k tokens of int8 back to bf16: 657 MB
+// in 150 us, 4.4 TB/s; 16 single tokens 5.6 us, one dependent load after
+// another.
+//
 // One workgroup takes one block of one head, keys or values (the two have
 // their own scales), so the scale is a workgroup's reduction and no two
 // workgroups share a byte.
@@ -126,8 +132,6 @@ __device__ __forceinline__ bool find_item(const KvSeqs &s, const KvCache &c, int
 // along their columns and codes written along the slots.
 constexpr int kCols = 4, kSlots = 8;
 
-// The rows are read twice, for the scale and for the codes; the second time
-// they come from the cache.
 template <int D, int FMT, typename T>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendLaunch a)
 {

@@ -462,12 +462,13 @@ typedef struct {
  * any length, 0 included.
  * The contents are read on the device and cannot be checked before the call;
  * whatever they hold, only the cache, the rows and the outputs are touched:
- * row_start is clamped to 0 .. rows, a sequence whose row_start[b + 1] lies below row_start[b] has no
- * rows, a negative length counts as 0, and a token whose block lies past max_blocks or whose id is
- * not in 0 .. blocks - 1 does not exist: it is not written, reads as zeros,
- * and is not attended to.  The same holds for a row before a sequence's first
- * token (more rows than tokens).  Rows that no sequence has are left alone;
- * where sequences share rows, either may give a row its result, or none. */
+ * row_start is clamped to 0 .. rows, a sequence whose row_start[b + 1] lies
+ * below row_start[b] has no rows, a negative length counts as 0, and a token
+ * whose block lies past max_blocks or whose id is not in 0 .. blocks - 1 does
+ * not exist: it is not written, reads as zeros, and is not attended to.  The
+ * same holds for a row before a sequence's first token (more rows than
+ * tokens).  Rows that no sequence has are left alone; where sequences share
+ * rows, either may give a row its result, or none. */
 typedef struct {
     const int32_t *row_start;    /* [batch + 1] */
     const int32_t *lengths;      /* [batch] */
