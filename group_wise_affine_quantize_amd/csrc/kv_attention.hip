@@ -29,7 +29,7 @@
 // per lane).  No value moves between lanes but the running maximum.
 //
 // What bounds it: reading the codes.  64 sequences of 1k to 8k tokens, 8 heads of
-// 128 in int8: 620 MB in 123 us, 5.0 TB/s (a 1 GiB copy moves 5.1), with two
+// 128 in int8: 620 MB in 121 us, 5.1 TB/s (a 1 GiB copy moves 5.1), with two
 // workgroups of four waves per compute unit, each wave with a tile of 16 KB on
 // the way.  With more than 16 query columns two or four waves read the same tile, and
 // less is on the way: 8 draft tokens over 131k tokens, 264 MB in 82 us.  One token at
@@ -87,6 +87,18 @@ __device__ __forceinline__ int stream_locate(const AttnArgs &A, int cols, At at,
         base += sum;
     }
     return -1;
+}
+
+// 16 bytes of codes.  ONCE: no other wave will want them, and they pass the
+// caches by (64 sequences of 1k to 8k tokens 123 -> 121 us; with two column
+// groups, which share them in the L1, it is 80 -> 104).
+template <bool ONCE> __device__ __forceinline__ uint4 load_codes(const uint8_t *p)
+{
+    const uint4_t *q = reinterpret_cast<const uint4_t *>(p);
+    uint4_t v;
+    if constexpr (ONCE) v = __builtin_nontemporal_load(q);
+    else v = *q;
+    return __builtin_bit_cast(uint4, v);
 }
 
 // The state of a wave's 16 columns.
@@ -183,14 +195,14 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j) kw[n][j] = *reinterpret_cast<const uint4 *>(kp + 4 * n * D + 64 * j);
+                for (int j = 0; j < D / 64; ++j) kw[n][j] = load_codes<CG == 1>(kp + 4 * n * D + 64 * j);
         };
         auto load_values = [&](int base, int idv) {
             const int pv = base + 16 * g;
             const int64_t slab = (int64_t)(idv < 0 ? 0 : idv) * a.c.kv_heads + head;
             const uint8_t *vp = a.c.v_codes + ((slab * D + r) << sh) + (pv & bmask);
 #pragma unroll
-            for (int dt = 0; dt < DT; ++dt) vw[dt] = *reinterpret_cast<const uint4 *>(vp + ((16 * dt) << sh));
+            for (int dt = 0; dt < DT; ++dt) vw[dt] = load_codes<CG == 1>(vp + ((16 * dt) << sh));
             sk = 0.0f, sv = 1.0f;
             if (idv >= 0) sk = a.c.k_scales[slab], sv = a.c.v_scales[slab];
         };

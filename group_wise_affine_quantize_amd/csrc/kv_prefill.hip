@@ -2,9 +2,9 @@
 // chunks); the mathematics is at the head of kv_attention.hip.
 //
 // A workgroup takes 32 query columns per wave (a column is a row of the call
-// and one of the head's queries) of one key/value head and runs over the tokens that they
-// see, 64 at a time.  The tile's codes are converted to fp16 once, into LDS,
-// where all waves read them as operands of 32x32x16 MFMAs: S^T = K q^T,
+// and one of the head's queries) of one key/value head and runs over the
+// tokens that they see, 64 at a time.  The tile's codes are converted to fp16
+// once, into LDS, where all waves read them as operands of 32x32x16 MFMAs: S^T = K q^T,
 // O^T = V^T P^T.  Eight waves (four for head_dim over 128, whose O and q take
 // twice the registers): two per SIMD, so that one's softmax runs under the
 // other's products.
@@ -20,12 +20,13 @@
 // passes it by kSlack: a move costs a pass over O, and weights may reach
 // 2^(kTop + kSlack) in fp16.
 //
-// 3 prompts of 2530 to 4096 tokens, 32 heads of 128 over 8 int8 key/value heads: 380 us, 737 TFLOP/s
-// of the visible products, where a large fp16 library product reaches 1131.
-// A tile takes about 4450 cycles at the 1.97 GHz that the card keeps up:
-// about 330 vector instructions for each of the two waves of a SIMD and 2048
-// cycles of MFMA per SIMD, overlapped as far as the two waves' phases differ.  The LDS (256 bytes
-// a cycle with the keys above) is a quarter used.
+// 3 prompts of 2530 to 4096 tokens, 32 heads of 128 over 8 int8 key/value
+// heads: 375 to 385 us by itself (340 in a row of calls), 740 TFLOP/s of the
+// visible products, where a large fp16 library product reaches 1131.  A tile
+// takes about 4450 cycles at the 1.97 GHz that the card keeps up: 324 vector
+// instructions for each of the two waves of a SIMD, and 2048 cycles of MFMA
+// per SIMD, overlapped as far as the two waves' phases differ.  The LDS (256
+// bytes a cycle with the placement below) is a quarter used.
 #include "nq_kv_attn.h"
 #include "nq_tiles.h"
 
