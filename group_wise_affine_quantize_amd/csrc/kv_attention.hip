@@ -484,9 +484,10 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 // Sequences with up to kFew query columns per head go through the streaming
 // kernel, which splits long contexts evenly; longer ones through the tile
 // kernel, whose operands serve more columns.  Which of them a batch holds is
-// only known on the device: both are launched, unless one sequence has all
-// rows or there are at most two rows per sequence (then all of them are
-// streamed).
+// only known on the device: both are launched, unless there is one sequence or
+// there are at most two rows per sequence (then all of them are streamed).
+// One sequence goes by the call's rows, of which it may own any number: the
+// kernel that is launched takes it whatever it owns.
 constexpr int kFew = 64;
 constexpr int kWholeShift = 4, kWholeTiles = 1 << kWholeShift;
 // Tiles per part: a window of 2048 in fp32, 3 x 8 column tiles: 27 + 7 us at 5, 31 + 6 at 8.
@@ -508,7 +509,7 @@ Route route_of(const KvAttnLaunch &a)
 {
     Route r;
     const int64_t group = a.q_heads / a.c.kv_heads, cols = a.s.rows * group, D = a.c.head_dim;
-    if (a.s.batch == 1) r.stream = cols <= kFew, r.tile = !r.stream, r.few = kFew;
+    if (a.s.batch == 1) r.stream = cols <= kFew, r.tile = !r.stream, r.few = r.stream ? kFew : 0;
     else if (cols <= kFew || a.s.rows <= 2 * (int64_t)a.s.batch) r.stream = true, r.tile = false, r.few = INT32_MAX;
     else r.stream = r.tile = true, r.few = kFew;
     const int64_t per = std::max<int64_t>(1, (a.s.rows + a.s.batch - 1) / a.s.batch) * group;
