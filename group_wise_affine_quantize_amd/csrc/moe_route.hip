@@ -248,7 +248,7 @@ __device__ __forceinline__ bool group_stays(const MoeRoute &r, const float *v, i
     float b1 = kNegInf, b2 = kNegInf;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        b2 = fmaxf(b2, fminf(b1, fmaxf(v[j], kNegInf)));
+        b2 = fmaxf(b2, fminf(b1, v[j]));
         b1 = fmaxf(b1, v[j]);
     }
     auto join = [&](float o1, float o2) {
@@ -295,7 +295,8 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeRouteLaunch a, i
         const bool is = e0 + j < r.experts;
         const float k = a.bias ? p[j] + bias[j] : x[j];
         key[j] = is ? ordered(k) : 0u;
-        v[j] = is ? (!a.bias && summed ? p[j] : k) : kNegInf;
+        // a NaN here would count its group's best twice: fminf(best, NaN) is the best
+        v[j] = is ? numbered(!a.bias && summed ? p[j] : k) : kNegInf;
     }
     if (LPT == 16 && lanes_per_group > 0) {
         if (!group_stays<EPL>(r, v, lanes_per_group, tl, lane))

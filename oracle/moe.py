@@ -3,7 +3,7 @@ import numpy as np
 
 
 def numbers(x):
-    """The logits, NaN as -inf."""
+    """Logits or keys, NaN as -inf."""
     x = np.asarray(x, np.float64)
     return np.where(np.isnan(x), -np.inf, x)
 
@@ -23,7 +23,7 @@ def route(x, kind, top_k, bias=None, groups=1, top_groups=1, group_best=1, renor
     """x [tokens, experts] -> ids [tokens, top_k], weights float64."""
     p = scores(x, kind)
     key = numbers(x) if bias is None else p + bias
-    summed = p if bias is None else key
+    summed = numbers(p if bias is None else key)
     ids = np.empty((len(x), top_k), np.int64)
     for t in range(len(x)):
         key_t = np.where(np.isnan(key[t]), -np.inf, key[t])

@@ -185,3 +185,38 @@ def test_nan_logits_and_biases_count_as_minus_infinity(experts, top_k, options, 
     bias[5] = float("nan")
     ids, _ = B.nq_moe_route(router, torch.zeros_like(x), bias=bias)
     assert not (ids == 5).any()
+
+
+# group sizes that a power of two of lanes holds, and others; more than 256 experts
+@pytest.mark.parametrize("experts,groups,top_k", [(32, 4, 3), (60, 4, 3), (120, 8, 9), (256, 8, 8), (480, 16, 5), (1024, 64, 8)])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_nan_biases_add_nothing_to_a_group(experts, groups, top_k, best, score):
+    """A NaN key counts as -infinity in its group's score too: it is not the second best, and does not stand in for it."""
+    options = {"groups": groups, "top_groups": 2, "group_best": best}
+    x = logits_of(experts, 25, experts, "f32")
+    size = experts // groups
+    bias = torch.arange(experts, device="cuda").float() % 7 / 64
+    bias[1::3] = float("nan")
+    bias[:size] = float("nan")                      # a group without any key,
+    bias[size:2 * size - 1] = float("nan")          # and one with a single one
+    bias[-size:-1:2] = float("-inf")
+    router = B.MoERouter(experts, top_k, score=score, **options)
+    ids, w = B.nq_moe_route(router, x, bias=bias)
+    want, ww = M.route(f64(x), score, top_k, f64(bias), **options)
+    assert np.array_equal(ids.cpu().numpy(), want)
+    assert np.all(np.abs(f64(w) - ww) <= (experts + top_k + 16) * 2.0 ** -24 * np.abs(ww))
+
+
+def test_the_second_best_of_a_group_is_a_number():
+    """{0.9, 0.1, NaN, 0.2} has 1.1, not 1.8, and {0.7, 0.6, 0, 0} is the better one."""
+    keys = torch.tensor([0.9, 0.1, float("nan"), 0.2, 0.7, 0.6, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0], device="cuda")
+    x = torch.full((1, 12), -100.0, device="cuda")      # sigmoids of zero: the keys are the bias
+    ids, _ = B.nq_moe_route(B.MoERouter(12, 2, score="sigmoid", groups=3, top_groups=1, group_best=2), x, bias=keys)
+    assert ids.tolist() == [[4, 5]]
+    # the same among 480 experts, whose groups of 30 no power of two of lanes holds
+    x = torch.full((1, 480), -100.0, device="cuda")
+    bias = torch.zeros(480, device="cuda")
+    bias[:4], bias[30:34] = keys[:4], keys[4:8]
+    ids, _ = B.nq_moe_route(B.MoERouter(480, 2, score="sigmoid", groups=16, top_groups=1, group_best=2), x, bias=bias)
+    assert ids.tolist() == [[30, 31]]

@@ -86,3 +86,11 @@ def test_routing_takes_the_lowest_index_among_equals():
     assert ids.tolist() == [[5, 0]]
     ids, w = M.route(np.full((1, 4), -np.inf), "softmax", 2, renormalise=True)
     assert ids.tolist() == [[0, 1]] and np.all(w == 0)
+
+
+@pytest.mark.parametrize("best,first", [(1, 0), (2, 1)])
+def test_a_nan_key_adds_nothing_to_its_group(best, first):
+    """{0.9, 0.1, NaN, 0.2} has the best single key, but with its second best only 1.1 against 1.3."""
+    keys = np.array([0.9, 0.1, np.nan, 0.2, 0.7, 0.6, 0.0, 0.0])
+    ids, _ = M.route(np.full((1, 8), -1000.0), "sigmoid", 1, bias=keys, groups=2, top_groups=1, group_best=best)
+    assert ids.tolist() == [[4 * first]]
