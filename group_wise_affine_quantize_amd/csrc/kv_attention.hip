@@ -586,8 +586,11 @@ hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream)
         const hipError_t e = launch_kv_prefill(A, stream);
         if (e != hipSuccess || !r.stream) return e;
     }
-    // Units of one tile, unless the list could then pass 32 bits.
-    const double segments = ((double)a.s.rows * A.group / (16 * r.ct) + a.s.batch) * a.c.kv_heads;
+    // Units of one tile, unless the list could then pass 32 bits.  Only sequences
+    // with rows have segments: with rows * q_heads below 2^30 there are fewer
+    // than 2^31, and the loop ends, at the latest where each is one unit.
+    const double segments =
+        ((double)a.s.rows * A.group / (16 * r.ct) + (double)std::min<int64_t>(a.s.batch, a.s.rows)) * a.c.kv_heads;
     while (segments * (double)((r.tiles >> A.unit_shift) + 1) >= 0x1p31) ++A.unit_shift;
     if (r.whole) A.unit_shift = kWholeShift;
     A.splits = r.tiles > (int64_t)1 << A.unit_shift;

@@ -155,3 +155,25 @@ def test_binding_refuses_cpu_tensors():
         B.nq_moe_route(B.MoERouter(8, 2), torch.zeros(3, 8))
     with pytest.raises(ValueError):
         B.MoERouter(8, 2, score="tanh")
+
+
+def test_attention_of_more_sequences_than_rows_returns():
+    """The bound of the list of work counts sequences that can have rows: with 2^24 sequences of 128 heads the search
+    for its unit size ends (no GPU is visible here, so the call then fails at the launch)."""
+    import os
+    import subprocess
+    import sys
+    program = """
+import ctypes, sys
+sys.path[:0] = sys.argv[1:]
+import test_abi_kv as t
+lib = t.B.load_library()
+c = t.cache(kv_heads=128, head_dim=64, block_tokens=128)
+s = t.seqs(batch=1 << 24, rows=4, max_blocks=8, table_stride=8)
+print(t.attend(lib, c, s, ldq=128 * 64, heads=128), flush=True)
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = {**os.environ, "HIP_VISIBLE_DEVICES": "-1", "ROCR_VISIBLE_DEVICES": ""}
+    done = subprocess.run([sys.executable, "-c", program, here, os.path.dirname(here)], env=env, capture_output=True,
+                          text=True, timeout=60)
+    assert done.stdout.split() == ["8"], done.stderr[-500:]
