@@ -51,8 +51,7 @@ constexpr int kWaves = 4;
 // do not fall into parts that cost more to join than to read.
 __device__ __forceinline__ uint32_t share_of(const AttnArgs &A, uint32_t total)
 {
-    const uint32_t share = (total + A.workers - 1) / A.workers, least = A.unit_shift ? 1 : 2 * kWaves;
-    return share < least ? least : share;
+    return list_share(total, (uint32_t)A.workers, A.unit_shift ? 1u : 2u * kWaves);
 }
 
 // Finds the sequence of unit `at(share)` of the list: its number (-1: past the
@@ -62,25 +61,26 @@ __device__ __forceinline__ int stream_locate(const AttnArgs &A, int cols, At at,
                                              uint32_t *share)
 {
     const int batch = A.a.s.batch, lane = (int)(threadIdx.x & 63u);
-    uint32_t work = lane < batch ? stream_seq(A, lane, cols).work : 0u;
-    uint32_t upto = wave_scan32(work);
+    uint32_t work = lane < batch ? stream_seq(A, lane, cols).work : 0u;     // below 2^31
+    uint32_t upto = wave_scan32_sat(work);
     uint32_t sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
     *total = sum;
     for (int b = 64 + lane; b - lane < batch; b += 64)
-        *total += (uint32_t)__builtin_amdgcn_readlane(
-            (int)wave_scan32(b < batch ? stream_seq(A, b, cols).work : 0u), 63);
+        *total = add_sat(*total, (uint32_t)__builtin_amdgcn_readlane(
+            (int)wave_scan32_sat(b < batch ? stream_seq(A, b, cols).work : 0u), 63));
+    *total = list_total(*total);
     *share = share_of(A, *total);
     const uint32_t want = at(*share);
     if (want >= *total) return -1;
-    uint32_t base = 0;
+    uint32_t base = 0;      // at most `want`
     for (int b0 = 0; b0 < batch; b0 += 64) {
         if (b0) {
             work = b0 + lane < batch ? stream_seq(A, b0 + lane, cols).work : 0u;
-            upto = wave_scan32(work);
+            upto = wave_scan32_sat(work);
             sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
         }
-        if (base + sum > want) {
-            const int l = __ffsll((unsigned long long)__ballot(base + upto > want)) - 1;
+        if (add_sat(base, sum) > want) {
+            const int l = __ffsll((unsigned long long)__ballot(add_sat(base, upto) > want)) - 1;
             *inside = want - base - (uint32_t)__builtin_amdgcn_readlane((int)(upto - work), l);
             return b0 + l;
         }
@@ -414,7 +414,8 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
     if (unit == 0 || unit > share) return;     // between segments, or not the first border inside
     const int head = (int)(seg / s.ct);
     // worker blockIdx.x has the first part, in its second slot; the others in their first
-    const int w0 = (int)blockIdx.x, parts = (int)(((blockIdx.x + 1) * share - unit + s.units - 1) / share) - w0 + 1;
+    const int w0 = (int)blockIdx.x, parts = list_parts(blockIdx.x + 1, share, total, unit, s.units);
+    if (parts == 0) return;
     for (int turn = 0; turn < COLS / (kJoinCols * join_blocks(CG)); ++turn) {
         const int col0 = ((int)blockIdx.y + turn * join_blocks(CG)) * kJoinCols;
         const int idx0 = (int)(seg - (uint32_t)head * s.ct) * COLS + col0;

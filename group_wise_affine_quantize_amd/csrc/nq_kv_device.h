@@ -4,6 +4,7 @@
 
 #include "nq_device.h"
 #include "nq_kv.h"
+#include "nq_kv_list.h"
 
 namespace nqk {
 
@@ -127,6 +128,19 @@ __device__ __forceinline__ uint32_t wave_scan32(uint32_t v)
     add(__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true));
     add(__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));   // row 0 -> 1, 2 -> 3
     add(__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));   // rows 0, 1 -> 2, 3
+    return v;
+}
+
+// The same, of sums that stay at 2^32 - 1 when they pass it.
+__device__ __forceinline__ uint32_t wave_scan32_sat(uint32_t v)
+{
+    auto add = [&](int o) { v = add_sat(v, (uint32_t)o); };
+    add(__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true));
+    add(__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true));
+    add(__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true));
+    add(__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true));
+    add(__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));
+    add(__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));
     return v;
 }
 
