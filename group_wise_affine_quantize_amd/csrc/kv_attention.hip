@@ -20,6 +20,15 @@
 // sum of two fp16 numbers (22 bits) and take two matrix products each.  Sums,
 // references and the states O and L are fp32.
 //
+// p_t / sv_t is 2^(z_t - R) (z in base 2 here), whose range is not p_t's: a sum
+// over tiny scales can pass fp32, and the p_t of a small scale beside a very
+// large one be flushed though its weight in L is not small.  With scales in 2^-48 .. 2^16
+// neither happens: p_t / sv_t is below 2^64, and p_t is only flushed for tokens
+// whose weight is below 2^-60 of the largest.  From the first tile on that
+// holds another scale, or a block of zeros (no logarithm: its tokens add to L
+// alone), a wave keeps L = sum_t 2^(z_t - U) over a reference U of its own, by
+// a second exponential of each score.
+//
 // Matrix products: S^T = K q^T and O^T = V^T P^T on 16x16x32 fp16 MFMA with
 // the tokens in the rows of the first product.  Lane l (r = l % 16, g = l / 16)
 // holds column (query row) r and, after the first product, tokens 16 g + 4 n +
@@ -106,6 +115,7 @@ template <int D, int NP> struct State {
     half8_t q[D / 32][NP];
     float c;                     // log2(e) * scale / row power of two
     float m, l;                  // m: the reference, 14 below the maximum when set; weights are 2^(x - m)
+    float u;                     // l's reference, where it is not m
     float4_t o[D / 16];
 };
 
@@ -117,7 +127,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
 {
     constexpr int NP = Parts<T>::n, COLS = 16 * CG, KS = D / 32, DT = D / 16, TL = kWaves / CG;
     constexpr int LDO = D + 4;
-    __shared__ float sh_m[TL][COLS], sh_l[TL][COLS];
+    __shared__ float2 sh_mu[TL][COLS];
+    __shared__ float sh_l[TL][COLS];
     __shared__ float sh_o[TL > 1 ? TL / 2 : 1][COLS][LDO];
     const KvAttnLaunch &a = A.a;
     const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
@@ -146,6 +157,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
         const int tile1 = unit0 + units == s.units ? s.nt : (int)((unit0 + units) << A.unit_shift);
 
         State<D, NP> st;
+        bool apart = false;     // whether l has a reference of its own
         int col_lo, col_hi;
         {
             const Column c = column(A, s, ctile * COLS + 16 * cg + r, head);
@@ -168,7 +180,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
                 split_half<NP>(f[ks], st.q[ks]);
             }
             st.c = a.scale * kLog2e * back;
-            st.m = kNegInf;
+            st.m = kNegInf, st.u = kNegInf;
             st.l = 0.0f;
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt) st.o[dt] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -255,8 +267,10 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
             idk = idk2;
             if (more) load_keys(next, idk2);
 
-            const float vs = sv == 0.0f ? kZeroBlockScale : sv;
+            const bool zeros = sv == 0.0f;
+            const float vs = zeros ? 1.0f : sv;
             const float lsv = fast_log2(vs), isv = 1.0f / vs;
+            const bool far = __any(scale_is_far(sv));
             half8_t P[2][NP];
             {
                 const float f = st.c * sk;
@@ -270,6 +284,13 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] = i < lo || i >= hi ? kNegInf : x[i];
                 }
+                if (__builtin_expect(apart || far, false)) {
+                    if (!apart) st.u = st.m;
+                    apart = true;
+                    add_weights(16, [&](int i) { return x[i] - lsv; }, st.l, st.u);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = zeros ? kNegInf : x[i];
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[i]);
                 // the reference moves, and O with it, when a maximum passes it by kSlack
@@ -278,7 +299,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
                     const float next = over > st.m + kSlack ? over : st.m;
                     const float alpha = next == kNegInf ? 0.0f : fast_exp2(st.m - next);
                     st.m = next;
-                    st.l *= alpha;
+                    if (!apart) st.l *= alpha;
 #pragma unroll
                     for (int dt = 0; dt < DT; ++dt) st.o[dt] *= alpha;
                 }
@@ -289,7 +310,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
                     x[i] = fast_exp2(x[i] - mref);
                     sum += x[i];
                 }
-                st.l = fmaf(sum, isv, st.l);
+                st.l = fmaf(sum, apart ? 0.0f : isv, st.l);
                 split_half<NP>(x, P[0]);
                 split_half<NP>(x + 8, P[1]);
             }
@@ -332,16 +353,21 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
         }
 
         // join the waves of a column group: references first, then sums by halves
+        if (apart) {
+            const float u = group_max(st.u, lane);
+            st.l *= exp2_below(st.u, u);
+            st.u = u;
+        } else st.u = st.m;
         st.l = group_sum(st.l, lane);
         const int col = 16 * cg + r;
-        if (g == 0) sh_m[turn][col] = st.m;
+        if (g == 0) sh_mu[turn][col] = make_float2(st.m, st.u);
         __syncthreads();
         {
-            float m = sh_m[0][col];
-            for (int w = 1; w < TL; ++w) m = fmaxf(m, sh_m[w][col]);
-            const float f = m == kNegInf ? 0.0f : fast_exp2(st.m - m);
-            st.m = m;
-            st.l *= f;
+            float m = kNegInf, u = kNegInf;
+            for (int w = 0; w < TL; ++w) m = fmaxf(m, sh_mu[w][col].x), u = fmaxf(u, sh_mu[w][col].y);
+            const float f = exp2_below(st.m, m);
+            st.l *= exp2_below(st.u, u);
+            st.m = m, st.u = u;
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt) st.o[dt] *= f;
             if (g == 0) sh_l[turn][col] = st.l;
@@ -363,22 +389,21 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
             float l = sh_l[0][col];
             for (int w = 1; w < TL; ++w) l += sh_l[w][col];
             if (whole) {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const float f = out_factor(l, st.m, st.u, 4 * DT, reinterpret_cast<float *>(st.o));
                 T *out = static_cast<T *>(a.out) + ((int64_t)c.row * a.q_heads + c.head) * D;
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt) {
                     float v[4];
-                    for (int i = 0; i < 4; ++i) v[i] = st.o[dt][i] * inv;
+                    for (int i = 0; i < 4; ++i) v[i] = st.o[dt][i] * f;
                     store_f32x4<T>(out + 16 * dt + 4 * g, v);
                 }
                 if (a.lse && g == 0)
-                    a.lse[(int64_t)c.row * a.q_heads + c.head] = l > 0.0f ? (st.m + fast_log2(l)) * kLn2 : kNegInf;
+                    a.lse[(int64_t)c.row * a.q_heads + c.head] = l > 0.0f ? (st.u + fast_log2(l)) * kLn2 : kNegInf;
             } else {
                 float *po = A.part_o + (slot * COLS + col) * D;
-                float *pm = A.part_ml + (slot * COLS + col) * 2;
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt) *reinterpret_cast<float4_t *>(po + 16 * dt + 4 * g) = st.o[dt];
-                if (g == 0) pm[0] = st.m, pm[1] = l;
+                if (g == 0) A.part_s[slot * COLS + col] = make_float4(st.m, l, st.u, 0.0f);
             }
         }
         __syncthreads();
@@ -401,8 +426,8 @@ template <int D, int CG, typename T>
 __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 {
     constexpr int COLS = 16 * CG, QUADS = D / 4, LANES = kJoinCols * QUADS, RUNS = kJoinThreads / LANES;
-    __shared__ float sh_f[kWorkers][kJoinCols];
-    __shared__ float sh_m[kJoinCols], sh_l[kJoinCols];
+    __shared__ float sh_f[kWorkers][kJoinCols], sh_l[kWorkers][kJoinCols], sh_u[kWorkers][kJoinCols];
+    __shared__ float4 sh_s[kJoinCols];
     __shared__ float4 sh_o[RUNS][LANES];
     const KvAttnLaunch &a = A.a;
     const int tid = (int)threadIdx.x;
@@ -422,31 +447,29 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
         if (idx0 >= s.n * A.group) return;
         auto slot = [&](int p) -> int64_t { return (2 * (int64_t)(w0 + p) + (p == 0 ? 1 : 0)) * COLS + col0; };
 
-        // each part's factor: 2^(M_part - M)
-        for (int i = tid; i < parts * kJoinCols; i += kJoinThreads)
-            sh_f[i / kJoinCols][i % kJoinCols] = A.part_ml[2 * (slot(i / kJoinCols) + i % kJoinCols)];
+        // each part's factor of O: 2^(R_part - R)
+        for (int i = tid; i < parts * kJoinCols; i += kJoinThreads) {
+            const int p = i / kJoinCols, c = i % kJoinCols;
+            const float4 t = A.part_s[slot(p) + c];
+            sh_f[p][c] = t.x, sh_l[p][c] = t.y, sh_u[p][c] = t.z;
+        }
         __syncthreads();
         if (tid < 64 * kJoinCols) {
             const int c = tid >> 6, lane = tid & 63;
-            float m = kNegInf;
-            for (int p = lane; p < parts; p += 64) m = fmaxf(m, sh_f[p][c]);
-            m = fmaxf(m, xor_lane<1>(m, lane));
-            m = fmaxf(m, xor_lane<2>(m, lane));
-            m = fmaxf(m, xor_lane<4>(m, lane));
-            m = fmaxf(m, xor_lane<8>(m, lane));
-            m = group_max(m, lane);
+            float m = kNegInf, u = kNegInf;
+            for (int p = lane; p < parts; p += 64) m = fmaxf(m, sh_f[p][c]), u = fmaxf(u, sh_u[p][c]);
+            m = wave_max(m, lane), u = wave_max(u, lane);
             float l = 0.0f;
             for (int p = lane; p < parts; p += 64) {
-                const float f = m == kNegInf ? 0.0f : fast_exp2(sh_f[p][c] - m);
-                sh_f[p][c] = f;
-                l = fmaf(f, A.part_ml[2 * (slot(p) + c) + 1], l);
+                sh_f[p][c] = exp2_below(sh_f[p][c], m);
+                l = fmaf(exp2_below(sh_u[p][c], u), sh_l[p][c], l);
             }
             l += xor_lane<1>(l, lane);
             l += xor_lane<2>(l, lane);
             l += xor_lane<4>(l, lane);
             l += xor_lane<8>(l, lane);
             l = group_sum(l, lane);
-            if (lane == 0) sh_m[c] = m, sh_l[c] = l;
+            if (lane == 0) sh_s[c] = make_float4(m, l, u, 0.0f);
         }
         __syncthreads();
 
@@ -470,11 +493,12 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
                 const float4 w = sh_o[k][i];
                 v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
             }
-            const float l = sh_l[c], inv = l > 0.0f ? 1.0f / l : 0.0f;
-            for (int e = 0; e < 4; ++e) v[e] *= inv;
+            const float4 t = sh_s[c];
+            const float l = t.y, f = out_factor(l, t.x, t.z, 4, v);
+            for (int e = 0; e < 4; ++e) v[e] *= f;
             store_f32x4<T>(static_cast<T *>(a.out) + ((int64_t)q.row * a.q_heads + q.head) * D + d, v);
             if (a.lse && d == 0)
-                a.lse[(int64_t)q.row * a.q_heads + q.head] = l > 0.0f ? (sh_m[c] + fast_log2(l)) * kLn2 : kNegInf;
+                a.lse[(int64_t)q.row * a.q_heads + q.head] = l > 0.0f ? (t.z + fast_log2(l)) * kLn2 : kNegInf;
         }
         __syncthreads();
     }
@@ -569,7 +593,7 @@ size_t kv_attn_ws_bytes(const KvAttnLaunch &a)
 {
     // the two kernels run one after the other: they share the workspace
     const Route r = route_of(a);
-    return std::max(r.stream_floats + 2 * r.stream_cols, r.tile_floats + 2 * r.tile_cols) * sizeof(float);
+    return std::max(r.stream_floats + 4 * r.stream_cols, r.tile_floats + 4 * r.tile_cols) * sizeof(float);
 }
 
 hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream)
@@ -583,7 +607,7 @@ hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream)
     A.unit_shift = 0, A.splits = false;
     A.part_o = static_cast<float *>(a.workspace);
     if (r.tile) {
-        A.part_ml = A.part_o + r.tile_floats;
+        A.part_s = reinterpret_cast<float4 *>(A.part_o + r.tile_floats);
         const hipError_t e = launch_kv_prefill(A, stream);
         if (e != hipSuccess || !r.stream) return e;
     }
@@ -595,7 +619,7 @@ hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream)
     while (segments * (double)((r.tiles >> A.unit_shift) + 1) >= 0x1p31) ++A.unit_shift;
     if (r.whole) A.unit_shift = kWholeShift;
     A.splits = r.tiles > (int64_t)1 << A.unit_shift;
-    A.part_ml = A.part_o + r.stream_floats;
+    A.part_s = reinterpret_cast<float4 *>(A.part_o + r.stream_floats);
     switch (a.c.head_dim) {
     case 64: return stream_groups<64>(A, r.ct, stream);
     case 128: return stream_groups<128>(A, r.ct, stream);

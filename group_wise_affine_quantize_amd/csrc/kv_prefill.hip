@@ -39,6 +39,9 @@ typedef float float16_t __attribute__((ext_vector_type(16)));
 // Weights are at most 2^12 where R is set, and 2^15.5 before it moves again.
 constexpr float kTop = 12.0f, kSlack = 3.5f;
 
+// What sixteen tokens of a tile are.
+constexpr float kAbsent = 0.0f, kThere = 1.0f, kFar = 2.0f;
+
 template <int D> struct Shape {
     static constexpr int W = D <= 128 ? 8 : 4;      // waves
     static constexpr int M = 32 * W;                // query columns
@@ -113,7 +116,9 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
     // keys [64 rows][D], values [D][64 tokens], fp16, chunks placed by key_of
     __shared__ uint4 sh_k[2][kTile * KC];
     __shared__ uint4 sh_v[2][D * 8];
-    __shared__ float4 sh_s[2][4];   // of each 16 tokens: key scale, log2 and reciprocal of the value scale, whether any is there
+    // of each 16 tokens: key scale, log2 and reciprocal of the value scale, and
+    // kThere, kFar (L cannot share O's reference) or kAbsent
+    __shared__ float4 sh_s[2][4];
     const KvAttnLaunch &a = A.a;
     const int tid = (int)threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -247,9 +252,10 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
         }
         if (tid < 4) {
             // all-zero keys (or none): any scale will do for scores of zero, and one
-            // keeps the factor of the scores above zero
-            const float k = !has || sk == 0.0f ? 1.0f : sk, v = !has ? 1.0f : (sv == 0.0f ? kZeroBlockScale : sv);
-            sh_s[buf][tid] = make_float4(k, fast_log2(v), 1.0f / v, has ? 1.0f : 0.0f);
+            // keeps the factor of the scores above zero; all-zero values add to L alone
+            const float k = !has || sk == 0.0f ? 1.0f : sk, v = !has ? 1.0f : sv, log = fast_log2(v);    // log2(0): -infinity
+            const float kind = !has ? kAbsent : (scale_is_far(v) ? kFar : kThere);
+            sh_s[buf][tid] = make_float4(k, log, v == 0.0f ? 0.0f : 1.0f / v, kind);
         }
     };
 
@@ -260,7 +266,8 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
         load_ids(t_begin < t_last ? t_begin + 1 : t_last);
     }
     half8_t q[KS][NP];
-    float cf = 1.0f, ref = kNegInf, l = 0.0f;
+    float cf = 1.0f, ref = kNegInf, l = 0.0f, lref = kNegInf;
+    bool apart = false;     // whether l's reference is lref, not ref
     {
         float top = 0.0f;
 #pragma unroll
@@ -319,10 +326,11 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
         }
         if (busy) {
             const float4 s0 = sh_s[buf][h], s1 = sh_s[buf][2 + h];
-            const bool masked = base < all_lo || base + kTile > all_hi || __any(s0.w * s1.w == 0.0f);
+            const bool special = __any(s0.w * s1.w != kThere);
+            const bool masked = base < all_lo || base + kTile > all_hi || special;
             if (__builtin_amdgcn_readfirstlane((int)masked)) {
                 const int lo = mine.lo - base - 16 * h, hi = mine.hi - base - 16 * h;
-                const int hi0 = s0.w == 0.0f ? -64 : hi, hi1 = s1.w == 0.0f ? -64 : hi;
+                const int hi0 = s0.w == kAbsent ? -64 : hi, hi1 = s1.w == kAbsent ? -64 : hi;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     S[0][i] = i < lo || i >= hi0 ? kNegInf : S[0][i];
@@ -331,6 +339,12 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
             }
             // factors above zero, so that the maximum is that of S
             const float f0 = fmaxf(cf * s0.x, 1e-37f), f1 = fmaxf(cf * s1.x, 1e-37f);
+            if (__builtin_expect(apart || (special && __any(s0.w == kFar || s1.w == kFar)), false)) {
+                if (!apart) lref = ref;
+                apart = true;
+                add_weights(16, [&](int i) { return S[0][i] * f0; }, l, lref);
+                add_weights(16, [&](int i) { return S[1][i] * f1; }, l, lref);
+            }
             float m0 = S[0][0], m1 = S[1][0];
 #pragma unroll
             for (int i = 1; i < 16; ++i) m0 = fmaxf(m0, S[0][i]), m1 = fmaxf(m1, S[1][i]);
@@ -340,7 +354,7 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
                 const float next = m > ref + kSlack ? m : ref;
                 const float alpha = next == kNegInf ? 0.0f : fast_exp2(ref - next);
                 ref = next;
-                l *= alpha;
+                if (!apart) l *= alpha;
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt) o[dt] *= alpha;
             }
@@ -354,11 +368,11 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     x[i] = fast_exp2(fmaf(S[u][i], f, add));
-                    sum += x[i];    // in fp32: tokens of all-zero values have weights far below fp16's
+                    sum += x[i];    // in fp32: weights far below fp16's count, divided by a small value scale
                 }
                 split_half<NP>(x, P[0]);
                 split_half<NP>(x + 8, P[1]);
-                l = fmaf(sum, u ? s1.z : s0.z, l);
+                if (!apart) l = fmaf(sum, u ? s1.z : s0.z, l);
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -374,20 +388,25 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
         lds_barrier();
     }
 
+    if (apart) {
+        const float top = fmaxf(lref, xor_lane<32>(lref, lane));
+        l *= exp2_below(lref, top);
+        lref = top;
+    } else lref = ref;
     const float sum = l + xor_lane<32>(l, lane);
     if (mine.row < 0) return;
     if (A.tile_splits == 1) {
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const float f = out_factor(sum, ref, lref, 16 * DT, reinterpret_cast<float *>(o));
         T *out = static_cast<T *>(a.out) + ((int64_t)mine.row * a.q_heads + mine.head) * D;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
-                const float v[4] = {o[dt][i] * inv, o[dt][i + 1] * inv, o[dt][i + 2] * inv, o[dt][i + 3] * inv};
+                const float v[4] = {o[dt][i] * f, o[dt][i + 1] * f, o[dt][i + 2] * f, o[dt][i + 3] * f};
                 store_f32x4<T>(out + 32 * dt + 2 * i + 4 * h, v);
             }
         if (a.lse && h == 0)
-            a.lse[(int64_t)mine.row * a.q_heads + mine.head] = sum > 0.0f ? (ref + fast_log2(sum)) * kLn2 : kNegInf;
+            a.lse[(int64_t)mine.row * a.q_heads + mine.head] = sum > 0.0f ? (lref + fast_log2(sum)) * kLn2 : kNegInf;
     } else {
         const int64_t at = (int64_t)blockIdx.x * M + wave * 32 + r;
         float *po = A.part_o + at * D;
@@ -397,7 +416,7 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
             for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<float4 *>(po + 32 * dt + 2 * i + 4 * h) =
                     make_float4(o[dt][i], o[dt][i + 1], o[dt][i + 2], o[dt][i + 3]);
-        if (h == 0) A.part_ml[2 * at] = ref, A.part_ml[2 * at + 1] = sum;
+        if (h == 0) A.part_s[at] = make_float4(ref, sum, lref, 0.0f);
     }
 }
 
@@ -421,23 +440,26 @@ template <int D, typename T> __global__ __launch_bounds__(256) void kv_tile_join
     auto at = [&](int p) -> int64_t {
         return ((int64_t)(blockIdx.x / heads * (uint32_t)A.tile_splits + p) * heads + head) * M + col;
     };
-    float m = kNegInf;
+    float m = kNegInf, u = kNegInf;
 #pragma unroll 8
-    for (int p = 0; p < A.tile_splits; ++p) m = fmaxf(m, A.part_ml[2 * at(p)]);
+    for (int p = 0; p < A.tile_splits; ++p) {
+        const float4 t = A.part_s[at(p)];
+        m = fmaxf(m, t.x), u = fmaxf(u, t.z);
+    }
     float l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int parts = m == kNegInf ? 0 : A.tile_splits;
 #pragma unroll 8
-    for (int p = 0; p < parts; ++p) {
-        const float f = fast_exp2(A.part_ml[2 * at(p)] - m);
+    for (int p = 0; p < A.tile_splits; ++p) {
+        const float4 t = A.part_s[at(p)];
+        const float f = exp2_below(t.x, m);
         const float4 o = *reinterpret_cast<const float4 *>(A.part_o + at(p) * D + d);
-        l = fmaf(f, A.part_ml[2 * at(p) + 1], l);
+        l = fmaf(exp2_below(t.z, u), t.y, l);
         v[0] = fmaf(f, o.x, v[0]), v[1] = fmaf(f, o.y, v[1]), v[2] = fmaf(f, o.z, v[2]), v[3] = fmaf(f, o.w, v[3]);
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    for (int e = 0; e < 4; ++e) v[e] *= inv;
+    const float f = out_factor(l, m, u, 4, v);
+    for (int e = 0; e < 4; ++e) v[e] *= f;
     store_f32x4<T>(static_cast<T *>(a.out) + ((int64_t)q.row * a.q_heads + q.head) * D + d, v);
     if (a.lse && d == 0)
-        a.lse[(int64_t)q.row * a.q_heads + q.head] = l > 0.0f ? (m + fast_log2(l)) * kLn2 : kNegInf;
+        a.lse[(int64_t)q.row * a.q_heads + q.head] = l > 0.0f ? (u + fast_log2(l)) * kLn2 : kNegInf;
 }
 
 template <int D, int FMT, typename T> hipError_t tile_go(const AttnArgs &A, hipStream_t stream)

@@ -16,11 +16,13 @@ constexpr int kTile = 64;        // tokens per tile
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kPScale = 14.0f;  // log2 of the largest weight
-// What stands for the scale of an all-zero block of values.  Any would do for
-// its zero codes; a small one keeps its tokens, however large their scores,
-// from raising M over the tokens that do add to O, and 2^80 of them still
-// count in L.
-constexpr float kZeroBlockScale = 0x1p-80f;
+// Value scales with which L can share O's reference: 2^-48 .. 2^16 (see the head
+// of kv_attention.hip).  One comparison of their bits finds zeros too.
+__device__ __forceinline__ bool scale_is_far(float s)
+{
+    constexpr uint32_t lo = (127 - 48) << 23, hi = (127 + 16) << 23;
+    return __float_as_uint(s) - lo > hi - lo;
+}
 constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -74,7 +76,7 @@ __device__ __forceinline__ float4_t mfma(half8_t a, half8_t b, float4_t c)
 struct AttnArgs {
     KvAttnLaunch a;
     float *part_o;      // [workers * 2][columns][D]
-    float *part_ml;     // [workers * 2][columns][2]
+    float4 *part_s;     // [workers * 2][columns] of R, L, U
     int workers;        // workgroups of the streaming kernel
     int group;          // query heads per key/value head
     int unit_shift;     // log2 of the tiles of a unit of work
@@ -207,6 +209,50 @@ __device__ __forceinline__ float group_sum(float v, int lane)
 {
     v += xor_lane<16>(v, lane);
     return v + xor_lane<32>(v, lane);
+}
+
+__device__ __forceinline__ float wave_max(float v, int lane)
+{
+    v = fmaxf(v, xor_lane<1>(v, lane));
+    v = fmaxf(v, xor_lane<2>(v, lane));
+    v = fmaxf(v, xor_lane<4>(v, lane));
+    v = fmaxf(v, xor_lane<8>(v, lane));
+    return group_max(v, lane);
+}
+
+// 2^(a - b), where a is at most b and -infinity stands for nothing: 0 then.
+__device__ __forceinline__ float exp2_below(float a, float b) { return a == kNegInf ? 0.0f : fast_exp2(a - b); }
+
+// Adds `count` tokens with scores z (base 2, -infinity where hidden) to l, the
+// sum of 2^z over 2^u; u moves to their maximum when that is larger.
+template <typename Score>
+__device__ __forceinline__ void add_weights(int count, Score z, float &l, float &u)
+{
+    float top = kNegInf;
+#pragma unroll
+    for (int i = 0; i < count; ++i) top = fmaxf(top, z(i));
+    const float at = top == kNegInf ? 0.0f : top;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < count; ++i) sum += fast_exp2(z(i) - at);
+    const float next = fmaxf(u, top);
+    l = fmaf(l, exp2_below(u, next), sum * (top == kNegInf ? 1.0f : fast_exp2(top - next)));
+    u = next;
+}
+
+// O / L, with O over 2^m and L over 2^u: returns O's factor, zero where no
+// token was seen.  Where the references differ, half of 2^(m - u) goes into
+// the `count` numbers o here: the whole of it can pass fp32 by itself.
+__device__ __forceinline__ float out_factor(float l, float m, float u, int count, float *o)
+{
+    float f = l > 0.0f ? 1.0f / l : 0.0f;
+    if (__any(m != u)) {
+        const float half = l > 0.0f ? fast_exp2(0.5f * (m - u)) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < count; ++i) o[i] *= half;
+        f *= half;
+    }
+    return f;
 }
 
 // The tile kernel (kv_prefill.hip).

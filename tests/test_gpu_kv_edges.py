@@ -60,3 +60,91 @@ def test_one_sequence_among_spare_rows(total, first, used):
     check(p, start, [90], table, q, out, lse, own)
     spare = torch.from_numpy(~own)
     assert (out.cpu()[spare] == 7).all() and (lse.cpu()[spare] == 7).all()
+
+
+# What the kernels see: few query columns of a head go through the streaming kernel, more through the tile kernel; a
+# table of more than 16 tiles of 64 tokens lets the first split its tokens, few workgroups the second.
+SHAPES = {"stream": (2, 4), "stream, two groups": (5, 4), "tile": (20, 4)}
+
+
+def blocks_of(seed, exponents, block, dim, fmt, wide=None):
+    """One sequence; the values of its block j lie about 2^exponents[j] (None: all zero)."""
+    n = len(exponents) * block - 3
+    wide = wide or len(exponents)
+    p = Pair(seed, wide + 2, 1, block, dim, fmt)
+    table = tables(seed + 1, 1, wide, wide + 2)
+    k, v = rows(seed + 2, n, 1, dim, "f32"), rows(seed + 3, n, 1, dim, "f32").clamp(-4, 4)
+    for j, e in enumerate(exponents):
+        v[block * j:block * (j + 1)] *= 0.0 if e is None else 2.0 ** e
+    p.append([0, n], [n], table, k, v)
+    return p, table, n
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("e", [0, 60, 75, 118, -95, None])
+def test_blocks_of_zeros_count_beside_values_of_any_size(e, dtype, split, shape):
+    """Half of the tokens are zeros: they have their share of the sum of weights, whatever the others' values."""
+    n, heads = SHAPES[shape]
+    exponents = [None, e] * (34 if split else 4)
+    p, table, length = blocks_of(50, exponents, 32, 64, "int8")
+    for q in (torch.zeros((n, heads, 64), device="cuda"), rows(51, n, heads, 64, "f32", 2.0)):
+        q = q.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+        out, lse = attend(p, [0, n], [length], table, q)
+        check(p, [0, n], [length], table, q, out, lse)
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+def test_value_scales_over_their_whole_range(fmt, split, shape):
+    """Scales from 2^-100 to 2^118 and zeros side by side, with scores in both directions."""
+    n, heads = SHAPES[shape]
+    some = [-98, 3, None, -60, 110, 0, -20, 70, -75, 30, None, 100]
+    for exponents in (some, some[::-1], [0, 0, -98, -98], [-98, None, -98, -90], [None, -98, 0, 5]):
+        exponents = exponents * (-(-70 // len(exponents)) if split else 1)
+        p, table, length = blocks_of(60, exponents, 16, 64, fmt, wide=80 if split else None)
+        for dtype, sigma in (("bf16", 1.0), ("f32", 12.0)):
+            q = rows(61, n, heads, 64, dtype, sigma)
+            out, lse = attend(p, [0, n], [length], table, q)
+            check(p, [0, n], [length], table, q, out, lse)
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_long_contexts_of_tiny_values(shape):
+    """30000 equal keys whose values have the smallest scale: the sum of weights over it passes fp32, the answer does
+    not, and the log of the sum does not depend on the values."""
+    n, heads = SHAPES[shape]
+    length, block, dim = 30000, 128, 64
+    wide = -(-length // block)
+    p = Pair(70, wide + 2, 1, block, dim, "int8")
+    table = tables(71, 1, wide, wide + 2)
+    k = rows(72, 1, 1, dim, "f32").expand(length, 1, dim).contiguous()
+    v = rows(73, length, 1, dim, "f32") * 1e-30
+    p.append([0, length], [length], table, k, v)
+    for dtype in ("bf16", "f32"):
+        q = rows(74, n, heads, dim, dtype)
+        out, lse = attend(p, [0, n], [length], table, q)
+        check(p, [0, n], [length], table, q, out, lse)
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+def test_sharp_scores_and_uneven_scales_in_every_kernel(fmt, shape):
+    """Scores of several hundred, value scales over 2^60, zero keys and zero values."""
+    n, heads = SHAPES[shape]
+    p = Pair(80, 12, 1, 16, 64, fmt)
+    table = tables(81, 1, 10, 12)
+    k, v = rows(82, 150, 1, 64, "f32", 20.0), rows(83, 150, 1, 64, "f32")
+    for j, e in enumerate((0, -40, 20, 3, -7, 0, 1, -30, 12, 0)):
+        v[16 * j:16 * j + 16] *= 2.0 ** e
+    v[48:64] = 0
+    k[96:112] = 0
+    p.append([0, 150], [150], table, k, v)
+    for dtype in ("bf16", "f32"):
+        q = rows(84, n, heads, 64, dtype, 6.0)
+        out, lse = attend(p, [0, n], [150], table, q)
+        check(p, [0, n], [150], table, q, out, lse)
+
+
