@@ -170,10 +170,11 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
                                       16 * g + 8 * (ks & 1), f[ks]);
                 else
                     for (int i = 0; i < 8; ++i) f[ks][i] = 0.0f;
-                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[ks][i]));
+                for (int i = 0; i < 8; ++i) top = larger(top, f[ks][i]);
             }
             float back;
-            const float up = row_scale(group_max(top, lane), &back);
+            top = larger(top, xor_lane<16>(top, lane));
+            const float up = row_scale(larger(top, xor_lane<32>(top, lane)), &back);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 for (int i = 0; i < 8; ++i) f[ks][i] *= up;
@@ -398,7 +399,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
                     store_f32x4<T>(out + 16 * dt + 4 * g, v);
                 }
                 if (a.lse && g == 0)
-                    a.lse[(int64_t)c.row * a.q_heads + c.head] = l > 0.0f ? (st.u + fast_log2(l)) * kLn2 : kNegInf;
+                    a.lse[(int64_t)c.row * a.q_heads + c.head] = log_sum(l, st.u);
             } else {
                 float *po = A.part_o + (slot * COLS + col) * D;
 #pragma unroll
@@ -498,7 +499,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
             for (int e = 0; e < 4; ++e) v[e] *= f;
             store_f32x4<T>(static_cast<T *>(a.out) + ((int64_t)q.row * a.q_heads + q.head) * D + d, v);
             if (a.lse && d == 0)
-                a.lse[(int64_t)q.row * a.q_heads + q.head] = l > 0.0f ? (t.z + fast_log2(l)) * kLn2 : kNegInf;
+                a.lse[(int64_t)q.row * a.q_heads + q.head] = log_sum(l, t.z);
         }
         __syncthreads();
     }

@@ -274,9 +274,9 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
         for (int ks = 0; ks < KS; ++ks) {
             float f[8];
             unpack_f32x8<T>(raw[ks], f);
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+            for (int i = 0; i < 8; ++i) top = larger(top, f[i]);
         }
-        top = fmaxf(top, xor_lane<32>(top, lane));
+        top = larger(top, xor_lane<32>(top, lane));
         float back;
         const float up = row_scale(top, &back);
 #pragma unroll
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
                 store_f32x4<T>(out + 32 * dt + 2 * i + 4 * h, v);
             }
         if (a.lse && h == 0)
-            a.lse[(int64_t)mine.row * a.q_heads + mine.head] = sum > 0.0f ? (lref + fast_log2(sum)) * kLn2 : kNegInf;
+            a.lse[(int64_t)mine.row * a.q_heads + mine.head] = log_sum(sum, lref);
     } else {
         const int64_t at = (int64_t)blockIdx.x * M + wave * 32 + r;
         float *po = A.part_o + at * D;
@@ -459,7 +459,7 @@ template <int D, typename T> __global__ __launch_bounds__(256) void kv_tile_join
     for (int e = 0; e < 4; ++e) v[e] *= f;
     store_f32x4<T>(static_cast<T *>(a.out) + ((int64_t)q.row * a.q_heads + q.head) * D + d, v);
     if (a.lse && d == 0)
-        a.lse[(int64_t)q.row * a.q_heads + q.head] = l > 0.0f ? (u + fast_log2(l)) * kLn2 : kNegInf;
+        a.lse[(int64_t)q.row * a.q_heads + q.head] = log_sum(l, u);
 }
 
 template <int D, int FMT, typename T> hipError_t tile_go(const AttnArgs &A, hipStream_t stream)

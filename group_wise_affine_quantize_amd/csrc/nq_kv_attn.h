@@ -190,12 +190,21 @@ template <> __device__ __forceinline__ void store_f32x4<bf16_bits>(bf16_bits *p,
     *reinterpret_cast<uint2 *>(p) = w;
 }
 
+// The larger magnitude, an infinity or a NaN above every number.
+__device__ __forceinline__ float larger(float top, float v)
+{
+    const uint32_t a = __float_as_uint(top), b = __float_as_uint(v) & 0x7fffffffu;
+    return __uint_as_float(a > b ? a : b);
+}
+
 // A row's power of two: f * 2^k has its largest element in [2^14, 2^15).
-// Returns 2^k; *back is 2^-k.
+// Returns 2^k; *back is 2^-k.  A row that holds an infinity or a NaN gets a
+// NaN, and with it every score that a token gives it.
 __device__ __forceinline__ float row_scale(float largest, float *back)
 {
     int e = (int)(__float_as_uint(largest) >> 23) & 255;   // biased exponent
-    e = e < 27 ? 27 : (e > 254 ? 254 : e);                 // both powers stay normal
+    if (e == 255) return *back = __builtin_nanf("");
+    e = e < 27 ? 27 : e;                                    // both powers stay normal
     *back = __uint_as_float((uint32_t)(e - 14) << 23);
     return __uint_as_float((uint32_t)(254 + 14 - e) << 23);
 }
@@ -245,15 +254,18 @@ __device__ __forceinline__ void add_weights(int count, Score z, float &l, float 
 // the `count` numbers o here: the whole of it can pass fp32 by itself.
 __device__ __forceinline__ float out_factor(float l, float m, float u, int count, float *o)
 {
-    float f = l > 0.0f ? 1.0f / l : 0.0f;
+    float f = l == 0.0f ? 0.0f : 1.0f / l;      // a NaN stays one
     if (__any(m != u)) {
-        const float half = l > 0.0f ? fast_exp2(0.5f * (m - u)) : 0.0f;
+        const float half = l == 0.0f ? 0.0f : fast_exp2(0.5f * (m - u));
 #pragma unroll
         for (int i = 0; i < count; ++i) o[i] *= half;
         f *= half;
     }
     return f;
 }
+
+// log of the sum of weights l over 2^u: -infinity for none, NaN for a NaN.
+__device__ __forceinline__ float log_sum(float l, float u) { return l == 0.0f ? kNegInf : (u + fast_log2(l)) * kLn2; }
 
 // The tile kernel (kv_prefill.hip).
 int prefill_columns(const KvAttnLaunch &a);     // query columns per workgroup

@@ -518,8 +518,9 @@ size_t nq_kv_attention_workspace_bytes(const nq_kv_cache *cache, const nq_kv_seq
  * visible: the sequence's tokens t; with causal != 0 those with t <= p, and
  * with window > 0 (causal only) those with t > p - window.  lse (null, or
  * [rows, q_heads] fp32): log of the sum of exp(scale * q . k_t).  A row that
- * sees nothing gives zeros, and lse -infinity.  softmax_scale must be finite
- * and positive.  Keys, values and sums are fp32-accurate; for bf16 queries
+ * sees nothing gives zeros, and lse -infinity; a query (one head of a row) that
+ * holds a NaN or an infinity gives NaN in both if it sees a token, and changes
+ * no other.  softmax_scale must be finite and positive.  Keys, values and sums are fp32-accurate; for bf16 queries
  * the weights of the second product keep 11 bits (fp16), for fp32 queries
  * both products take their operands with 22 bits; weights times their values'
  * scale lose bits from 2^-26 of a row's largest down and end at 2^-37 of it.  The workspace (16-byte

@@ -148,3 +148,22 @@ def test_sharp_scores_and_uneven_scales_in_every_kernel(fmt, shape):
         check(p, [0, n], [150], table, q, out, lse)
 
 
+# ---- numbers that are none
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("length", [150, 2500])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_query_that_is_no_number_gives_nan_in_both_outputs(bad, dtype, length, shape):
+    n, heads = SHAPES[shape]
+    p, table = filled(90, "fp8", 16, 64, 1, [length])
+    q = rows(91, n, heads, 64, dtype)
+    want, want_lse = attend(p, [0, n], [length], table, q)
+    q[1, 2, 13] = bad
+    got, lse = attend(p, [0, n], [length], table, q)
+    keep = torch.ones((n, heads), dtype=torch.bool)
+    keep[1, 2] = False
+    assert bits_equal(got.cpu()[keep], want.cpu()[keep]) and bits_equal(lse.cpu()[keep], want_lse.cpu()[keep])
+    assert got[1, 2].isnan().all() and lse[1, 2].isnan()
+    # a row that sees nothing has no answer to spoil
+    out, lse = attend(p, [0, n], [0], table, q)
+    assert not out.any() and torch.isneginf(lse).all()
