@@ -288,7 +288,9 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
                 if (__builtin_expect(apart || far, false)) {
                     if (!apart) st.u = st.m;
                     apart = true;
-                    add_weights(16, [&](int i) { return x[i] - lsv; }, st.l, st.u);
+                    // a scale that is no number has made x NaN where tokens are seen
+                    const float shift = lsv == lsv ? lsv : 0.0f;
+                    add_weights(16, [&](int i) { return x[i] - shift; }, st.l, st.u);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] = zeros ? kNegInf : x[i];
                 }

@@ -8,7 +8,8 @@
 // the smallest j that holds a, and its older codes are rounded to the new
 // scale.  Growing by powers of two bounds an old code's total error by one
 // step of the last scale (each rounding adds half a step, and the steps at
-// least double), where growing to a / qmax each time would let it drift.
+// least double), where growing to a / qmax each time would let it drift.  An
+// a that is no finite number makes s a NaN, and with it all of the block.
 //
 // Both are bound by memory: a token of a head is read and written once (by the
 // write its row is read twice, for the scale and for the codes, the second
@@ -33,15 +34,15 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ float block_max(float a, float *shared)
 {
     const int lane = (int)(threadIdx.x & 63u);
-    a = fmaxf(a, xor_lane<1>(a, lane));
-    a = fmaxf(a, xor_lane<2>(a, lane));
-    a = fmaxf(a, xor_lane<4>(a, lane));
-    a = fmaxf(a, xor_lane<8>(a, lane));
-    a = fmaxf(a, xor_lane<16>(a, lane));
-    a = fmaxf(a, xor_lane<32>(a, lane));
+    a = larger(a, xor_lane<1>(a, lane));
+    a = larger(a, xor_lane<2>(a, lane));
+    a = larger(a, xor_lane<4>(a, lane));
+    a = larger(a, xor_lane<8>(a, lane));
+    a = larger(a, xor_lane<16>(a, lane));
+    a = larger(a, xor_lane<32>(a, lane));
     if (lane == 0) shared[threadIdx.x >> 6] = a;
     __syncthreads();
-    return fmaxf(fmaxf(shared[0], shared[1]), fmaxf(shared[2], shared[3]));
+    return larger(larger(shared[0], shared[1]), larger(shared[2], shared[3]));
 }
 
 // 2^-j and the grown scale for a held block; *shrink multiplies older codes.
@@ -153,14 +154,15 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendLaunch a)
         const int t = i / (D / 8), d = (i % (D / 8)) * 8;
         const T *p = x + (int64_t)(it.lo + t) * ld + d;
         const float4 v = load4<T>(p), w = load4<T>(p + 4);
-        m = fmaxf(m, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-        m = fmaxf(m, fmaxf(fmaxf(fabsf(w.x), fabsf(w.y)), fmaxf(fabsf(w.z), fabsf(w.w))));
+        const float all[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
+        for (int e = 0; e < 8; ++e) m = larger(m, all[e]);
     }
     const float held = it.lo > 0 ? *scale : 0.0f;   // read before thread 0 stores it below
     m = block_max(m, red);
     const float fresh = m > 0.0f ? fmaxf(m / KvFmt<FMT>::qmax, kKvMinScale) : 0.0f;
     float shrink = 1.0f;
-    const float s = it.lo > 0 ? grown_scale<FMT>(held, m, fresh, &shrink) : fresh;
+    float s = it.lo > 0 ? grown_scale<FMT>(held, m, fresh, &shrink) : fresh;     // a held NaN stays
+    if (!(m < __builtin_inff())) s = __builtin_nanf(""), shrink = 1.0f;
     const float inv = s > 0.0f ? 1.0f / s : 0.0f;
     if (tid == 0) *scale = s;
 

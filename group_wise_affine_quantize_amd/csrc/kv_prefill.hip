@@ -39,8 +39,8 @@ typedef float float16_t __attribute__((ext_vector_type(16)));
 // Weights are at most 2^12 where R is set, and 2^15.5 before it moves again.
 constexpr float kTop = 12.0f, kSlack = 3.5f;
 
-// What sixteen tokens of a tile are.
-constexpr float kAbsent = 0.0f, kThere = 1.0f, kFar = 2.0f;
+// What sixteen tokens of a tile are; kLost: a scale is no number.
+constexpr float kAbsent = 0.0f, kThere = 1.0f, kFar = 2.0f, kLost = 3.0f;
 
 template <int D> struct Shape {
     static constexpr int W = D <= 128 ? 8 : 4;      // waves
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
     __shared__ uint4 sh_k[2][kTile * KC];
     __shared__ uint4 sh_v[2][D * 8];
     // of each 16 tokens: key scale, log2 and reciprocal of the value scale, and
-    // kThere, kFar (L cannot share O's reference) or kAbsent
+    // kThere, kFar (L cannot share O's reference), kLost or kAbsent
     __shared__ float4 sh_s[2][4];
     const KvAttnLaunch &a = A.a;
     const int tid = (int)threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
@@ -253,8 +253,9 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
         if (tid < 4) {
             // all-zero keys (or none): any scale will do for scores of zero, and one
             // keeps the factor of the scores above zero; all-zero values add to L alone
-            const float k = !has || sk == 0.0f ? 1.0f : sk, v = !has ? 1.0f : sv, log = fast_log2(v);    // log2(0): -infinity
-            const float kind = !has ? kAbsent : (scale_is_far(v) ? kFar : kThere);
+            const bool lost = has && !(sk - sk + (sv - sv) == 0.0f);
+            const float k = !has || lost || sk == 0.0f ? 1.0f : sk, v = !has || lost ? 1.0f : sv, log = fast_log2(v);    // log2(0): -infinity
+            const float kind = !has ? kAbsent : lost ? kLost : scale_is_far(v) ? kFar : kThere;
             sh_s[buf][tid] = make_float4(k, log, v == 0.0f ? 0.0f : 1.0f / v, kind);
         }
     };
@@ -335,6 +336,13 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
                 for (int i = 0; i < 16; ++i) {
                     S[0][i] = i < lo || i >= hi0 ? kNegInf : S[0][i];
                     S[1][i] = 32 + i < lo || 32 + i >= hi1 ? kNegInf : S[1][i];
+                }
+            }
+            if (special && __any(s0.w == kLost || s1.w == kLost)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (s0.w == kLost && S[0][i] != kNegInf) S[0][i] = __builtin_nanf("");
+                    if (s1.w == kLost && S[1][i] != kNegInf) S[1][i] = __builtin_nanf("");
                 }
             }
             // factors above zero, so that the maximum is that of S

@@ -190,13 +190,6 @@ template <> __device__ __forceinline__ void store_f32x4<bf16_bits>(bf16_bits *p,
     *reinterpret_cast<uint2 *>(p) = w;
 }
 
-// The larger magnitude, an infinity or a NaN above every number.
-__device__ __forceinline__ float larger(float top, float v)
-{
-    const uint32_t a = __float_as_uint(top), b = __float_as_uint(v) & 0x7fffffffu;
-    return __uint_as_float(a > b ? a : b);
-}
-
 // A row's power of two: f * 2^k has its largest element in [2^14, 2^15).
 // Returns 2^k; *back is 2^-k.  A row that holds an infinity or a NaN gets a
 // NaN, and with it every score that a token gives it.

@@ -77,6 +77,13 @@ template <int FMT> __device__ __forceinline__ uint8_t kv_code(float v)
     return (uint8_t)(kv_codes4<FMT>(t) & 255u);
 }
 
+// The larger magnitude, an infinity or a NaN above every number.
+__device__ __forceinline__ float larger(float top, float v)
+{
+    const uint32_t a = __float_as_uint(top), b = __float_as_uint(v) & 0x7fffffffu;
+    return __uint_as_float(a > b ? a : b);
+}
+
 // One sequence of a call, every value clamped: rows r0 .. r0 + n of the call
 // are its tokens first .. len (first may be negative: such rows have no
 // token).

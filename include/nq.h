@@ -493,8 +493,11 @@ typedef struct {
  *     over 2^20, it takes a new block's scale and the earlier codes become zero;
  *   - code = the code nearest to fp32(x * fp32(1 / scale)), ties to even,
  *     clamped to +-qmax (zero codes for scale = 0).
- * All in fp32, bit-exact.  Non-finite values are outside the contract.  Rows
- * of two sequences must not fall into the same block. */
+ * All in fp32, bit-exact.  A row with a NaN or an infinity makes the scale of
+ * its head's block a NaN, and it stays one until the block's first token is written
+ * again: all of the block's keys (or values) of that head then read as NaN, and
+ * attention gives NaN to the rows that see one of them.  Rows of two sequences
+ * must not fall into the same block. */
 nq_status nq_kv_append(const nq_kv_cache *cache, const nq_kv_seqs *seqs, const void *k, int64_t ldk,
                        const void *v, int64_t ldv, nq_dtype x_dt, hipStream_t stream);
 
@@ -518,13 +521,15 @@ size_t nq_kv_attention_workspace_bytes(const nq_kv_cache *cache, const nq_kv_seq
  * visible: the sequence's tokens t; with causal != 0 those with t <= p, and
  * with window > 0 (causal only) those with t > p - window.  lse (null, or
  * [rows, q_heads] fp32): log of the sum of exp(scale * q . k_t).  A row that
- * sees nothing gives zeros, and lse -infinity; a query (one head of a row) that
- * holds a NaN or an infinity gives NaN in both if it sees a token, and changes
- * no other.  softmax_scale must be finite and positive.  Keys, values and sums are fp32-accurate; for bf16 queries
- * the weights of the second product keep 11 bits (fp16), for fp32 queries
- * both products take their operands with 22 bits; weights times their values'
- * scale lose bits from 2^-26 of a row's largest down and end at 2^-37 of it.  The workspace (16-byte
- * aligned) is scratch of one call at a time. */
+ * sees nothing gives zeros, and lse -infinity.  A query (one head of a row)
+ * that sees a token and holds a NaN or an infinity, or that sees a token of a
+ * block whose scale is no number, gives NaN in both, and changes no other.
+ * softmax_scale must be finite and positive.  Keys, values and sums are
+ * fp32-accurate; for bf16 queries the weights of the second product keep 11
+ * bits (fp16), for fp32 queries both products take their operands with 22
+ * bits; weights times their values' scale lose bits from 2^-26 of a row's
+ * largest down and end at 2^-37 of it.  The workspace (16-byte aligned) is
+ * scratch of one call at a time. */
 nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, const void *q, nq_dtype x_dt,
                           int64_t ldq, int32_t q_heads, float softmax_scale, int32_t causal, int64_t window,
                           void *out, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream);

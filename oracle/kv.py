@@ -73,9 +73,13 @@ def _write_block(cache, part, i, h, lo, x):
     qmax = F(QMAX[cache.fmt])
     scales = cache.scales(part)
     a = F(np.abs(x).max())
+    codes = cache.slab(part, i, h)
+    if not np.isfinite(a):      # from here on the block holds no numbers; codes do not matter
+        scales[i, h] = np.nan
+        codes[lo:lo + len(x)] = encode(np.zeros_like(x), cache.fmt)
+        return
     fresh = max(F(a / qmax), MIN_SCALE) if a > 0 else F(0)
     s = fresh
-    codes = cache.slab(part, i, h)
     if lo > 0:
         s = scales[i, h]
         reach = F(s * qmax)

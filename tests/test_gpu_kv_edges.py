@@ -167,3 +167,68 @@ def test_a_query_that_is_no_number_gives_nan_in_both_outputs(bad, dtype, length,
     # a row that sees nothing has no answer to spoil
     out, lse = attend(p, [0, n], [0], table, q)
     assert not out.any() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("fmt,dtype", [("int8", "bf16"), ("fp8", "f32")])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_number_that_is_none_makes_its_block_nan(bad, fmt, dtype):
+    """The head's block reads as NaN from then on, also for tokens written before and after, until its first token is
+    written again; other blocks, heads and the other part are as they would be."""
+    block, dim, heads = 16, 64, 2
+    p, clean = Pair(95, 6, heads, block, dim, fmt), Pair(95, 6, heads, block, dim, fmt)
+    table = tables(96, 1, 4, 6)
+    calls = [(20, 20), (5, 25), (1, 26), (30, 56)]      # rows, length after them
+    for i, (n, length) in enumerate(calls):
+        k, v = rows(97 + i, n, heads, dim, dtype), rows(107 + i, n, heads, dim, dtype)
+        clean.append([0, n], [length], table, k, v)
+        if i == 1:
+            k[2, 1, 7] = bad        # token 22, block 1
+        if i == 3:
+            v[20, 0, 63] = bad      # token 46, block 2
+        p.append([0, n], [length], table, k, v)
+    for name, block_no, head in (("k", 1, 1), ("v", 2, 0)):
+        got, want = getattr(p.dev, name + "_scales").cpu(), getattr(clean.dev, name + "_scales").cpu().clone()
+        assert got[table[0, block_no], head].isnan()
+        want[table[0, block_no], head] = float("nan")
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(), want.nan_to_num())
+    seqs = B.KVSequences(i32([0, 56]), i32([56]), i32(table), 56)
+    for out in (torch.float32, torch.bfloat16):
+        got, want = B.nq_kv_read(p.dev, seqs, out_dtype=out), B.nq_kv_read(clean.dev, seqs, out_dtype=out)
+        for g, w, lo, hi, head in ((got[0], want[0], 16, 32, 1), (got[1], want[1], 32, 48, 0)):
+            assert g[lo:hi, head].isnan().all()
+            g[lo:hi, head] = w[lo:hi, head]
+            assert bits_equal(g, w)
+    host = K.read(p.host, [0, 56], [56], table)
+    got = B.nq_kv_read(p.dev, seqs, out_dtype=torch.float32)
+    assert all(np.array_equal(g.cpu().numpy(), w, equal_nan=True) for g, w in zip(got, host))
+    # written anew from its first token, a block is whole again: tokens 32 on, of block 2
+    k, v = rows(120, 24, heads, dim, dtype), rows(121, 24, heads, dim, dtype)
+    p.append([0, 24], [56], table, k, v)
+    assert torch.isfinite(p.dev.v_scales.cpu()[table[0]]).all()
+
+
+@pytest.mark.parametrize("part", ["k", "v"])
+@pytest.mark.parametrize("fmt,dtype", [("int8", "bf16"), ("fp8", "f32")])
+@pytest.mark.parametrize("n,length", [(3, 150), (150, 150), (5, 1500), (90, 1500)])
+def test_a_block_of_nan_reaches_the_rows_that_see_it_and_no_other(n, length, fmt, dtype, part):
+    """Masked rows and the other head keep their bits; rows that see a token of the block get NaN."""
+    block, dim, kv, heads = 16, 64, 2, 4
+    p, table = filled(130, fmt, block, dim, kv, [length])
+    q = rows(131, n, heads, dim, dtype)
+    want, want_lse = attend(p, [0, n], [length], table, q)
+    near = attend(p, [0, n], [length], table, q, window=9)
+    hurt = (length - n // 2) // block       # the block of a token that some of the rows may not see
+    getattr(p.dev, part + "_scales")[int(table[0, hurt]), 1] = float("nan")
+    got, lse = attend(p, [0, n], [length], table, q)
+    pos = np.arange(length - n, length)
+    sees = torch.from_numpy(pos >= hurt * block)
+    for r in range(n):
+        assert bits_equal(got[r, :2], want[r, :2]) and bits_equal(lse[r, :2], want_lse[r, :2])
+        if sees[r]:
+            assert got[r, 2:].isnan().all() and lse[r, 2:].isnan().all()
+        else:
+            assert bits_equal(got[r, 2:], want[r, 2:]) and bits_equal(lse[r, 2:], want_lse[r, 2:])
+    got, lse = attend(p, [0, n], [length], table, q, window=9)
+    sees = torch.from_numpy((pos >= hurt * block) & (pos - 8 < (hurt + 1) * block)).cuda()
+    assert torch.equal(got[:, 2:].isnan().all(-1).all(-1), sees) and torch.equal(lse[:, 2:].isnan().all(-1), sees)
+    assert bits_equal(got[~sees], near[0][~sees]) and bits_equal(got[:, :2], near[0][:, :2])

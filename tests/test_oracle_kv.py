@@ -94,3 +94,19 @@ def test_a_nan_key_adds_nothing_to_its_group(best, first):
     keys = np.array([0.9, 0.1, np.nan, 0.2, 0.7, 0.6, 0.0, 0.0])
     ids, _ = M.route(np.full((1, 8), -1000.0), "sigmoid", 1, bias=keys, groups=2, top_groups=1, group_best=best)
     assert ids.tolist() == [[4 * first]]
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_a_number_that_is_none_takes_its_block_along(bad):
+    c = _cache("fp8", heads=2)
+    table = np.array([[2, 0]], np.int32)
+    x = np.random.default_rng(4).standard_normal((20, 2, 64)).astype(np.float32)
+    K.append(c, [0, 5], [5], table, x[:5], x[:5])
+    y = x[5:9].copy()
+    y[1, 1, 3] = bad
+    K.append(c, [0, 4], [9], table, x[5:9], y)
+    K.append(c, [0, 11], [20], table, x[9:], x[9:])
+    k, v = K.read(c, [0, 20], [20], table)
+    assert np.isfinite(k).all() and np.isnan(v[:16, 1]).all() and np.isfinite(v[:16, 0]).all() and np.isfinite(v[16:]).all()
+    K.append(c, [0, 20], [20], table, x, x)
+    assert np.isfinite(K.read(c, [0, 20], [20], table)[1]).all()
