@@ -630,7 +630,18 @@ class _MoERouterStruct(ctypes.Structure):
                 ("top_k", _I32), ("renormalise", _I32), ("scale", ctypes.c_float)]
 
 
-class KVCache:
+class _Described:
+    """What a struct that calls pass describes.  Shapes are checked against the
+    attributes and kernels go by the struct, so neither changes once it is made:
+    a new description takes a new object."""
+
+    def __setattr__(self, name, value):
+        if "_ref" in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} cannot be set; make a new {type(self).__name__}")
+        object.__setattr__(self, name, value)
+
+
+class KVCache(_Described):
     """A paged key/value cache in 8 bits (nq_kv_cache): k_codes [blocks,
     kv_heads, block_tokens, head_dim] and v_codes [blocks, kv_heads, head_dim,
     block_tokens] uint8, k_scales and v_scales [blocks, kv_heads] float32;
@@ -674,12 +685,13 @@ class KVCache:
         self._ref = ctypes.byref(self._struct)
 
 
-class KVSequences:
+class KVSequences(_Described):
     """The sequences of a call (nq_kv_seqs): row_start [batch + 1], lengths
     [batch] and block_table [batch, max_blocks] int32 on the GPU, rows the
     number of rows of the call's arrays.  Row i of sequence b is token
     lengths[b] - row_start[b + 1] + i.  The tensors may be updated in place
-    between calls."""
+    between calls; other tensors, or another number of rows, take a new
+    object."""
 
     def __init__(self, row_start, lengths, block_table, rows):
         torch = _torch()
@@ -800,7 +812,7 @@ def nq_kv_attention(cache, seqs, q, scale=None, causal=True, window=0, out=None,
 
 
 # ---------------------------------------------------------------- expert routing
-class MoERouter:
+class MoERouter(_Described):
     """How tokens choose experts (nq_moe_router): the top_k largest of score
     "softmax" or "sigmoid" (plus a bias), from the top_groups best of `groups`
     groups of neighbouring experts -- a group's score is its largest key

@@ -177,3 +177,11 @@ print(t.attend(lib, c, s, ldq=128 * 64, heads=128), flush=True)
     done = subprocess.run([sys.executable, "-c", program, here, os.path.dirname(here)], env=env, capture_output=True,
                           text=True, timeout=60)
     assert done.stdout.split() == ["8"], done.stderr[-500:]
+
+
+def test_a_router_that_calls_go_by_does_not_change():
+    router = B.MoERouter(32, 4, renormalise=True)
+    for name in ("top_k", "experts", "scale", "score", "groups", "_struct"):
+        with pytest.raises(AttributeError):
+            setattr(router, name, 8)
+    assert router.top_k == router._struct.top_k == 4

@@ -232,3 +232,17 @@ def test_a_block_of_nan_reaches_the_rows_that_see_it_and_no_other(n, length, fmt
     sees = torch.from_numpy((pos >= hurt * block) & (pos - 8 < (hurt + 1) * block)).cuda()
     assert torch.equal(got[:, 2:].isnan().all(-1).all(-1), sees) and torch.equal(lse[:, 2:].isnan().all(-1), sees)
     assert bits_equal(got[~sees], near[0][~sees]) and bits_equal(got[:, :2], near[0][:, :2])
+
+
+def test_descriptions_that_calls_go_by_do_not_change():
+    """Shapes are checked against a description's attributes, kernels go by its struct: were the two apart, rows past
+    a tensor's end would be read and written."""
+    cache = B.KVCache(4, 1, 16, 64, "int8")
+    seqs = B.KVSequences(i32([0, 2]), i32([2]), i32([[1, 2]]), 2)
+    for one, names in ((cache, ("k_codes", "v_scales", "blocks", "kv_heads", "format", "block_tokens")),
+                       (seqs, ("rows", "lengths", "row_start", "block_table", "batch"))):
+        for name in names:
+            with pytest.raises(AttributeError):
+                setattr(one, name, getattr(one, name))
+    seqs.lengths.add_(1)    # in place: the same tensor
+    assert seqs.lengths.item() == 3
