@@ -515,7 +515,8 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 // only known on the device: both are launched, unless there is one sequence or
 // there are at most two rows per sequence (then all of them are streamed).
 // One sequence goes by the call's rows, of which it may own any number: the
-// kernel that is launched takes it whatever it owns.
+// kernel that is launched takes it whatever it owns.  More sequences than a
+// launch of the tile kernel has workgroups for are all streamed too.
 constexpr int kFew = 64;
 constexpr int kWholeShift = 4, kWholeTiles = 1 << kWholeShift;
 // Tiles per part: a window of 2048 in fp32, 3 x 8 column tiles: 27 + 7 us at 5, 31 + 6 at 8.
@@ -542,6 +543,8 @@ Route route_of(const KvAttnLaunch &a)
     else r.stream = r.tile = true, r.few = kFew;
     const int64_t per = std::max<int64_t>(1, (a.s.rows + a.s.batch - 1) / a.s.batch) * group;
     r.ct = per <= 16 ? 1 : per <= 32 ? 2 : 4;
+    const int64_t M = prefill_columns(a), bound = std::min<int64_t>(cols / M + a.s.batch, cols);
+    if (r.tile && bound * a.c.kv_heads > most_workgroups(512)) r.stream = true, r.tile = false, r.few = INT32_MAX;
     // Contexts that can have no more than 16 tiles are one unit: four tiles for
     // each wave, which take less than a second launch, and no parts.
     r.tiles = ((a.s.max_blocks << a.c.block_shift) >> 6) + 1;
@@ -550,8 +553,6 @@ Route route_of(const KvAttnLaunch &a)
     r.stream_floats = r.stream_cols * D;
     r.tile_bound = 0, r.tile_splits = 1, r.tile_cols = 0, r.tile_floats = 0;
     if (r.tile) {
-        const int64_t M = prefill_columns(a);
-        const int64_t bound = std::min<int64_t>(cols / M + a.s.batch, cols);
         r.tile_bound = (unsigned)bound;
         // too few workgroups for 256 compute units: tokens are split, at least
         // kPartTiles tiles that a column tile can see to a part

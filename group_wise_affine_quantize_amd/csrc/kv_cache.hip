@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendLaunch a)
 {
     __shared__ float red[4];
     Item it;
-    if (!find_item(a.s, a.c, blockIdx.x, &it) || it.id < 0) return;
+    if (!find_item(a.s, a.c, a.item0 + blockIdx.x, &it) || it.id < 0) return;
     const int sh = a.c.block_shift, tid = (int)threadIdx.x;
     const int64_t head = blockIdx.y, slab = it.id * a.c.kv_heads + head;
     const bool is_v = blockIdx.z != 0;
@@ -219,7 +219,7 @@ template <int D, int FMT, typename T>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadLaunch a)
 {
     Item it;
-    if (!find_item(a.s, a.c, blockIdx.x, &it)) return;
+    if (!find_item(a.s, a.c, a.item0 + blockIdx.x, &it)) return;
     const int sh = a.c.block_shift, tid = (int)threadIdx.x;
     const int64_t head = blockIdx.y, ld = (int64_t)a.c.kv_heads * D;
     const bool is_v = blockIdx.z != 0, absent = it.id < 0;
@@ -269,6 +269,18 @@ int64_t max_items(const KvSeqs &s, const KvCache &c)
     return s.rows < some ? s.rows : some;
 }
 
+// Calls go(item0, grid) for all blocks, as many at a time as a launch may have.
+template <typename Go> hipError_t by_items(const KvSeqs &s, const KvCache &c, Go go)
+{
+    const int64_t items = max_items(s, c), most = most_workgroups(kThreads);
+    for (int64_t at = 0; at < items; at += most) {
+        go(at, dim3((unsigned)(items - at < most ? items - at : most), (unsigned)c.kv_heads, 2));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 template <typename Go> void by_head_dim(int head_dim, Go go)
 {
     switch (head_dim) {
@@ -281,36 +293,40 @@ template <typename Go> void by_head_dim(int head_dim, Go go)
 
 }  // namespace
 
-hipError_t launch_kv_append(const KvAppendLaunch &a, hipStream_t stream)
+hipError_t launch_kv_append(const KvAppendLaunch &call, hipStream_t stream)
 {
-    const dim3 grid((unsigned)max_items(a.s, a.c), (unsigned)a.c.kv_heads, 2);
-    by_head_dim(a.c.head_dim, [&](auto dim) {
-        constexpr int D = decltype(dim)::value;
-        if (a.format == KV_INT8) {
-            if (a.x_dt == 0) kv_append_kernel<D, KV_INT8, float><<<grid, kThreads, 0, stream>>>(a);
-            else kv_append_kernel<D, KV_INT8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
-        } else {
-            if (a.x_dt == 0) kv_append_kernel<D, KV_FP8, float><<<grid, kThreads, 0, stream>>>(a);
-            else kv_append_kernel<D, KV_FP8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
-        }
+    KvAppendLaunch a = call;
+    return by_items(a.s, a.c, [&](int64_t item0, dim3 grid) {
+        a.item0 = item0;
+        by_head_dim(a.c.head_dim, [&](auto dim) {
+            constexpr int D = decltype(dim)::value;
+            if (a.format == KV_INT8) {
+                if (a.x_dt == 0) kv_append_kernel<D, KV_INT8, float><<<grid, kThreads, 0, stream>>>(a);
+                else kv_append_kernel<D, KV_INT8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
+            } else {
+                if (a.x_dt == 0) kv_append_kernel<D, KV_FP8, float><<<grid, kThreads, 0, stream>>>(a);
+                else kv_append_kernel<D, KV_FP8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
+            }
+        });
     });
-    return hipGetLastError();
 }
 
-hipError_t launch_kv_read(const KvReadLaunch &a, hipStream_t stream)
+hipError_t launch_kv_read(const KvReadLaunch &call, hipStream_t stream)
 {
-    const dim3 grid((unsigned)max_items(a.s, a.c), (unsigned)a.c.kv_heads, 2);
-    by_head_dim(a.c.head_dim, [&](auto dim) {
-        constexpr int D = decltype(dim)::value;
-        if (a.format == KV_INT8) {
-            if (a.out_dt == 0) kv_read_kernel<D, KV_INT8, float><<<grid, kThreads, 0, stream>>>(a);
-            else kv_read_kernel<D, KV_INT8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
-        } else {
-            if (a.out_dt == 0) kv_read_kernel<D, KV_FP8, float><<<grid, kThreads, 0, stream>>>(a);
-            else kv_read_kernel<D, KV_FP8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
-        }
+    KvReadLaunch a = call;
+    return by_items(a.s, a.c, [&](int64_t item0, dim3 grid) {
+        a.item0 = item0;
+        by_head_dim(a.c.head_dim, [&](auto dim) {
+            constexpr int D = decltype(dim)::value;
+            if (a.format == KV_INT8) {
+                if (a.out_dt == 0) kv_read_kernel<D, KV_INT8, float><<<grid, kThreads, 0, stream>>>(a);
+                else kv_read_kernel<D, KV_INT8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
+            } else {
+                if (a.out_dt == 0) kv_read_kernel<D, KV_FP8, float><<<grid, kThreads, 0, stream>>>(a);
+                else kv_read_kernel<D, KV_FP8, bf16_bits><<<grid, kThreads, 0, stream>>>(a);
+            }
+        });
     });
-    return hipGetLastError();
 }
 
 }  // namespace nqk

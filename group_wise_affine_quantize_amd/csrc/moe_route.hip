@@ -499,7 +499,20 @@ template <typename T, int LPT, int EPL> void go(const MoeGradLaunch &a, int wide
     moe_grad_kernel<T, LPT, EPL><<<grid_of(a, LPT), kThreads, 0, s>>>(a, wide);
 }
 
-template <typename T, typename L> hipError_t by_experts(const L &a, hipStream_t s)
+// The launch's tokens from `t` on.
+template <typename T> MoeRouteLaunch from_token(MoeRouteLaunch a, int64_t t)
+{
+    a.logits = static_cast<const T *>(a.logits) + t * a.ldl, a.ids += t * a.r.top_k, a.weights += t * a.r.top_k;
+    return a;
+}
+template <typename T> MoeGradLaunch from_token(MoeGradLaunch a, int64_t t)
+{
+    a.logits = static_cast<const T *>(a.logits) + t * a.ldl, a.ids += t * a.r.top_k, a.dweights += t * a.r.top_k;
+    a.dlogits = static_cast<T *>(a.dlogits) + t * a.r.experts;
+    return a;
+}
+
+template <typename T, typename L> void by_experts(const L &a, hipStream_t s)
 {
     const int wide = wide_rows(a.logits, a.ldl, (int)sizeof(T));
     const int e = a.r.experts;
@@ -508,19 +521,32 @@ template <typename T, typename L> hipError_t by_experts(const L &a, hipStream_t 
     else if (e <= 256) go<T, 16, 16>(a, wide, s);
     else if (e <= 512) go<T, 64, 8>(a, wide, s);
     else go<T, 64, 16>(a, wide, s);
-    return hipGetLastError();
+}
+
+// All tokens, as many at a time as a launch may have with the fewest tokens to a workgroup.
+template <typename T, typename L> hipError_t by_tokens(const L &call, hipStream_t s)
+{
+    constexpr int64_t most = most_workgroups(kThreads) * (kThreads / 64);
+    for (int64_t at = 0; at < call.tokens; at += most) {
+        L a = from_token<T>(call, at);
+        a.tokens = call.tokens - at < most ? call.tokens - at : most;
+        by_experts<T>(a, s);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
 
 hipError_t launch_moe_route(const MoeRouteLaunch &a, hipStream_t s)
 {
-    return a.x_dt == 0 ? by_experts<float>(a, s) : by_experts<bf16_bits>(a, s);
+    return a.x_dt == 0 ? by_tokens<float>(a, s) : by_tokens<bf16_bits>(a, s);
 }
 
 hipError_t launch_moe_route_grad(const MoeGradLaunch &a, hipStream_t s)
 {
-    return a.x_dt == 0 ? by_experts<float>(a, s) : by_experts<bf16_bits>(a, s);
+    return a.x_dt == 0 ? by_tokens<float>(a, s) : by_tokens<bf16_bits>(a, s);
 }
 
 }  // namespace nqk

@@ -9,6 +9,10 @@
 
 namespace nqk {
 
+// Workgroups that one launch may have along x: the runtime counts its threads
+// in 32 bits, and takes more of them modulo 2^32 without an error.
+constexpr int64_t most_workgroups(int threads) { return (((int64_t)1 << 32) - 1) / threads; }
+
 enum { KV_INT8 = 1, KV_FP8 = 2 };
 
 // The cache's arrays (layouts in include/nq.h).
@@ -33,6 +37,7 @@ struct KvAppendLaunch {
     KvSeqs s;
     const void *k, *v;
     int64_t ldk, ldv;
+    int64_t item0 = 0;      // first block of the launch (see max_items)
     int x_dt, format;
 };
 hipError_t launch_kv_append(const KvAppendLaunch &a, hipStream_t stream);
@@ -41,6 +46,7 @@ struct KvReadLaunch {
     KvCache c;
     KvSeqs s;
     void *k, *v;
+    int64_t item0 = 0;
     int out_dt, format;
 };
 hipError_t launch_kv_read(const KvReadLaunch &a, hipStream_t stream);

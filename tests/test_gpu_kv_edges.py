@@ -246,3 +246,39 @@ def test_descriptions_that_calls_go_by_do_not_change():
                 setattr(one, name, getattr(one, name))
     seqs.lengths.add_(1)    # in place: the same tensor
     assert seqs.lengths.item() == 3
+
+
+def test_more_blocks_than_one_launch_has_threads_for():
+    """Two sequences of 2^27 rows and some in blocks of 16, nearly all of which do not exist: the last ones are written
+    and read as those of a short sequence are, the others read as zeros."""
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB of memory")
+    half, block, dim, tail = 1 << 27, 16, 64, 55
+    n = 2 * half + 23
+    wide = -(-(half + 23) // block)
+    table = torch.full((2, wide), -1, dtype=torch.int32, device="cuda")
+    table[1, -4:] = torch.tensor([3, 0, 2, 1], dtype=torch.int32)
+    k = torch.empty((n, 1, dim), dtype=torch.bfloat16, device="cuda")
+    first = n - tail        # the first token of the table's last four blocks
+    assert first - half == (wide - 4) * block
+    k[first:] = rows(140, tail, 1, dim, "bf16")
+    cache, small = B.KVCache(4, 1, block, dim, "int8"), B.KVCache(4, 1, block, dim, "int8")
+    for c in (cache, small):
+        for t in (c.k_codes, c.v_codes, c.k_scales, c.v_scales):
+            t.zero_()
+    seqs = B.KVSequences(i32([0, half, n]), i32([half, half + 23]), table, n)
+    B.nq_kv_append(cache, seqs, k, k)
+    short = B.KVSequences(i32([0, tail]), i32([tail]), i32([[3, 0, 2, 1]]), tail)
+    x = k[first:].contiguous()
+    B.nq_kv_append(small, short, x, x)
+    for a, b in ((cache.k_codes, small.k_codes), (cache.v_codes, small.v_codes), (cache.k_scales, small.k_scales),
+                 (cache.v_scales, small.v_scales)):
+        assert torch.equal(a, b)
+    k.fill_(3.0)
+    v = torch.full_like(k, 3.0)
+    B.nq_kv_read(cache, seqs, k=k, v=v)
+    want = B.nq_kv_read(small, short)
+    for got, w in zip((k, v), want):
+        assert torch.equal(got[first:], w) and not got[:first].any()
+    del k, v
+    torch.cuda.empty_cache()

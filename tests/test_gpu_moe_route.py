@@ -220,3 +220,22 @@ def test_the_second_best_of_a_group_is_a_number():
     bias[:4], bias[30:34] = keys[:4], keys[4:8]
     ids, _ = B.nq_moe_route(B.MoERouter(480, 2, score="sigmoid", groups=16, top_groups=1, group_best=2), x, bias=bias)
     assert ids.tolist() == [[30, 31]]
+
+
+def test_more_tokens_than_one_launch_has_threads_for():
+    """2^28 tokens and some: at 16 lanes to a token their threads pass 32 bits."""
+    tokens = (1 << 28) + 40
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB of memory")
+    x = (torch.arange(tokens, device="cuda") % 7).to(torch.bfloat16)[:, None]
+    router = B.MoERouter(1, 1, score="sigmoid")
+    ids = torch.full((tokens, 1), 9, dtype=torch.int32, device="cuda")
+    w = torch.full((tokens, 1), 9.0, device="cuda")
+    B.nq_moe_route(router, x, ids=ids, weights=w)
+    assert not ids.any()
+    want, at = B.nq_moe_route(router, x[:7])[1], torch.arange(tokens, device="cuda") % 7
+    assert torch.equal(w[:, 0], want[:, 0][at])
+    dx = torch.full((tokens, 1), 9.0, dtype=torch.bfloat16, device="cuda")
+    B.nq_moe_route_grad(router, x, ids, w, dlogits=dx)
+    want = B.nq_moe_route_grad(router, x[:7], ids[:7], w[:7])
+    assert torch.equal(dx[:, 0], want[:, 0][at])
