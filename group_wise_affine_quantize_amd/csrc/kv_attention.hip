@@ -157,7 +157,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
         const int tile1 = unit0 + units == s.units ? s.nt : (int)((unit0 + units) << A.unit_shift);
 
         State<D, NP> st;
-        bool apart = false;     // whether l has a reference of its own
+        uint32_t near = kNearScales;    // 0 where l has a reference of its own
         int col_lo, col_hi;
         {
             const Column c = column(A, s, ctile * COLS + 16 * cg + r, head);
@@ -270,8 +270,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
 
             const bool zeros = sv == 0.0f;
             const float vs = zeros ? 1.0f : sv;
-            const float lsv = fast_log2(vs), isv = 1.0f / vs;
-            const bool far = __any(scale_is_far(sv));
+            const float lsv = fast_log2(vs);
+            float isv = 1.0f / vs;
             half8_t P[2][NP];
             {
                 const float f = st.c * sk;
@@ -285,9 +285,10 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] = i < lo || i >= hi ? kNegInf : x[i];
                 }
-                if (__builtin_expect(apart || far, false)) {
-                    if (!apart) st.u = st.m;
-                    apart = true;
+                if (__any(scale_place(sv) >= near)) {
+                    if (near) st.u = st.m;
+                    near = 0;
+                    isv = 0.0f;
                     // a scale that is no number has made x NaN where tokens are seen
                     const float shift = lsv == lsv ? lsv : 0.0f;
                     add_weights(16, [&](int i) { return x[i] - shift; }, st.l, st.u);
@@ -302,7 +303,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
                     const float next = over > st.m + kSlack ? over : st.m;
                     const float alpha = next == kNegInf ? 0.0f : fast_exp2(st.m - next);
                     st.m = next;
-                    if (!apart) st.l *= alpha;
+                    if (near) st.l *= alpha;
 #pragma unroll
                     for (int dt = 0; dt < DT; ++dt) st.o[dt] *= alpha;
                 }
@@ -313,7 +314,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
                     x[i] = fast_exp2(x[i] - mref);
                     sum += x[i];
                 }
-                st.l = fmaf(sum, apart ? 0.0f : isv, st.l);
+                st.l = fmaf(sum, isv, st.l);
                 split_half<NP>(x, P[0]);
                 split_half<NP>(x + 8, P[1]);
             }
@@ -356,7 +357,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
         }
 
         // join the waves of a column group: references first, then sums by halves
-        if (apart) {
+        if (!near) {
             const float u = group_max(st.u, lane);
             st.l *= exp2_below(st.u, u);
             st.u = u;
@@ -429,7 +430,7 @@ template <int D, int CG, typename T>
 __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 {
     constexpr int COLS = 16 * CG, QUADS = D / 4, LANES = kJoinCols * QUADS, RUNS = kJoinThreads / LANES;
-    __shared__ float sh_f[kWorkers][kJoinCols], sh_l[kWorkers][kJoinCols], sh_u[kWorkers][kJoinCols];
+    __shared__ float sh_f[kWorkers][kJoinCols];
     __shared__ float4 sh_s[kJoinCols];
     __shared__ float4 sh_o[RUNS][LANES];
     const KvAttnLaunch &a = A.a;
@@ -450,22 +451,23 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
         if (idx0 >= s.n * A.group) return;
         auto slot = [&](int p) -> int64_t { return (2 * (int64_t)(w0 + p) + (p == 0 ? 1 : 0)) * COLS + col0; };
 
-        // each part's factor of O: 2^(R_part - R)
-        for (int i = tid; i < parts * kJoinCols; i += kJoinThreads) {
-            const int p = i / kJoinCols, c = i % kJoinCols;
-            const float4 t = A.part_s[slot(p) + c];
-            sh_f[p][c] = t.x, sh_l[p][c] = t.y, sh_u[p][c] = t.z;
-        }
-        __syncthreads();
+        // each part's factor of O: 2^(R_part - R); a wave to a column
         if (tid < 64 * kJoinCols) {
             const int c = tid >> 6, lane = tid & 63;
-            float m = kNegInf, u = kNegInf;
-            for (int p = lane; p < parts; p += 64) m = fmaxf(m, sh_f[p][c]), u = fmaxf(u, sh_u[p][c]);
+            float4 first = make_float4(kNegInf, 0.0f, kNegInf, 0.0f);
+            if (lane < parts) first = A.part_s[slot(lane) + c];
+            float m = first.x, u = first.z;
+            for (int p = lane + 64; p < parts; p += 64) {
+                const float4 t = A.part_s[slot(p) + c];
+                m = fmaxf(m, t.x), u = fmaxf(u, t.z);
+            }
             m = wave_max(m, lane), u = wave_max(u, lane);
-            float l = 0.0f;
-            for (int p = lane; p < parts; p += 64) {
-                sh_f[p][c] = exp2_below(sh_f[p][c], m);
-                l = fmaf(exp2_below(sh_u[p][c], u), sh_l[p][c], l);
+            if (lane < parts) sh_f[lane][c] = exp2_below(first.x, m);
+            float l = exp2_below(first.z, u) * first.y;
+            for (int p = lane + 64; p < parts; p += 64) {
+                const float4 t = A.part_s[slot(p) + c];
+                sh_f[p][c] = exp2_below(t.x, m);
+                l = fmaf(exp2_below(t.z, u), t.y, l);
             }
             l += xor_lane<1>(l, lane);
             l += xor_lane<2>(l, lane);

@@ -255,7 +255,7 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
             // keeps the factor of the scores above zero; all-zero values add to L alone
             const bool lost = has && !(sk - sk + (sv - sv) == 0.0f);
             const float k = !has || lost || sk == 0.0f ? 1.0f : sk, v = !has || lost ? 1.0f : sv, log = fast_log2(v);    // log2(0): -infinity
-            const float kind = !has ? kAbsent : lost ? kLost : scale_is_far(v) ? kFar : kThere;
+            const float kind = !has ? kAbsent : lost ? kLost : scale_place(v) >= kNearScales ? kFar : kThere;
             sh_s[buf][tid] = make_float4(k, log, v == 0.0f ? 0.0f : 1.0f / v, kind);
         }
     };

@@ -17,12 +17,11 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kPScale = 14.0f;  // log2 of the largest weight
 // Value scales with which L can share O's reference: 2^-48 .. 2^16 (see the head
-// of kv_attention.hip).  One comparison of their bits finds zeros too.
-__device__ __forceinline__ bool scale_is_far(float s)
-{
-    constexpr uint32_t lo = (127 - 48) << 23, hi = (127 + 16) << 23;
-    return __float_as_uint(s) - lo > hi - lo;
-}
+// of kv_attention.hip).  One comparison of their bits, taken from the lower
+// end, finds zeros too.
+constexpr uint32_t kNearScales = ((uint32_t)(48 + 16) << 23) + 1;
+__device__ __forceinline__ uint32_t scale_place(float s) { return __float_as_uint(s) - ((127u - 48u) << 23); }
+
 constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
