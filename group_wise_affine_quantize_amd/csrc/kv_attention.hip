@@ -12,13 +12,16 @@
 // L are scaled) when a later maximum passes R + 14 by more than kSlack; the
 // largest p_t lies in [2^14, 2^15.5).  Drawing sv into x makes p_t the whole
 // weight of a code row, so that the second product runs on bare codes, and
-// p_t fits fp16: 11 bits for weights within 2^-28 of the largest, a floor
-// about 2^-39 below it.  (bf16 would keep 8 bits, which shows in a bf16
-// result.)  Codes are exact in fp16.  A query row is taken times a power of
+// p_t fits fp16: 11 bits for weights within 2^-28 of the largest, an error of
+// 2^-39 of it below (the tile kernel, whose weights start at 2^12: 2^-26 and
+// 2^-37).  (bf16 would keep 8 bits, which shows in a bf16 result.)  Codes are exact in fp16.  A query row is taken times a power of
 // two that brings its largest element to [2^14, 2^15); a bf16 element then is
 // exact in fp16 down to 2^-28 of the largest.  fp32 rows and weights are the
-// sum of two fp16 numbers (22 bits) and take two matrix products each.  Sums,
-// references and the states O and L are fp32.
+// sum of two fp16 numbers and take two matrix products each: 22 bits while the
+// second, at most 2^-11 of the number, is one of fp16's normal numbers (from
+// 2^-14 up), that is for numbers from 2^-3 up -- 2^-17 of the largest, 2^-15 in
+// the tile kernel's weights -- and an error of 2^-25 below.  Sums, references
+// and the states O and L are fp32.
 //
 // p_t / sv_t is 2^(z_t - R) (z in base 2 here), whose range is not p_t's: a sum
 // over tiny scales can pass fp32, and the p_t of a small scale beside a very
@@ -38,11 +41,11 @@
 // per lane).  No value moves between lanes but the running maximum.
 //
 // What bounds it: reading the codes.  64 sequences of 1k to 8k tokens, 8 heads of
-// 128 in int8: 620 MB in 121 us, 5.1 TB/s (a 1 GiB copy moves 5.1), with two
+// 128 in int8: 620 MB in 118 us, 5.2 TB/s (a 1 GiB copy moves 5.1), with two
 // workgroups of four waves per compute unit, each wave with a tile of 16 KB on
 // the way.  With more than 16 query columns two or four waves read the same tile, and
 // less is on the way: 8 draft tokens over 131k tokens, 264 MB in 82 us.  One token at
-// 333 is latency: 9.3 us.
+// 333 is latency: 9.5 us.
 #include <algorithm>
 
 #include "nq_kv_attn.h"

@@ -14,7 +14,7 @@
 // Both are bound by memory: a token of a head is read and written once (by the
 // write its row is read twice, for the scale and for the codes, the second
 // time from the cache: 77 MB fetched for 59).  14.3k tokens of 8 heads of 128,
-// bf16 to E4M3: 88 MB in 25 to 28 us; 107k tokens of int8 back to bf16: 657 MB
+// bf16 to E4M3: 88 MB in 24 to 28 us; 107k tokens of int8 back to bf16: 657 MB
 // in 150 us, 4.4 TB/s; 16 single tokens 5.6 us, one dependent load after
 // another.
 //

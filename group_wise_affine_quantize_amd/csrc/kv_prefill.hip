@@ -21,9 +21,9 @@
 // 2^(kTop + kSlack) in fp16.
 //
 // 3 prompts of 2530 to 4096 tokens, 32 heads of 128 over 8 int8 key/value
-// heads: 375 to 385 us by itself (340 in a row of calls), 740 TFLOP/s of the
+// heads: 370 to 380 us by itself (a call in a row of calls 341 to 352), 740 TFLOP/s of the
 // visible products, where a large fp16 library product reaches 1131.  A tile
-// takes about 4450 cycles at the 1.97 GHz that the card keeps up: 324 vector
+// takes about 4450 cycles at the 1.97 GHz that the card keeps up: 329 vector
 // instructions for each of the two waves of a SIMD, and 2048 cycles of MFMA
 // per SIMD, overlapped as far as the two waves' phases differ.  The LDS (256
 // bytes a cycle with the placement below) is a quarter used.

@@ -525,11 +525,14 @@ size_t nq_kv_attention_workspace_bytes(const nq_kv_cache *cache, const nq_kv_seq
  * that sees a token and holds a NaN or an infinity, or that sees a token of a
  * block whose scale is no number, gives NaN in both, and changes no other.
  * softmax_scale must be finite and positive.  Keys, values and sums are
- * fp32-accurate; for bf16 queries the weights of the second product keep 11
- * bits (fp16), for fp32 queries both products take their operands with 22
- * bits; weights times their values' scale lose bits from 2^-26 of a row's
- * largest down and end at 2^-37 of it.  The workspace (16-byte aligned) is
- * scratch of one call at a time. */
+ * fp32-accurate.  What the products take of queries and weights: for bf16
+ * queries all bits of elements from 2^-28 of the query's largest up, and 11
+ * bits of weights; for fp32 queries 22 bits, of elements from 2^-17 of the
+ * query's largest up (an error of 2^-39 of the largest below that) and of
+ * weights.  Weights, here each times its value's scale, have these bits from
+ * 2^-26 (bf16) or 2^-15 (fp32) of a row's largest up, and an error of up to
+ * 2^-37 of the largest below that.  The workspace (16-byte aligned) is scratch
+ * of one call at a time. */
 nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, const void *q, nq_dtype x_dt,
                           int64_t ldq, int32_t q_heads, float softmax_scale, int32_t causal, int64_t window,
                           void *out, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream);
