@@ -21,6 +21,7 @@ FP_MODES = {"mxfp4": (NQ_MXFP4, 4, 32), "mxfp8": (NQ_MXFP8, 8, 32), "nvfp4": (NQ
 NQ_KV_INT8, NQ_KV_FP8 = 1, 2
 KV_FORMATS = {"int8": NQ_KV_INT8, "fp8": NQ_KV_FP8}
 NQ_MOE_SOFTMAX, NQ_MOE_SIGMOID = 1, 2
+ROPE_LAYOUTS = {"halves": 1, "pairs": 2}
 MOE_SCORES = {"softmax": NQ_MOE_SOFTMAX, "sigmoid": NQ_MOE_SIGMOID}
 
 _lib = None
@@ -94,6 +95,18 @@ _SIGNATURES = {
     "nq_kv_attention": [_P, _P, _P, _I32, _I64, _I32, ctypes.c_float, _I32, _I64, _P, _P, _P, _SZ, _P],
     "nq_moe_route": [_P, _P, _I32, _I64, _I64, _P, _P, _P, _P],
     "nq_moe_route_grad": [_P, _P, _I32, _I64, _I64, _P, _P, _P, _P],
+    "nq_moe_sort_workspace_bytes": [_I64, _I32, _I32],
+    "nq_moe_sort": [_P, _I64, _I32, _I32, _P, _P, _P, _P, _P, _SZ, _P],
+    "nq_moe_dispatch": [_P, _P, _I32, _I64, _I64, _P, _P],
+    "nq_moe_dispatch_grad": [_P, _P, _I32, _I64, _P, _P],
+    "nq_moe_combine": [_P, _P, _I32, _I64, _P, _P, _I64, _P, _P],
+    "nq_moe_combine_grad": [_P, _P, _I32, _I64, _I64, _P, _P, _P, _P, _P],
+    "nq_block_norm": [_P, _P, _I64, _P, _I64, _I32, _P, _P, _I64, _P, _I32, _P, _P, _P],
+    "nq_block_norm_grad_workspace_bytes": [_P],
+    "nq_block_norm_grad": [_P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _P, _I64, _P, _I32, _P, _P, _P, _P,
+                           _P, _P, _SZ, _P],
+    "nq_rope": [_P, _P, _I32, _I64, _I64, _I32, _I32, _P, _I64, _P, _I64, _P],
+    "nq_rope_grad": [_P, _P, _I32, _I64, _I64, _I32, _I32, _P, _I64, _P, _I64, _P],
     "nq_status_string": [_I32],
     "nq_last_error": [],
     "nq_version": [],
@@ -101,6 +114,7 @@ _SIGNATURES = {
 _RESTYPES = {"nq_qmm_workspace_bytes": _SZ, "nq_gather_qmm_workspace_bytes": _SZ,
              "nq_qmm_notrans_workspace_bytes": _SZ, "nq_fp_gather_qmm_workspace_bytes": _SZ,
              "nq_fp_qmm_notrans_workspace_bytes": _SZ, "nq_kv_attention_workspace_bytes": _SZ,
+             "nq_moe_sort_workspace_bytes": _SZ, "nq_block_norm_grad_workspace_bytes": _SZ,
              "nq_status_string": ctypes.c_char_p, "nq_last_error": ctypes.c_char_p,
              "nq_version": ctypes.c_char_p}
 
@@ -891,3 +905,396 @@ def nq_moe_route_grad(router, logits, ids, dweights, dlogits=None, stream=None):
     if status:
         _check(status)
     return dlogits
+
+
+# ---------------------------------------------------------------- tokens sorted by expert
+class _MoEOrderStruct(ctypes.Structure):
+    _fields_ = [("starts", _P), ("place", _P), ("tokens", _I64), ("top_k", _I32), ("experts", _I32)]
+
+
+class _BlockNormStruct(ctypes.Structure):
+    _fields_ = [("rows", _I64), ("dim", _I64), ("gates", _I64), ("eps", ctypes.c_float), ("offset", ctypes.c_float),
+                ("scale", ctypes.c_float)]
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("freq", _P), ("axis", _P), ("rotary_dim", _I32), ("axes", _I32), ("layout", _I32),
+                ("scale", ctypes.c_float)]
+
+
+def _one_device(stream, *tensors):
+    """All tensors (None left out) are on the GPU of the call's stream."""
+    torch = _torch()
+    at = torch.cuda.current_device() if stream is None else stream.device.index
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != at):
+            raise ValueError(f"a tensor on {t.device} in a call on cuda:{at}; make that device the current one "
+                             "or pass a stream of it")
+
+
+def _given(name, t, shape, dtype):
+    """A caller's dense output tensor."""
+    _contig(name, t)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _matrix(name, t, rows=None, dim=None, dtype=None):
+    """The row stride of a [rows, dim] tensor whose rows are dense."""
+    if t.dim() != 2 or (rows is not None and tuple(t.shape) != (rows, dim)):
+        raise ValueError(f"{name} must be " + ("a matrix" if rows is None else f"{(rows, dim)}") +
+                         f", got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class MoEOrder(_Described):
+    """Pairs (token, choice) in the order of their experts (nq_moe_order), int32
+    tensors: starts [experts + 1], place [tokens, top_k] (each pair's row),
+    row_token and row_expert [tokens * top_k] (each row's token and expert id,
+    which nq_gather_qmm_lhs takes as lhs_idx and rhs_idx)."""
+
+    def __init__(self, starts, place, row_token, row_expert):
+        torch = _torch()
+        if place.dim() != 2:
+            raise ValueError("place must be [tokens, top_k]")
+        tokens, top_k = place.shape
+        for name, t, n in (("starts", starts, starts.numel()), ("place", place, tokens * top_k),
+                           ("row_token", row_token, tokens * top_k), ("row_expert", row_expert, tokens * top_k)):
+            _contig(name, t)
+            if t.dtype != torch.int32 or t.numel() != n:
+                raise ValueError(f"{name} must hold {n} int32 numbers")
+        self.starts, self.place, self.row_token, self.row_expert = starts, place, row_token, row_expert
+        self.tokens, self.top_k, self.experts = tokens, top_k, starts.numel() - 1
+        self._struct = _MoEOrderStruct(starts.data_ptr(), place.data_ptr(), tokens, top_k, self.experts)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, tokens, top_k, experts, device="cuda", stream=None):
+        torch = _torch()
+        pairs = tokens * top_k
+        # one allocation; the arrays start at multiples of 16 bytes
+        up = lambda n: -(-n // 4) * 4
+        a, b, c = up(experts + 1), up(pairs), up(pairs)
+        buf = _empty(stream, (a + b + c + pairs,), torch.int32, device)
+        return cls(buf[:experts + 1], buf[a:a + pairs].view(tokens, top_k), buf[a + b:a + b + pairs],
+                   buf[a + b + c:])
+
+
+def nq_moe_sort_workspace_bytes(tokens, top_k, experts):
+    return load_library().nq_moe_sort_workspace_bytes(tokens, top_k, experts)
+
+
+def nq_moe_sort(ids, experts, order=None, workspace=None, stream=None):
+    """ids [tokens, top_k] (uint32 as int32) -> a MoEOrder: pairs in the stable order of
+    their experts, ids outside 0 .. experts - 1 dropped (behind the others).
+    order: an existing MoEOrder of these sizes to write to.  The workspace is
+    allocated here when not given."""
+    torch = _torch()
+    lib = _lib or load_library()
+    _contig("ids", ids)
+    if ids.dim() != 2 or ids.dtype != torch.int32:
+        raise ValueError("ids must be int32 [tokens, top_k]")
+    tokens, top_k = ids.shape
+    if order is None:
+        order = MoEOrder.empty(tokens, top_k, experts, ids.device, stream)
+    elif (order.tokens, order.top_k, order.experts) != (tokens, top_k, experts):
+        raise ValueError("order was made for other sizes")
+    if workspace is None:
+        ws_bytes = lib.nq_moe_sort_workspace_bytes(tokens, top_k, experts)
+        if ws_bytes:
+            workspace = _empty(stream, ws_bytes, torch.uint8, ids.device)
+    else:
+        _contig("workspace", workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _one_device(stream, ids, order.starts, workspace)
+    status = lib.nq_moe_sort(ids.data_ptr(), tokens, top_k, experts, order.starts.data_ptr(), order.place.data_ptr(),
+                             order.row_token.data_ptr(), order.row_expert.data_ptr(),
+                             None if workspace is None else workspace.data_ptr(), ws_bytes, _raw_stream(stream))
+    if status:
+        _check(status)
+    return order
+
+
+def nq_moe_dispatch(order, x, xs=None, stream=None):
+    """x [tokens, hidden] (f32 or bf16, any row stride) -> xs [tokens * top_k,
+    hidden], the tokens' rows in the order of their experts; rows of dropped
+    pairs are zeros."""
+    lib = _lib or load_library()
+    ldx = _matrix("x", x)
+    hidden = x.shape[1]
+    if x.shape[0] != order.tokens:
+        raise ValueError(f"x must have {order.tokens} rows")
+    shape = (order.tokens * order.top_k, hidden)
+    xs = _empty(stream, shape, x.dtype, x.device) if xs is None else _given("xs", xs, shape, x.dtype)
+    _one_device(stream, order.place, x, xs)
+    status = lib.nq_moe_dispatch(order._ref, x.data_ptr(), _dt(x), ldx, hidden, xs.data_ptr(), _raw_stream(stream))
+    if status:
+        _check(status)
+    return xs
+
+
+def _expert_rows(name, order, t):
+    _contig(name, t)
+    if t.dim() != 2 or t.shape[0] != order.tokens * order.top_k:
+        raise ValueError(f"{name} must be [{order.tokens * order.top_k}, hidden]")
+    return t.shape[1]
+
+
+def nq_moe_dispatch_grad(order, dxs, dx=None, stream=None):
+    """The gradient of x in nq_moe_dispatch: dxs [tokens * top_k, hidden] -> dx
+    [tokens, hidden]."""
+    lib = _lib or load_library()
+    hidden = _expert_rows("dxs", order, dxs)
+    shape = (order.tokens, hidden)
+    dx = _empty(stream, shape, dxs.dtype, dxs.device) if dx is None else _given("dx", dx, shape, dxs.dtype)
+    _one_device(stream, order.place, dxs, dx)
+    status = lib.nq_moe_dispatch_grad(order._ref, dxs.data_ptr(), _dt(dxs), hidden, dx.data_ptr(), _raw_stream(stream))
+    if status:
+        _check(status)
+    return dx
+
+
+def _pair_weights(order, weights):
+    if weights is None:
+        return None
+    return _given("weights", weights, (order.tokens, order.top_k), _torch().float32).data_ptr()
+
+
+def nq_moe_combine(order, ys, weights=None, residual=None, y=None, stream=None):
+    """ys [tokens * top_k, hidden], weights [tokens, top_k] float32 (None: ones),
+    residual [tokens, hidden] or None -> y [tokens, hidden] = residual + the
+    weighted sum of each token's rows."""
+    lib = _lib or load_library()
+    hidden = _expert_rows("ys", order, ys)
+    shape = (order.tokens, hidden)
+    ldr = 0 if residual is None else _matrix("residual", residual, *shape, ys.dtype)
+    y = _empty(stream, shape, ys.dtype, ys.device) if y is None else _given("y", y, shape, ys.dtype)
+    _one_device(stream, order.place, ys, weights, residual, y)
+    status = lib.nq_moe_combine(order._ref, ys.data_ptr(), _dt(ys), hidden, _pair_weights(order, weights),
+                                None if residual is None else residual.data_ptr(), ldr, y.data_ptr(),
+                                _raw_stream(stream))
+    if status:
+        _check(status)
+    return y
+
+
+def nq_moe_combine_grad(order, dy, ys=None, weights=None, dys=None, dweights=None, stream=None):
+    """The gradients of nq_moe_combine: dy [tokens, hidden] (any row stride), ys and
+    weights as there -> (dys [tokens * top_k, hidden], dweights [tokens, top_k]
+    float32).  ys None: only dys, dweights is None.  The residual's gradient is dy."""
+    torch = _torch()
+    lib = _lib or load_library()
+    ldd = _matrix("dy", dy)
+    hidden, pairs = dy.shape[1], order.tokens * order.top_k
+    if dy.shape[0] != order.tokens:
+        raise ValueError(f"dy must have {order.tokens} rows")
+    if ys is not None and (_expert_rows("ys", order, ys) != hidden or ys.dtype != dy.dtype):
+        raise ValueError("ys must have dy's columns and dtype")
+    if ys is None and dweights is not None:
+        raise ValueError("dweights needs ys")
+    dys = _empty(stream, (pairs, hidden), dy.dtype, dy.device) if dys is None else \
+        _given("dys", dys, (pairs, hidden), dy.dtype)
+    if ys is not None:
+        shape = (order.tokens, order.top_k)
+        dweights = _empty(stream, shape, torch.float32, dy.device) if dweights is None else \
+            _given("dweights", dweights, shape, torch.float32)
+    _one_device(stream, order.place, dy, ys, weights, dys, dweights)
+    status = lib.nq_moe_combine_grad(order._ref, dy.data_ptr(), _dt(dy), ldd, hidden,
+                                     None if ys is None else ys.data_ptr(), _pair_weights(order, weights),
+                                     dys.data_ptr(), None if dweights is None else dweights.data_ptr(),
+                                     _raw_stream(stream))
+    if status:
+        _check(status)
+    return dys, dweights
+
+
+# ---------------------------------------------------------------- norms, gate and residual
+def _norm_call(stream, like, rows, dim, post, gate, pre, scale, offset, eps):
+    """The shape struct, the parameters' dtype, and gate's row stride."""
+    p = next((t for t in (post, gate, pre) if t is not None), like)
+    for name, t in (("post", post), ("pre", pre)):
+        if t is not None:
+            _given(name, t, (dim,), p.dtype)
+    gates, ldg = 1, 0
+    if gate is not None:
+        if gate.dtype != p.dtype:
+            raise TypeError("post, gate and pre must have the same dtype")
+        if gate.dim() == 1:
+            _given("gate", gate, (dim,), p.dtype)
+            ldg = dim
+        else:
+            if gate.dim() != 2 or gate.shape[1] != dim:
+                raise ValueError(f"gate must be [{dim}] or [gates, {dim}], got {tuple(gate.shape)}")
+            ldg, gates = _matrix("gate", gate), max(1, gate.shape[0])
+    return _BlockNormStruct(rows, dim, gates, eps, offset, scale), _dt(p), ldg
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def nq_block_norm_grad_workspace_bytes(rows, dim, gates=1):
+    return load_library().nq_block_norm_grad_workspace_bytes(
+        ctypes.byref(_BlockNormStruct(rows, dim, gates, 1e-6, 0.0, 1.0)))
+
+
+def nq_block_norm(h, y=None, post=None, gate=None, pre=None, scale=1.0, offset=0.0, eps=1e-6, h_out=None, z=None,
+                  stream=None):
+    """A block's output y joins the residual stream h, both [rows, dim] (f32 or
+    bf16, any row stride), and the next block's input leaves it:
+      h_out = h + scale * gate * norm(y) * (post + offset),
+      z = norm(h_out) * (pre + offset),   norm(t) = t / sqrt(mean(t^2) + eps).
+    post None: y itself; gate [dim], [gates, dim] (rows / gates neighbouring rows
+    each) or None; y None: h_out is h; pre None: no z.  post, gate and pre share a
+    dtype.  -> (h_out, z)."""
+    lib = _lib or load_library()
+    ldh = _matrix("h", h)
+    rows, dim = h.shape
+    ldy = 0 if y is None else _matrix("y", y, rows, dim, h.dtype)
+    shape, p_dt, ldg = _norm_call(stream, h, rows, dim, post, gate, pre, scale, offset, eps)
+    if y is not None:
+        h_out = _empty(stream, (rows, dim), h.dtype, h.device) if h_out is None else \
+            _given("h_out", h_out, (rows, dim), h.dtype)
+    elif h_out is not None:
+        raise ValueError("h_out needs y")
+    if pre is not None:
+        z = _empty(stream, (rows, dim), h.dtype, h.device) if z is None else _given("z", z, (rows, dim), h.dtype)
+    elif z is not None:
+        raise ValueError("z needs pre")
+    _one_device(stream, h, y, post, gate, pre, h_out, z)
+    status = lib.nq_block_norm(ctypes.byref(shape), h.data_ptr(), ldh, _address(y), ldy, _dt(h), _address(post),
+                               _address(gate), ldg, _address(pre), p_dt, _address(h_out), _address(z),
+                               _raw_stream(stream))
+    if status:
+        _check(status)
+    return (h if y is None else h_out), z
+
+
+def nq_block_norm_grad(h_out, y=None, dh_out=None, dz=None, post=None, gate=None, pre=None, scale=1.0, offset=0.0,
+                       eps=1e-6, parameters=True, dh=None, dy=None, workspace=None, stream=None):
+    """The gradients of nq_block_norm, from h_out as it returned it and the
+    gradients dh_out and dz of its outputs (None: zero) -> (dh, dy, dpost,
+    dgate, dpre), None where there is no such input; dpost, dgate and dpre in their
+    parameters' dtype, None with parameters=False.  The workspace is allocated here
+    when not given."""
+    torch = _torch()
+    lib = _lib or load_library()
+    ldh = _matrix("h_out", h_out)
+    rows, dim = h_out.shape
+    dt, dev = h_out.dtype, h_out.device
+    lds = [0 if t is None else _matrix(name, t, rows, dim, dt) for name, t in
+           (("y", y), ("dh_out", dh_out), ("dz", dz))]
+    shape, p_dt, ldg = _norm_call(stream, h_out, rows, dim, post, gate, pre, scale, offset, eps)
+    dh = _empty(stream, (rows, dim), dt, dev) if dh is None else _given("dh", dh, (rows, dim), dt)
+    if y is not None:
+        dy = _empty(stream, (rows, dim), dt, dev) if dy is None else _given("dy", dy, (rows, dim), dt)
+    elif dy is not None:
+        raise ValueError("dy needs y")
+    like = lambda t, wanted: _empty(stream, t.shape, t.dtype, dev) if parameters and wanted else None
+    dpost, dgate = like(post, post is not None), like(gate, gate is not None)
+    dpre = like(pre, pre is not None and dz is not None)
+    if workspace is None:
+        ws_bytes = lib.nq_block_norm_grad_workspace_bytes(ctypes.byref(shape))
+        if ws_bytes:
+            workspace = _empty(stream, ws_bytes, torch.uint8, dev)
+    else:
+        _contig("workspace", workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _one_device(stream, h_out, y, dh_out, dz, post, gate, pre, dh, dy, workspace)
+    status = lib.nq_block_norm_grad(ctypes.byref(shape), h_out.data_ptr(), ldh, _address(y), lds[0], _address(dh_out),
+                                    lds[1], _address(dz), lds[2], _dt(h_out), _address(post), _address(gate), ldg,
+                                    _address(pre), p_dt, dh.data_ptr(), _address(dy), _address(dpost), _address(dgate),
+                                    _address(dpre), _address(workspace), ws_bytes, _raw_stream(stream))
+    if status:
+        _check(status)
+    return dh, dy, dpost, dgate, dpre
+
+
+# ---------------------------------------------------------------- rotary positions
+class Rope(_Described):
+    """How heads are turned by their position (nq_rope_plan): the first rotary_dim
+    columns of a head are pairs -- "halves": column i with column i + rotary_dim
+    / 2, "pairs": neighbours -- and pair i is turned by freq[i] times the position
+    on axis[i].  freq: rotary_dim / 2 numbers (default theta^(-2 i /
+    rotary_dim)), kept in float64.  axis: the axis of each pair, or sections: how many
+    neighbouring pairs each axis has; by default there is one axis.  scale multiplies
+    the result."""
+
+    def __init__(self, rotary_dim, theta=10000.0, sections=None, axis=None, freq=None, layout="halves", scale=1.0,
+                 device="cuda"):
+        torch = _torch()
+        half = rotary_dim // 2
+        if rotary_dim < 2 or rotary_dim % 2:
+            raise ValueError("rotary_dim must be even and positive")
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError(f"unknown layout {layout!r} (one of {sorted(ROPE_LAYOUTS)})")
+        if sections is not None:
+            if axis is not None:
+                raise ValueError("give axis or sections, not both")
+            axis = [a for a, n in enumerate(sections) for _ in range(n)]
+            axes = len(sections)
+        else:
+            axis = None if axis is None else [int(a) for a in axis]
+            axes = 1 if axis is None else max(axis, default=0) + 1
+        if axis is not None and (len(axis) != half or min(axis) < 0):
+            raise ValueError(f"axis (or sections) must give each of the {half} pairs an axis")
+        if freq is None:
+            freq = theta ** (-torch.arange(half, dtype=torch.float64) / half)
+        self.freq = torch.as_tensor(freq, dtype=torch.float64).to(device).contiguous().clone()
+        if tuple(self.freq.shape) != (half,):
+            raise ValueError(f"freq must hold {half} numbers")
+        if not self.freq.is_cuda:
+            raise ValueError("a Rope lives on a GPU")
+        self.axis = None if axis is None else torch.tensor(axis, dtype=torch.int32).to(self.freq.device)
+        self.rotary_dim, self.axes, self.layout, self.scale = rotary_dim, axes, layout, scale
+        self._struct = _RopeStruct(self.freq.data_ptr(), _address(self.axis), rotary_dim, axes, ROPE_LAYOUTS[layout],
+                                   scale)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _turn(name, rope, x, positions, out, stream, names):
+    torch = _torch()
+    lib = _lib or load_library()
+    if x.dim() != 3:
+        raise ValueError(f"{names[0]} must be [rows, heads, head_dim]")
+    rows, heads, dim = x.shape
+    ldx = _row_stride(names[0], x, rows, heads, dim)
+    if positions.dtype != torch.int32 or not positions.is_cuda:
+        raise TypeError("positions must be an int32 GPU tensor")
+    if positions.dim() == 1 and rope.axes == 1:
+        positions = positions[None]
+    if tuple(positions.shape) != (rope.axes, rows):
+        raise ValueError(f"positions must be [{rope.axes}, {rows}], got {tuple(positions.shape)}")
+    if rows > 1 and positions.stride(1) != 1:
+        raise ValueError("the positions of an axis must be contiguous")
+    ldp = positions.stride(0) if rope.axes > 1 else rows
+    if out is None:
+        out = _empty(stream, (rows, heads, dim), x.dtype, x.device)
+        ldo = heads * dim
+    else:
+        if out.dtype != x.dtype:
+            raise TypeError(f"{names[1]} must have {names[0]}'s dtype")
+        ldo = _row_stride(names[1], out, rows, heads, dim)
+    _one_device(stream, rope.freq, x, positions, out)
+    status = getattr(lib, name)(rope._ref, x.data_ptr(), _dt(x), rows, ldx, heads, dim, positions.data_ptr(), ldp,
+                                out.data_ptr(), ldo, _raw_stream(stream))
+    if status:
+        _check(status)
+    return out
+
+
+def nq_rope(rope, x, positions, out=None, stream=None):
+    """x [rows, heads, head_dim] (f32 or bf16, any row stride, e.g. columns of a
+    fused projection) turned by positions, int32 [axes, rows] (or [rows] with one
+    axis) -> out, dense unless given; out=x turns in place."""
+    return _turn("nq_rope", rope, x, positions, out, stream, ("x", "out"))
+
+
+def nq_rope_grad(rope, dout, positions, dx=None, stream=None):
+    """The gradient of x in nq_rope: dout [rows, heads, head_dim] turned back."""
+    return _turn("nq_rope_grad", rope, dout, positions, dx, stream, ("dout", "dx"))

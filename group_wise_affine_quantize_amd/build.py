@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libnq.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["nq_api.hip", "quantize.hip", "gemv.hip", "gemv_mfma.hip", "tiled.hip", "notrans.hip", "fp.hip",
-           "kv_cache.hip", "kv_attention.hip", "kv_prefill.hip", "moe_route.hip"]
+           "kv_cache.hip", "kv_attention.hip", "kv_prefill.hip", "moe_route.hip", "moe_order.hip", "norm.hip", "rope.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -12,6 +12,7 @@
 #include "nq.h"
 #include "nq_internal.h"
 #include "nq_kv.h"
+#include "nq_layer.h"
 
 namespace {
 
@@ -519,6 +520,109 @@ nqk::MoeRoute moe_of(const nq_moe_router *r)
     m.experts = r->experts, m.score = r->score, m.groups = r->groups, m.top_groups = r->top_groups;
     m.group_best = r->group_best, m.top_k = r->top_k, m.renormalise = r->renormalise, m.scale = r->scale;
     return m;
+}
+
+// ---- steps between a layer's products
+// Whether any two of the arrays `from` .. `outs` - 1 (the outputs), or one of
+// them and any other of the `count`, overlap.
+bool any_overlap(const Span *s, int from, int outs, int count)
+{
+    for (int i = from; i < outs; ++i)
+        for (int j = 0; j < count; ++j)
+            if (j != i && overlap(s[i], s[j])) return true;
+    return false;
+}
+
+nq_status check_workspace(const char *op, const void *workspace, size_t bytes, size_t need)
+{
+    if (!need) return NQ_OK;
+    if (!workspace || bytes < need)
+        return fail(NQ_ERR_WORKSPACE, "%s: workspace of %zu bytes needed (got %zu)", op, need, workspace ? bytes : (size_t)0);
+    if (!aligned16(workspace)) return fail(NQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", op);
+    return NQ_OK;
+}
+
+// Rows that need only be aligned to their elements.
+nq_status check_plain_rows(const char *op, const char *name, const void *p, int64_t ld, int64_t width, int64_t bytes)
+{
+    if (!p) return fail(NQ_ERR_NULL, "%s: %s must be non-null", op, name);
+    if (!aligned_to(p, bytes)) return fail(NQ_ERR_ALIGN, "%s: %s is not aligned to its element size", op, name);
+    if (ld < width || ld >= kMaxDim)
+        return fail(NQ_ERR_SHAPE, "%s: row stride %lld of %s is below its %lld columns or too large", op, (long long)ld,
+                    name, (long long)width);
+    return NQ_OK;
+}
+
+nq_status check_moe_sizes(const char *op, int64_t tokens, int32_t top_k, int32_t experts)
+{
+    if (experts < 1 || experts > 1024) return fail(NQ_ERR_SHAPE, "%s: experts=%d is not in 1 .. 1024", op, experts);
+    if (top_k < 1 || top_k > 32) return fail(NQ_ERR_SHAPE, "%s: top_k=%d is not in 1 .. 32", op, top_k);
+    if (tokens < 0 || tokens * top_k >= kMaxDim || tokens >= kMaxDim)
+        return fail(NQ_ERR_SHAPE, "%s: tokens=%lld is negative, or times top_k=%d not below 2^31", op, (long long)tokens, top_k);
+    return NQ_OK;
+}
+
+nq_status check_moe_order(const char *op, const nq_moe_order *o, int x_dt, int64_t hidden, bool *empty)
+{
+    g_last_error.clear();
+    *empty = false;
+    if (!o) return fail(NQ_ERR_NULL, "%s: order is null", op);
+    if (!dtype_ok(x_dt)) return fail(NQ_ERR_DTYPE, "%s: unknown dtype x_dt=%d", op, x_dt);
+    const nq_status st = check_moe_sizes(op, o->tokens, o->top_k, o->experts);
+    if (st) return st;
+    if (hidden < 1 || hidden >= kMaxDim || o->tokens * o->top_k > kMaxElems / hidden)
+        return fail(NQ_ERR_SHAPE, "%s: hidden=%lld is not positive or too large", op, (long long)hidden);
+    *empty = o->tokens == 0;
+    if (*empty) return NQ_OK;
+    if (!o->starts || !o->place) return fail(NQ_ERR_NULL, "%s: order's starts and place must be non-null", op);
+    if (!aligned_to(o->starts, 4) || !aligned_to(o->place, 4))
+        return fail(NQ_ERR_ALIGN, "%s: order's starts and place must be 4-byte aligned", op);
+    return NQ_OK;
+}
+
+bool overlaps_order(const nq_moe_order *o, Span s)
+{
+    return overlap(s, Span{o->starts, (o->experts + 1) * (int64_t)4}) || overlap(s, Span{o->place, o->tokens * o->top_k * 4});
+}
+
+nqk::MoeRowsLaunch moe_rows_of(const nq_moe_order *o, int64_t hidden, int x_dt)
+{
+    nqk::MoeRowsLaunch a{};
+    a.kept = o->starts + o->experts, a.place = o->place, a.tokens = o->tokens, a.hidden = hidden;
+    a.top_k = o->top_k, a.x_dt = x_dt;
+    return a;
+}
+
+nq_status check_norm_shape(const char *op, const nq_block_norm_shape *s, int x_dt, int p_dt)
+{
+    g_last_error.clear();
+    if (!s) return fail(NQ_ERR_NULL, "%s: shape is null", op);
+    if (!dtype_ok(x_dt) || !dtype_ok(p_dt)) return fail(NQ_ERR_DTYPE, "%s: unknown dtype x_dt=%d or p_dt=%d", op, x_dt, p_dt);
+    if (s->dim < 1 || s->dim > nqk::kNormMaxDim)
+        return fail(NQ_ERR_SHAPE, "%s: dim=%lld is not in 1 .. %d", op, (long long)s->dim, nqk::kNormMaxDim);
+    if (s->rows < 0 || s->rows >= kMaxDim) return fail(NQ_ERR_SHAPE, "%s: rows=%lld is negative or too large", op, (long long)s->rows);
+    if (s->gates < 1 || s->rows % s->gates)
+        return fail(NQ_ERR_SHAPE, "%s: gates=%lld is not positive or does not divide rows=%lld", op, (long long)s->gates,
+                    (long long)s->rows);
+    if (!finite(s->eps) || !(s->eps > 0.0f) || !finite(s->offset) || !finite(s->scale))
+        return fail(NQ_ERR_SHAPE, "%s: eps is not positive, or eps, offset or scale not finite", op);
+    return NQ_OK;
+}
+
+nq_status check_norm_params(const char *op, const nq_block_norm_shape *s, const void *post, const void *gate, int64_t ldg,
+                            const void *pre, int p_dt)
+{
+    const int64_t pb = dtype_bytes(p_dt);
+    if (!aligned_to(post, pb) || !aligned_to(gate, pb) || !aligned_to(pre, pb))
+        return fail(NQ_ERR_ALIGN, "%s: post, gate or pre is not aligned to its element size", op);
+    if (gate && (ldg < s->dim || ldg >= kMaxDim))
+        return fail(NQ_ERR_SHAPE, "%s: row stride %lld of gate is below dim=%lld or too large", op, (long long)ldg, (long long)s->dim);
+    return NQ_OK;
+}
+
+Span param_span(const void *p, int64_t rows, int64_t ld, int64_t dim, int p_dt)
+{
+    return Span{p, p ? rows_span(rows, ld, dim, dtype_bytes(p_dt)) : 0};
 }
 
 }  // namespace
@@ -1368,6 +1472,253 @@ nq_status nq_moe_route_grad(const nq_moe_router *router, const void *logits, nq_
     a.r = moe_of(router), a.logits = logits, a.ids = ids, a.dweights = dweights, a.dlogits = dlogits;
     a.tokens = tokens, a.ldl = ld, a.x_dt = x_dt;
     return check_launch(op, nqk::launch_moe_route_grad(a, stream));
+}
+
+// ---- tokens sorted by expert
+size_t nq_moe_sort_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts)
+{
+    g_last_error.clear();
+    if (check_moe_sizes("nq_moe_sort_workspace_bytes", tokens, top_k, experts)) return 0;
+    return nqk::moe_sort_ws_bytes(tokens * top_k, experts);
+}
+
+nq_status nq_moe_sort(const uint32_t *ids, int64_t tokens, int32_t top_k, int32_t experts, int32_t *starts,
+                      int32_t *place, uint32_t *row_token, uint32_t *row_expert, void *workspace,
+                      size_t workspace_bytes, hipStream_t stream)
+{
+    const char *op = "nq_moe_sort";
+    g_last_error.clear();
+    nq_status st = check_moe_sizes(op, tokens, top_k, experts);
+    if (st) return st;
+    if (!starts || (tokens > 0 && (!ids || !place || !row_token || !row_expert)))
+        return fail(NQ_ERR_NULL, "%s: ids, starts, place, row_token and row_expert must be non-null", op);
+    if (!aligned_to(ids, 4) || !aligned_to(starts, 4) || !aligned_to(place, 4) || !aligned_to(row_token, 4) ||
+        !aligned_to(row_expert, 4))
+        return fail(NQ_ERR_ALIGN, "%s: an array is not 4-byte aligned", op);
+    const int64_t pairs = tokens * top_k;
+    const size_t need = nqk::moe_sort_ws_bytes(pairs, experts);
+    if ((st = check_workspace(op, workspace, workspace_bytes, need))) return st;
+    const Span all[] = {{ids, pairs * 4}, {starts, (experts + 1) * (int64_t)4}, {place, pairs * 4},
+                        {row_token, pairs * 4}, {row_expert, pairs * 4}, {workspace, (int64_t)need}};
+    if (any_overlap(all, 1, 6, 6)) return fail(NQ_ERR_ALIAS, "%s: two arrays overlap", op);
+    nqk::MoeSortLaunch a;
+    a.ids = ids, a.pairs = pairs, a.top_k = top_k, a.experts = experts, a.starts = starts, a.place = place;
+    a.row_token = row_token, a.row_expert = row_expert, a.counts = static_cast<int32_t *>(workspace);
+    return check_launch(op, nqk::launch_moe_sort(a, stream));
+}
+
+nq_status nq_moe_dispatch(const nq_moe_order *order, const void *x, nq_dtype x_dt, int64_t ldx, int64_t hidden,
+                          void *xs, hipStream_t stream)
+{
+    const char *op = "nq_moe_dispatch";
+    bool empty;
+    nq_status st = check_moe_order(op, order, x_dt, hidden, &empty);
+    if (st || empty) return st;
+    const int64_t xb = dtype_bytes(x_dt), pairs = order->tokens * order->top_k;
+    if ((st = check_plain_rows(op, "x", x, ldx, hidden, xb)) || (st = check_plain_rows(op, "xs", xs, hidden, hidden, xb)))
+        return st;
+    const Span out{xs, pairs * hidden * xb};
+    if (overlap(out, Span{x, rows_span(order->tokens, ldx, hidden, xb)}) || overlaps_order(order, out))
+        return fail(NQ_ERR_ALIAS, "%s: xs overlaps an input", op);
+    nqk::MoeRowsLaunch a = moe_rows_of(order, hidden, x_dt);
+    a.in = x, a.ldi = ldx, a.out = xs;
+    return check_launch(op, nqk::launch_moe_dispatch(a, stream));
+}
+
+static nq_status moe_combine_impl(const char *op, const nq_moe_order *order, const void *ys, nq_dtype x_dt, int64_t hidden,
+                                  const float *weights, const void *residual, int64_t ldr, void *y, hipStream_t stream)
+{
+    bool empty;
+    nq_status st = check_moe_order(op, order, x_dt, hidden, &empty);
+    if (st || empty) return st;
+    const int64_t xb = dtype_bytes(x_dt), pairs = order->tokens * order->top_k;
+    const bool grad = !strcmp(op, "nq_moe_dispatch_grad");
+    if ((st = check_plain_rows(op, grad ? "dxs" : "ys", ys, hidden, hidden, xb)) ||
+        (st = check_plain_rows(op, grad ? "dx" : "y", y, hidden, hidden, xb)))
+        return st;
+    if (residual && (st = check_plain_rows(op, "residual", residual, ldr, hidden, xb))) return st;
+    if (!aligned_to(weights, 4)) return fail(NQ_ERR_ALIGN, "%s: weights must be 4-byte aligned", op);
+    const Span out{y, order->tokens * hidden * xb};
+    if (overlap(out, Span{ys, pairs * hidden * xb}) || overlap(out, Span{weights, weights ? pairs * 4 : 0}) ||
+        overlap(out, Span{residual, residual ? rows_span(order->tokens, ldr, hidden, xb) : 0}) || overlaps_order(order, out))
+        return fail(NQ_ERR_ALIAS, "%s: the output overlaps an input", op);
+    nqk::MoeRowsLaunch a = moe_rows_of(order, hidden, x_dt);
+    a.in = ys, a.out = y, a.weights = weights, a.residual = residual, a.ldr = residual ? ldr : 0;
+    return check_launch(op, nqk::launch_moe_combine(a, stream));
+}
+
+nq_status nq_moe_dispatch_grad(const nq_moe_order *order, const void *dxs, nq_dtype x_dt, int64_t hidden, void *dx,
+                               hipStream_t stream)
+{
+    return moe_combine_impl("nq_moe_dispatch_grad", order, dxs, x_dt, hidden, nullptr, nullptr, 0, dx, stream);
+}
+
+nq_status nq_moe_combine(const nq_moe_order *order, const void *ys, nq_dtype x_dt, int64_t hidden,
+                         const float *weights, const void *residual, int64_t ldr, void *y, hipStream_t stream)
+{
+    return moe_combine_impl("nq_moe_combine", order, ys, x_dt, hidden, weights, residual, ldr, y, stream);
+}
+
+nq_status nq_moe_combine_grad(const nq_moe_order *order, const void *dy, nq_dtype x_dt, int64_t ldd, int64_t hidden,
+                              const void *ys, const float *weights, void *dys, float *dweights, hipStream_t stream)
+{
+    const char *op = "nq_moe_combine_grad";
+    bool empty;
+    nq_status st = check_moe_order(op, order, x_dt, hidden, &empty);
+    if (st || empty) return st;
+    const int64_t xb = dtype_bytes(x_dt), pairs = order->tokens * order->top_k;
+    if ((st = check_plain_rows(op, "dy", dy, ldd, hidden, xb)) || (st = check_plain_rows(op, "dys", dys, hidden, hidden, xb)) ||
+        (dweights && (st = check_plain_rows(op, "ys", ys, hidden, hidden, xb))))
+        return st;
+    if (!aligned_to(weights, 4) || !aligned_to(dweights, 4))
+        return fail(NQ_ERR_ALIGN, "%s: weights and dweights must be 4-byte aligned", op);
+    const Span out{dys, pairs * hidden * xb}, sw{dweights, dweights ? pairs * 4 : 0},
+        sd{dy, rows_span(order->tokens, ldd, hidden, xb)}, sy{ys, dweights ? pairs * hidden * xb : 0},
+        si{weights, weights ? pairs * 4 : 0};
+    if (overlap(out, sw) || overlap(out, sd) || overlap(out, sy) || overlap(out, si) || overlap(sw, sd) || overlap(sw, sy) ||
+        overlap(sw, si) || overlaps_order(order, out) || overlaps_order(order, sw))
+        return fail(NQ_ERR_ALIAS, "%s: an output overlaps an input or the other output", op);
+    nqk::MoeRowsLaunch a = moe_rows_of(order, hidden, x_dt);
+    a.in = dy, a.ldi = ldd, a.out = dys, a.weights = weights, a.ys = dweights ? ys : nullptr, a.dweights = dweights;
+    return check_launch(op, nqk::launch_moe_combine_grad(a, stream));
+}
+
+// ---- norms, gate and residual
+nq_status nq_block_norm(const nq_block_norm_shape *shape, const void *h, int64_t ldh, const void *y, int64_t ldy,
+                        nq_dtype x_dt, const void *post, const void *gate, int64_t ldg, const void *pre,
+                        nq_dtype p_dt, void *h_out, void *z, hipStream_t stream)
+{
+    const char *op = "nq_block_norm";
+    nq_status st = check_norm_shape(op, shape, x_dt, p_dt);
+    if (st) return st;
+    const int64_t rows = shape->rows, dim = shape->dim, xb = dtype_bytes(x_dt);
+    if (rows == 0) return NQ_OK;
+    if (!y && !pre) return fail(NQ_ERR_NULL, "%s: y or pre must be non-null", op);
+    if (!y && (post || gate || h_out)) return fail(NQ_ERR_NULL, "%s: post, gate and h_out need y", op);
+    if ((pre && !z) || (!pre && z)) return fail(NQ_ERR_NULL, "%s: z and pre come together", op);
+    if ((st = check_plain_rows(op, "h", h, ldh, dim, xb)) || (y && (st = check_plain_rows(op, "y", y, ldy, dim, xb))) ||
+        (y && (st = check_plain_rows(op, "h_out", h_out, dim, dim, xb))) ||
+        (z && (st = check_plain_rows(op, "z", z, dim, dim, xb))) ||
+        (st = check_norm_params(op, shape, post, gate, ldg, pre, p_dt)))
+        return st;
+    const Span all[] = {{h_out, h_out ? rows * dim * xb : 0}, {z, z ? rows * dim * xb : 0},
+                        {h, rows_span(rows, ldh, dim, xb)}, {y, y ? rows_span(rows, ldy, dim, xb) : 0},
+                        param_span(post, 1, dim, dim, p_dt), param_span(gate, shape->gates, ldg, dim, p_dt),
+                        param_span(pre, 1, dim, dim, p_dt)};
+    if (any_overlap(all, 0, 2, 7)) return fail(NQ_ERR_ALIAS, "%s: an output overlaps an input or the other output", op);
+    nqk::BlockNormLaunch a;
+    a.h = h, a.y = y, a.post = post, a.gate = gate, a.pre = pre, a.rows = rows, a.dim = dim;
+    a.ldh = ldh, a.ldy = y ? ldy : 0, a.ldg = gate ? ldg : 0, a.gates = shape->gates, a.h_out = h_out, a.z = z;
+    a.eps = shape->eps, a.offset = shape->offset, a.scale = shape->scale, a.x_dt = x_dt, a.p_dt = p_dt;
+    return check_launch(op, nqk::launch_block_norm(a, stream));
+}
+
+size_t nq_block_norm_grad_workspace_bytes(const nq_block_norm_shape *shape)
+{
+    if (check_norm_shape("nq_block_norm_grad_workspace_bytes", shape, NQ_F32, NQ_F32)) return 0;
+    return nqk::block_norm_grad_ws_bytes(shape->rows, shape->dim, shape->gates);
+}
+
+nq_status nq_block_norm_grad(const nq_block_norm_shape *shape, const void *h_out, int64_t ldh, const void *y,
+                             int64_t ldy, const void *dh_out, int64_t ldd, const void *dz, int64_t ldz,
+                             nq_dtype x_dt, const void *post, const void *gate, int64_t ldg, const void *pre,
+                             nq_dtype p_dt, void *dh, void *dy, void *dpost, void *dgate, void *dpre,
+                             void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const char *op = "nq_block_norm_grad";
+    nq_status st = check_norm_shape(op, shape, x_dt, p_dt);
+    if (st) return st;
+    const int64_t rows = shape->rows, dim = shape->dim, xb = dtype_bytes(x_dt), pb = dtype_bytes(p_dt);
+    if (rows > 0) {
+        if (!dh_out && !dz) return fail(NQ_ERR_NULL, "%s: dh_out or dz must be non-null", op);
+        if (dz && !pre) return fail(NQ_ERR_NULL, "%s: dz needs pre", op);
+        if (!y && (post || gate)) return fail(NQ_ERR_NULL, "%s: post and gate need y", op);
+        if ((dpost && !post) || (dgate && !gate) || (dpre && !dz))
+            return fail(NQ_ERR_NULL, "%s: dpost needs post, dgate needs gate, dpre needs dz", op);
+        if ((y && !dy) || (!y && dy)) return fail(NQ_ERR_NULL, "%s: dy and y come together", op);
+        if ((st = check_plain_rows(op, "h_out", h_out, ldh, dim, xb)) ||
+            (y && (st = check_plain_rows(op, "y", y, ldy, dim, xb))) ||
+            (dh_out && (st = check_plain_rows(op, "dh_out", dh_out, ldd, dim, xb))) ||
+            (dz && (st = check_plain_rows(op, "dz", dz, ldz, dim, xb))) ||
+            (st = check_plain_rows(op, "dh", dh, dim, dim, xb)) || (y && (st = check_plain_rows(op, "dy", dy, dim, dim, xb))) ||
+            (st = check_norm_params(op, shape, post, gate, ldg, pre, p_dt)))
+            return st;
+    }
+    if (!aligned_to(dpost, pb) || !aligned_to(dgate, pb) || !aligned_to(dpre, pb))
+        return fail(NQ_ERR_ALIGN, "%s: a parameter's gradient is not aligned to its element size", op);
+    const size_t need = nqk::block_norm_grad_ws_bytes(rows, dim, shape->gates);
+    if ((st = check_workspace(op, workspace, workspace_bytes, need))) return st;
+    const Span all[] = {{dh, rows * dim * xb}, {dy, dy ? rows * dim * xb : 0}, param_span(dpost, 1, dim, dim, p_dt),
+                        param_span(dgate, shape->gates, dim, dim, p_dt), param_span(dpre, 1, dim, dim, p_dt),
+                        {workspace, (int64_t)need}, {h_out, rows_span(rows, ldh, dim, xb)},
+                        {y, y ? rows_span(rows, ldy, dim, xb) : 0}, {dh_out, dh_out ? rows_span(rows, ldd, dim, xb) : 0},
+                        {dz, dz ? rows_span(rows, ldz, dim, xb) : 0}, param_span(post, 1, dim, dim, p_dt),
+                        param_span(gate, shape->gates, ldg, dim, p_dt), param_span(pre, 1, dim, dim, p_dt)};
+    if (any_overlap(all, 0, 6, 13)) return fail(NQ_ERR_ALIAS, "%s: an output overlaps another array", op);
+    nqk::BlockNormGradLaunch a;
+    a.h_out = h_out, a.y = y, a.dh_out = dh_out, a.dz = dz, a.post = post, a.gate = gate, a.pre = pre;
+    a.rows = rows, a.dim = dim, a.ldh = ldh, a.ldy = y ? ldy : 0, a.ldd = dh_out ? ldd : 0, a.ldz = dz ? ldz : 0;
+    a.ldg = gate ? ldg : 0, a.gates = gate || rows == 0 ? shape->gates : 1, a.dh = dh, a.dy = dy;
+    a.dpost = dpost, a.dgate = dgate, a.dpre = dpre, a.partials = static_cast<float *>(workspace);
+    a.eps = shape->eps, a.offset = shape->offset, a.scale = shape->scale, a.x_dt = x_dt, a.p_dt = p_dt;
+    return check_launch(op, nqk::launch_block_norm_grad(a, stream));
+}
+
+// ---- rotary positions
+static nq_status rope_impl(const char *op, bool back, const nq_rope_plan *plan, const void *x, nq_dtype x_dt, int64_t rows,
+                           int64_t ldx, int32_t heads, int32_t head_dim, const int32_t *positions, int64_t ldp, void *out,
+                           int64_t ldo, hipStream_t stream)
+{
+    g_last_error.clear();
+    if (!dtype_ok(x_dt)) return fail(NQ_ERR_DTYPE, "%s: unknown dtype x_dt=%d", op, (int)x_dt);
+    if (!plan) return fail(NQ_ERR_NULL, "%s: plan is null", op);
+    if (plan->layout != NQ_ROPE_HALVES && plan->layout != NQ_ROPE_PAIRS)
+        return fail(NQ_ERR_SHAPE, "%s: unknown layout=%d", op, plan->layout);
+    if (plan->rotary_dim < 2 || plan->rotary_dim % 2 || plan->rotary_dim > head_dim || head_dim > 1024)
+        return fail(NQ_ERR_SHAPE, "%s: rotary_dim=%d is not even in 2 .. head_dim=%d, or head_dim is over 1024", op,
+                    plan->rotary_dim, head_dim);
+    if (plan->axes < 1 || plan->axes > 16) return fail(NQ_ERR_SHAPE, "%s: axes=%d is not in 1 .. 16", op, plan->axes);
+    if (!finite(plan->scale) || plan->scale == 0.0f) return fail(NQ_ERR_SHAPE, "%s: scale is zero or not finite", op);
+    if (heads < 1 || heads > 65535) return fail(NQ_ERR_SHAPE, "%s: heads=%d is not in 1 .. 65535", op, heads);
+    const int64_t width = (int64_t)heads * head_dim, xb = dtype_bytes(x_dt);
+    if (rows < 0 || rows >= kMaxDim || (rows > 0 && rows > kMaxElems / width))
+        return fail(NQ_ERR_SHAPE, "%s: rows=%lld is negative or too large", op, (long long)rows);
+    if (ldp < rows && plan->axes > 1)
+        return fail(NQ_ERR_SHAPE, "%s: axis stride %lld of positions is below rows=%lld", op, (long long)ldp, (long long)rows);
+    if (ldp > kMaxElems) return fail(NQ_ERR_SHAPE, "%s: axis stride %lld of positions is too large", op, (long long)ldp);
+    if (rows == 0) return NQ_OK;
+    if (!plan->freq || !positions) return fail(NQ_ERR_NULL, "%s: freq and positions must be non-null", op);
+    nq_status st;
+    if ((st = check_plain_rows(op, back ? "dout" : "x", x, ldx, width, xb)) ||
+        (st = check_plain_rows(op, back ? "dx" : "out", out, ldo, width, xb)))
+        return st;
+    if (!aligned_to(plan->freq, 8) || !aligned_to(plan->axis, 4) || !aligned_to(positions, 4))
+        return fail(NQ_ERR_ALIGN, "%s: freq, axis or positions is not aligned to its element size", op);
+    const Span so{out, rows_span(rows, ldo, width, xb)};
+    const bool in_place = out == x && ldo == ldx;
+    if ((!in_place && overlap(so, Span{x, rows_span(rows, ldx, width, xb)})) ||
+        overlap(so, Span{plan->freq, plan->rotary_dim * 4}) || overlap(so, Span{plan->axis, plan->axis ? plan->rotary_dim * 2 : 0}) ||
+        overlap(so, Span{positions, rows_span(plan->axes, ldp, rows, 4)}))
+        return fail(NQ_ERR_ALIAS, "%s: the output overlaps an input without being it", op);
+    nqk::RopeLaunch a;
+    a.x = x, a.out = out, a.positions = positions, a.freq = plan->freq, a.axis = plan->axis;
+    a.rows = rows, a.ldx = ldx, a.ldo = ldo, a.ldp = ldp, a.heads = heads, a.head_dim = head_dim;
+    a.rotary = plan->rotary_dim, a.axes = plan->axes, a.pairs = plan->layout == NQ_ROPE_PAIRS;
+    a.cos_scale = plan->scale, a.sin_scale = back ? -plan->scale : plan->scale, a.x_dt = x_dt;
+    return check_launch(op, nqk::launch_rope(a, stream));
+}
+
+nq_status nq_rope(const nq_rope_plan *plan, const void *x, nq_dtype x_dt, int64_t rows, int64_t ldx, int32_t heads,
+                  int32_t head_dim, const int32_t *positions, int64_t ldp, void *out, int64_t ldo, hipStream_t stream)
+{
+    return rope_impl("nq_rope", false, plan, x, x_dt, rows, ldx, heads, head_dim, positions, ldp, out, ldo, stream);
+}
+
+nq_status nq_rope_grad(const nq_rope_plan *plan, const void *dout, nq_dtype x_dt, int64_t rows, int64_t ldd,
+                       int32_t heads, int32_t head_dim, const int32_t *positions, int64_t ldp, void *dx, int64_t ldx,
+                       hipStream_t stream)
+{
+    return rope_impl("nq_rope_grad", true, plan, dout, x_dt, rows, ldd, heads, head_dim, positions, ldp, dx, ldx, stream);
 }
 
 const char *nq_status_string(nq_status s)

@@ -1,0 +1,110 @@
+// Runs of E neighbouring elements as fp32, moved by the widest accesses that
+// their size has.  A run of more than one element is aligned to its size (or
+// to 16 bytes).
+#pragma once
+
+#include "nq_device.h"
+
+namespace nqk {
+
+typedef uint32_t words4 __attribute__((ext_vector_type(4)));
+typedef uint32_t words2 __attribute__((ext_vector_type(2)));
+
+// E elements as they lie in memory.
+template <typename T, int E> struct Raw {
+    static constexpr int bytes = E * (int)sizeof(T), words = bytes < 4 ? 1 : bytes / 4;
+    uint32_t w[words];
+};
+
+template <typename T, int E> __device__ __forceinline__ Raw<T, E> load_raw(const T *p)
+{
+    Raw<T, E> r;
+    if constexpr (Raw<T, E>::bytes % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < Raw<T, E>::words / 4; ++i) {
+            const words4 v = reinterpret_cast<const words4 *>(p)[i];
+            r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (Raw<T, E>::bytes == 8) {
+        const words2 v = *reinterpret_cast<const words2 *>(p);
+        r.w[0] = v.x, r.w[1] = v.y;
+    } else if constexpr (Raw<T, E>::bytes == 4) r.w[0] = *reinterpret_cast<const uint32_t *>(p);
+    else r.w[0] = *reinterpret_cast<const uint16_t *>(p);
+    return r;
+}
+
+template <typename T, int E> __device__ __forceinline__ void store_raw(T *p, const Raw<T, E> &r)
+{
+    if constexpr (Raw<T, E>::bytes % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < Raw<T, E>::words / 4; ++i)
+            reinterpret_cast<words4 *>(p)[i] = words4{r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]};
+    } else if constexpr (Raw<T, E>::bytes == 8) *reinterpret_cast<words2 *>(p) = words2{r.w[0], r.w[1]};
+    else if constexpr (Raw<T, E>::bytes == 4) *reinterpret_cast<uint32_t *>(p) = r.w[0];
+    else *reinterpret_cast<uint16_t *>(p) = (uint16_t)r.w[0];
+}
+
+template <typename T, int E> __device__ __forceinline__ Raw<T, E> raw_zero()
+{
+    Raw<T, E> r;
+#pragma unroll
+    for (int i = 0; i < Raw<T, E>::words; ++i) r.w[i] = 0u;
+    return r;
+}
+
+template <typename T, int E> __device__ __forceinline__ void unpack(const Raw<T, E> &r, float *v)
+{
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = __uint_as_float(r.w[i]);
+    } else if constexpr (E == 1) v[0] = __uint_as_float(r.w[0] << 16);
+    else {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            v[2 * i] = __uint_as_float(r.w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+        }
+    }
+}
+
+// Rounded to nearest, ties to even; a NaN stays one.
+template <typename T, int E> __device__ __forceinline__ Raw<T, E> pack(const float *v)
+{
+    Raw<T, E> r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) r.w[i] = __float_as_uint(v[i]);
+    } else if constexpr (E == 1) r.w[0] = f32_to_bf16(v[0]);
+    else {
+        typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            const bf2 b = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
+            r.w[i] = __builtin_bit_cast(uint32_t, b);
+        }
+    }
+    return r;
+}
+
+template <typename T, int E> __device__ __forceinline__ void load_run(const T *p, float *v)
+{
+    unpack<T, E>(load_raw<T, E>(p), v);
+}
+template <typename T, int E> __device__ __forceinline__ void store_run(T *p, const float *v)
+{
+    store_raw<T, E>(p, pack<T, E>(v));
+}
+
+// The sum over the first LANES lanes' group of each lane (LANES a power of two).
+template <int LANES> __device__ __forceinline__ float lane_sum(float v, int lane)
+{
+    if constexpr (LANES > 1) v += xor_lane<1>(v, lane);
+    if constexpr (LANES > 2) v += xor_lane<2>(v, lane);
+    if constexpr (LANES > 4) v += xor_lane<4>(v, lane);
+    if constexpr (LANES > 8) v += xor_lane<8>(v, lane);
+    if constexpr (LANES > 16) v += xor_lane<16>(v, lane);
+    if constexpr (LANES > 32) v += xor_lane<32>(v, lane);
+    return v;
+}
+
+}  // namespace nqk

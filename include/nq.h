@@ -576,6 +576,142 @@ nq_status nq_moe_route_grad(const nq_moe_router *router, const void *logits, nq_
                             int64_t ld, const uint32_t *ids, const float *dweights, void *dlogits,
                             hipStream_t stream);
 
+/* ---------------------------------------------------------------- tokens sorted by expert */
+
+/* The pairs (token, choice) that nq_moe_route chose, in the order of their
+ * experts, so that each expert's rows are neighbours.  Pair (t, j) has the number
+ * t * top_k + j; among pairs of one expert the lower number comes first.  ids
+ * [tokens, top_k] as nq_moe_route gives them, or any: an id >= experts is
+ * dropped (an expert of another device, say), and dropped pairs come last.
+ * Outputs:
+ *   starts [experts + 1] int32: expert e has rows starts[e] .. starts[e + 1] - 1;
+ *     starts[experts] rows are not dropped;
+ *   place [tokens, top_k] int32: each pair's row;
+ *   row_token, row_expert [tokens * top_k] uint32: each row's token and its id as
+ *     it was in ids -- what nq_gather_qmm_lhs takes as lhs_idx and rhs_idx.
+ * experts is 1 .. 1024, top_k 1 .. 32, tokens * top_k below 2^31.  tokens == 0
+ * writes starts (zeros).  All arrays are 4-byte aligned. */
+size_t nq_moe_sort_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts);
+nq_status nq_moe_sort(const uint32_t *ids, int64_t tokens, int32_t top_k, int32_t experts, int32_t *starts,
+                      int32_t *place, uint32_t *row_token, uint32_t *row_expert, void *workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+
+/* What nq_moe_sort made, for the calls below.  They read starts[experts] and
+ * place on the device: a place outside 0 .. tokens * top_k - 1 has no row and
+ * counts as a dropped pair; two pairs with one place race for its row. */
+typedef struct {
+    const int32_t *starts;   /* [experts + 1] */
+    const int32_t *place;    /* [tokens, top_k] */
+    int64_t tokens;
+    int32_t top_k, experts;
+} nq_moe_order;
+
+/* Tokens to their experts: xs [tokens * top_k, hidden] (dense, x_dt), row
+ * place[t, j] of it x[t]; rows of dropped pairs are zeros.  x [tokens, hidden],
+ * hidden at least 1, with row stride ldx in elements.  Here and below arrays need only be aligned
+ * to their elements; 16-byte aligned rows are moved faster. */
+nq_status nq_moe_dispatch(const nq_moe_order *order, const void *x, nq_dtype x_dt, int64_t ldx, int64_t hidden,
+                          void *xs, hipStream_t stream);
+
+/* Its gradient: dx[t] = sum over j of dxs[place[t, j]], dropped pairs left out;
+ * dxs [tokens * top_k, hidden] and dx [tokens, hidden] dense, fp32 sums in the
+ * order of j. */
+nq_status nq_moe_dispatch_grad(const nq_moe_order *order, const void *dxs, nq_dtype x_dt, int64_t hidden, void *dx,
+                               hipStream_t stream);
+
+/* The experts' rows back to their tokens: y[t] = residual[t] + sum over j of
+ * weights[t, j] * ys[place[t, j]], dropped pairs left out.  ys [tokens * top_k,
+ * hidden] and y [tokens, hidden] dense (x_dt); weights [tokens, top_k] fp32, or
+ * null for ones; residual [tokens, hidden] with row stride ldr, or null for
+ * zeros.  fp32 sums in the order of j, rounded once. */
+nq_status nq_moe_combine(const nq_moe_order *order, const void *ys, nq_dtype x_dt, int64_t hidden,
+                         const float *weights, const void *residual, int64_t ldr, void *y, hipStream_t stream);
+
+/* Its gradient: dys[place[t, j]] = weights[t, j] * dy[t] (zeros for dropped
+ * pairs) and, unless dweights is null, dweights[t, j] = sum of dy[t] *
+ * ys[place[t, j]] (fp32; zero for dropped pairs).  dy [tokens, hidden] with row
+ * stride ldd; ys is not read without dweights and may then be null.  The
+ * gradient of the residual is dy. */
+nq_status nq_moe_combine_grad(const nq_moe_order *order, const void *dy, nq_dtype x_dt, int64_t ldd, int64_t hidden,
+                              const void *ys, const float *weights, void *dys, float *dweights, hipStream_t stream);
+
+/* ---------------------------------------------------------------- norms, gate and residual */
+
+/* A block's output joins the residual stream and the next block's input
+ * leaves it.  For each of `rows` rows of `dim` columns (1 .. 16384), h the
+ * stream and y the block's output:
+ *   u     = y / sqrt(mean(y^2) + eps) * (post + offset), or y where post is null;
+ *   h_out = h + scale * gate * u             (gate 1 where it is null);
+ *   z     = h_out / sqrt(mean(h_out^2) + eps) * (pre + offset).
+ * y null: h_out = h (not written, h_out null too; post and gate null).  pre and
+ * z null: no z.  At least one of the two is there.  h, y in x_dt with row
+ * strides ldh, ldy; h_out, z dense in x_dt; post, gate, pre in p_dt; post and
+ * pre [dim]; gate [gates, dim] with row stride ldg, row r taking gate r / (rows /
+ * gates), so gates divides rows: 1 for a gate per column, the number of
+ * sequences for one per sequence, rows for one per row.  z is made of h_out
+ * before its rounding to x_dt.  Squares are summed in fp32: rows past 2^63 give a
+ * norm of zero.  eps is positive and finite, offset and scale finite.  Arrays need
+ * only be aligned to their elements; 16-byte aligned rows are moved faster. */
+typedef struct {
+    int64_t rows, dim, gates;
+    float eps, offset, scale;
+} nq_block_norm_shape;
+nq_status nq_block_norm(const nq_block_norm_shape *shape, const void *h, int64_t ldh, const void *y, int64_t ldy,
+                        nq_dtype x_dt, const void *post, const void *gate, int64_t ldg, const void *pre,
+                        nq_dtype p_dt, void *h_out, void *z, hipStream_t stream);
+
+/* Its gradient, from h_out as it was stored (h where y is null), y and the
+ * gradients of both outputs, dh_out and dz (null: zero; at least one of them):
+ *   dh [rows, dim]: of h;   dy [rows, dim]: of y (null exactly where y is);
+ *   dpost, dpre [dim], dgate [gates, dim] in p_dt: of the parameters, each null
+ *   where it is not wanted (and where its parameter is null).
+ * All inputs' row strides are in elements; outputs are dense.  dpre needs dz,
+ * and dz needs pre.  Parameter gradients are sums over rows in fp32 in a fixed order.
+ * rows == 0 writes zeros to the parameters' gradients.  workspace: 16-byte aligned, at
+ * least nq_block_norm_grad_workspace_bytes (room for partial sums of all three
+ * parameters). */
+size_t nq_block_norm_grad_workspace_bytes(const nq_block_norm_shape *shape);
+nq_status nq_block_norm_grad(const nq_block_norm_shape *shape, const void *h_out, int64_t ldh, const void *y,
+                             int64_t ldy, const void *dh_out, int64_t ldd, const void *dz, int64_t ldz,
+                             nq_dtype x_dt, const void *post, const void *gate, int64_t ldg, const void *pre,
+                             nq_dtype p_dt, void *dh, void *dy, void *dpost, void *dgate, void *dpre,
+                             void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------- rotary positions */
+
+/* How heads are turned by their position.  The first rotary_dim columns of a
+ * head are pairs: pair i is columns i and i + rotary_dim / 2 (NQ_ROPE_HALVES) or 2 i
+ * and 2 i + 1 (NQ_ROPE_PAIRS).  freq [rotary_dim / 2] float64 and axis
+ * [rotary_dim / 2] int32 (null: axis 0 for all) are device arrays. */
+typedef enum { NQ_ROPE_HALVES = 1, NQ_ROPE_PAIRS = 2 } nq_rope_layout;
+typedef struct {
+    const double *freq;
+    const int32_t *axis;
+    int32_t rotary_dim;   /* even, 2 .. 1024 */
+    int32_t axes;         /* 1 .. 16 */
+    int32_t layout;       /* nq_rope_layout */
+    float scale;          /* finite, nonzero */
+} nq_rope_plan;
+
+/* out = x with each row's heads turned: with t = freq[i] * positions[axis[i],
+ * row] (taken in float64), pair (a, b) becomes scale * (a cos t - b sin t) and
+ * scale * (b cos t + a sin t); columns from rotary_dim on are copied.  x and out
+ * [rows, heads, head_dim] (x_dt) with row strides ldx and ldo in elements;
+ * positions [axes, rows] int32 with axis stride ldp, any values.  heads is 1 ..
+ * 65535, head_dim rotary_dim .. 1024.  An axis outside 0 .. axes - 1 turns by
+ * nothing.  out may be x itself (with ldo = ldx): heads are then turned in
+ * place, e.g. the queries and keys among a fused projection's columns.  Arrays
+ * need only be aligned to their elements; 16-byte aligned rows and halves are
+ * moved faster. */
+nq_status nq_rope(const nq_rope_plan *plan, const void *x, nq_dtype x_dt, int64_t rows, int64_t ldx, int32_t heads,
+                  int32_t head_dim, const int32_t *positions, int64_t ldp, void *out, int64_t ldo,
+                  hipStream_t stream);
+
+/* Its gradient for x: dout turned back, by -t and with the same scale. */
+nq_status nq_rope_grad(const nq_rope_plan *plan, const void *dout, nq_dtype x_dt, int64_t rows, int64_t ldd,
+                       int32_t heads, int32_t head_dim, const int32_t *positions, int64_t ldp, void *dx, int64_t ldx,
+                       hipStream_t stream);
+
 /* ---------------------------------------------------------------- errors */
 
 /* A static description of a status code. */

@@ -1,0 +1,560 @@
+"""The steps between a decoder layer's products (norms with gate and residual
+scale, rotary positions, tokens sorted by expert) on the GPU against the plain
+references of oracle/layer.py in float64.
+
+Tolerances count roundings: U = 2^-24 for each fp32 operation on the way, and
+half a step of the output's type for its own rounding."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import bits_equal
+from group_wise_affine_quantize_amd import _binding as B
+from oracle import layer as L
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+U = 2.0 ** -24
+HALF = {t: torch.finfo(t).eps / 2 for t in DT.values()}
+SMALLEST = 2.0 ** -126      # fp32's and bf16's normal numbers; below, a step is absolute
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    torch.cuda.set_device(0)
+    B.load_library()
+
+
+def f64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def normal(seed, shape, dtype, sigma=1.0):
+    return torch.from_numpy(np.random.default_rng(seed).standard_normal(shape) * sigma).cuda().to(DT[dtype])
+
+
+def within(got, want, bound):
+    """|got - want| <= bound (from fp32 roundings) + half a step of got's type."""
+    err = np.abs(f64(got) - want)
+    limit = bound + HALF[got.dtype] * (np.abs(want) + bound) + SMALLEST
+    bad = ~(err <= limit)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3].tolist(), float((err / limit)[bad].max()))
+
+
+def strided(t, before=3, behind=5):
+    """The same rows as columns of a wider tensor, off any alignment when `before` is odd."""
+    wide = torch.full((t.shape[0], before + t.shape[1] + behind), float("nan"), dtype=t.dtype, device="cuda")
+    wide[:, before:before + t.shape[1]] = t
+    return wide[:, before:before + t.shape[1]]
+
+
+# ---------------------------------------------------------------- norms, gate and residual
+# Sums of squares: at most 16 terms in a thread, 6 steps in a wave, 16 waves, each
+# relative to the sum of positive terms: 38 U; half of it reaches 1 / sqrt, which adds 2,
+# and the products behind it 5 more.
+C = 32 * U
+
+
+def norm_inputs(seed, rows, dim, dt, pdt, post, gates, pre, y=True):
+    t = {"h": normal(seed, (rows, dim), dt, 2.0), "y": normal(seed + 1, (rows, dim), dt, 0.7) if y else None,
+         "post": normal(seed + 2, (dim,), pdt) if post else None,
+         "gate": normal(seed + 3, (gates, dim) if gates != "channel" else (dim,), pdt) if gates else None,
+         "pre": normal(seed + 4, (dim,), pdt) if pre else None}
+    return t
+
+
+def check_norm(t, got, o):
+    """h_out and z of a call."""
+    n = {k: f64(v) for k, v in t.items()}
+    want_h, want_z = L.block_norm(**n, **o)
+    h_out, z = got
+    bound = np.zeros_like(want_h)
+    if t["y"] is not None:
+        bound = C * np.abs(want_h - n["h"]) + U * np.abs(want_h)
+        within(h_out, want_h, bound)
+    if t["pre"] is not None:
+        r = 1 / np.sqrt((want_h ** 2).mean(-1, keepdims=True) + o["eps"])
+        w = np.abs(n["pre"] + o["offset"]) + U * np.abs(n["pre"])
+        # an element's own error, and the norm's: the mean of the errors times the elements
+        spread = (bound * np.abs(want_h)).mean(-1, keepdims=True) * r * r
+        within(z, want_z, (bound * r + np.abs(want_h) * r * (C + spread)) * w)
+    else:
+        assert z is None
+
+
+def check_norm_grad(t, h_out, dh_out, dz, got, o):
+    n = {k: f64(v) for k, v in t.items()}
+    x, a, b = f64(h_out), f64(dh_out), f64(dz)
+    want = L.block_norm_grad(x, n["y"], a, b, n["post"], n["gate"], n["pre"], **o)
+    dh, dy, dpost, dgate, dpre = got
+    rows = len(x)
+    in_order = (rows + 64) * U      # a sum over rows, whatever its order
+    d_bound = U * np.abs(want[0])
+    if b is not None:
+        r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + o["eps"])
+        v, xh = np.abs(b * (n["pre"] + o["offset"])) + 2 * U * np.abs(b * n["pre"]), np.abs(x * r)
+        d_bound = d_bound + 2 * C * r * (v + xh * (v * xh).mean(-1, keepdims=True))
+        if dpre is not None:
+            terms = np.abs(b) * xh
+            within(dpre, want[4], (in_order + C) * terms.sum(0))
+    within(dh, want[0], d_bound)
+    if n["y"] is None:
+        assert dy is None and dpost is None and dgate is None
+        return
+    gate = np.abs(L.rows_of_gate(n["gate"], rows)) if n["gate"] is not None else np.ones_like(x)
+    s = abs(o["scale"])
+    ry = 1 / np.sqrt((n["y"] ** 2).mean(-1, keepdims=True) + o["eps"])
+    yh = np.abs(n["y"] * ry)
+    weight = np.ones(x.shape[1]) if n["post"] is None else np.abs(n["post"] + o["offset"]) + U * np.abs(n["post"])
+    size, off = s * gate * weight * np.abs(want[0]), s * gate * weight * d_bound
+    if n["post"] is None:
+        within(dy, want[1], off + 4 * U * size)
+        u = np.abs(n["y"])
+    else:
+        within(dy, want[1], ry * (off + yh * (off * yh).mean(-1, keepdims=True)) +
+               2 * C * ry * (size + yh * (size * yh).mean(-1, keepdims=True)))
+        u = yh * weight
+        if dpost is not None:
+            terms = s * gate * yh
+            within(dpost, want[2], (terms * d_bound).sum(0) + (in_order + C) * (terms * np.abs(want[0])).sum(0))
+    if n["gate"] is not None and dgate is not None:
+        gates = len(n["gate"]) if n["gate"].ndim == 2 else 1
+        summed = lambda m: m.reshape(gates, rows // gates, -1).sum(1).reshape(n["gate"].shape)
+        within(dgate, want[3], summed(s * u * d_bound) + (in_order + C) * summed(s * u * np.abs(want[0])))
+
+
+# rows, dim, x dtype, parameters' dtype, post, gates, pre
+NORMS = [
+    (1, 1, "f32", "f32", True, "channel", True),
+    (3, 2, "bf16", "f32", True, 3, True),
+    (5, 7, "f32", "bf16", True, 0, True),
+    (4, 64, "bf16", "bf16", True, "channel", True),
+    (9, 65, "bf16", "bf16", True, 3, True),
+    (2, 256, "f32", "f32", True, 2, True),
+    (7, 257, "f32", "f32", True, 7, True),
+    (33, 512, "bf16", "bf16", True, "channel", True),
+    (6, 520, "bf16", "f32", False, 3, True),
+    (16, 1000, "bf16", "bf16", True, 0, True),
+    (31, 1407, "f32", "f32", True, 31, True),
+    (20, 1408, "bf16", "f32", True, 4, False),
+    (100, 2048, "bf16", "f32", True, 4, True),
+    (11, 2049, "bf16", "bf16", True, 11, True),
+    (40, 4096, "bf16", "bf16", True, "channel", True),
+    (6, 4096, "f32", "f32", False, 0, True),
+    (5, 5000, "f32", "bf16", True, 5, True),
+    (4, 8192, "bf16", "bf16", True, 2, True),
+    (3, 8193, "f32", "f32", True, "channel", True),
+    (5, 16384, "bf16", "bf16", True, 5, True),
+    (4, 16384, "f32", "f32", True, "channel", True),
+    (3, 16383, "bf16", "f32", True, 3, True),
+]
+
+
+@pytest.mark.parametrize("rows,dim,dt,pdt,post,gates,pre", NORMS)
+def test_block_norm_and_gradient(rows, dim, dt, pdt, post, gates, pre):
+    o = dict(scale=0.75, offset=1.0 if dim % 2 else 0.0, eps=1e-5)
+    t = norm_inputs(rows * 7 + dim, rows, dim, dt, pdt, post, gates, pre)
+    got = B.nq_block_norm(**t, **o)
+    assert got[0].dtype == DT[dt]
+    check_norm(t, got, o)
+    dh_out, dz = normal(91, (rows, dim), dt, 0.1), normal(92, (rows, dim), dt, 0.1) if pre else None
+    grads = B.nq_block_norm_grad(got[0], t["y"], dh_out, dz, t["post"], t["gate"], t["pre"], **o)
+    check_norm_grad(t, got[0], dh_out, dz, grads, o)
+    # the same rows as columns of wider tensors, at odd offsets: the same values
+    s = {k: strided(v) if k in ("h", "y") or (k == "gate" and v is not None and v.dim() == 2) else v for k, v in t.items()}
+    again = B.nq_block_norm(**s, **o)
+    check_norm(t, again, o)
+    grads = B.nq_block_norm_grad(strided(again[0]), s["y"], strided(dh_out), None if dz is None else strided(dz),
+                                 s["post"], s["gate"], s["pre"], **o)
+    check_norm_grad(t, again[0], dh_out, dz, grads, o)
+
+
+def test_norm_forms():
+    """z alone, no gradient of one of the outputs, no parameters' gradients."""
+    o = dict(scale=1.0, offset=0.0, eps=1e-6)
+    t = norm_inputs(5, 12, 192, "bf16", "bf16", False, 0, True, y=False)
+    h_out, z = B.nq_block_norm(**t, **o)
+    assert h_out is t["h"]
+    check_norm(t, (h_out, z), o)
+    dh_out, dz = normal(6, (12, 192), "bf16"), normal(7, (12, 192), "bf16")
+    for a, b in ((dh_out, dz), (None, dz), (dh_out, None)):
+        check_norm_grad(t, h_out, a, b, B.nq_block_norm_grad(h_out, None, a, b, pre=t["pre"], **o), o)
+    t = norm_inputs(8, 12, 192, "f32", "f32", True, "channel", True)
+    h_out, _ = B.nq_block_norm(**t, **o)
+    dh_out, dz = normal(6, (12, 192), "f32"), normal(7, (12, 192), "f32")
+    p = {k: t[k] for k in ("post", "gate", "pre")}
+    for a, b in ((None, dz), (dh_out, None)):
+        check_norm_grad(t, h_out, a, b, B.nq_block_norm_grad(h_out, t["y"], a, b, **p, **o), o)
+    grads = B.nq_block_norm_grad(h_out, t["y"], dh_out, dz, **p, **o)
+    bare = B.nq_block_norm_grad(h_out, t["y"], dh_out, dz, parameters=False, **p, **o)
+    assert bits_equal(bare[0], grads[0]) and bits_equal(bare[1], grads[1]) and bare[2:] == (None, None, None)
+
+
+@pytest.mark.parametrize("rows,gates", [(700, 0), (700, "channel"), (700, 7), (700, 350), (9000, 3), (9000, 1125), (2048, 2048),
+                                        (17, "channel")])
+def test_norm_parameter_gradients_over_many_rows(rows, gates):
+    """Chunks that are parts of a gate's rows, one gate's, or several gates'."""
+    o = dict(scale=0.5, offset=0.0, eps=1e-6)
+    t = norm_inputs(rows, rows, 96, "f32", "f32", True, gates, True)
+    h_out, _ = B.nq_block_norm(**t, **o)
+    dh_out, dz = normal(1, (rows, 96), "f32"), normal(2, (rows, 96), "f32")
+    p = {k: t[k] for k in ("post", "gate", "pre")}
+    grads = B.nq_block_norm_grad(h_out, t["y"], dh_out, dz, **p, **o)
+    check_norm_grad(t, h_out, dh_out, dz, grads, o)
+    again = B.nq_block_norm_grad(h_out, t["y"], dh_out, dz, **p, **o)
+    assert all(a is b is None or bits_equal(a, b) for a, b in zip(grads, again))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_norm_rows_with_no_numbers(dt):
+    """NaN, infinities, zeros and rows whose squares leave fp32 stay in their row."""
+    o = dict(scale=1.0, offset=0.0, eps=1e-6)
+    t = norm_inputs(3, 9, 300, dt, dt, True, 9, True)
+    clean = B.nq_block_norm(**t, **o)
+    t["y"][1, 7] = float("nan")
+    t["h"][2, 3] = float("inf")
+    t["y"][4] = 0.0
+    t["h"][5] = 0.0
+    t["y"][5] = 0.0
+    t["y"][6] = 1e30        # squares pass fp32: a norm of zero
+    got = B.nq_block_norm(**t, **o)
+    for r in (0, 3, 7, 8):
+        assert all(bits_equal(a[r], b[r]) for a, b in zip(got, clean))
+    assert got[0][1].isnan().all() and got[1][1].isnan().all()
+    assert got[0][2, 3] == float("inf") and got[1][2, 3].isnan()
+    assert bits_equal(got[0][4], t["h"][4]) and (got[1][5] == 0).all() and bits_equal(got[0][6], t["h"][6])
+    d = normal(4, (9, 300), dt)
+    p = {k: t[k] for k in ("post", "gate", "pre")}
+    dh, dy, _, dgate, _ = B.nq_block_norm_grad(got[0], t["y"], d, d, **p, **o)
+    for r in (0, 3, 4, 5, 6, 7, 8):
+        assert dh[r].isfinite().all() and dy[r].isfinite().all() and dgate[r].isfinite().all()
+    # a row of zeros: 1 / sqrt(eps) times what arrives
+    want = f64(d)[5] + f64(d)[5] * f64(t["pre"]) * 1e3
+    within(dh[5], want, 8 * U * np.abs(f64(d)[5]) * (1 + np.abs(f64(t["pre"])) * 1e3))
+
+
+def test_norm_of_more_rows_than_workgroups():
+    rows = (1 << 22) + 5000
+    h = (torch.arange(rows, device="cuda") % 1001 - 500).float()[:, None].to(torch.bfloat16)
+    one = torch.ones(1, device="cuda")
+    h_out, z = B.nq_block_norm(h, h, pre=one, scale=2.0)
+    assert torch.equal(h_out, (3 * h.float()).to(torch.bfloat16))
+    assert torch.equal(z, torch.where(h == 0, 0.0, torch.sign(h.float())).to(torch.bfloat16))
+
+
+def test_norm_of_no_rows():
+    e = torch.empty((0, 40), device="cuda")
+    p = torch.ones(40, device="cuda")
+    h_out, z = B.nq_block_norm(e, e, p, p, p)
+    assert h_out.shape == z.shape == (0, 40)
+    dh, dy, dpost, dgate, dpre = B.nq_block_norm_grad(e, e, e, e, p, p, p)
+    assert dh.shape == dy.shape == (0, 40)
+    assert (dpost == 0).all() and (dgate == 0).all() and (dpre == 0).all()
+
+
+# ---------------------------------------------------------------- rotary positions
+ROPES = [  # rows, heads, behind, head_dim, rotary, layout, axes, dtype, scale
+    (1, 1, 0, 2, 2, "halves", 1, "f32", 1.0),
+    (5, 3, 1, 6, 4, "pairs", 2, "f32", 1.0),
+    (7, 2, 0, 10, 6, "halves", 3, "bf16", 1.5),
+    (16, 40, 8, 128, 128, "halves", 1, "bf16", 1.0),
+    (33, 18, 2, 64, 48, "pairs", 3, "f32", 1.0),
+    (9, 5, 3, 80, 80, "halves", 1, "bf16", 1.0),
+    (9, 5, 3, 96, 48, "halves", 3, "f32", 0.5),
+    (12, 7, 0, 96, 72, "pairs", 2, "bf16", 1.0),
+    (4, 6, 1, 192, 64, "halves", 1, "f32", 1.0),
+    (3, 2, 0, 256, 256, "pairs", 4, "bf16", 1.0),
+    (2, 3, 1, 1024, 1024, "halves", 16, "f32", 1.0),
+    (2, 1, 0, 1023, 1022, "pairs", 1, "bf16", 1.0),
+]
+
+
+def rope_bound(x, rotary, layout, scale):
+    """Cosine, sine and their scale rounded, two products and a sum: 4 U of both elements."""
+    a = np.abs(x[..., :rotary])
+    pair = np.concatenate([a[..., rotary // 2:], a[..., :rotary // 2]], -1) if layout == "halves" else \
+        a.reshape(*a.shape[:-1], -1, 2)[..., ::-1].reshape(a.shape)
+    return np.concatenate([4 * U * scale * (a + pair), 0 * x[..., rotary:]], -1)
+
+
+@pytest.mark.parametrize("rows,heads,behind,dim,rotary,layout,axes,dt,scale", ROPES)
+def test_rope_and_gradient(rows, heads, behind, dim, rotary, layout, axes, dt, scale):
+    rng = np.random.default_rng(rows + dim)
+    half = rotary // 2
+    axis = rng.integers(0, axes, half)
+    axis[-1] = axes - 1
+    freq = 10000.0 ** (-np.arange(half) / half)
+    pos = rng.integers(-1_000_000, 1_000_000, (axes, rows))
+    rope = B.Rope(rotary, axis=axis.tolist(), freq=torch.from_numpy(freq), layout=layout, scale=scale)
+    positions = torch.from_numpy(pos).to(torch.int32).cuda()
+    fused = normal(rows, (rows, heads + behind, dim), dt)
+    x = fused[:, :heads]
+    kept = fused.clone()
+    out = B.nq_rope(rope, x, positions)
+    n = f64(x)
+    bound = rope_bound(n, rotary, layout, scale)
+    within(out, L.rope(n, pos, freq, axis, layout, scale), bound)
+    assert bits_equal(out[..., rotary:].contiguous(), x[..., rotary:].contiguous()) and bits_equal(fused, kept)
+    dx = B.nq_rope_grad(rope, x, positions)
+    within(dx, L.rope(n, pos, freq, axis, layout, scale, back=True), bound)
+    # in place among the other columns; positions with a stride between axes
+    wide = torch.zeros((axes, rows + 3), dtype=torch.int32, device="cuda")
+    wide[:, :rows] = positions
+    assert B.nq_rope(rope, x, wide[:, :rows], out=x) is x
+    assert bits_equal(x.contiguous(), out) and bits_equal(fused[:, heads:].contiguous(), kept[:, heads:].contiguous())
+    # rows off any alignment
+    odd = torch.empty(rows * (heads * dim + 1) + 1, dtype=DT[dt], device="cuda")[1:]
+    odd = odd.as_strided((rows, heads, dim), (heads * dim + 1, dim, 1))
+    odd.copy_(kept[:, :heads])
+    again = B.nq_rope(rope, odd, positions, out=torch.empty_like(out))
+    assert bits_equal(again, out)
+
+
+def test_rope_defaults_and_sections():
+    x = normal(3, (6, 2, 64), "f32")
+    pos = torch.arange(6, dtype=torch.int32, device="cuda") * 1000
+    freq = 500.0 ** (-np.arange(32) / 32)
+    got = B.nq_rope(B.Rope(64, theta=500.0), x, pos)
+    within(got, L.rope(f64(x), f64(pos[None]), freq), rope_bound(f64(x), 64, "halves", 1.0))
+    three = torch.stack([pos, pos // 7, pos // 11])
+    got = B.nq_rope(B.Rope(64, theta=500.0, sections=[16, 8, 8]), x, three)
+    want = L.rope(f64(x), f64(three), freq, [0] * 16 + [1] * 8 + [2] * 8)
+    within(got, want, rope_bound(f64(x), 64, "halves", 1.0))
+    assert B.nq_rope(B.Rope(64), x[:0], pos[:0]).shape == (0, 2, 64)
+
+
+def test_rope_far_positions_and_odd_axes():
+    """The angle is right to 64 bits at both ends of int32; a pair without an axis is not turned."""
+    pos = torch.tensor([[2 ** 31 - 1, -2 ** 31, 2 ** 31 - 2, 0]], dtype=torch.int32, device="cuda")
+    freq = np.array([1.0, 0.999, 1e-3, 0.0, np.pi, 1e-9])
+    rope = B.Rope(12, freq=freq)
+    x = normal(8, (4, 1, 12), "f32")
+    # position times frequency is up to 7e9, rounded to 2^-21: 2^-20 covers both elements
+    within(B.nq_rope(rope, x, pos), L.rope(f64(x), f64(pos), freq), rope_bound(f64(x), 12, "halves", 1.0) + 2.0 ** -20)
+    rope = B.Rope(12, freq=freq, axis=[0] * 6)
+    rope.axis.copy_(torch.tensor([0, 1, -1, 0, 7, 0], dtype=torch.int32))
+    got = B.nq_rope(rope, x, pos)
+    axis = [0, 1, -1, 0, 7, 0]
+    within(got, L.rope(f64(x), f64(pos), freq, axis), rope_bound(f64(x), 12, "halves", 1.0) + 2.0 ** -20)
+    assert bits_equal(got[..., [1, 2, 4, 7, 8, 10]].contiguous(), x[..., [1, 2, 4, 7, 8, 10]].contiguous())
+
+
+# ---------------------------------------------------------------- tokens sorted by expert
+def ids_of(seed, tokens, k, experts, dropped=0.0):
+    rng = np.random.default_rng(seed)
+    ids = rng.integers(0, experts, (tokens, k)).astype(np.uint32)       # the same expert twice, too
+    gone = rng.random((tokens, k)) < dropped
+    return np.where(gone, rng.choice(np.array([experts, experts + 7, 2 ** 32 - 1], np.uint32), (tokens, k)), ids)
+
+
+def on_gpu(ids):
+    return torch.from_numpy(ids.astype(np.uint32).view(np.int32)).cuda()
+
+
+def check_sort(order, ids, experts):
+    starts, place, token, expert = L.moe_sort(ids, experts)
+    host = lambda t: t.cpu().numpy()
+    assert np.array_equal(host(order.starts), starts) and np.array_equal(host(order.place), place)
+    assert np.array_equal(host(order.row_token), token)
+    assert np.array_equal(host(order.row_expert).view(np.uint32).astype(np.int64), expert)
+    return place, int(starts[-1])
+
+
+SORTS = [(0, 3, 5, 0.0), (1, 1, 1, 0.0), (1, 8, 8, 0.0), (1, 4, 2, 1.0), (3, 32, 1024, 0.2), (64, 1, 64, 0.0), (65, 1, 2, 0.5),
+         (1000, 6, 64, 0.0), (1024, 8, 256, 0.3), (1025, 8, 256, 0.0), (4097, 2, 7, 0.1), (9000, 8, 160, 0.0), (50000, 1, 1024, 0.05),
+         (40000, 8, 33, 0.8), (300000, 4, 1, 0.0)]
+
+
+@pytest.mark.parametrize("tokens,k,experts,dropped", SORTS)
+def test_sort(tokens, k, experts, dropped):
+    ids = ids_of(tokens + k, tokens, k, experts, dropped)
+    order = B.nq_moe_sort(on_gpu(ids), experts)
+    check_sort(order, ids, experts)
+    # into an order that is there, past a workspace of any content
+    other = ids_of(tokens + k + 1, tokens, k, experts, dropped)
+    need = B.nq_moe_sort_workspace_bytes(tokens, k, experts)
+    ws = torch.full((max(16, need),), 255, dtype=torch.uint8, device="cuda")
+    assert B.nq_moe_sort(on_gpu(other), experts, order=order, workspace=ws) is order
+    check_sort(order, other, experts)
+
+
+MOVES = [(1, 1, 1, 1, "f32", 0.0), (3, 2, 4, 3, "bf16", 0.4), (2, 32, 40, 8, "bf16", 0.1), (17, 4, 32, 64, "bf16", 0.0),
+         (9, 3, 8, 100, "f32", 0.3), (5, 9, 20, 136, "bf16", 0.0), (30, 6, 64, 1000, "f32", 0.0), (12, 8, 256, 1407, "bf16", 0.5),
+         (16, 4, 32, 2048, "bf16", 0.0), (6, 5, 8, 4096, "f32", 0.2), (3, 8, 8, 8200, "bf16", 0.0), (4, 2, 8, 70001, "bf16", 0.3),
+         (2000, 2, 5, 8, "f32", 0.1), (700, 3, 16, 24, "bf16", 0.0)]
+
+
+@pytest.mark.parametrize("tokens,k,experts,hidden,dt,dropped", MOVES)
+def test_dispatch_combine_and_gradients(tokens, k, experts, hidden, dt, dropped):
+    ids = ids_of(hidden, tokens, k, experts, dropped)
+    order = B.nq_moe_sort(on_gpu(ids), experts)
+    place, kept = check_sort(order, ids, experts)
+    x, residual, dy = (normal(i, (tokens, hidden), dt) for i in (1, 2, 3))
+    ys, dxs = (normal(i, (tokens * k, hidden), dt) for i in (4, 5))
+    if kept < tokens * k:       # rows behind the last expert hold anything
+        ys[kept:] = float("nan")
+        dxs[kept:] = float("inf")
+    w = normal(6, (tokens, k), "f32")
+    for xx in (x, strided(x), strided(x, 8, 8)):
+        xs = B.nq_moe_dispatch(order, xx)
+        assert np.array_equal(f64(xs), L.moe_dispatch(f64(x), place, kept))
+    dx = B.nq_moe_dispatch_grad(order, dxs)
+    n = {"ys": f64(ys), "dxs": f64(dxs), "dy": f64(dy), "w": f64(w)}
+    size = lambda rows, weights=None, add=None: L.moe_combine(np.abs(rows), place, kept, weights, add)
+    within(dx, L.moe_combine(n["dxs"], place, kept), (k + 1) * U * size(n["dxs"]))
+    for weights, res in ((w, None), (None, residual), (w, strided(residual)), (w, strided(residual, 16, 8))):
+        y = B.nq_moe_combine(order, ys, weights, residual=res)
+        nw = None if weights is None else n["w"]
+        nr = None if res is None else f64(residual)
+        bound = (k + 1) * U * size(n["ys"], None if nw is None else np.abs(nw), None if nr is None else np.abs(nr))
+        within(y, L.moe_combine(n["ys"], place, kept, nw, nr), bound)
+    for d in (dy, strided(dy), strided(dy, 8, 0)):
+        dys, dw = B.nq_moe_combine_grad(order, d, ys, w)
+        want_dys, want_dw = L.moe_combine_grad(n["dy"], n["ys"], place, kept, n["w"])
+        within(dys, want_dys, U * np.abs(want_dys))
+        terms = L.moe_combine_grad(np.abs(n["dy"]), np.abs(n["ys"]), place, kept, n["w"])[1]
+        # a thread's share of the row, 6 steps in a wave and 4 waves
+        within(dw, want_dw, (hidden / 16 + 24) * U * terms)
+        bare, none = B.nq_moe_combine_grad(order, d, None, w)
+        assert none is None and bits_equal(bare, dys)
+
+
+def test_moving_past_foreign_places():
+    """Places that are none of the rows are left out, as dropped pairs are; nothing outside the rows is touched."""
+    order = B.nq_moe_sort(on_gpu(ids_of(1, 6, 2, 4)), 4)
+    place = torch.tensor([[0, -1], [12, 2 ** 31 - 1], [-2 ** 31, 3], [4, 5], [6, 7], [8, 11]], dtype=torch.int32, device="cuda")
+    order.place.copy_(place)
+    x, ys, w = normal(2, (6, 40), "f32"), normal(3, (12, 40), "f32"), normal(4, (6, 2), "f32")
+    xs = B.nq_moe_dispatch(order, x, xs=torch.full((12, 40), 7.0, device="cuda"))
+    p, host = place.cpu().numpy(), xs.cpu()
+    valid = (p >= 0) & (p < 12)
+    want = torch.full((12, 40), 7.0)
+    for t, j in np.argwhere(valid):
+        want[p[t, j]] = x[t].cpu()
+    assert torch.equal(host, want)
+    there = np.where(valid, p, 12)
+    y = B.nq_moe_combine(order, ys, w)
+    within(y, L.moe_combine(f64(ys), there, 12, f64(w)), 4 * U * L.moe_combine(np.abs(f64(ys)), there, 12, np.abs(f64(w))))
+    dys, dw = B.nq_moe_combine_grad(order, x, ys, w, dys=torch.full((12, 40), 7.0, device="cuda"))
+    assert (dys[[1, 2, 9, 10]] == 7).all() and (dw[torch.from_numpy(~valid).cuda()] == 0).all()
+
+
+# ---------------------------------------------------------------- streams, graphs, refusals
+def everything(t, out=None):
+    """A forward and a backward pass through all of them; with `out`, into its tensors."""
+    o = dict(scale=0.5, offset=1.0, eps=1e-6)
+    p = {k: t[k] for k in ("post", "gate", "pre")}
+    h_out, z = B.nq_block_norm(t["h"], t["y"], **p, **o)
+    heads = B.nq_rope(t["rope"], z.view(len(z), 4, 64), t["positions"])
+    order = B.nq_moe_sort(t["ids"], 8)
+    xs = B.nq_moe_dispatch(order, heads.view(len(z), 256))
+    y = B.nq_moe_combine(order, xs, t["w"], residual=h_out)
+    dys, dw = B.nq_moe_combine_grad(order, t["d"], xs, t["w"])
+    dx = B.nq_moe_dispatch_grad(order, dys)
+    dz = B.nq_rope_grad(t["rope"], dx.view(len(z), 4, 64), t["positions"]).view(len(z), 256)
+    grads = B.nq_block_norm_grad(h_out, t["y"], t["d"], dz, **p, **o)
+    return [h_out, z, heads, order.starts, order.place, xs, y, dys, dw, dx, dz, *grads]
+
+
+def together(seed, rows, big=False):
+    return {"h": normal(seed, (rows, 256), "bf16"), "y": normal(seed + 1, (rows, 256), "bf16"),
+            "post": normal(1, (256,), "f32"), "gate": normal(2, (256,), "f32"), "pre": normal(3, (256,), "f32"),
+            "rope": ROPE, "positions": torch.arange(rows, dtype=torch.int32, device="cuda"),
+            "ids": on_gpu(ids_of(seed + 2, rows, 2, 9)), "w": normal(seed + 3, (rows, 2), "f32"),
+            "d": normal(seed + 4, (rows, 256), "bf16")}
+
+
+ROPE = None
+
+
+@pytest.fixture(autouse=True)
+def rope_of_the_run():
+    global ROPE
+    ROPE = B.Rope(64)
+
+
+def same(a, b):
+    return all(x is y is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("rows", [5, 5000])
+def test_a_captured_run_replays(rows):
+    """A graph of a forward and a backward pass, replayed on other inputs between eager runs of the same."""
+    t = together(1, rows)
+    everything(t)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = everything(t)
+    for seed in (1, 20, 40, 60):
+        for k, v in together(seed, rows).items():
+            if isinstance(v, torch.Tensor):
+                t[k].copy_(v)
+        graph.replay()
+        got = [None if x is None else x.clone() for x in out]
+        want = everything(t)
+        torch.cuda.synchronize()
+        assert same(got, want)
+
+
+def test_other_streams_and_devices():
+    t = together(7, 300)
+    want = everything(t)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append(everything(t))
+    torch.cuda.synchronize()
+    assert all(same(g, want) for g in got)
+    # a stream by hand
+    s = streams[0]
+    x, p = t["y"], t["pre"]
+    a = B.nq_block_norm(t["h"], x, pre=p, stream=s)
+    b = B.nq_rope(ROPE, x.view(300, 4, 64), t["positions"], stream=s)
+    o = B.nq_moe_sort(t["ids"], 8, stream=s)
+    c = B.nq_moe_dispatch(o, x, stream=s)
+    s.synchronize()
+    assert bits_equal(b, B.nq_rope(ROPE, x.view(300, 4, 64), t["positions"]))
+    assert bits_equal(a[1], B.nq_block_norm(t["h"], x, pre=p)[1]) and bits_equal(c, B.nq_moe_dispatch(o, x))
+
+
+def test_refusals_of_the_binding():
+    h, p = normal(1, (4, 64), "f32"), normal(2, (64,), "f32")
+    bad = [lambda: B.nq_block_norm(h, h[:3], pre=p), lambda: B.nq_block_norm(h, h.bfloat16(), pre=p),
+           lambda: B.nq_block_norm(h, h, post=p, pre=p.bfloat16()), lambda: B.nq_block_norm(h, h, gate=normal(3, (3, 64), "f32")),
+           lambda: B.nq_block_norm(h), lambda: B.nq_block_norm(h, post=p, pre=p), lambda: B.nq_block_norm(h, pre=p, eps=0.0),
+           lambda: B.nq_block_norm(h.t(), pre=normal(2, (4,), "f32")), lambda: B.nq_block_norm(h.cpu(), pre=p),
+           lambda: B.nq_block_norm(h, h, pre=p, z=h), lambda: B.nq_block_norm(h.half(), pre=p.half()),
+           lambda: B.nq_block_norm_grad(h, pre=p), lambda: B.nq_block_norm_grad(h, dz=h, dh=h),
+           lambda: B.nq_block_norm_grad(h, h, h, post=p, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           lambda: B.nq_rope(B.Rope(128), h.view(4, 1, 64), torch.zeros(4, dtype=torch.int32, device="cuda")),
+           lambda: B.nq_rope(B.Rope(64), h.view(4, 1, 64), torch.zeros(4, dtype=torch.int64, device="cuda")),
+           lambda: B.nq_rope(B.Rope(64, sections=[16, 16]), h.view(4, 1, 64), torch.zeros(4, dtype=torch.int32, device="cuda")),
+           lambda: B.nq_rope(B.Rope(64), h.view(4, 1, 64), torch.zeros(5, dtype=torch.int32, device="cuda")),
+           lambda: B.nq_rope(B.Rope(64), h.view(4, 1, 64)[:3], torch.zeros(3, dtype=torch.int32, device="cuda"),
+                             out=h.view(4, 1, 64)[1:]),
+           lambda: B.Rope(63), lambda: B.Rope(64, sections=[16, 15]), lambda: B.Rope(64, layout="thirds"),
+           lambda: B.Rope(64, axis=[0] * 31 + [-1]), lambda: B.Rope(64, freq=torch.ones(31)), lambda: B.Rope(64, scale=0.0) and
+           B.nq_rope(B.Rope(64, scale=0.0), h.view(4, 1, 64), torch.zeros(4, dtype=torch.int32, device="cuda")),
+           lambda: B.nq_moe_sort(torch.zeros((4, 2), dtype=torch.int64, device="cuda"), 4),
+           lambda: B.nq_moe_sort(torch.zeros((4, 33), dtype=torch.int32, device="cuda"), 4),
+           lambda: B.nq_moe_sort(torch.zeros((4, 2), dtype=torch.int32, device="cuda"), 1025)]
+    order = B.nq_moe_sort(torch.zeros((4, 2), dtype=torch.int32, device="cuda"), 3)
+    ys, w = normal(4, (8, 64), "f32"), normal(5, (4, 2), "f32")
+    bad += [lambda: B.nq_moe_dispatch(order, ys), lambda: B.nq_moe_dispatch(order, h, xs=ys[:, :32]),
+            lambda: B.nq_moe_dispatch_grad(order, h), lambda: B.nq_moe_combine(order, ys, w.bfloat16()),
+            lambda: B.nq_moe_combine(order, ys, w[:3]), lambda: B.nq_moe_combine(order, ys, residual=ys),
+            lambda: B.nq_moe_combine(order, ys, w, y=ys[:4]), lambda: B.nq_moe_combine(order, ys.double()),
+            lambda: B.nq_moe_combine_grad(order, h, ys.bfloat16(), w), lambda: B.nq_moe_combine_grad(order, h, dweights=w),
+            lambda: B.nq_moe_combine_grad(order, h, ys, w, dys=ys), lambda: setattr(order, "tokens", 5),
+            lambda: B.nq_moe_sort(torch.zeros((5, 2), dtype=torch.int32, device="cuda"), 3, order=order)]
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, TypeError, AttributeError, B.NQError)):
+            call()
+            pytest.fail(f"call {i} was taken")
