@@ -93,6 +93,8 @@ _SIGNATURES = {
     "nq_kv_read": [_P, _P, _P, _P, _I32, _P],
     "nq_kv_attention_workspace_bytes": [_P, _P, _I32, _I32],
     "nq_kv_attention": [_P, _P, _P, _I32, _I64, _I32, ctypes.c_float, _I32, _I64, _P, _P, _P, _SZ, _P],
+    "nq_kv_attention_shared_workspace_bytes": [_P, _P, _P, _I32, _I32],
+    "nq_kv_attention_shared": [_P, _P, _P, _P, _I32, _I64, _I32, ctypes.c_float, _I32, _P, _P, _P, _SZ, _P],
     "nq_moe_route": [_P, _P, _I32, _I64, _I64, _P, _P, _P, _P],
     "nq_moe_route_grad": [_P, _P, _I32, _I64, _I64, _P, _P, _P, _P],
     "nq_moe_sort_workspace_bytes": [_I64, _I32, _I32],
@@ -114,7 +116,8 @@ _SIGNATURES = {
 _RESTYPES = {"nq_qmm_workspace_bytes": _SZ, "nq_gather_qmm_workspace_bytes": _SZ,
              "nq_qmm_notrans_workspace_bytes": _SZ, "nq_fp_gather_qmm_workspace_bytes": _SZ,
              "nq_fp_qmm_notrans_workspace_bytes": _SZ, "nq_kv_attention_workspace_bytes": _SZ,
-             "nq_moe_sort_workspace_bytes": _SZ, "nq_block_norm_grad_workspace_bytes": _SZ,
+             "nq_kv_attention_shared_workspace_bytes": _SZ, "nq_moe_sort_workspace_bytes": _SZ,
+              "nq_block_norm_grad_workspace_bytes": _SZ,
              "nq_status_string": ctypes.c_char_p, "nq_last_error": ctypes.c_char_p,
              "nq_version": ctypes.c_char_p}
 
@@ -820,6 +823,46 @@ def nq_kv_attention(cache, seqs, q, scale=None, causal=True, window=0, out=None,
                                  cache.head_dim ** -0.5 if scale is None else scale, int(bool(causal)), window,
                                  out.data_ptr(), None if lse is None else lse.data_ptr(),
                                  None if workspace is None else workspace.data_ptr(), ws_bytes, _raw_stream(stream))
+    if status:
+        _check(status)
+    return out
+
+
+def nq_kv_attention_shared_workspace_bytes(cache, prefix, seqs, q_heads, x_dtype):
+    torch = _torch()
+    xd = NQ_F32 if x_dtype == torch.float32 else NQ_BF16
+    return load_library().nq_kv_attention_shared_workspace_bytes(cache._ref, prefix._ref, seqs._ref, q_heads, xd)
+
+
+def nq_kv_attention_shared(cache, prefix, seqs, q, scale=None, causal=True, out=None, lse=None, workspace=None,
+                           stream=None):
+    """nq_kv_attention for a batch whose sequences share prefixes, each read once
+    for all of its rows.  prefix: a KVSequences over the same rows, of which rows
+    row_start[p] .. row_start[p + 1] see all lengths[p] tokens of prefix p before
+    those of their own sequence (seqs, whose lengths count own tokens only).  The
+    workspace is allocated here when not given."""
+    torch = _torch()
+    lib = _lib or load_library()
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, q_heads, head_dim]")
+    heads = q.shape[1]
+    ldq = _row_stride("q", q, seqs.rows, heads, cache.head_dim)
+    dt = _dt(q)
+    out = _empty(stream, q.shape, q.dtype, q.device) if out is None else _given("out", out, q.shape, q.dtype)
+    if lse is not None:
+        _given("lse", lse, (seqs.rows, heads), torch.float32)
+    if workspace is None:
+        ws_bytes = lib.nq_kv_attention_shared_workspace_bytes(cache._ref, prefix._ref, seqs._ref, heads, dt)
+        if ws_bytes:
+            workspace = _empty(stream, ws_bytes, torch.uint8, q.device)
+    else:
+        _contig("workspace", workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _one_device(stream, cache.k_codes, prefix.lengths, seqs.lengths, q, out, lse, workspace)
+    status = lib.nq_kv_attention_shared(cache._ref, prefix._ref, seqs._ref, q.data_ptr(), dt, ldq, heads,
+                                        cache.head_dim ** -0.5 if scale is None else scale, int(bool(causal)),
+                                        out.data_ptr(), _address(lse), _address(workspace), ws_bytes,
+                                        _raw_stream(stream))
     if status:
         _check(status)
     return out

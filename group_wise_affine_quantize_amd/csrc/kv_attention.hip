@@ -125,7 +125,8 @@ template <int D, int NP> struct State {
 // CG groups of 16 columns; the waves of a group share its tiles.  A group's
 // waves load the tiles of the other groups' waves too, out of the L1: two
 // blocks of columns in one wave's registers would leave one wave per SIMD.
-template <int D, int CG, int FMT, typename T>
+// SHARED: a pass of attention behind shared prefixes (see AttnArgs).
+template <int D, int CG, int FMT, typename T, bool SHARED>
 __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kernel(AttnArgs A)
 {
     constexpr int NP = Parts<T>::n, COLS = 16 * CG, KS = D / 32, DT = D / 16, TL = kWaves / CG;
@@ -395,7 +396,20 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
             const int64_t slot = 2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0);
             float l = sh_l[0][col];
             for (int w = 1; w < TL; ++w) l += sh_l[w][col];
-            if (whole) {
+            if (SHARED && whole && A.state_s) {
+                const int64_t at = (int64_t)c.row * a.q_heads + c.head;
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt)
+                    *reinterpret_cast<float4_t *>(A.state_o + at * D + 16 * dt + 4 * g) = st.o[dt];
+                if (g == 0) A.state_s[at] = make_float4(st.m, l, st.u, 0.0f);
+            } else if (whole) {
+                if constexpr (SHARED) {
+                    const Before before = take_before(A, c.row, c.head, l, st.m, st.u);
+                    if (before.o)
+#pragma unroll
+                        for (int dt = 0; dt < DT; ++dt)
+                            add_before(before, 16 * dt + 4 * g, reinterpret_cast<float *>(&st.o[dt]));
+                }
                 const float f = out_factor(l, st.m, st.u, 4 * DT, reinterpret_cast<float *>(st.o));
                 T *out = static_cast<T *>(a.out) + ((int64_t)c.row * a.q_heads + c.head) * D;
 #pragma unroll
@@ -429,7 +443,7 @@ constexpr int join_blocks(int groups) { return groups == 4 ? 4 : 16 * groups / k
 // j + 1; the one at the first border inside a segment joins it.  Two runs of
 // threads or more take turns at the parts (7 us for 64 sequences of 8 heads, 13
 // us where 8 segments of 32 columns have 64 parts each).
-template <int D, int CG, typename T>
+template <int D, int CG, typename T, bool SHARED>
 __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 {
     constexpr int COLS = 16 * CG, QUADS = D / 4, LANES = kJoinCols * QUADS, RUNS = kJoinThreads / LANES;
@@ -501,12 +515,21 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
                 const float4 w = sh_o[k][i];
                 v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
             }
-            const float4 t = sh_s[c];
-            const float l = t.y, f = out_factor(l, t.x, t.z, 4, v);
-            for (int e = 0; e < 4; ++e) v[e] *= f;
-            store_f32x4<T>(static_cast<T *>(a.out) + ((int64_t)q.row * a.q_heads + q.head) * D + d, v);
-            if (a.lse && d == 0)
-                a.lse[(int64_t)q.row * a.q_heads + q.head] = log_sum(l, t.z);
+            float4 t = sh_s[c];
+            const int64_t at = (int64_t)q.row * a.q_heads + q.head;
+            if (SHARED && A.state_s) {
+                store_f32x4<float>(A.state_o + at * D + d, v);
+                if (d == 0) A.state_s[at] = t;
+            } else {
+                if constexpr (SHARED) {
+                    const Before before = take_before(A, q.row, q.head, t.y, t.x, t.z);
+                    if (before.o) add_before(before, d, v);
+                }
+                const float l = t.y, f = out_factor(l, t.x, t.z, 4, v);
+                for (int e = 0; e < 4; ++e) v[e] *= f;
+                store_f32x4<T>(static_cast<T *>(a.out) + at * D + d, v);
+                if (a.lse && d == 0) a.lse[at] = log_sum(l, t.z);
+            }
         }
         __syncthreads();
     }
@@ -574,21 +597,27 @@ Route route_of(const KvAttnLaunch &a)
     return r;
 }
 
-template <int D, int CG, int FMT, typename T> hipError_t stream_go(const AttnArgs &A, hipStream_t stream)
+template <int D, int CG, int FMT, typename T, bool SHARED> hipError_t stream_go(const AttnArgs &A, hipStream_t stream)
 {
-    kv_stream_kernel<D, CG, FMT, T><<<A.workers, 64 * kWaves, 0, stream>>>(A);
+    kv_stream_kernel<D, CG, FMT, T, SHARED><<<A.workers, 64 * kWaves, 0, stream>>>(A);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (!A.splits) return e;
-    kv_join_kernel<D, CG, T><<<dim3(A.workers - 1, join_blocks(CG)), kJoinThreads, 0, stream>>>(A);
+    kv_join_kernel<D, CG, T, SHARED><<<dim3(A.workers - 1, join_blocks(CG)), kJoinThreads, 0, stream>>>(A);
     return hipGetLastError();
+}
+
+template <int D, int CG, int FMT, typename T> hipError_t stream_shared(const AttnArgs &A, hipStream_t stream)
+{
+    return A.state_s || A.before_s ? stream_go<D, CG, FMT, T, true>(A, stream) : stream_go<D, CG, FMT, T, false>(A, stream);
 }
 
 template <int D, int CG> hipError_t stream_types(const AttnArgs &A, hipStream_t stream)
 {
     if (A.a.format == KV_INT8)
-        return A.a.x_dt == 0 ? stream_go<D, CG, KV_INT8, float>(A, stream) : stream_go<D, CG, KV_INT8, bf16_bits>(A, stream);
-    return A.a.x_dt == 0 ? stream_go<D, CG, KV_FP8, float>(A, stream) : stream_go<D, CG, KV_FP8, bf16_bits>(A, stream);
+        return A.a.x_dt == 0 ? stream_shared<D, CG, KV_INT8, float>(A, stream)
+                             : stream_shared<D, CG, KV_INT8, bf16_bits>(A, stream);
+    return A.a.x_dt == 0 ? stream_shared<D, CG, KV_FP8, float>(A, stream) : stream_shared<D, CG, KV_FP8, bf16_bits>(A, stream);
 }
 
 template <int D> hipError_t stream_groups(const AttnArgs &A, int groups, hipStream_t stream)
@@ -598,17 +627,17 @@ template <int D> hipError_t stream_groups(const AttnArgs &A, int groups, hipStre
 
 }  // namespace
 
-size_t kv_attn_ws_bytes(const KvAttnLaunch &a)
+// The two kernels of a pass run one after the other: they share the workspace.
+static size_t pass_ws_floats(const KvAttnLaunch &a)
 {
-    // the two kernels run one after the other: they share the workspace
     const Route r = route_of(a);
-    return std::max(r.stream_floats + 4 * r.stream_cols, r.tile_floats + 4 * r.tile_cols) * sizeof(float);
+    return std::max(r.stream_floats + 4 * r.stream_cols, r.tile_floats + 4 * r.tile_cols);
 }
 
-hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream)
+// A pass over the sequences a.s.  `A` comes with the states of a two-pass call set.
+static hipError_t launch_pass(AttnArgs A, const KvAttnLaunch &a, hipStream_t stream)
 {
     const Route r = route_of(a);
-    AttnArgs A;
     A.a = a;
     A.workers = kWorkers;
     A.group = a.q_heads / a.c.kv_heads;
@@ -635,6 +664,46 @@ hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream)
     case 192: return stream_groups<192>(A, r.ct, stream);
     default: return stream_groups<256>(A, r.ct, stream);
     }
+}
+
+size_t kv_attn_ws_bytes(const KvAttnLaunch &a) { return pass_ws_floats(a) * sizeof(float); }
+
+hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream) { return launch_pass(AttnArgs{}, a, stream); }
+
+// Behind a shared prefix: the prefixes' pass takes all rows that share one as
+// one sequence's queries, which see all of its tokens, and leaves their states
+// in the workspace; the sequences' own pass takes them up where it ends.
+static KvAttnLaunch prefix_pass(const KvAttnLaunch &a, const KvSeqs &prefix)
+{
+    KvAttnLaunch p = a;
+    p.s = prefix;
+    p.causal = 0, p.window = 0;
+    p.out = nullptr, p.lse = nullptr;
+    return p;
+}
+// Floats of the states, a multiple of four.
+static size_t state_floats(const KvAttnLaunch &a) { return (size_t)a.s.rows * a.q_heads * (a.c.head_dim + 4); }
+
+size_t kv_shared_ws_bytes(const KvAttnLaunch &a, const KvSeqs &prefix)
+{
+    if (prefix.batch == 0) return kv_attn_ws_bytes(a);
+    return (state_floats(a) + std::max(pass_ws_floats(a), pass_ws_floats(prefix_pass(a, prefix)))) * sizeof(float);
+}
+
+hipError_t launch_kv_shared(const KvAttnLaunch &a, const KvSeqs &prefix, hipStream_t stream)
+{
+    if (prefix.batch == 0) return launch_kv_attention(a, stream);
+    float *states = static_cast<float *>(a.workspace);
+    float4 *sums = reinterpret_cast<float4 *>(states + (size_t)a.s.rows * a.q_heads * a.c.head_dim);
+    KvAttnLaunch own = a, first = prefix_pass(a, prefix);
+    own.workspace = first.workspace = states + state_floats(a);
+    AttnArgs A{};
+    A.state_o = states, A.state_s = sums;
+    const hipError_t e = launch_pass(A, first, stream);
+    if (e != hipSuccess) return e;
+    AttnArgs O{};
+    O.before_o = states, O.before_s = sums, O.before_start = prefix.row_start, O.before_batch = prefix.batch;
+    return launch_pass(O, own, stream);
 }
 
 }  // namespace nqk

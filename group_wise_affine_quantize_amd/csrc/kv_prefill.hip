@@ -107,7 +107,8 @@ template <int M> __device__ __forceinline__ int tile_locate(const AttnArgs &A, u
     return -1;
 }
 
-template <int D, int FMT, typename T>
+// SHARED: a pass of attention behind shared prefixes (see AttnArgs).
+template <int D, int FMT, typename T, bool SHARED>
 __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
 {
     constexpr int NP = Parts<T>::n, M = Shape<D>::M, THREADS = Shape<D>::THREADS, PIECES = Shape<D>::PIECES;
@@ -401,9 +402,31 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
         l *= exp2_below(lref, top);
         lref = top;
     } else lref = ref;
-    const float sum = l + xor_lane<32>(l, lane);
+    float sum = l + xor_lane<32>(l, lane);
     if (mine.row < 0) return;
-    if (A.tile_splits == 1) {
+    if (SHARED && A.tile_splits == 1 && A.state_s) {
+        const int64_t at = (int64_t)mine.row * a.q_heads + mine.head;
+        float *po = A.state_o + at * D;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4 *>(po + 32 * dt + 2 * i + 4 * h) =
+                    make_float4(o[dt][i], o[dt][i + 1], o[dt][i + 2], o[dt][i + 3]);
+        if (h == 0) A.state_s[at] = make_float4(ref, sum, lref, 0.0f);
+    } else if (A.tile_splits == 1) {
+        if constexpr (SHARED) {
+            const Before before = take_before(A, mine.row, mine.head, sum, ref, lref);
+            if (before.o)
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        float v[4] = {o[dt][i], o[dt][i + 1], o[dt][i + 2], o[dt][i + 3]};
+                        add_before(before, 32 * dt + 2 * i + 4 * h, v);
+                        o[dt][i] = v[0], o[dt][i + 1] = v[1], o[dt][i + 2] = v[2], o[dt][i + 3] = v[3];
+                    }
+        }
         const float f = out_factor(sum, ref, lref, 16 * DT, reinterpret_cast<float *>(o));
         T *out = static_cast<T *>(a.out) + ((int64_t)mine.row * a.q_heads + mine.head) * D;
 #pragma unroll
@@ -430,7 +453,7 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
 
 // Joins the parts of a column tile's tokens, in their order; one workgroup
 // takes 1024 / D columns.
-template <int D, typename T> __global__ __launch_bounds__(256) void kv_tile_join_kernel(AttnArgs A)
+template <int D, typename T, bool SHARED> __global__ __launch_bounds__(256) void kv_tile_join_kernel(AttnArgs A)
 {
     constexpr int M = Shape<D>::M, COLS = 1024 / D, QUADS = D / 4;
     const KvAttnLaunch &a = A.a;
@@ -463,29 +486,43 @@ template <int D, typename T> __global__ __launch_bounds__(256) void kv_tile_join
         l = fmaf(exp2_below(t.z, u), t.y, l);
         v[0] = fmaf(f, o.x, v[0]), v[1] = fmaf(f, o.y, v[1]), v[2] = fmaf(f, o.z, v[2]), v[3] = fmaf(f, o.w, v[3]);
     }
+    const int64_t row = (int64_t)q.row * a.q_heads + q.head;
+    if (SHARED && A.state_s) {
+        store_f32x4<float>(A.state_o + row * D + d, v);
+        if (d == 0) A.state_s[row] = make_float4(m, l, u, 0.0f);
+        return;
+    }
+    if constexpr (SHARED) {
+        const Before before = take_before(A, q.row, q.head, l, m, u);
+        if (before.o) add_before(before, d, v);
+    }
     const float f = out_factor(l, m, u, 4, v);
     for (int e = 0; e < 4; ++e) v[e] *= f;
-    store_f32x4<T>(static_cast<T *>(a.out) + ((int64_t)q.row * a.q_heads + q.head) * D + d, v);
-    if (a.lse && d == 0)
-        a.lse[(int64_t)q.row * a.q_heads + q.head] = log_sum(l, u);
+    store_f32x4<T>(static_cast<T *>(a.out) + row * D + d, v);
+    if (a.lse && d == 0) a.lse[row] = log_sum(l, u);
 }
 
-template <int D, int FMT, typename T> hipError_t tile_go(const AttnArgs &A, hipStream_t stream)
+template <int D, int FMT, typename T, bool SHARED> hipError_t tile_go(const AttnArgs &A, hipStream_t stream)
 {
     const unsigned segments = A.tile_bound * (unsigned)A.a.c.kv_heads;
-    kv_tile_kernel<D, FMT, T><<<segments * (unsigned)A.tile_splits, Shape<D>::THREADS, 0, stream>>>(A);
+    kv_tile_kernel<D, FMT, T, SHARED><<<segments * (unsigned)A.tile_splits, Shape<D>::THREADS, 0, stream>>>(A);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || A.tile_splits == 1) return e;
     constexpr int cols = 1024 / D;
-    kv_tile_join_kernel<D, T><<<dim3(segments, (Shape<D>::M + cols - 1) / cols), 256, 0, stream>>>(A);
+    kv_tile_join_kernel<D, T, SHARED><<<dim3(segments, (Shape<D>::M + cols - 1) / cols), 256, 0, stream>>>(A);
     return hipGetLastError();
+}
+
+template <int D, int FMT, typename T> hipError_t tile_shared(const AttnArgs &A, hipStream_t stream)
+{
+    return A.state_s || A.before_s ? tile_go<D, FMT, T, true>(A, stream) : tile_go<D, FMT, T, false>(A, stream);
 }
 
 template <int D> hipError_t tile_types(const AttnArgs &A, hipStream_t stream)
 {
     if (A.a.format == KV_INT8)
-        return A.a.x_dt == 0 ? tile_go<D, KV_INT8, float>(A, stream) : tile_go<D, KV_INT8, bf16_bits>(A, stream);
-    return A.a.x_dt == 0 ? tile_go<D, KV_FP8, float>(A, stream) : tile_go<D, KV_FP8, bf16_bits>(A, stream);
+        return A.a.x_dt == 0 ? tile_shared<D, KV_INT8, float>(A, stream) : tile_shared<D, KV_INT8, bf16_bits>(A, stream);
+    return A.a.x_dt == 0 ? tile_shared<D, KV_FP8, float>(A, stream) : tile_shared<D, KV_FP8, bf16_bits>(A, stream);
 }
 
 }  // namespace

@@ -1367,28 +1367,44 @@ nq_status nq_kv_read(const nq_kv_cache *cache, const nq_kv_seqs *seqs, void *k, 
     return check_launch(op, nqk::launch_kv_read(a, stream));
 }
 
-size_t nq_kv_attention_workspace_bytes(const nq_kv_cache *cache, const nq_kv_seqs *seqs, int32_t q_heads,
-                                       nq_dtype x_dt)
+static size_t kv_attention_ws(const char *op, const nq_kv_cache *cache, const nq_kv_seqs *prefix, const nq_kv_seqs *seqs,
+                              int32_t q_heads, nq_dtype x_dt)
 {
-    const char *op = "nq_kv_attention_workspace_bytes";
     g_last_error.clear();
-    if (check_kv_cache(op, cache) || check_kv_seqs(op, seqs) || !dtype_ok(x_dt) || q_heads < 1 ||
-        q_heads % cache->kv_heads || seqs->rows == 0 || seqs->batch == 0)
+    if (check_kv_cache(op, cache) || check_kv_seqs(op, seqs) || (prefix && check_kv_seqs(op, prefix)) || !dtype_ok(x_dt) ||
+        q_heads < 1 || q_heads > 65535 || q_heads % cache->kv_heads || seqs->rows == 0 || seqs->batch == 0 ||
+        seqs->rows * q_heads >= kMaxDim / 2 || (prefix && prefix->rows != seqs->rows))
         return 0;
     nqk::KvAttnLaunch a{};
     a.c = kv_cache_of(cache), a.s = kv_seqs_of(seqs), a.q_heads = q_heads, a.x_dt = x_dt, a.format = cache->format;
-    return nqk::kv_attn_ws_bytes(a);
+    return prefix ? nqk::kv_shared_ws_bytes(a, kv_seqs_of(prefix)) : nqk::kv_attn_ws_bytes(a);
 }
 
-nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, const void *q, nq_dtype x_dt,
-                          int64_t ldq, int32_t q_heads, float softmax_scale, int32_t causal, int64_t window,
-                          void *out, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream)
+size_t nq_kv_attention_workspace_bytes(const nq_kv_cache *cache, const nq_kv_seqs *seqs, int32_t q_heads,
+                                       nq_dtype x_dt)
 {
-    const char *op = "nq_kv_attention";
+    return kv_attention_ws("nq_kv_attention_workspace_bytes", cache, nullptr, seqs, q_heads, x_dt);
+}
+
+size_t nq_kv_attention_shared_workspace_bytes(const nq_kv_cache *cache, const nq_kv_seqs *prefix, const nq_kv_seqs *seqs,
+                                              int32_t q_heads, nq_dtype x_dt)
+{
+    return prefix ? kv_attention_ws("nq_kv_attention_shared_workspace_bytes", cache, prefix, seqs, q_heads, x_dt) : 0;
+}
+
+// Attention over `seqs`, behind `prefix` unless it is null.
+static nq_status kv_attention_impl(const char *op, const nq_kv_cache *cache, const nq_kv_seqs *prefix, const nq_kv_seqs *seqs,
+                                   const void *q, nq_dtype x_dt, int64_t ldq, int32_t q_heads, float softmax_scale,
+                                   int32_t causal, int64_t window, void *out, float *lse, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream)
+{
     g_last_error.clear();
     if (!dtype_ok(x_dt)) return fail(NQ_ERR_DTYPE, "%s: unknown dtype x_dt=%d", op, (int)x_dt);
     nq_status st;
-    if ((st = check_kv_cache(op, cache)) || (st = check_kv_seqs(op, seqs))) return st;
+    if ((st = check_kv_cache(op, cache)) || (st = check_kv_seqs(op, seqs)) || (prefix && (st = check_kv_seqs(op, prefix))))
+        return st;
+    if (prefix && prefix->rows != seqs->rows)
+        return fail(NQ_ERR_SHAPE, "%s: prefix has %lld rows, seqs %lld", op, (long long)prefix->rows, (long long)seqs->rows);
     if (q_heads < 1 || q_heads > 65535 || q_heads % cache->kv_heads)
         return fail(NQ_ERR_SHAPE, "%s: q_heads=%d is not a multiple of kv_heads=%d in 1 .. 65535", op, q_heads,
                     cache->kv_heads);
@@ -1400,6 +1416,8 @@ nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, cons
         return fail(NQ_ERR_SHAPE, "%s: window=%lld is negative, or set without causal", op, (long long)window);
     if (seqs->rows == 0 || seqs->batch == 0) return NQ_OK;
     if ((st = check_kv_pointers(op, cache, seqs))) return st;
+    if (prefix && prefix->batch == 0) prefix = nullptr;     // rows without any prefix
+    if (prefix && (st = check_kv_pointers(op, cache, prefix))) return st;
     const int64_t width = (int64_t)q_heads * cache->head_dim, xb = dtype_bytes(x_dt);
     if ((st = check_kv_rows(op, "q", q, ldq, width, xb)) || (st = check_kv_rows(op, "out", out, width, width, xb)))
         return st;
@@ -1407,24 +1425,45 @@ nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, cons
     const Span so{out, seqs->rows * width * xb}, sl{lse, lse ? seqs->rows * q_heads * 4 : 0},
         sq{q, rows_span(seqs->rows, ldq, width, xb)};
     if (overlap(so, sq) || overlap(so, sl) || overlap(sl, sq) || overlaps_cache(cache, so) || overlaps_cache(cache, sl) ||
-        overlaps_seqs(seqs, so) || overlaps_seqs(seqs, sl))
+        overlaps_seqs(seqs, so) || overlaps_seqs(seqs, sl) ||
+        (prefix && (overlaps_seqs(prefix, so) || overlaps_seqs(prefix, sl))))
         return fail(NQ_ERR_ALIAS, "%s: an output overlaps an input or the other output", op);
     nqk::KvAttnLaunch a{};
     a.c = kv_cache_of(cache), a.s = kv_seqs_of(seqs);
     a.q = q, a.ldq = ldq, a.out = out, a.lse = lse, a.workspace = workspace, a.q_heads = q_heads, a.x_dt = x_dt;
     a.format = cache->format, a.causal = causal != 0, a.scale = softmax_scale;
     a.window = std::min<int64_t>(window, (int64_t)1 << 32);   // past every length
-    const size_t need = nqk::kv_attn_ws_bytes(a);
+    nqk::KvSeqs p{};
+    if (prefix) p = kv_seqs_of(prefix);
+    const size_t need = prefix ? nqk::kv_shared_ws_bytes(a, p) : nqk::kv_attn_ws_bytes(a);
+    if ((st = check_workspace(op, workspace, workspace_bytes, need))) return st;
     if (need) {
-        if (!workspace || workspace_bytes < need)
-            return fail(NQ_ERR_WORKSPACE, "%s: workspace of %zu bytes needed (got %zu)", op, need,
-                        workspace ? workspace_bytes : (size_t)0);
-        if (!aligned16(workspace)) return fail(NQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", op);
         const Span sw{workspace, (int64_t)need};
-        if (overlap(sw, so) || overlap(sw, sl) || overlap(sw, sq) || overlaps_cache(cache, sw) || overlaps_seqs(seqs, sw))
+        if (overlap(sw, so) || overlap(sw, sl) || overlap(sw, sq) || overlaps_cache(cache, sw) || overlaps_seqs(seqs, sw) ||
+            (prefix && overlaps_seqs(prefix, sw)))
             return fail(NQ_ERR_ALIAS, "%s: the workspace overlaps an argument", op);
     }
-    return check_launch(op, nqk::launch_kv_attention(a, stream));
+    return check_launch(op, prefix ? nqk::launch_kv_shared(a, p, stream) : nqk::launch_kv_attention(a, stream));
+}
+
+nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, const void *q, nq_dtype x_dt,
+                          int64_t ldq, int32_t q_heads, float softmax_scale, int32_t causal, int64_t window,
+                          void *out, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    return kv_attention_impl("nq_kv_attention", cache, nullptr, seqs, q, x_dt, ldq, q_heads, softmax_scale, causal, window, out,
+                             lse, workspace, workspace_bytes, stream);
+}
+
+nq_status nq_kv_attention_shared(const nq_kv_cache *cache, const nq_kv_seqs *prefix, const nq_kv_seqs *seqs, const void *q,
+                                 nq_dtype x_dt, int64_t ldq, int32_t q_heads, float softmax_scale, int32_t causal, void *out,
+                                 float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!prefix) {
+        g_last_error.clear();
+        return fail(NQ_ERR_NULL, "nq_kv_attention_shared: prefix is null");
+    }
+    return kv_attention_impl("nq_kv_attention_shared", cache, prefix, seqs, q, x_dt, ldq, q_heads, softmax_scale, causal, 0, out,
+                             lse, workspace, workspace_bytes, stream);
 }
 
 // ---- expert routing

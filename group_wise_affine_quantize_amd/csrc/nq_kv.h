@@ -65,6 +65,9 @@ struct KvAttnLaunch {
 };
 size_t kv_attn_ws_bytes(const KvAttnLaunch &a);
 hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream);
+// The same behind prefixes that rows share (prefix.rows = a.s.rows).
+size_t kv_shared_ws_bytes(const KvAttnLaunch &a, const KvSeqs &prefix);
+hipError_t launch_kv_shared(const KvAttnLaunch &a, const KvSeqs &prefix, hipStream_t stream);
 
 enum { MOE_SOFTMAX = 1, MOE_SIGMOID = 2 };
 struct MoeRoute {

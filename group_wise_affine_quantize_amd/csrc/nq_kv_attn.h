@@ -84,6 +84,15 @@ struct AttnArgs {
                         // streaming kernel's, the others the tile kernel's
     int tile_splits;    // parts that the tile kernel cuts a segment's tokens into
     unsigned tile_bound;    // tile kernel: column tiles at most, over all sequences
+    // Attention in two passes (a prefix, then the sequences' own tokens).  The
+    // first keeps each row's O, R, L and U here instead of giving a result,
+    // [rows][q_heads][D] and [rows][q_heads]; the second takes them up.
+    float *state_o;                 // or null
+    float4 *state_s;
+    const float *before_o;          // or null
+    const float4 *before_s;
+    const int32_t *before_start;    // the prefixes' rows (see KvSeqs::row_start)
+    int before_batch;
 };
 
 // The streaming kernel's work is a flat list of units (runs of 64-token
@@ -258,6 +267,43 @@ __device__ __forceinline__ float out_factor(float l, float m, float u, int count
 
 // log of the sum of weights l over 2^u: -infinity for none, NaN for a NaN.
 __device__ __forceinline__ float log_sum(float l, float u) { return l == 0.0f ? kNegInf : (u + fast_log2(l)) * kLn2; }
+
+// What the first pass left of a row and head, and the factors with which it
+// and the second pass's O go into their sum.
+struct Before {
+    const float *o;     // null: no prefix has the row
+    float mine, its;
+};
+
+// Takes the first pass's state into l and the references m and u.
+__device__ __forceinline__ Before take_before(const AttnArgs &A, int row, int head, float &l, float &m, float &u)
+{
+    Before b{nullptr, 1.0f, 0.0f};
+    if (!A.before_s) return b;
+    // the last prefix that starts at this row or before it
+    int lo = 0, hi = A.before_batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (A.before_start[mid] <= row) lo = mid;
+        else hi = mid;
+    }
+    if (A.before_start[lo] > row || A.before_start[lo + 1] <= row) return b;
+    const int64_t at = (int64_t)row * A.a.q_heads + head;
+    const float4 t = A.before_s[at];
+    const float top = fmaxf(m, t.x), utop = fmaxf(u, t.z);
+    b.o = A.before_o + at * A.a.c.head_dim;
+    b.mine = exp2_below(m, top), b.its = exp2_below(t.x, top);
+    l = fmaf(exp2_below(t.z, utop), t.y, l * exp2_below(u, utop));
+    m = top, u = utop;
+    return b;
+}
+// Four columns of O, from column d on, become those of both passes.
+__device__ __forceinline__ void add_before(const Before &b, int d, float *v)
+{
+    const float4 w = *reinterpret_cast<const float4 *>(b.o + d);
+    v[0] = fmaf(b.its, w.x, v[0] * b.mine), v[1] = fmaf(b.its, w.y, v[1] * b.mine);
+    v[2] = fmaf(b.its, w.z, v[2] * b.mine), v[3] = fmaf(b.its, w.w, v[3] * b.mine);
+}
 
 // The tile kernel (kv_prefill.hip).
 int prefill_columns(const KvAttnLaunch &a);     // query columns per workgroup

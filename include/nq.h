@@ -537,6 +537,22 @@ nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, cons
                           int64_t ldq, int32_t q_heads, float softmax_scale, int32_t causal, int64_t window,
                           void *out, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Attention of a batch whose sequences share prefixes (a system prompt, a
+ * document): a prefix's tokens are read once for all of its rows.  `prefix`
+ * describes the prefixes over the same rows as `seqs` (rows equal in both): rows
+ * prefix->row_start[p] .. prefix->row_start[p + 1] - 1, those of any number of
+ * neighbouring sequences, see all prefix->lengths[p] tokens of prefix p, before
+ * what they see of their own sequence, whose lengths count its own tokens only.
+ * row_start rises; rows that no prefix has see their own tokens alone.  The rest
+ * is nq_kv_attention's, over the tokens of both: out, lse (of both), rows that see
+ * nothing, NaN, precision, and what device arrays of any content may do. */
+size_t nq_kv_attention_shared_workspace_bytes(const nq_kv_cache *cache, const nq_kv_seqs *prefix,
+                                              const nq_kv_seqs *seqs, int32_t q_heads, nq_dtype x_dt);
+nq_status nq_kv_attention_shared(const nq_kv_cache *cache, const nq_kv_seqs *prefix, const nq_kv_seqs *seqs,
+                                 const void *q, nq_dtype x_dt, int64_t ldq, int32_t q_heads, float softmax_scale,
+                                 int32_t causal, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+
 /* ---------------------------------------------------------------- expert routing */
 
 /* How tokens choose experts (ids that nq_gather_qmm and its kin take). */

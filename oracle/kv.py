@@ -181,3 +181,51 @@ def attention(cache, row_start, lengths, table, q, scale, causal=True, window=0)
                 lse[r, h] = m + np.log(w.sum())
                 reach[r, h] = scale * (np.abs(k[see, h // group]) @ np.abs(q[r, h])).max()
     return {"out": out, "lse": lse, "spread": spread, "reach": reach, "largest": largest, "seen": seen}
+
+
+def attention_shared(cache, prefix_start, prefix_lengths, prefix_table, row_start, lengths, table, q, scale, causal=True):
+    """As attention(), rows prefix_start[p] .. prefix_start[p + 1] seeing all of prefix p's tokens first."""
+    rows, heads, dim = q.shape
+    group = heads // cache.heads
+    out, spread = np.zeros((2, rows, heads, dim))
+    lse, reach, seen = np.full((rows, heads), -np.inf), np.zeros((rows, heads)), np.zeros(rows, np.int64)
+    largest = np.zeros((rows, heads))
+
+    def whole(b, length, table):
+        """Keys, values, what a value's scale can hold, and whether the token is there."""
+        k, there = tokens(cache, "k", b, 0, length, table)
+        v, _ = tokens(cache, "v", b, 0, length, table)
+        holds = np.zeros((length, cache.heads))
+        for i in np.flatnonzero(there):
+            holds[i] = QMAX[cache.fmt] * cache.v_scales[table[b, i // cache.block]]
+        return k.astype(np.float64), v.astype(np.float64), holds, there
+
+    before = [whole(p, max(0, int(n)), prefix_table) for p, n in enumerate(prefix_lengths)]
+    for b in range(len(lengths)):
+        r0, r1, length = int(row_start[b]), int(row_start[b + 1]), max(0, int(lengths[b]))
+        if r1 <= r0:
+            continue
+        own = whole(b, length, table)
+        for r in range(r0, r1):
+            see = own[3].copy()
+            if causal:
+                see &= np.arange(length) <= length - r1 + r
+            parts = [[a[see] for a in own[:3]]]
+            for p in range(len(prefix_lengths)):
+                if prefix_start[p] <= r < prefix_start[p + 1]:
+                    parts.insert(0, [a[before[p][3]] for a in before[p][:3]])
+            k, v, holds = (np.concatenate(a) for a in zip(*parts))
+            seen[r] = len(k)
+            if not len(k):
+                continue
+            for h in range(heads):
+                j = h // group
+                z = scale * (k[:, j] @ q[r, h])
+                m = z.max()
+                w = np.exp(z - m)
+                out[r, h] = w @ v[:, j] / w.sum()
+                spread[r, h] = w @ np.abs(v[:, j]) / w.sum()
+                largest[r, h] = (w * holds[:, j]).max() / w.sum()
+                lse[r, h] = m + np.log(w.sum())
+                reach[r, h] = scale * (np.abs(k[:, j]) @ np.abs(q[r, h])).max()
+    return {"out": out, "lse": lse, "spread": spread, "reach": reach, "largest": largest, "seen": seen}

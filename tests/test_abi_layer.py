@@ -198,3 +198,39 @@ def test_combine_arguments(lib):
     for bad in (dict(ys=AT["xs"]), dict(weights=AT["xs"]), dict(dw=AT["xs"]), dict(dw=AT["x"]), dict(dw=AT["y"]),
                 dict(dw=AT["weights"]), dict(dw=AT["place"])):
         assert combine_grad(lib, o, **bad) == ALIAS, bad
+
+
+def test_shared_attention_arguments(lib):
+    from test_abi_kv import AT as KV
+    from test_abi_kv import BAD_CACHES, BAD_SEQS, QUANT, cache, seqs  # noqa: F401
+    far = {n: a + (1 << 50) for n, a in KV.items()}
+
+    def prefix(**s):
+        return seqs(**{**dict(row_start=far["row_start"], lengths=far["lengths"], block_table=far["table"], batch=2), **s})
+
+    def attend(c=cache(), p=prefix(), s=seqs(), q=KV["q"], dt=1, ldq=1024, heads=8, scale=0.1, causal=1, out=KV["out"], lse=None,
+               ws=KV["ws"], ws_bytes=1 << 31):
+        r = lambda x: x and ctypes.byref(x)
+        return lib.nq_kv_attention_shared(r(c), r(p), r(s), q, dt, ldq, heads, scale, causal, out, lse, ws, ws_bytes, None)
+
+    assert attend(c=None) == NULL and attend(p=None) == NULL and attend(s=None) == NULL
+    for bad, status in BAD_CACHES:
+        assert attend(c=cache(**bad)) == status, bad
+        assert b"nq_kv_attention_shared" in lib.nq_last_error()
+    for bad, status in BAD_SEQS:
+        assert attend(s=seqs(**bad)) == status, bad
+        assert attend(p=prefix(**bad)) == status, bad
+    assert attend(p=prefix(rows=8)) == SHAPE and attend(s=seqs(rows=6)) == SHAPE
+    assert attend(dt=9) == DTYPE and attend(heads=7) == SHAPE and attend(scale=0.0) == SHAPE and attend(ldq=1025) == ALIGN
+    assert attend(q=None) == NULL and attend(out=0) == NULL and attend(lse=KV["lse"] + 2) == ALIGN
+    for bad in (dict(out=KV["q"]), dict(out=far["table"]), dict(lse=far["lengths"]), dict(lse=KV["out"]), dict(out=KV["k_codes"]),
+                dict(ws=far["row_start"]), dict(ws=KV["out"])):
+        assert attend(**bad) == ALIAS, bad
+    need = lib.nq_kv_attention_shared_workspace_bytes(ctypes.byref(cache()), ctypes.byref(prefix()), ctypes.byref(seqs()), 8, 1)
+    # the prefix's states: O and three sums for every row and head
+    assert need >= 7 * 8 * (128 + 4) * 4
+    assert attend(ws=None) == WORKSPACE and attend(ws_bytes=need - 1) == WORKSPACE and attend(ws=KV["ws"] + 8) == ALIGN
+    assert lib.nq_kv_attention_shared_workspace_bytes(ctypes.byref(cache()), ctypes.byref(prefix(rows=9)), ctypes.byref(seqs()), 8, 1) == 0
+    assert lib.nq_kv_attention_shared_workspace_bytes(ctypes.byref(cache()), None, ctypes.byref(seqs()), 8, 1) == 0
+    empty = dict(row_start=0, lengths=0, block_table=0, rows=0)
+    assert attend(p=prefix(**empty), s=seqs(**empty), q=None, out=None) == OK

@@ -95,3 +95,19 @@ def test_moving_is_linear_and_its_gradient_the_adjoint():
     # linear in ys and in the weights
     assert abs((y * dy).sum() - (dys * ys).sum()) < 1e-12 and abs((y * dy).sum() - (dw * w).sum()) < 1e-12
     assert np.all(dys[kept:] == 0) and np.all(dw[ids >= 5] == 0)
+
+
+def test_shared_attention_is_attention_over_the_joined_tokens():
+    """A prefix of whole blocks can also be had by repeating its blocks in every sequence's table."""
+    from oracle import kv as K
+    rng = np.random.default_rng(4)
+    cache = K.Cache(rng.integers(0, 256, (9, 2, 4, 8), dtype=np.uint8), rng.random((9, 2)).astype(np.float32),
+                    rng.integers(0, 256, (9, 2, 8, 4), dtype=np.uint8), rng.random((9, 2)).astype(np.float32), "int8")
+    q = rng.standard_normal((5, 4, 8))
+    start, lengths, table = [0, 1, 3, 5], [3, 6, 2], np.array([[2, 0], [3, 4], [5, 0]])
+    # rows 1 .. 4 (the second and third sequence) behind blocks 7 and 8
+    for causal in (True, False):
+        got = K.attention_shared(cache, [1, 5], [8], np.array([[7, 8]]), start, lengths, table, q, 0.01, causal)
+        want = K.attention(cache, start, [3, 14, 10], np.array([[2, 0, 0, 0], [7, 8, 3, 4], [7, 8, 5, 0]]), q, 0.01, causal)
+        for name in want:
+            assert np.allclose(got[name], want[name], rtol=1e-13), name
