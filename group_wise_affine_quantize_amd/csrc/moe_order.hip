@@ -32,7 +32,7 @@ constexpr int kSortWaves = 16, kSortThreads = 64 * kSortWaves;
 constexpr int kMaxBuckets = 1025;       // 1024 experts and those that do not exist
 // Pairs up to which one workgroup sorts them all; more are cut into parts.
 constexpr int64_t kOnePart = 8192;
-constexpr int64_t kPart = 4096;
+constexpr int64_t kPart = 2048;
 constexpr int kMostParts = 256;
 
 int64_t sort_parts(int64_t pairs)
@@ -62,7 +62,7 @@ __device__ __forceinline__ Run run_of(const MoeSortLaunch &a, int64_t part, int6
     return r;
 }
 
-// counts[bucket][part], for parts that several workgroups sort.
+// counts[part][bucket], for parts that several workgroups sort.
 __global__ __launch_bounds__(kSortThreads) void moe_count_kernel(MoeSortLaunch a, int64_t size)
 {
     __shared__ int hist[kMaxBuckets];
@@ -72,58 +72,57 @@ __global__ __launch_bounds__(kSortThreads) void moe_count_kernel(MoeSortLaunch a
     const int64_t first = blockIdx.x * size, last = first + size < a.pairs ? first + size : a.pairs;
     for (int64_t p = first + tid; p < last; p += kSortThreads) atomicAdd(&hist[bucket_of(a.ids[p], a.experts)], 1);
     __syncthreads();
-    for (int b = tid; b < buckets; b += kSortThreads) a.counts[(int64_t)b * gridDim.x + blockIdx.x] = hist[b];
+    for (int b = tid; b < buckets; b += kSortThreads) a.counts[(int64_t)blockIdx.x * buckets + b] = hist[b];
 }
 
 __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(MoeSortLaunch a, int64_t size)
 {
     __shared__ int hist[kSortWaves][kMaxBuckets];
-    __shared__ int base[kMaxBuckets + 7];
+    __shared__ int base[kMaxBuckets];
     __shared__ int sums[kSortWaves];
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6, buckets = a.experts + 1;
     const int parts = (int)gridDim.x, part = (int)blockIdx.x;
-    for (int i = tid; i < kSortWaves * buckets; i += kSortThreads) hist[i / buckets][i % buckets] = 0;
+    for (int b = lane; b < buckets; b += 64) hist[wave][b] = 0;
     __syncthreads();
     const Run run = run_of(a, part, size, wave);
     for (int64_t p = run.first + lane; p < run.last; p += 64) atomicAdd(&hist[wave][bucket_of(a.ids[p], a.experts)], 1);
     __syncthreads();
     // per bucket: waves' first places inside the part, the whole count, and the earlier parts'
-    int before[2], total[2];
+    auto count = [&](int b, int &before, int &total) {
+        int in_part = 0;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int b = 2 * tid + k;      // neighbouring buckets to a thread, for the scan
-        before[k] = 0, total[k] = 0;
-        if (b < buckets) {
-            int in_part = 0;
-            for (int w = 0; w < kSortWaves; ++w) {
-                const int n = hist[w][b];
-                hist[w][b] = in_part;
-                in_part += n;
-            }
-            if (parts == 1) total[k] = in_part;
-            else
-                for (int q = 0; q < parts; ++q) {
-                    const int n = a.counts[(int64_t)b * parts + q];
-                    if (q < part) before[k] += n;
-                    total[k] += n;
-                }
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int n = hist[w][b];
+            hist[w][b] = in_part;
+            in_part += n;
         }
-    }
-    // exclusive sums over the buckets
-    const int mine = total[0] + total[1];
-    const int upto = (int)wave_scan32((uint32_t)mine);
+        before = 0, total = in_part;
+        if (parts == 1) return;
+        total = 0;
+#pragma unroll 16
+        for (int q = 0; q < parts; ++q) {
+            const int n = a.counts[(int64_t)q * buckets + b];
+            before += q < part ? n : 0;
+            total += n;
+        }
+    };
+    int before = 0, total = 0;
+    if (tid < buckets) count(tid, before, total);
+    // exclusive sums over the buckets; of 1025, the last comes behind all others
+    const int upto = (int)wave_scan32((uint32_t)total);
     if (lane == 63) sums[wave] = upto;
     __syncthreads();
-    int at = upto - mine;
+    int at = upto - total;
     for (int w = 0; w < wave; ++w) at += sums[w];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int b = 2 * tid + k;
-        if (b < buckets) {
-            base[b] = at + before[k];
-            if (part == 0) a.starts[b] = at;
-        }
-        at += total[k];
+    if (tid < buckets) {
+        base[tid] = at + before;
+        if (part == 0) a.starts[tid] = at;
+    }
+    if (buckets > kSortThreads && tid == kSortThreads - 1) {
+        at += total;
+        count(kSortThreads, before, total);
+        base[kSortThreads] = at + before;
+        if (part == 0) a.starts[kSortThreads] = at;
     }
     __syncthreads();
     // places, in the order of the pairs
@@ -167,7 +166,7 @@ struct Teams {
     int64_t token0;
 };
 
-template <typename T, int E> __global__ __launch_bounds__(kRowThreads) void moe_dispatch_kernel(MoeRowsLaunch a, Teams m)
+template <typename T, int E, bool AL> __global__ __launch_bounds__(kRowThreads) void moe_dispatch_kernel(MoeRowsLaunch a, Teams m)
 {
     const int lane = (int)threadIdx.x & ((1 << m.shift) - 1);
     const int64_t t = m.token0 + ((int64_t)blockIdx.x << (8 - m.shift)) + ((int)threadIdx.x >> m.shift);
@@ -178,15 +177,15 @@ template <typename T, int E> __global__ __launch_bounds__(kRowThreads) void moe_
     const T *x = static_cast<const T *>(a.in) + t * a.ldi;
     T *out = static_cast<T *>(a.out);
     for (int64_t c = lane + ((int64_t)blockIdx.y << m.shift); c < m.pieces; c += (int64_t)gridDim.y << m.shift) {
-        const Raw<T, E> v = load_raw<T, E>(x + c * E);
+        const Raw<T, E> v = load_cols<T, E, AL>(x, c * E, a.hidden);
         for (int j = 0; j < a.top_k; ++j) {
             const int64_t r = checked(place[j], rows);
-            if (r >= 0) store_raw<T, E>(out + r * a.hidden + c * E, r < kept ? v : raw_zero<T, E>());
+            if (r >= 0) store_cols<T, E, AL>(out + r * a.hidden, c * E, a.hidden, r < kept ? v : raw_zero<T, E>());
         }
     }
 }
 
-template <typename T, int E> __global__ __launch_bounds__(kRowThreads) void moe_combine_kernel(MoeRowsLaunch a, Teams m)
+template <typename T, int E, bool AL> __global__ __launch_bounds__(kRowThreads) void moe_combine_kernel(MoeRowsLaunch a, Teams m)
 {
     constexpr int K = 8;        // rows on the way at once
     const int lane = (int)threadIdx.x & ((1 << m.shift) - 1);
@@ -198,7 +197,7 @@ template <typename T, int E> __global__ __launch_bounds__(kRowThreads) void moe_
     const T *in = static_cast<const T *>(a.in);
     for (int64_t c = lane + ((int64_t)blockIdx.y << m.shift); c < m.pieces; c += (int64_t)gridDim.y << m.shift) {
         float sum[E];
-        if (a.residual) load_run<T, E>(static_cast<const T *>(a.residual) + t * a.ldr + c * E, sum);
+        if (a.residual) unpack<T, E>(load_cols<T, E, AL>(static_cast<const T *>(a.residual) + t * a.ldr, c * E, a.hidden), sum);
         else
 #pragma unroll
             for (int e = 0; e < E; ++e) sum[e] = 0.0f;
@@ -211,7 +210,7 @@ template <typename T, int E> __global__ __launch_bounds__(kRowThreads) void moe_
                 if (j0 + j >= a.top_k) continue;
                 const int64_t r = checked(place[j0 + j], rows);
                 if (r < 0) continue;
-                v[j] = load_raw<T, E>(in + r * a.hidden + c * E);
+                v[j] = load_cols<T, E, AL>(in + r * a.hidden, c * E, a.hidden);
                 w[j] = weights ? weights[j0 + j] : 1.0f;
             }
 #pragma unroll
@@ -222,12 +221,12 @@ template <typename T, int E> __global__ __launch_bounds__(kRowThreads) void moe_
                 for (int e = 0; e < E; ++e) sum[e] = fmaf(w[j], f[e], sum[e]);
             }
         }
-        store_run<T, E>(static_cast<T *>(a.out) + t * a.hidden + c * E, sum);
+        store_cols<T, E, AL>(static_cast<T *>(a.out) + t * a.hidden, c * E, a.hidden, pack<T, E>(sum));
     }
 }
 
 // A team takes a whole row here (its sums), TEAM threads.
-template <typename T, int E, int TEAM>
+template <typename T, int E, int TEAM, bool AL>
 __global__ __launch_bounds__(kRowThreads) void moe_combine_grad_kernel(MoeRowsLaunch a, Teams m)
 {
     constexpr int K = 8, WAVES = TEAM > 64 ? TEAM / 64 : 1;
@@ -252,13 +251,13 @@ __global__ __launch_bounds__(kRowThreads) void moe_combine_grad_kernel(MoeRowsLa
         }
         for (int64_t c = lane; c < m.pieces; c += TEAM) {
             float g[E];
-            load_run<T, E>(dy + c * E, g);
+            unpack<T, E>(load_cols<T, E, AL>(dy, c * E, a.hidden), g);
             Raw<T, E> v[K];
             if (a.dweights) {
 #pragma unroll
                 for (int j = 0; j < K; ++j) {
                     v[j] = raw_zero<T, E>();
-                    if (at[j] >= 0 && at[j] < kept) v[j] = load_raw<T, E>(ys + at[j] * a.hidden + c * E);
+                    if (at[j] >= 0 && at[j] < kept) v[j] = load_cols<T, E, AL>(ys + at[j] * a.hidden, c * E, a.hidden);
                 }
             }
 #pragma unroll
@@ -273,7 +272,7 @@ __global__ __launch_bounds__(kRowThreads) void moe_combine_grad_kernel(MoeRowsLa
                 }
 #pragma unroll
                 for (int e = 0; e < E; ++e) d[e] = there ? w[j] * g[e] : 0.0f;
-                store_run<T, E>(dys + at[j] * a.hidden + c * E, d);
+                store_cols<T, E, AL>(dys + at[j] * a.hidden, c * E, a.hidden, pack<T, E>(d));
             }
         }
         if (!a.dweights) continue;
@@ -300,7 +299,7 @@ __global__ __launch_bounds__(kRowThreads) void moe_combine_grad_kernel(MoeRowsLa
     }
 }
 
-bool wide(const MoeRowsLaunch &a, int e)
+bool aligned_rows(const MoeRowsLaunch &a, int e)
 {
     const uintptr_t bits = (uintptr_t)a.in | (uintptr_t)a.out | (uintptr_t)a.residual | (uintptr_t)a.ys;
     return (bits & 15) == 0 && a.hidden % e == 0 && a.ldi % e == 0 && a.ldr % e == 0;
@@ -333,26 +332,38 @@ template <typename Kernel> hipError_t over_tokens(const MoeRowsLaunch &a, Teams 
 // Workgroups to a row: one for every two rounds of its pieces.
 unsigned rounds(const Teams &m) { return (unsigned)std::min<int64_t>(64, ((m.pieces >> m.shift) + 1) / 2 + (m.pieces >> m.shift == 0)); }
 
-template <typename T, int E> hipError_t dispatch_go(const MoeRowsLaunch &a, hipStream_t stream)
-{
-    const Teams m = teams_of(a, E);
-    return over_tokens(a, m, rounds(m), moe_dispatch_kernel<T, E>, stream);
-}
-template <typename T, int E> hipError_t combine_go(const MoeRowsLaunch &a, hipStream_t stream)
-{
-    const Teams m = teams_of(a, E);
-    return over_tokens(a, m, rounds(m), moe_combine_kernel<T, E>, stream);
-}
-template <typename T, int E> hipError_t grad_go(const MoeRowsLaunch &a, hipStream_t stream)
-{
-    Teams m = teams_of(a, E);
-    if (m.shift == 8) return over_tokens(a, m, 1, moe_combine_grad_kernel<T, E, 256>, stream);
-    if (m.shift > 4) {
-        m.shift = 6;
-        return over_tokens(a, m, 1, moe_combine_grad_kernel<T, E, 64>, stream);
+template <typename T, int E, bool AL> struct Dispatch {
+    static hipError_t run(const MoeRowsLaunch &a, hipStream_t stream)
+    {
+        const Teams m = teams_of(a, E);
+        return over_tokens(a, m, rounds(m), moe_dispatch_kernel<T, E, AL>, stream);
     }
-    m.shift = 4;
-    return over_tokens(a, m, 1, moe_combine_grad_kernel<T, E, 16>, stream);
+};
+template <typename T, int E, bool AL> struct Combine {
+    static hipError_t run(const MoeRowsLaunch &a, hipStream_t stream)
+    {
+        const Teams m = teams_of(a, E);
+        return over_tokens(a, m, rounds(m), moe_combine_kernel<T, E, AL>, stream);
+    }
+};
+template <typename T, int E, bool AL> struct CombineGrad {
+    static hipError_t run(const MoeRowsLaunch &a, hipStream_t stream)
+    {
+        Teams m = teams_of(a, E);
+        if (m.shift == 8) return over_tokens(a, m, 1, moe_combine_grad_kernel<T, E, 256, AL>, stream);
+        if (m.shift > 4) {
+            m.shift = 6;
+            return over_tokens(a, m, 1, moe_combine_grad_kernel<T, E, 64, AL>, stream);
+        }
+        m.shift = 4;
+        return over_tokens(a, m, 1, moe_combine_grad_kernel<T, E, 16, AL>, stream);
+    }
+};
+
+template <template <typename, int, bool> class Go> hipError_t rows_go(const MoeRowsLaunch &a, hipStream_t stream)
+{
+    if (a.x_dt == 0) return aligned_rows(a, 4) ? Go<float, 4, true>::run(a, stream) : Go<float, 4, false>::run(a, stream);
+    return aligned_rows(a, 8) ? Go<bf16_bits, 8, true>::run(a, stream) : Go<bf16_bits, 8, false>::run(a, stream);
 }
 
 }  // namespace
@@ -375,15 +386,8 @@ hipError_t launch_moe_sort(const MoeSortLaunch &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-#define NQ_ROWS_LAUNCH(name, go)                                                              \
-    hipError_t name(const MoeRowsLaunch &a, hipStream_t stream)                               \
-    {                                                                                         \
-        if (a.x_dt == 0) return wide(a, 4) ? go<float, 4>(a, stream) : go<float, 1>(a, stream); \
-        return wide(a, 8) ? go<bf16_bits, 8>(a, stream) : go<bf16_bits, 1>(a, stream);        \
-    }
-NQ_ROWS_LAUNCH(launch_moe_dispatch, dispatch_go)
-NQ_ROWS_LAUNCH(launch_moe_combine, combine_go)
-NQ_ROWS_LAUNCH(launch_moe_combine_grad, grad_go)
-#undef NQ_ROWS_LAUNCH
+hipError_t launch_moe_dispatch(const MoeRowsLaunch &a, hipStream_t stream) { return rows_go<Dispatch>(a, stream); }
+hipError_t launch_moe_combine(const MoeRowsLaunch &a, hipStream_t stream) { return rows_go<Combine>(a, stream); }
+hipError_t launch_moe_combine_grad(const MoeRowsLaunch &a, hipStream_t stream) { return rows_go<CombineGrad>(a, stream); }
 
 }  // namespace nqk

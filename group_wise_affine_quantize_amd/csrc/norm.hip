@@ -24,6 +24,7 @@
 
 #include "nq_kv.h"
 #include "nq_layer.h"
+#include "nq_tiles.h"
 #include "nq_vec.h"
 
 namespace nqk {
@@ -31,7 +32,7 @@ namespace nqk {
 namespace {
 
 // Sums over a team of W waves, N at a time.  Slots alternate, so that one
-// barrier per exchange is enough.
+// barrier per exchange is enough; it leaves global loads in flight.
 template <int W, int N> struct TeamSum {
     float (*sh)[W][N];      // two slots
     int slot;
@@ -44,7 +45,7 @@ template <int W, int N> struct TeamSum {
             if (lane == 0)
 #pragma unroll
                 for (int i = 0; i < N; ++i) sh[slot][wave][i] = v[i];
-            __syncthreads();
+            lds_barrier();
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 float s = sh[slot][0][i];
@@ -60,7 +61,7 @@ template <int W, int N> struct TeamSum {
 // Teams of W waves; a row is V pieces of E elements for each thread.
 template <int W> constexpr int teams() { return W == 1 ? 4 : 1; }
 
-template <typename T, typename P, int E, int W, int V>
+template <typename T, typename P, int E, int W, int V, bool AL>
 __global__ __launch_bounds__(64 * W * teams<W>()) void block_norm_kernel(BlockNormLaunch a)
 {
     constexpr int TEAMS = teams<W>(), STRIDE = 64 * W * E;
@@ -71,27 +72,18 @@ __global__ __launch_bounds__(64 * W * teams<W>()) void block_norm_kernel(BlockNo
     const int dim = (int)a.dim, col0 = (64 * wave + lane) * E;
     const float inv = 1.0f / (float)dim;
     const int64_t per_gate = a.gate ? a.rows / a.gates : 1;
+    const P *post = static_cast<const P *>(a.post), *pre = static_cast<const P *>(a.pre);
     for (int64_t row = (int64_t)blockIdx.x * TEAMS + team; row < a.rows; row += (int64_t)gridDim.x * TEAMS) {
         const T *h = static_cast<const T *>(a.h) + row * a.ldh;
         float x[V][E];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = col0 + i * STRIDE;
-            if (c < dim) load_run<T, E>(h + c, x[i]);
-            else
-#pragma unroll
-                for (int e = 0; e < E; ++e) x[i][e] = 0.0f;
-        }
+        for (int i = 0; i < V; ++i) unpack<T, E>(load_cols<T, E, AL>(h, col0 + i * STRIDE, dim), x[i]);
         if (a.y) {
             const T *y = static_cast<const T *>(a.y) + row * a.ldy;
             float u[V][E], s = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int c = col0 + i * STRIDE;
-                if (c < dim) load_run<T, E>(y + c, u[i]);
-                else
-#pragma unroll
-                    for (int e = 0; e < E; ++e) u[i][e] = 0.0f;
+                unpack<T, E>(load_cols<T, E, AL>(y, col0 + i * STRIDE, dim), u[i]);
 #pragma unroll
                 for (int e = 0; e < E; ++e) s = fmaf(u[i][e], u[i][e], s);
             }
@@ -104,23 +96,22 @@ __global__ __launch_bounds__(64 * W * teams<W>()) void block_norm_kernel(BlockNo
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int c = col0 + i * STRIDE;
-                if (c >= dim) continue;
                 float w[E];
 #pragma unroll
                 for (int e = 0; e < E; ++e) u[i][e] *= f;
                 if (a.post) {
-                    load_run<P, E>(static_cast<const P *>(a.post) + c, w);
+                    unpack<P, E>(load_cols<P, E, AL>(post, c, dim), w);
 #pragma unroll
                     for (int e = 0; e < E; ++e) u[i][e] *= w[e] + a.offset;
                 }
                 if (a.gate) {
-                    load_run<P, E>(gate + c, w);
+                    unpack<P, E>(load_cols<P, E, AL>(gate, c, dim), w);
 #pragma unroll
                     for (int e = 0; e < E; ++e) u[i][e] *= w[e];
                 }
 #pragma unroll
                 for (int e = 0; e < E; ++e) x[i][e] += u[i][e];
-                store_run<T, E>(static_cast<T *>(a.h_out) + row * dim + c, x[i]);
+                store_cols<T, E, AL>(static_cast<T *>(a.h_out) + row * dim, c, dim, pack<T, E>(x[i]));
             }
         }
         if (a.z) {
@@ -134,12 +125,11 @@ __global__ __launch_bounds__(64 * W * teams<W>()) void block_norm_kernel(BlockNo
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int c = col0 + i * STRIDE;
-                if (c >= dim) continue;
                 float w[E], z[E];
-                load_run<P, E>(static_cast<const P *>(a.pre) + c, w);
+                unpack<P, E>(load_cols<P, E, AL>(pre, c, dim), w);
 #pragma unroll
                 for (int e = 0; e < E; ++e) z[e] = x[i][e] * r * (w[e] + a.offset);
-                store_run<T, E>(static_cast<T *>(a.z) + row * dim + c, z);
+                store_cols<T, E, AL>(static_cast<T *>(a.z) + row * dim, c, dim, pack<T, E>(z));
             }
         }
     }
@@ -159,7 +149,7 @@ struct Chunks {
 
 Chunks chunks_of(int64_t rows, int64_t gates)
 {
-    constexpr int64_t kMost = 1024, kLeast = 8;
+    constexpr int64_t kMost = 512, kLeast = 8;
     Chunks c{};
     if (rows == 0) return c;
     const int64_t want = std::max<int64_t>(kLeast, (rows + kMost - 1) / kMost);
@@ -178,260 +168,287 @@ Chunks chunks_of(int64_t rows, int64_t gates)
     return c;
 }
 
-template <typename T, typename P, int E, int W, int V>
-__global__ __launch_bounds__(64 * W) void block_norm_grad_kernel(BlockNormGradLaunch a, Chunks ch, float *part_pre,
-                                                                 float *part_post, float *part_gate)
+// Teams of a workgroup of the gradient: they take the rows of a chunk (or its
+// gates' runs of rows) by turns and add up their sums at the end.
+template <int W> constexpr int grad_teams() { return W >= 8 ? 1 : 8 / W; }
+
+template <typename T, typename P, int E, int W, int V, bool AL>
+__global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kernel(BlockNormGradLaunch a, Chunks ch, float *part_pre,
+                                                                                  float *part_post, float *part_gate)
 {
-    constexpr int STRIDE = 64 * W * E;
-    __shared__ float sh3[2][W][3], sh1[2][W][1];
-    const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
-    TeamSum<W, 3> total3{sh3, 0};
-    TeamSum<W, 1> total1{sh1, 0};
+    constexpr int TEAMS = grad_teams<W>(), STRIDE = 64 * W * E, COLS = STRIDE * V;
+    __shared__ float sh3[TEAMS][2][W][3], sh1[TEAMS][2][W][1];
+    __shared__ float sh_sum[TEAMS > 1 ? TEAMS - 1 : 1][TEAMS > 1 ? COLS : 1];
+    const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6) % W;
+    const int team = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) / W);
+    TeamSum<W, 3> total3{sh3[team], 0};
+    TeamSum<W, 1> total1{sh1[team], 0};
     const int dim = (int)a.dim, col0 = (64 * wave + lane) * E;
     const float inv = 1.0f / (float)dim;
-    int64_t first, last;
-    if (ch.gates) first = blockIdx.x * ch.size, last = first + ch.size < a.rows ? first + ch.size : a.rows;
-    else {
+
+    // The team's rows: runs of `run` rows, its k-th starting `team` + k * TEAMS
+    // runs behind `first`.  All teams take the same number of steps (they
+    // meet at barriers), some past the chunk's end.
+    int64_t first, last, run = 1;
+    if (ch.gates) {
+        first = blockIdx.x * ch.size, last = first + ch.size < a.rows ? first + ch.size : a.rows;
+        run = ch.per_gate;
+    } else {
         const int64_t g = blockIdx.x / ch.cuts, k = blockIdx.x - g * ch.cuts;
         first = g * ch.per_gate + k * ch.size;
         last = (k + 1) * ch.size < ch.per_gate ? first + ch.size : (g + 1) * ch.per_gate;
     }
+    const int64_t steps = ((last - first) / run + TEAMS - 1) / TEAMS * run;
+    int64_t gate_row = a.gate ? (ch.gates ? first / ch.per_gate + team : first / ch.per_gate) : 0;
+
     float dpre[V][E], dpost[V][E], dgate[V][E];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int e = 0; e < E; ++e) dpre[i][e] = dpost[i][e] = dgate[i][e] = 0.0f;
+    Raw<P, E> wpre[V], wpost[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = col0 + i * STRIDE;
+        wpre[i] = a.pre ? load_cols<P, E, AL>(static_cast<const P *>(a.pre), c, dim) : raw_zero<P, E>();
+        wpost[i] = a.post ? load_cols<P, E, AL>(static_cast<const P *>(a.post), c, dim) : raw_zero<P, E>();
+    }
 
-    int64_t gate_row = a.gate ? first / ch.per_gate : 0, gate_end = (gate_row + 1) * ch.per_gate;
-    for (int64_t row = first; row < last; ++row) {
-        float x[V][E], y[V][E], d[V][E], t[V][E];
+    Raw<T, E> x[V], t[V], d0[V], y[V];
+    auto load = [&](const void *p, int64_t ld, int64_t row, Raw<T, E> *to) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            to[i] = p && row < last ? load_cols<T, E, AL>(static_cast<const T *>(p) + row * ld, col0 + i * STRIDE, dim) : raw_zero<T, E>();
+    };
+    int64_t row = first + team * run;
+    load(a.h_out, a.ldh, row, x), load(a.dz, a.ldz, row, t), load(a.dh_out, a.ldd, row, d0), load(a.y, a.ldy, row, y);
+    int64_t in_run = 0;
+    for (int64_t step = 0; step < steps; ++step) {
+        const bool there = row < last;
+        int64_t next = row + 1;
+        if (++in_run == run) in_run = 0, next = row + 1 + (TEAMS - 1) * run;
         float s[3] = {0.0f, 0.0f, 0.0f};    // of h'^2, v h', y^2
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = col0 + i * STRIDE;
-            const bool in = c < dim;
-            auto get = [&](const void *p, int64_t ld, float *v) {
-                if (p && in) load_run<T, E>(static_cast<const T *>(p) + row * ld + c, v);
-                else
-#pragma unroll
-                    for (int e = 0; e < E; ++e) v[e] = 0.0f;
-            };
-            get(a.h_out, a.ldh, x[i]);
-            get(a.dz, a.ldz, t[i]);
-            get(a.dh_out, a.ldd, d[i]);
-            get(a.y, a.ldy, y[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = col0 + i * STRIDE;
-            float w[E];
-            if (a.pre && c < dim) load_run<P, E>(static_cast<const P *>(a.pre) + c, w);
-            else
-#pragma unroll
-                for (int e = 0; e < E; ++e) w[e] = 0.0f;
+            float w[E], xf[E], tf[E], yf[E];
+            unpack<P, E>(wpre[i], w);
+            unpack<T, E>(x[i], xf), unpack<T, E>(t[i], tf), unpack<T, E>(y[i], yf);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                s[0] = fmaf(x[i][e], x[i][e], s[0]);
-                s[1] = fmaf(t[i][e] * (w[e] + a.offset), x[i][e], s[1]);
-                s[2] = fmaf(y[i][e], y[i][e], s[2]);
+                s[0] = fmaf(xf[e], xf[e], s[0]);
+                s[1] = fmaf(tf[e] * (w[e] + a.offset), xf[e], s[1]);
+                s[2] = fmaf(yf[e], yf[e], s[2]);
             }
         }
         total3(s, lane, wave);
-        if (a.dz) {
-            const float rh = rsqrtf(fmaf(s[0], inv, a.eps));
-            const float k = -(s[1] * inv * rh) * rh;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = col0 + i * STRIDE;
-                float w[E];
-                if (c < dim) load_run<P, E>(static_cast<const P *>(a.pre) + c, w);
-                else
-#pragma unroll
-                    for (int e = 0; e < E; ++e) w[e] = 0.0f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float xh = x[i][e] * rh;
-                    dpre[i][e] = fmaf(t[i][e], xh, dpre[i][e]);
-                    d[i][e] += fmaf(k, xh, t[i][e] * rh * (w[e] + a.offset));
-                }
-            }
-        }
+        const float rh = rsqrtf(fmaf(s[0], inv, a.eps)), kh = -(s[1] * inv * rh) * rh;
+        float d[V][E];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = col0 + i * STRIDE;
-            if (c < dim) store_run<T, E>(static_cast<T *>(a.dh) + row * dim + c, d[i]);
+            float w[E], xf[E], tf[E];
+            unpack<T, E>(d0[i], d[i]);
+            if (a.dz) {
+                unpack<P, E>(wpre[i], w);
+                unpack<T, E>(x[i], xf), unpack<T, E>(t[i], tf);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float xh = xf[e] * rh;
+                    dpre[i][e] = fmaf(tf[e], xh, dpre[i][e]);
+                    d[i][e] += fmaf(kh, xh, tf[e] * rh * (w[e] + a.offset));
+                }
+            }
+            if (there) store_cols<T, E, AL>(static_cast<T *>(a.dh) + row * dim, col0 + i * STRIDE, dim, pack<T, E>(d[i]));
         }
+        // the next row's, while this one's second half runs
+        load(a.h_out, a.ldh, next, x), load(a.dz, a.ldz, next, t), load(a.dh_out, a.ldd, next, d0);
         if (a.y) {
-            if (row >= gate_end) ++gate_row, gate_end += ch.per_gate;
             const P *gate = static_cast<const P *>(a.gate) + gate_row * a.ldg;
             const float ry = a.post ? rsqrtf(fmaf(s[2], inv, a.eps)) : 1.0f;
             float sw = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int c = col0 + i * STRIDE;
-                float g[E], p[E];
+                float g[E], p[E], yf[E];
 #pragma unroll
                 for (int e = 0; e < E; ++e) g[e] = 1.0f, p[e] = 1.0f;
-                if (a.gate && c < dim) load_run<P, E>(gate + c, g);
-                if (a.post && c < dim) {
-                    load_run<P, E>(static_cast<const P *>(a.post) + c, p);
+                if (a.gate && there) unpack<P, E>(load_cols<P, E, AL>(gate, col0 + i * STRIDE, dim), g);
+                if (a.post) {
+                    unpack<P, E>(wpost[i], p);
 #pragma unroll
                     for (int e = 0; e < E; ++e) p[e] += a.offset;
                 }
+                unpack<T, E>(y[i], yf);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    const float yh = y[i][e] * ry, sd = a.scale * d[i][e];
+                    const float yh = yf[e] * ry, sd = a.scale * d[i][e];
                     const float du = sd * g[e];
                     dgate[i][e] = fmaf(sd, yh * p[e], dgate[i][e]);
                     dpost[i][e] = fmaf(du, yh, dpost[i][e]);
-                    t[i][e] = du * p[e];
-                    sw = fmaf(t[i][e], y[i][e], sw);
+                    d[i][e] = du * p[e];
+                    sw = fmaf(d[i][e], yf[e], sw);
                 }
             }
-            float k = 0.0f;
+            float ky = 0.0f;
             if (a.post) {
                 total1(&sw, lane, wave);
-                k = -(sw * inv * ry) * ry;
+                ky = -(sw * inv * ry) * ry;
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int c = col0 + i * STRIDE;
-                float v[E];
+                float v[E], yf[E];
+                unpack<T, E>(y[i], yf);
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[e] = fmaf(k, y[i][e] * ry, t[i][e] * ry);
-                if (c < dim) store_run<T, E>(static_cast<T *>(a.dy) + row * dim + c, v);
+                for (int e = 0; e < E; ++e) v[e] = fmaf(ky, yf[e] * ry, d[i][e] * ry);
+                if (there) store_cols<T, E, AL>(static_cast<T *>(a.dy) + row * dim, col0 + i * STRIDE, dim, pack<T, E>(v));
             }
-            if (a.dgate && ch.gates && row + 1 == gate_end) {
+            if (ch.gates && in_run == 0) {
+                if (a.dgate && there)
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int c = col0 + i * STRIDE;
-                    if (c < dim) store_run<P, E>(static_cast<P *>(a.dgate) + gate_row * dim + c, dgate[i]);
+                    for (int i = 0; i < V; ++i)
+                        store_cols<P, E, AL>(static_cast<P *>(a.dgate) + gate_row * dim, col0 + i * STRIDE, dim, pack<P, E>(dgate[i]));
+#pragma unroll
+                for (int i = 0; i < V; ++i)
 #pragma unroll
                     for (int e = 0; e < E; ++e) dgate[i][e] = 0.0f;
-                }
+                if (a.gate) gate_row += TEAMS;
             }
         }
+        load(a.y, a.ldy, next, y);
+        row = next;
     }
-    const int64_t at = (int64_t)blockIdx.x * dim;
+
+    // the chunk's sums, the teams' in their order
+    auto finish = [&](float (*sum)[E], float *part) {
+        if (!part) return;
+        if constexpr (TEAMS > 1) {
+            __syncthreads();
+            if (team > 0)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = col0 + i * STRIDE;
-        if (c >= dim) continue;
-        if (part_pre) store_run<float, E>(part_pre + at + c, dpre[i]);
-        if (part_post) store_run<float, E>(part_post + at + c, dpost[i]);
-        if (part_gate) store_run<float, E>(part_gate + at + c, dgate[i]);
-    }
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) sh_sum[team - 1][col0 + i * STRIDE + e] = sum[i][e];
+            __syncthreads();
+            if (team > 0) return;
+#pragma unroll
+            for (int k = 0; k < TEAMS - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) sum[i][e] += sh_sum[k][col0 + i * STRIDE + e];
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            store_cols<float, E, AL>(part + (int64_t)blockIdx.x * dim, col0 + i * STRIDE, dim, pack<float, E>(sum[i]));
+    };
+    finish(dpre, part_pre);
+    finish(dpost, part_post);
+    finish(dgate, part_gate);
 }
 
 // out[g][c] = sum over the chunks g * cuts .. of part[chunk][c], in order within
-// each of the workgroup's runs and over them.
+// each of the workgroup's runs and over them: of up to three parameters, of
+// which the last may have many gates.
 constexpr int kSumRuns = 16, kSumCols = 64;
-template <typename P>
-__global__ __launch_bounds__(kSumRuns * kSumCols) void column_sum_kernel(const float *part, int64_t cuts, int dim, P *out,
-                                                                         int64_t gate0)
+struct ColumnSums {
+    const float *part[3];
+    void *out[3];
+    int64_t cuts[3], gates[3];
+    int dim;
+};
+template <typename P> __global__ __launch_bounds__(kSumRuns * kSumCols) void column_sum_kernel(ColumnSums a)
 {
     __shared__ float sh[kSumRuns][kSumCols];
     const int lane = (int)threadIdx.x % kSumCols, run = (int)threadIdx.x / kSumCols;
-    const int c = (int)blockIdx.x * kSumCols + lane;
-    const int64_t g = gate0 + blockIdx.y;
-    float s = 0.0f;
-    if (c < dim) {
-        const float *p = part + g * cuts * dim + c;
+    const int c = (int)blockIdx.x * kSumCols + lane, which = (int)blockIdx.z;
+    P *out = static_cast<P *>(a.out[which]);
+    if (!out) return;
+    const int64_t cuts = a.cuts[which];
+    for (int64_t g = blockIdx.y; g < a.gates[which]; g += gridDim.y) {
+        float s = 0.0f;
+        if (c < a.dim) {
+            const float *p = a.part[which] + g * cuts * a.dim + c;
 #pragma unroll 8
-        for (int64_t k = run; k < cuts; k += kSumRuns) s += p[k * dim];
-    }
-    sh[run][lane] = s;
-    __syncthreads();
-    if (run == 0 && c < dim) {
+            for (int64_t k = run; k < cuts; k += kSumRuns) s += p[k * a.dim];
+        }
+        sh[run][lane] = s;
+        __syncthreads();
+        if (run == 0 && c < a.dim) {
 #pragma unroll
-        for (int r = 1; r < kSumRuns; ++r) s += sh[r][lane];
-        Elt<P>::store(out, g * dim + c, s);
+            for (int r = 1; r < kSumRuns; ++r) s += sh[r][lane];
+            Elt<P>::store(out, g * a.dim + c, s);
+        }
+        __syncthreads();
     }
-}
-
-template <typename P> hipError_t column_sum(const float *part, int64_t gates, int64_t cuts, int64_t dim, void *out, hipStream_t stream)
-{
-    for (int64_t g = 0; g < gates; g += 65535) {
-        const dim3 grid((unsigned)((dim + kSumCols - 1) / kSumCols), (unsigned)std::min<int64_t>(65535, gates - g));
-        column_sum_kernel<P><<<grid, kSumRuns * kSumCols, 0, stream>>>(part, cuts, (int)dim, static_cast<P *>(out), g);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
 }
 
 bool aligned(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-template <typename T, typename P, int E, int W, int V> hipError_t forward(const BlockNormLaunch &a, hipStream_t stream)
-{
-    const int64_t groups = (a.rows + teams<W>() - 1) / teams<W>();
-    const unsigned grid = (unsigned)std::min<int64_t>(groups, 1 << 20);
-    block_norm_kernel<T, P, E, W, V><<<grid, 64 * W * teams<W>(), 0, stream>>>(a);
-    return hipGetLastError();
-}
-
-template <typename T, typename P, int E, int W, int V> hipError_t backward(const BlockNormGradLaunch &a, hipStream_t stream)
-{
-    const Chunks ch = chunks_of(a.rows, a.gates);
-    const int64_t part = ch.chunks * a.dim;
-    float *at = a.partials, *pre = nullptr, *post = nullptr, *gate = nullptr;
-    if (a.dpre) pre = at, at += part;
-    if (a.dpost) post = at, at += part;
-    if (a.dgate && !ch.gates) gate = at;
-    hipError_t e = hipSuccess;
-    if (ch.chunks) {
-        block_norm_grad_kernel<T, P, E, W, V><<<(unsigned)ch.chunks, 64 * W, 0, stream>>>(a, ch, pre, post, gate);
-        e = hipGetLastError();
+template <typename T, typename P, int E, int W, int V, bool AL> struct Forward {
+    static hipError_t run(const BlockNormLaunch &a, hipStream_t stream)
+    {
+        const int64_t groups = (a.rows + teams<W>() - 1) / teams<W>();
+        const unsigned grid = (unsigned)std::min<int64_t>(groups, 1 << 20);
+        block_norm_kernel<T, P, E, W, V, AL><<<grid, 64 * W * teams<W>(), 0, stream>>>(a);
+        return hipGetLastError();
     }
-    if (e == hipSuccess && a.dpre) e = column_sum<P>(pre, 1, ch.chunks, a.dim, a.dpre, stream);
-    if (e == hipSuccess && a.dpost) e = column_sum<P>(post, 1, ch.chunks, a.dim, a.dpost, stream);
-    if (e == hipSuccess && a.dgate && !ch.gates) e = column_sum<P>(gate, a.gates, ch.cuts, a.dim, a.dgate, stream);
-    return e;
-}
+};
+template <typename T, typename P, int E, int W, int V, bool AL> struct Backward {
+    static hipError_t run(const BlockNormGradLaunch &a, hipStream_t stream)
+    {
+        const Chunks ch = chunks_of(a.rows, a.gates);
+        const int64_t part = ch.chunks * a.dim;
+        float *at = a.partials, *pre = nullptr, *post = nullptr, *gate = nullptr;
+        if (a.dpre) pre = at, at += part;
+        if (a.dpost) post = at, at += part;
+        if (a.dgate && !ch.gates) gate = at;
+        if (ch.chunks) {
+            block_norm_grad_kernel<T, P, E, W, V, AL><<<(unsigned)ch.chunks, 64 * W * grad_teams<W>(), 0, stream>>>(a, ch, pre, post, gate);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        const bool gates = a.dgate && !ch.gates;
+        if (!a.dpre && !a.dpost && !gates) return hipSuccess;
+        const ColumnSums c{{pre, post, gate}, {a.dpre, a.dpost, gates ? a.dgate : nullptr}, {ch.chunks, ch.chunks, ch.cuts},
+                           {1, 1, a.gates}, (int)a.dim};
+        const dim3 grid((unsigned)((a.dim + kSumCols - 1) / kSumCols), (unsigned)(gates ? std::min<int64_t>(a.gates, 1024) : 1), gates ? 3 : 2);
+        column_sum_kernel<P><<<grid, kSumRuns * kSumCols, 0, stream>>>(c);
+        return hipGetLastError();
+    }
+};
 
-// The smallest team that holds a row in 16 elements per thread (32 in fp32
-// past 8192).
-template <template <typename, typename, int, int, int> class Go, typename T, typename P, int E, typename A>
+// The smallest team that holds a row in 16 elements per thread.
+template <template <typename, typename, int, int, int, bool> class Go, typename T, typename P, bool AL, typename A>
 hipError_t by_width(const A &a, hipStream_t stream)
 {
-    constexpr int V = 16 / E;
+    constexpr int E = 16 / (int)sizeof(T), V = 16 / E;
     const int64_t dim = a.dim;
-    if (dim <= 64 * E) return Go<T, P, E, 1, 1>::run(a, stream);
-    if (dim <= 1024) return Go<T, P, E, 1, V>::run(a, stream);
-    if (dim <= 2048) return Go<T, P, E, 2, V>::run(a, stream);
-    if (dim <= 4096) return Go<T, P, E, 4, V>::run(a, stream);
-    if (dim <= 8192) return Go<T, P, E, 8, V>::run(a, stream);
-    return Go<T, P, E, 16, V>::run(a, stream);
+    if (dim <= 64 * E) return Go<T, P, E, 1, 1, AL>::run(a, stream);
+    if (dim <= 1024) return Go<T, P, E, 1, V, AL>::run(a, stream);
+    if (dim <= 2048) return Go<T, P, E, 2, V, AL>::run(a, stream);
+    if (dim <= 4096) return Go<T, P, E, 4, V, AL>::run(a, stream);
+    if (dim <= 8192) return Go<T, P, E, 8, V, AL>::run(a, stream);
+    return Go<T, P, E, 16, V, AL>::run(a, stream);
 }
 
-template <typename T, typename P, int E, int W, int V> struct Forward {
-    static hipError_t run(const BlockNormLaunch &a, hipStream_t s) { return forward<T, P, E, W, V>(a, s); }
-};
-template <typename T, typename P, int E, int W, int V> struct Backward {
-    static hipError_t run(const BlockNormGradLaunch &a, hipStream_t s) { return backward<T, P, E, W, V>(a, s); }
-};
-
-// Whether all rows can be moved 16 bytes of T at a time.
-bool wide(const BlockNormLaunch &a, int e)
+// Whether all rows start at multiples of 16 bytes and end with a whole piece.
+bool aligned_rows(const BlockNormLaunch &a, int e)
 {
     return a.dim % e == 0 && a.ldh % e == 0 && a.ldy % e == 0 && a.ldg % e == 0 && aligned(a.h) && aligned(a.y) &&
            aligned(a.post) && aligned(a.gate) && aligned(a.pre) && aligned(a.h_out) && aligned(a.z);
 }
-bool wide(const BlockNormGradLaunch &a, int e)
+bool aligned_rows(const BlockNormGradLaunch &a, int e)
 {
     return a.dim % e == 0 && a.ldh % e == 0 && a.ldy % e == 0 && a.ldd % e == 0 && a.ldz % e == 0 && a.ldg % e == 0 &&
            aligned(a.h_out) && aligned(a.y) && aligned(a.dh_out) && aligned(a.dz) && aligned(a.post) && aligned(a.gate) &&
            aligned(a.pre) && aligned(a.dh) && aligned(a.dy) && aligned(a.dpost) && aligned(a.dgate) && aligned(a.dpre);
 }
 
-template <template <typename, typename, int, int, int> class Go, typename T, typename P, typename A>
+template <template <typename, typename, int, int, int, bool> class Go, typename T, typename P, typename A>
 hipError_t by_alignment(const A &a, hipStream_t stream)
 {
-    constexpr int E = 16 / (int)sizeof(T);
-    return wide(a, E) ? by_width<Go, T, P, E>(a, stream) : by_width<Go, T, P, 1>(a, stream);
+    return aligned_rows(a, 8) ? by_width<Go, T, P, true>(a, stream) : by_width<Go, T, P, false>(a, stream);
 }
 
-template <template <typename, typename, int, int, int> class Go, typename A> hipError_t by_types(const A &a, hipStream_t stream)
+template <template <typename, typename, int, int, int, bool> class Go, typename A> hipError_t by_types(const A &a, hipStream_t stream)
 {
     if (a.x_dt == 0)
         return a.p_dt == 0 ? by_alignment<Go, float, float>(a, stream) : by_alignment<Go, float, bf16_bits>(a, stream);

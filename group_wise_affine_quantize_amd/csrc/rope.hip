@@ -9,13 +9,15 @@
 // would be off by 0.03.  It is counted in quarter turns, q = t * 2 / pi; the
 // nearest whole number leaves |q| <= 1/2, where the series of sine and cosine
 // to the terms x^13 and x^14 are within 2^-45.  One thread takes one pair of one row;
-// all of the row's heads use it, out of LDS.
+// all of the row's heads use it, out of LDS.  A thread keeps to the same columns of
+// the heads it takes, so that it divides by sizes only once.
 //
 // What bounds it: reading and writing the heads once.
 #include <algorithm>
 
 #include "nq_kv.h"
 #include "nq_layer.h"
+#include "nq_tiles.h"
 #include "nq_vec.h"
 
 namespace nqk {
@@ -23,7 +25,7 @@ namespace nqk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxPairs = 512;      // head_dim up to 1024
+constexpr int kTurns = 1024;        // pairs of all of a workgroup's rows
 
 // cos and sin of t, t in 64 bits.
 __device__ __forceinline__ float2 cos_sin(double t)
@@ -41,85 +43,135 @@ __device__ __forceinline__ float2 cos_sin(double t)
     return make_float2(turn == 1 || turn == 2 ? -a : a, turn >= 2 ? -b : b);
 }
 
-// A workgroup takes one row, of which each thread takes the same columns of
-// every few heads.  E: elements of an access (1: pairs of single elements).
-template <typename T, int E> __global__ __launch_bounds__(kThreads) void rope_kernel(RopeLaunch a, int64_t row0)
-{
-    __shared__ float2 turn[kMaxPairs];
-    const int64_t row = row0 + blockIdx.x;
-    const int half = a.rotary >> 1, tid = (int)threadIdx.x;
-    for (int i = tid; i < half; i += kThreads) {
-        const int ax = a.axis ? a.axis[i] : 0;
-        const double p = (unsigned)ax < (unsigned)a.axes ? (double)a.positions[(int64_t)ax * a.ldp + row] : 0.0;
-        const float2 t = cos_sin(p * a.freq[i]);
-        turn[i] = make_float2(t.x * a.cos_scale, t.y * a.sin_scale);
+// A piece of a head: E columns of both halves, E neighbouring columns that
+// are whole pairs, or E columns that are only copied.
+template <typename T, int E> struct Piece {
+    Raw<T, E> a, b;     // b: of the second half, or a pair's second element
+};
+
+// Where a thread is among the pieces of a workgroup's rows: `lanes` threads
+// take the pieces of one head, and heads follow each other over the rows.
+struct Walk {
+    int row, head, j;
+    __device__ __forceinline__ void carry(int heads)
+    {
+        while (head >= heads) head -= heads, ++row;
     }
-    __syncthreads();
-    const T *x = static_cast<const T *>(a.x) + row * a.ldx;
-    T *out = static_cast<T *>(a.out) + row * a.ldo;
+};
+
+// A workgroup takes `rows_each` rows.  Its first loads are on their way while
+// the angles are computed, kAhead of them to a thread.
+template <typename T, int E, bool PAIRS, bool AL>
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeLaunch a, int64_t row0, int rows_each)
+{
+    constexpr int kAhead = 4, P = E == 1 ? 1 : PAIRS ? E / 2 : E;   // pairs of a piece
+    __shared__ float2 turn[kTurns];
+    const int half = a.rotary >> 1, tid = (int)threadIdx.x;
+    const int64_t first = row0 + (int64_t)blockIdx.x * rows_each;
+    const int rows = a.rows - first < rows_each ? (int)(a.rows - first) : rows_each;
+    const T *x = static_cast<const T *>(a.x) + first * a.ldx;
+    T *out = static_cast<T *>(a.out) + first * a.ldo;
     // pieces of a head: those that turn, then those that are copied
-    constexpr int P = E == 1 ? 1 : E / 2;       // pairs of a piece of neighbouring pairs
-    const int turning = a.pairs ? half / P : half / E;
-    const int behind = a.x == a.out ? 0 : (a.head_dim - a.rotary) / E;
-    const int per = turning + behind;
-    const int count = a.heads * per;
-    for (int item = tid + (int)blockIdx.y * kThreads; item < count; item += kThreads * (int)gridDim.y) {
-        const int head = (int)((unsigned)item / (unsigned)per), j = item - head * per;
-        const int64_t at = (int64_t)head * a.head_dim;
-        if (j >= turning) {
-            const int64_t c = at + a.rotary + (j - turning) * E;
-            store_raw<T, E>(out + c, load_raw<T, E>(x + c));
-        } else if (!a.pairs) {
-            float u[E], v[E], p[E], q[E];
-            load_run<T, E>(x + at + j * E, u);
-            load_run<T, E>(x + at + half + j * E, v);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float2 t = turn[j * E + e];
-                p[e] = fmaf(u[e], t.x, -(v[e] * t.y));
-                q[e] = fmaf(v[e], t.x, u[e] * t.y);
-            }
-            store_run<T, E>(out + at + j * E, p);
-            store_run<T, E>(out + at + half + j * E, q);
-        } else {
-            constexpr int W = 2 * P;
-            float u[W], p[W];
-            if constexpr (E == 1) u[0] = Elt<T>::load(x, at + 2 * j), u[1] = Elt<T>::load(x, at + 2 * j + 1);
-            else load_run<T, W>(x + at + j * W, u);
+    const int turning = half / P, per = turning + (a.x == a.out ? 0 : (a.head_dim - a.rotary) / E);
+    const int lanes = per < kThreads ? per : kThreads, side = kThreads / lanes, mine = tid / lanes;
+    Walk w{0, mine, tid - mine * lanes};
+    w.carry(a.heads);
+    if (mine >= side) w.row = rows;     // no place for another head
+    const int start = w.j;
+    auto advance = [&](Walk &v) {
+        v.j += lanes;
+        if (v.j >= per) v.j = start, v.head += side, v.carry(a.heads);
+    };
+    auto load = [&](const Walk &v, Piece<T, E> &p) {
+        if (v.row >= rows) return;
+        const T *at = x + v.row * a.ldx + (int64_t)v.head * a.head_dim;
+        if (v.j >= turning) p.a = load_raw<T, E, AL>(at + a.rotary + (v.j - turning) * E);
+        else if (PAIRS && E > 1) p.a = load_raw<T, E, AL>(at + v.j * E);
+        else if (PAIRS) p.a = load_raw<T, E, AL>(at + 2 * v.j), p.b = load_raw<T, E, AL>(at + 2 * v.j + 1);
+        else p.a = load_raw<T, E, AL>(at + v.j * E), p.b = load_raw<T, E, AL>(at + half + v.j * E);
+    };
+    auto finish = [&](const Walk &v, const Piece<T, E> &p) {
+        if (v.row >= rows) return;
+        T *at = out + v.row * a.ldo + (int64_t)v.head * a.head_dim;
+        const float2 *t = turn + v.row * half + v.j * P;
+        if (v.j >= turning) store_raw<T, E, AL>(at + a.rotary + (v.j - turning) * E, p.a);
+        else if constexpr (PAIRS && E > 1) {
+            float u[E], r[E];
+            unpack<T, E>(p.a, u);
 #pragma unroll
             for (int e = 0; e < P; ++e) {
-                const float2 t = turn[j * P + e];
-                p[2 * e] = fmaf(u[2 * e], t.x, -(u[2 * e + 1] * t.y));
-                p[2 * e + 1] = fmaf(u[2 * e + 1], t.x, u[2 * e] * t.y);
+                r[2 * e] = fmaf(u[2 * e], t[e].x, -(u[2 * e + 1] * t[e].y));
+                r[2 * e + 1] = fmaf(u[2 * e + 1], t[e].x, u[2 * e] * t[e].y);
             }
-            if constexpr (E == 1) Elt<T>::store(out, at + 2 * j, p[0]), Elt<T>::store(out, at + 2 * j + 1, p[1]);
-            else store_run<T, W>(out + at + j * W, p);
+            store_run<T, E, AL>(at + v.j * E, r);
+        } else {
+            float u[E], z[E], r[E], q[E];
+            unpack<T, E>(p.a, u), unpack<T, E>(p.b, z);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                r[e] = fmaf(u[e], t[e].x, -(z[e] * t[e].y));
+                q[e] = fmaf(z[e], t[e].x, u[e] * t[e].y);
+            }
+            store_run<T, E, AL>(at + (PAIRS ? 2 * v.j : v.j * E), r);
+            store_run<T, E, AL>(at + (PAIRS ? 2 * v.j + 1 : half + v.j * E), q);
         }
+    };
+    Walk ahead[kAhead];
+    Piece<T, E> p[kAhead];
+    auto fetch = [&]() {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) ahead[i] = w, load(w, p[i]), advance(w);
+    };
+    fetch();
+    for (int i = tid; i < rows * half; i += kThreads) {
+        const int r = i / half, k = i - r * half, ax = a.axis ? a.axis[k] : 0;
+        const double pos = (unsigned)ax < (unsigned)a.axes ? (double)a.positions[(int64_t)ax * a.ldp + first + r] : 0.0;
+        const float2 t = cos_sin(pos * a.freq[k]);
+        turn[i] = make_float2(t.x * a.cos_scale, t.y * a.sin_scale);
+    }
+    lds_barrier();
+    while (ahead[0].row < rows) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) finish(ahead[i], p[i]);
+        fetch();
     }
 }
 
-template <typename T> hipError_t rope_go(const RopeLaunch &a, hipStream_t stream)
+template <typename T, int E> hipError_t rope_go(const RopeLaunch &a, bool aligned, hipStream_t stream)
 {
-    constexpr int E = 16 / (int)sizeof(T);
-    const int half = a.rotary / 2;
-    const bool wide = (((uintptr_t)a.x | (uintptr_t)a.out) & 15) == 0 && a.ldx % E == 0 && a.ldo % E == 0 &&
-                      a.head_dim % E == 0 && a.rotary % E == 0 && (a.pairs || half % E == 0);
-    const int64_t most = most_workgroups(kThreads);
+    const int half = a.rotary / 2, per = a.pairs && E > 1 ? a.head_dim / E : half / E + (a.head_dim - a.rotary) / E;
+    // rows of a workgroup: about four pieces to a thread, but no fewer than 512 workgroups
+    int64_t each = std::max<int64_t>(1, std::min<int64_t>(4 * kThreads / ((int64_t)a.heads * per), kTurns / half));
+    each = std::max<int64_t>(1, std::min<int64_t>(each, a.rows / 512));
+    const int64_t most = most_workgroups(kThreads) * each;
     for (int64_t row0 = 0; row0 < a.rows; row0 += most) {
-        const unsigned rows = (unsigned)std::min<int64_t>(most, a.rows - row0);
-        if (wide) rope_kernel<T, E><<<rows, kThreads, 0, stream>>>(a, row0);
-        else rope_kernel<T, 1><<<rows, kThreads, 0, stream>>>(a, row0);
+        const unsigned groups = (unsigned)((std::min<int64_t>(most, a.rows - row0) + each - 1) / each);
+        auto go = [&](auto kernel) { kernel<<<groups, kThreads, 0, stream>>>(a, row0, (int)each); };
+        if (a.pairs) aligned ? go(rope_kernel<T, E, true, true>) : go(rope_kernel<T, E, true, false>);
+        else aligned ? go(rope_kernel<T, E, false, true>) : go(rope_kernel<T, E, false, false>);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
+// The widest pieces that a head and its halves are made of.
+template <typename T> hipError_t rope_width(const RopeLaunch &a, hipStream_t stream)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    const int fit = a.head_dim | a.rotary | (a.pairs ? 0 : a.rotary / 2);
+    const bool aligned = ((uintptr_t)a.x | (uintptr_t)a.out) % 16 == 0 && a.ldx % E == 0 && a.ldo % E == 0;
+    if (fit % E == 0) return rope_go<T, E>(a, aligned, stream);
+    if (E > 4 && fit % 4 == 0) return rope_go<T, 4>(a, aligned, stream);
+    if (fit % 2 == 0) return rope_go<T, 2>(a, aligned, stream);
+    return rope_go<T, 1>(a, aligned, stream);
+}
+
 }  // namespace
 
 hipError_t launch_rope(const RopeLaunch &a, hipStream_t stream)
 {
-    return a.x_dt == 0 ? rope_go<float>(a, stream) : rope_go<bf16_bits>(a, stream);
+    return a.x_dt == 0 ? rope_width<float>(a, stream) : rope_width<bf16_bits>(a, stream);
 }
 
 }  // namespace nqk
