@@ -965,34 +965,56 @@ class _RopeStruct(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+# As for the cache, these calls are made for every layer and step: checks are kept
+# to what the tensors cannot show by themselves, outputs made here are not
+# checked, and each is one call of the allocator.
+_TYPES = {}
+
+
+def _type(t):
+    """nq_dtype of a tensor."""
+    if not _TYPES:
+        torch = _torch()
+        _TYPES.update({torch.float32: NQ_F32, torch.bfloat16: NQ_BF16})
+    dt = _TYPES.get(t.dtype)
+    return _dt(t) if dt is None else dt     # _dt refuses
+
+
 def _one_device(stream, *tensors):
     """All tensors (None left out) are on the GPU of the call's stream."""
-    torch = _torch()
-    at = torch.cuda.current_device() if stream is None else stream.device.index
+    at = _torch().cuda.current_device() if stream is None else stream.device.index
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != at):
+        if t is not None and t.get_device() != at:
             raise ValueError(f"a tensor on {t.device} in a call on cuda:{at}; make that device the current one "
                              "or pass a stream of it")
 
 
 def _given(name, t, shape, dtype):
-    """A caller's dense output tensor."""
+    """A caller's dense tensor."""
     _contig(name, t)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     return t
 
 
+def _fresh(stream, like, shape, dtype=None):
+    """A new dense tensor on the device of `like`, in its dtype unless given."""
+    if stream is None:
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+    return _empty(stream, shape, dtype or like.dtype, like.device)
+
+
 def _matrix(name, t, rows=None, dim=None, dtype=None):
     """The row stride of a [rows, dim] tensor whose rows are dense."""
-    if t.dim() != 2 or (rows is not None and tuple(t.shape) != (rows, dim)):
-        raise ValueError(f"{name} must be " + ("a matrix" if rows is None else f"{(rows, dim)}") +
-                         f", got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and (shape[0] != rows or shape[1] != dim)):
+        raise ValueError(f"{name} must be " + ("a matrix" if rows is None else f"{(rows, dim)}") + f", got {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return ld if shape[0] > 1 else shape[1]
 
 
 class MoEOrder(_Described):
@@ -1005,27 +1027,28 @@ class MoEOrder(_Described):
         torch = _torch()
         if place.dim() != 2:
             raise ValueError("place must be [tokens, top_k]")
-        tokens, top_k = place.shape
-        for name, t, n in (("starts", starts, starts.numel()), ("place", place, tokens * top_k),
-                           ("row_token", row_token, tokens * top_k), ("row_expert", row_expert, tokens * top_k)):
+        pairs = place.numel()
+        for name, t, n in (("starts", starts, starts.numel()), ("place", place, pairs), ("row_token", row_token, pairs),
+                           ("row_expert", row_expert, pairs)):
             _contig(name, t)
             if t.dtype != torch.int32 or t.numel() != n:
                 raise ValueError(f"{name} must hold {n} int32 numbers")
-        self.starts, self.place, self.row_token, self.row_expert = starts, place, row_token, row_expert
-        self.tokens, self.top_k, self.experts = tokens, top_k, starts.numel() - 1
-        self._struct = _MoEOrderStruct(starts.data_ptr(), place.data_ptr(), tokens, top_k, self.experts)
-        self._ref = ctypes.byref(self._struct)
+        self._bind(starts, place, row_token, row_expert, *place.shape, starts.numel() - 1)
+
+    def _bind(self, starts, place, row_token, row_expert, tokens, top_k, experts):
+        struct = _MoEOrderStruct(starts.data_ptr(), place.data_ptr(), tokens, top_k, experts)
+        self.__dict__.update(starts=starts, place=place, row_token=row_token, row_expert=row_expert, tokens=tokens,
+                             top_k=top_k, experts=experts, _struct=struct, _ref=ctypes.byref(struct))
 
     @classmethod
     def empty(cls, tokens, top_k, experts, device="cuda", stream=None):
-        torch = _torch()
+        """An order of these sizes, its contents undefined until nq_moe_sort."""
         pairs = tokens * top_k
-        # one allocation; the arrays start at multiples of 16 bytes
-        up = lambda n: -(-n // 4) * 4
-        a, b, c = up(experts + 1), up(pairs), up(pairs)
-        buf = _empty(stream, (a + b + c + pairs,), torch.int32, device)
-        return cls(buf[:experts + 1], buf[a:a + pairs].view(tokens, top_k), buf[a + b:a + b + pairs],
-                   buf[a + b + c:])
+        buf = _empty(stream, (3 * pairs + experts + 1,), _torch().int32, device)
+        place, row_token, row_expert, starts = buf.split_with_sizes((pairs, pairs, pairs, experts + 1))
+        self = cls.__new__(cls)
+        self._bind(starts, place.view(tokens, top_k), row_token, row_expert, tokens, top_k, experts)
+        return self
 
 
 def nq_moe_sort_workspace_bytes(tokens, top_k, experts):
@@ -1044,17 +1067,19 @@ def nq_moe_sort(ids, experts, order=None, workspace=None, stream=None):
         raise ValueError("ids must be int32 [tokens, top_k]")
     tokens, top_k = ids.shape
     if order is None:
+        if not 1 <= experts <= 1024:
+            raise ValueError(f"experts must be 1 .. 1024, got {experts}")
         order = MoEOrder.empty(tokens, top_k, experts, ids.device, stream)
     elif (order.tokens, order.top_k, order.experts) != (tokens, top_k, experts):
         raise ValueError("order was made for other sizes")
     if workspace is None:
         ws_bytes = lib.nq_moe_sort_workspace_bytes(tokens, top_k, experts)
         if ws_bytes:
-            workspace = _empty(stream, ws_bytes, torch.uint8, ids.device)
+            workspace = _fresh(stream, ids, (ws_bytes,), torch.uint8)
     else:
         _contig("workspace", workspace)
         ws_bytes = workspace.numel() * workspace.element_size()
-    _one_device(stream, ids, order.starts, workspace)
+    _one_device(stream, ids, order.place, workspace)
     status = lib.nq_moe_sort(ids.data_ptr(), tokens, top_k, experts, order.starts.data_ptr(), order.place.data_ptr(),
                              order.row_token.data_ptr(), order.row_expert.data_ptr(),
                              None if workspace is None else workspace.data_ptr(), ws_bytes, _raw_stream(stream))
@@ -1069,13 +1094,13 @@ def nq_moe_dispatch(order, x, xs=None, stream=None):
     pairs are zeros."""
     lib = _lib or load_library()
     ldx = _matrix("x", x)
-    hidden = x.shape[1]
-    if x.shape[0] != order.tokens:
+    tokens, hidden = x.shape
+    if tokens != order.tokens:
         raise ValueError(f"x must have {order.tokens} rows")
-    shape = (order.tokens * order.top_k, hidden)
-    xs = _empty(stream, shape, x.dtype, x.device) if xs is None else _given("xs", xs, shape, x.dtype)
+    shape = (tokens * order.top_k, hidden)
+    xs = _fresh(stream, x, shape) if xs is None else _given("xs", xs, shape, x.dtype)
     _one_device(stream, order.place, x, xs)
-    status = lib.nq_moe_dispatch(order._ref, x.data_ptr(), _dt(x), ldx, hidden, xs.data_ptr(), _raw_stream(stream))
+    status = lib.nq_moe_dispatch(order._ref, x.data_ptr(), _type(x), ldx, hidden, xs.data_ptr(), _raw_stream(stream))
     if status:
         _check(status)
     return xs
@@ -1094,9 +1119,9 @@ def nq_moe_dispatch_grad(order, dxs, dx=None, stream=None):
     lib = _lib or load_library()
     hidden = _expert_rows("dxs", order, dxs)
     shape = (order.tokens, hidden)
-    dx = _empty(stream, shape, dxs.dtype, dxs.device) if dx is None else _given("dx", dx, shape, dxs.dtype)
+    dx = _fresh(stream, dxs, shape) if dx is None else _given("dx", dx, shape, dxs.dtype)
     _one_device(stream, order.place, dxs, dx)
-    status = lib.nq_moe_dispatch_grad(order._ref, dxs.data_ptr(), _dt(dxs), hidden, dx.data_ptr(), _raw_stream(stream))
+    status = lib.nq_moe_dispatch_grad(order._ref, dxs.data_ptr(), _type(dxs), hidden, dx.data_ptr(), _raw_stream(stream))
     if status:
         _check(status)
     return dx
@@ -1116,9 +1141,9 @@ def nq_moe_combine(order, ys, weights=None, residual=None, y=None, stream=None):
     hidden = _expert_rows("ys", order, ys)
     shape = (order.tokens, hidden)
     ldr = 0 if residual is None else _matrix("residual", residual, *shape, ys.dtype)
-    y = _empty(stream, shape, ys.dtype, ys.device) if y is None else _given("y", y, shape, ys.dtype)
+    y = _fresh(stream, ys, shape) if y is None else _given("y", y, shape, ys.dtype)
     _one_device(stream, order.place, ys, weights, residual, y)
-    status = lib.nq_moe_combine(order._ref, ys.data_ptr(), _dt(ys), hidden, _pair_weights(order, weights),
+    status = lib.nq_moe_combine(order._ref, ys.data_ptr(), _type(ys), hidden, _pair_weights(order, weights),
                                 None if residual is None else residual.data_ptr(), ldr, y.data_ptr(),
                                 _raw_stream(stream))
     if status:
@@ -1133,21 +1158,21 @@ def nq_moe_combine_grad(order, dy, ys=None, weights=None, dys=None, dweights=Non
     torch = _torch()
     lib = _lib or load_library()
     ldd = _matrix("dy", dy)
-    hidden, pairs = dy.shape[1], order.tokens * order.top_k
-    if dy.shape[0] != order.tokens:
+    tokens, hidden = dy.shape
+    if tokens != order.tokens:
         raise ValueError(f"dy must have {order.tokens} rows")
     if ys is not None and (_expert_rows("ys", order, ys) != hidden or ys.dtype != dy.dtype):
         raise ValueError("ys must have dy's columns and dtype")
     if ys is None and dweights is not None:
         raise ValueError("dweights needs ys")
-    dys = _empty(stream, (pairs, hidden), dy.dtype, dy.device) if dys is None else \
-        _given("dys", dys, (pairs, hidden), dy.dtype)
+    shape = (tokens * order.top_k, hidden)
+    dys = _fresh(stream, dy, shape) if dys is None else _given("dys", dys, shape, dy.dtype)
     if ys is not None:
-        shape = (order.tokens, order.top_k)
-        dweights = _empty(stream, shape, torch.float32, dy.device) if dweights is None else \
+        shape = (tokens, order.top_k)
+        dweights = _fresh(stream, dy, shape, torch.float32) if dweights is None else \
             _given("dweights", dweights, shape, torch.float32)
     _one_device(stream, order.place, dy, ys, weights, dys, dweights)
-    status = lib.nq_moe_combine_grad(order._ref, dy.data_ptr(), _dt(dy), ldd, hidden,
+    status = lib.nq_moe_combine_grad(order._ref, dy.data_ptr(), _type(dy), ldd, hidden,
                                      None if ys is None else ys.data_ptr(), _pair_weights(order, weights),
                                      dys.data_ptr(), None if dweights is None else dweights.data_ptr(),
                                      _raw_stream(stream))
@@ -1157,28 +1182,28 @@ def nq_moe_combine_grad(order, dy, ys=None, weights=None, dys=None, dweights=Non
 
 
 # ---------------------------------------------------------------- norms, gate and residual
-def _norm_call(stream, like, rows, dim, post, gate, pre, scale, offset, eps):
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_call(like, rows, dim, post, gate, pre, scale, offset, eps):
     """The shape struct, the parameters' dtype, and gate's row stride."""
-    p = next((t for t in (post, gate, pre) if t is not None), like)
-    for name, t in (("post", post), ("pre", pre)):
-        if t is not None:
-            _given(name, t, (dim,), p.dtype)
+    p = post if post is not None else gate if gate is not None else pre if pre is not None else like
+    dtype = p.dtype
+    if post is not None:
+        _given("post", post, (dim,), dtype)
+    if pre is not None:
+        _given("pre", pre, (dim,), dtype)
     gates, ldg = 1, 0
     if gate is not None:
-        if gate.dtype != p.dtype:
-            raise TypeError("post, gate and pre must have the same dtype")
         if gate.dim() == 1:
-            _given("gate", gate, (dim,), p.dtype)
+            _given("gate", gate, (dim,), dtype)
             ldg = dim
         else:
             if gate.dim() != 2 or gate.shape[1] != dim:
                 raise ValueError(f"gate must be [{dim}] or [gates, {dim}], got {tuple(gate.shape)}")
-            ldg, gates = _matrix("gate", gate), max(1, gate.shape[0])
-    return _BlockNormStruct(rows, dim, gates, eps, offset, scale), _dt(p), ldg
-
-
-def _address(t):
-    return None if t is None else t.data_ptr()
+            ldg, gates = _matrix("gate", gate, dtype=dtype), max(1, gate.shape[0])
+    return _BlockNormStruct(rows, dim, gates, eps, offset, scale), _type(p), ldg
 
 
 def nq_block_norm_grad_workspace_bytes(rows, dim, gates=1):
@@ -1198,19 +1223,19 @@ def nq_block_norm(h, y=None, post=None, gate=None, pre=None, scale=1.0, offset=0
     lib = _lib or load_library()
     ldh = _matrix("h", h)
     rows, dim = h.shape
-    ldy = 0 if y is None else _matrix("y", y, rows, dim, h.dtype)
-    shape, p_dt, ldg = _norm_call(stream, h, rows, dim, post, gate, pre, scale, offset, eps)
+    shape, p_dt, ldg = _norm_call(h, rows, dim, post, gate, pre, scale, offset, eps)
+    ldy = 0
     if y is not None:
-        h_out = _empty(stream, (rows, dim), h.dtype, h.device) if h_out is None else \
-            _given("h_out", h_out, (rows, dim), h.dtype)
+        ldy = _matrix("y", y, rows, dim, h.dtype)
+        h_out = _fresh(stream, h, (rows, dim)) if h_out is None else _given("h_out", h_out, (rows, dim), h.dtype)
     elif h_out is not None:
         raise ValueError("h_out needs y")
     if pre is not None:
-        z = _empty(stream, (rows, dim), h.dtype, h.device) if z is None else _given("z", z, (rows, dim), h.dtype)
+        z = _fresh(stream, h, (rows, dim)) if z is None else _given("z", z, (rows, dim), h.dtype)
     elif z is not None:
         raise ValueError("z needs pre")
     _one_device(stream, h, y, post, gate, pre, h_out, z)
-    status = lib.nq_block_norm(ctypes.byref(shape), h.data_ptr(), ldh, _address(y), ldy, _dt(h), _address(post),
+    status = lib.nq_block_norm(ctypes.byref(shape), h.data_ptr(), ldh, _address(y), ldy, _type(h), _address(post),
                                _address(gate), ldg, _address(pre), p_dt, _address(h_out), _address(z),
                                _raw_stream(stream))
     if status:
@@ -1229,28 +1254,34 @@ def nq_block_norm_grad(h_out, y=None, dh_out=None, dz=None, post=None, gate=None
     lib = _lib or load_library()
     ldh = _matrix("h_out", h_out)
     rows, dim = h_out.shape
-    dt, dev = h_out.dtype, h_out.device
-    lds = [0 if t is None else _matrix(name, t, rows, dim, dt) for name, t in
-           (("y", y), ("dh_out", dh_out), ("dz", dz))]
-    shape, p_dt, ldg = _norm_call(stream, h_out, rows, dim, post, gate, pre, scale, offset, eps)
-    dh = _empty(stream, (rows, dim), dt, dev) if dh is None else _given("dh", dh, (rows, dim), dt)
+    dt = h_out.dtype
+    shape, p_dt, ldg = _norm_call(h_out, rows, dim, post, gate, pre, scale, offset, eps)
+    ldy = 0 if y is None else _matrix("y", y, rows, dim, dt)
+    ldd = 0 if dh_out is None else _matrix("dh_out", dh_out, rows, dim, dt)
+    ldz = 0 if dz is None else _matrix("dz", dz, rows, dim, dt)
+    dh = _fresh(stream, h_out, (rows, dim)) if dh is None else _given("dh", dh, (rows, dim), dt)
     if y is not None:
-        dy = _empty(stream, (rows, dim), dt, dev) if dy is None else _given("dy", dy, (rows, dim), dt)
+        dy = _fresh(stream, h_out, (rows, dim)) if dy is None else _given("dy", dy, (rows, dim), dt)
     elif dy is not None:
         raise ValueError("dy needs y")
-    like = lambda t, wanted: _empty(stream, t.shape, t.dtype, dev) if parameters and wanted else None
-    dpost, dgate = like(post, post is not None), like(gate, gate is not None)
-    dpre = like(pre, pre is not None and dz is not None)
+    dpost = dgate = dpre = None
+    if parameters:
+        if post is not None:
+            dpost = _fresh(stream, post, (dim,))
+        if gate is not None:
+            dgate = _fresh(stream, gate, gate.shape)
+        if pre is not None and dz is not None:
+            dpre = _fresh(stream, pre, (dim,))
     if workspace is None:
         ws_bytes = lib.nq_block_norm_grad_workspace_bytes(ctypes.byref(shape))
         if ws_bytes:
-            workspace = _empty(stream, ws_bytes, torch.uint8, dev)
+            workspace = _fresh(stream, h_out, (ws_bytes,), torch.uint8)
     else:
         _contig("workspace", workspace)
         ws_bytes = workspace.numel() * workspace.element_size()
     _one_device(stream, h_out, y, dh_out, dz, post, gate, pre, dh, dy, workspace)
-    status = lib.nq_block_norm_grad(ctypes.byref(shape), h_out.data_ptr(), ldh, _address(y), lds[0], _address(dh_out),
-                                    lds[1], _address(dz), lds[2], _dt(h_out), _address(post), _address(gate), ldg,
+    status = lib.nq_block_norm_grad(ctypes.byref(shape), h_out.data_ptr(), ldh, _address(y), ldy, _address(dh_out),
+                                    ldd, _address(dz), ldz, _type(h_out), _address(post), _address(gate), ldg,
                                     _address(pre), p_dt, dh.data_ptr(), _address(dy), _address(dpost), _address(dgate),
                                     _address(dpre), _address(workspace), ws_bytes, _raw_stream(stream))
     if status:
@@ -1317,14 +1348,14 @@ def _turn(name, rope, x, positions, out, stream, names):
         raise ValueError("the positions of an axis must be contiguous")
     ldp = positions.stride(0) if rope.axes > 1 else rows
     if out is None:
-        out = _empty(stream, (rows, heads, dim), x.dtype, x.device)
+        out = _fresh(stream, x, (rows, heads, dim))
         ldo = heads * dim
     else:
         if out.dtype != x.dtype:
             raise TypeError(f"{names[1]} must have {names[0]}'s dtype")
         ldo = _row_stride(names[1], out, rows, heads, dim)
     _one_device(stream, rope.freq, x, positions, out)
-    status = getattr(lib, name)(rope._ref, x.data_ptr(), _dt(x), rows, ldx, heads, dim, positions.data_ptr(), ldp,
+    status = getattr(lib, name)(rope._ref, x.data_ptr(), _type(x), rows, ldx, heads, dim, positions.data_ptr(), ldp,
                                 out.data_ptr(), ldo, _raw_stream(stream))
     if status:
         _check(status)
