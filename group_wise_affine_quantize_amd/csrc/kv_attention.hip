@@ -12,16 +12,13 @@
 // L are scaled) when a later maximum passes R + 14 by more than kSlack; the
 // largest p_t lies in [2^14, 2^15.5).  Drawing sv into x makes p_t the whole
 // weight of a code row, so that the second product runs on bare codes, and
-// p_t fits fp16: 11 bits for weights within 2^-28 of the largest, an error of
-// 2^-39 of it below (the tile kernel, whose weights start at 2^12: 2^-26 and
-// 2^-37).  (bf16 would keep 8 bits, which shows in a bf16 result.)  Codes are exact in fp16.  A query row is taken times a power of
+// p_t fits fp16: 11 bits for weights within 2^-28 of the largest, a floor
+// about 2^-39 below it.  (bf16 would keep 8 bits, which shows in a bf16
+// result.)  Codes are exact in fp16.  A query row is taken times a power of
 // two that brings its largest element to [2^14, 2^15); a bf16 element then is
 // exact in fp16 down to 2^-28 of the largest.  fp32 rows and weights are the
-// sum of two fp16 numbers and take two matrix products each: 22 bits while the
-// second, at most 2^-11 of the number, is one of fp16's normal numbers (from
-// 2^-14 up), that is for numbers from 2^-3 up -- 2^-17 of the largest, 2^-15 in
-// the tile kernel's weights -- and an error of 2^-25 below.  Sums, references
-// and the states O and L are fp32.
+// sum of two fp16 numbers (22 bits) and take two matrix products each.  Sums,
+// references and the states O and L are fp32.
 //
 // p_t / sv_t is 2^(z_t - R) (z in base 2 here), whose range is not p_t's: a sum
 // over tiny scales can pass fp32, and the p_t of a small scale beside a very
@@ -41,11 +38,11 @@
 // per lane).  No value moves between lanes but the running maximum.
 //
 // What bounds it: reading the codes.  64 sequences of 1k to 8k tokens, 8 heads of
-// 128 in int8: 620 MB in 118 us, 5.2 TB/s (a 1 GiB copy moves 5.1), with two
+// 128 in int8: 620 MB in 121 us, 5.1 TB/s (a 1 GiB copy moves 5.1), with two
 // workgroups of four waves per compute unit, each wave with a tile of 16 KB on
 // the way.  With more than 16 query columns two or four waves read the same tile, and
 // less is on the way: 8 draft tokens over 131k tokens, 264 MB in 82 us.  One token at
-// 333 is latency: 9.5 us.
+// 333 is latency: 9.3 us.
 #include <algorithm>
 
 #include "nq_kv_attn.h"
@@ -58,48 +55,6 @@ constexpr int kWorkers = 512;    // two workgroups of four waves per compute uni
 constexpr int kJoinThreads = 512, kJoinCols = 4;
 constexpr float kSlack = 1.5f;   // weights stay below 2^15.5, within fp16
 constexpr int kWaves = 4;
-
-// Units per worker.  At least two tiles for each wave, so that short contexts
-// do not fall into parts that cost more to join than to read.
-__device__ __forceinline__ uint32_t share_of(const AttnArgs &A, uint32_t total)
-{
-    return list_share(total, (uint32_t)A.workers, A.unit_shift ? 1u : 2u * kWaves);
-}
-
-// Finds the sequence of unit `at(share)` of the list: its number (-1: past the
-// list's end), the unit's number inside it, the list's length and the share.
-template <typename At>
-__device__ __forceinline__ int stream_locate(const AttnArgs &A, int cols, At at, uint32_t *inside, uint32_t *total,
-                                             uint32_t *share)
-{
-    const int batch = A.a.s.batch, lane = (int)(threadIdx.x & 63u);
-    uint32_t work = lane < batch ? stream_seq(A, lane, cols).work : 0u;     // below 2^31
-    uint32_t upto = wave_scan32_sat(work);
-    uint32_t sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
-    *total = sum;
-    for (int b = 64 + lane; b - lane < batch; b += 64)
-        *total = add_sat(*total, (uint32_t)__builtin_amdgcn_readlane(
-            (int)wave_scan32_sat(b < batch ? stream_seq(A, b, cols).work : 0u), 63));
-    *total = list_total(*total);
-    *share = share_of(A, *total);
-    const uint32_t want = at(*share);
-    if (want >= *total) return -1;
-    uint32_t base = 0;      // at most `want`
-    for (int b0 = 0; b0 < batch; b0 += 64) {
-        if (b0) {
-            work = b0 + lane < batch ? stream_seq(A, b0 + lane, cols).work : 0u;
-            upto = wave_scan32_sat(work);
-            sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
-        }
-        if (add_sat(base, sum) > want) {
-            const int l = __ffsll((unsigned long long)__ballot(add_sat(base, upto) > want)) - 1;
-            *inside = want - base - (uint32_t)__builtin_amdgcn_readlane((int)(upto - work), l);
-            return b0 + l;
-        }
-        base += sum;
-    }
-    return -1;
-}
 
 // 16 bytes of codes.  ONCE: no other wave will want them, and they pass the
 // caches by (64 sequences of 1k to 8k tokens 123 -> 121 us; with two column
@@ -125,7 +80,7 @@ template <int D, int NP> struct State {
 // CG groups of 16 columns; the waves of a group share its tiles.  A group's
 // waves load the tiles of the other groups' waves too, out of the L1: two
 // blocks of columns in one wave's registers would leave one wave per SIMD.
-// SHARED: a pass of attention behind shared prefixes (see AttnArgs).
+// SHARED: a pass of attention behind shared prefixes.
 template <int D, int CG, int FMT, typename T, bool SHARED>
 __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kernel(AttnArgs A)
 {
@@ -396,20 +351,13 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
             const int64_t slot = 2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0);
             float l = sh_l[0][col];
             for (int w = 1; w < TL; ++w) l += sh_l[w][col];
-            if (SHARED && whole && A.state_s) {
+            if (SHARED && whole) {
                 const int64_t at = (int64_t)c.row * a.q_heads + c.head;
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt)
                     *reinterpret_cast<float4_t *>(A.state_o + at * D + 16 * dt + 4 * g) = st.o[dt];
                 if (g == 0) A.state_s[at] = make_float4(st.m, l, st.u, 0.0f);
             } else if (whole) {
-                if constexpr (SHARED) {
-                    const Before before = take_before(A, c.row, c.head, l, st.m, st.u);
-                    if (before.o)
-#pragma unroll
-                        for (int dt = 0; dt < DT; ++dt)
-                            add_before(before, 16 * dt + 4 * g, reinterpret_cast<float *>(&st.o[dt]));
-                }
                 const float f = out_factor(l, st.m, st.u, 4 * DT, reinterpret_cast<float *>(st.o));
                 T *out = static_cast<T *>(a.out) + ((int64_t)c.row * a.q_heads + c.head) * D;
 #pragma unroll
@@ -443,7 +391,7 @@ constexpr int join_blocks(int groups) { return groups == 4 ? 4 : 16 * groups / k
 // j + 1; the one at the first border inside a segment joins it.  Two runs of
 // threads or more take turns at the parts (7 us for 64 sequences of 8 heads, 13
 // us where 8 segments of 32 columns have 64 parts each).
-template <int D, int CG, typename T, bool SHARED>
+template <int D, int CG, typename T>
 __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 {
     constexpr int COLS = 16 * CG, QUADS = D / 4, LANES = kJoinCols * QUADS, RUNS = kJoinThreads / LANES;
@@ -515,24 +463,175 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
                 const float4 w = sh_o[k][i];
                 v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
             }
-            float4 t = sh_s[c];
-            const int64_t at = (int64_t)q.row * a.q_heads + q.head;
-            if (SHARED && A.state_s) {
-                store_f32x4<float>(A.state_o + at * D + d, v);
-                if (d == 0) A.state_s[at] = t;
-            } else {
-                if constexpr (SHARED) {
-                    const Before before = take_before(A, q.row, q.head, t.y, t.x, t.z);
-                    if (before.o) add_before(before, d, v);
-                }
-                const float l = t.y, f = out_factor(l, t.x, t.z, 4, v);
-                for (int e = 0; e < 4; ++e) v[e] *= f;
-                store_f32x4<T>(static_cast<T *>(a.out) + at * D + d, v);
-                if (a.lse && d == 0) a.lse[at] = log_sum(l, t.z);
-            }
+            const float4 t = sh_s[c];
+            const float l = t.y, f = out_factor(l, t.x, t.z, 4, v);
+            for (int e = 0; e < 4; ++e) v[e] *= f;
+            store_f32x4<T>(static_cast<T *>(a.out) + ((int64_t)q.row * a.q_heads + q.head) * D + d, v);
+            if (a.lse && d == 0)
+                a.lse[(int64_t)q.row * a.q_heads + q.head] = log_sum(l, t.z);
         }
         __syncthreads();
     }
+}
+
+// Where the parts of a query column lie: part k at
+//   k == 0 ? first : rest + 2 * k * cols
+// of a pass's slots, or, where there is one part, at `first` of its states.
+// parts 0: no sequence of the pass has the row.
+struct Column0 {
+    int parts, first, rest;
+};
+
+// For each lane's row and head (row -1: none); all lanes of the wave call it.
+// The list that the pass ran over is counted again, 64 sequences at a time.
+__device__ __forceinline__ Column0 find_parts(const Pass &p, const KvCache &cache, int group, int q_heads, int row, int head)
+{
+    const int lane = (int)(threadIdx.x & 63u), batch = p.s.batch;
+    bool found = false;
+    int col = 0;
+    uint32_t total = 0, base = 0, units = 0, ct = 0;
+    for (int b0 = 0; b0 < batch; b0 += 64) {
+        int r0 = 0, n = 0;
+        uint32_t u = 0, c = 0;
+        if (b0 + lane < batch) {
+            const KvSeq q = kv_seq(p.s, b0 + lane);
+            const int64_t cap = p.s.max_blocks << cache.block_shift, len = q.len < cap ? q.len : cap;
+            const int tiles = len > 0 ? (int)((len + 63) >> 6) : 1;
+            r0 = (int)q.r0, n = (int)q.n;
+            u = (uint32_t)(tiles + (1 << p.unit_shift) - 1) >> p.unit_shift;
+            c = n * group <= p.few ? (uint32_t)(n * group + p.cols - 1) / (uint32_t)p.cols : 0u;
+        }
+        const uint32_t work = c * u * (uint32_t)cache.kv_heads, upto = wave_scan32_sat(work);
+        // the wave's rows one after the other; most often there is one
+        uint64_t open = __ballot(row >= 0 && !found);
+        while (open) {
+            const int who = __builtin_amdgcn_readlane(row, __ffsll((unsigned long long)open) - 1);
+            const uint64_t has = __ballot(who >= r0 && who < r0 + n);
+            if (has) {
+                const int at = __ffsll((unsigned long long)has) - 1;
+                auto get = [&](int v) { return __builtin_amdgcn_readlane(v, at); };
+                if (row == who && !found) {
+                    found = true;
+                    base = add_sat(total, (uint32_t)get((int)(upto - work)));
+                    col = row - get(r0), units = (uint32_t)get((int)u), ct = (uint32_t)get((int)c);
+                }
+            }
+            open &= ~__ballot(row == who);
+        }
+        total = add_sat(total, (uint32_t)__builtin_amdgcn_readlane((int)upto, 63));
+    }
+    total = list_total(total);
+    Column0 f{0, 0, 0};
+    if (!found) return f;
+    f.parts = 1, f.first = row * q_heads + head;
+    if (ct == 0) return f;
+    const uint32_t share = list_share(total, (uint32_t)p.workers, p.least);
+    const int kv_head = head / group;
+    col = col * group + (head - kv_head * group);
+    const uint32_t tile = (uint32_t)col / (uint32_t)p.cols, c = (uint32_t)col - tile * (uint32_t)p.cols;
+    const uint64_t off = (uint64_t)base + (uint64_t)((uint32_t)kv_head * ct + tile) * units;
+    if (off + units > total) {      // past the list's end: not done
+        f.parts = 0;
+        return f;
+    }
+    const uint32_t w0 = (uint32_t)off / share, w1 = (uint32_t)(off + units - 1) / share;
+    f.parts = (int)(w1 - w0) + 1;
+    f.rest = (int)(w0 * 2 * (uint32_t)p.cols + c);
+    if (f.parts > 1) f.first = f.rest + p.cols;
+    return f;
+}
+
+struct SharedJoin {
+    KvAttnLaunch a;
+    Pass prefix, own;
+    int group;
+};
+
+// Joins the two passes' parts of each row and head: the prefix's, then the
+// sequence's own, each in the order of the tokens.  A workgroup takes 1024 / D
+// neighbouring heads and rows.  A wave to a column finds its parts and their
+// factors, 64 at a time; then four runs of threads take turns at them.
+constexpr int kSharedRuns = 4;
+template <int D, typename T> __global__ __launch_bounds__(256 * kSharedRuns) void kv_shared_join_kernel(SharedJoin J)
+{
+    constexpr int COLS = 1024 / D, QUADS = D / 4;
+    __shared__ const float *sh_p[COLS][64];
+    __shared__ float sh_f[COLS][64];
+    __shared__ float4 sh_s[COLS];       // m, l, u, and what O so far is scaled by
+    __shared__ int sh_n[COLS];
+    __shared__ float4 sh_o[kSharedRuns - 1][256];
+    const KvAttnLaunch &a = J.a;
+    const int64_t at0 = (int64_t)blockIdx.x * COLS, count = a.s.rows * a.q_heads;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = (int)threadIdx.x & 63;
+    const int tid = (int)threadIdx.x & 255, run = (int)threadIdx.x >> 8, c = tid / QUADS, d = (tid % QUADS) * 4;
+
+    Column0 p{0, 0, 0}, o{0, 0, 0};
+    if (wave < COLS && at0 + wave < count) {
+        const int row = (int)((at0 + wave) / a.q_heads), head = (int)(at0 + wave - (int64_t)row * a.q_heads);
+        p = find_parts(J.prefix, a.c, J.group, a.q_heads, row, head);
+        o = find_parts(J.own, a.c, J.group, a.q_heads, row, head);
+        if (o.parts == 0) p.parts = 0;      // a row that no sequence has is left alone
+    }
+    const int parts = p.parts + o.parts;
+    if (wave < COLS && lane == 0) sh_n[wave] = parts;
+    float m = kNegInf, u = kNegInf, l = 0.0f;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k0 = 0;; k0 += 64) {
+        if (wave < COLS) {
+            float4 t = make_float4(kNegInf, 0.0f, kNegInf, 0.0f);
+            const int k = k0 + lane;
+            if (k < parts) {
+                const bool first = k < p.parts;
+                const Pass &q = first ? J.prefix : J.own;
+                const Column0 f = first ? p : o;
+                const int i = first ? k : k - p.parts;
+                const int64_t slot = i == 0 ? f.first : f.rest + 2 * (int64_t)i * q.cols;
+                t = (f.parts == 1 ? q.state_s : q.part_s)[slot];
+                sh_p[wave][lane] = (f.parts == 1 ? q.state_o : q.part_o) + slot * D;
+            }
+            const float mm = fmaxf(m, wave_max(t.x, lane)), uu = fmaxf(u, wave_max(t.z, lane));
+            sh_f[wave][lane] = exp2_below(t.x, mm);
+            float sum = exp2_below(t.z, uu) * t.y;
+            sum += xor_lane<1>(sum, lane);
+            sum += xor_lane<2>(sum, lane);
+            sum += xor_lane<4>(sum, lane);
+            sum += xor_lane<8>(sum, lane);
+            sum = group_sum(sum, lane);
+            l = fmaf(l, exp2_below(u, uu), sum);
+            if (lane == 0) sh_s[wave] = make_float4(mm, l, uu, exp2_below(m, mm));
+            m = mm, u = uu;
+        }
+        __syncthreads();
+        int most = 0;
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) most = sh_n[i] > most ? sh_n[i] : most;
+        if (c < COLS) {
+            const float again = sh_s[c].w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] *= again;
+            const int n = sh_n[c] - k0 < 64 ? sh_n[c] - k0 : 64;
+#pragma unroll 8
+            for (int k = run; k < n; k += kSharedRuns) {
+                const float f = sh_f[c][k];
+                const float4 x = *reinterpret_cast<const float4 *>(sh_p[c][k] + d);
+                v[0] = fmaf(f, x.x, v[0]), v[1] = fmaf(f, x.y, v[1]), v[2] = fmaf(f, x.z, v[2]), v[3] = fmaf(f, x.w, v[3]);
+            }
+        }
+        if (k0 + 64 >= most) break;
+        __syncthreads();
+    }
+    if (run) sh_o[run - 1][tid] = make_float4(v[0], v[1], v[2], v[3]);
+    __syncthreads();
+    if (run || c >= COLS || sh_n[c] == 0) return;
+    for (int k = 0; k < kSharedRuns - 1; ++k) {
+        const float4 x = sh_o[k][tid];
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+    }
+    const float4 t = sh_s[c];
+    const float f = out_factor(t.y, t.x, t.z, 4, v);
+    for (int e = 0; e < 4; ++e) v[e] *= f;
+    store_f32x4<T>(static_cast<T *>(a.out) + (at0 + c) * D + d, v);
+    if (a.lse && d == 0) a.lse[at0 + c] = log_sum(t.y, t.z);
 }
 
 // The kernels a call takes, and their workspace: functions of sizes only.
@@ -547,6 +646,9 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 // launch of the tile kernel has workgroups for are all streamed too.
 constexpr int kFew = 64;
 constexpr int kWholeShift = 4, kWholeTiles = 1 << kWholeShift;
+// The tile kernel over a list of work: one workgroup per compute unit, which
+// its registers fill.
+constexpr int kTileWorkers = 256;
 // Tiles per part: a window of 2048 in fp32, 3 x 8 column tiles: 27 + 7 us at 5, 31 + 6 at 8.
 constexpr int kPartTiles = 5;
 
@@ -562,7 +664,8 @@ struct Route {
     size_t stream_cols, tile_cols;      // columns that these stand for
 };
 
-Route route_of(const KvAttnLaunch &a)
+// `joined`: behind shared prefixes, where a call is three launches at least.
+Route route_of(const KvAttnLaunch &a, bool joined = false)
 {
     Route r;
     const int64_t group = a.q_heads / a.c.kv_heads, cols = a.s.rows * group, D = a.c.head_dim;
@@ -571,6 +674,8 @@ Route route_of(const KvAttnLaunch &a)
     else r.stream = r.tile = true, r.few = kFew;
     const int64_t per = std::max<int64_t>(1, (a.s.rows + a.s.batch - 1) / a.s.batch) * group;
     r.ct = per <= 16 ? 1 : per <= 32 ? 2 : 4;
+    // up to 64 columns in the mean: two launches that most often find nothing are saved
+    if (joined && a.s.batch > 1 && per <= kFew) r.stream = true, r.tile = false, r.few = INT32_MAX;
     const int64_t M = prefill_columns(a), bound = std::min<int64_t>(cols / M + a.s.batch, cols);
     if (r.tile && bound * a.c.kv_heads > most_workgroups(512)) r.stream = true, r.tile = false, r.few = INT32_MAX;
     // Contexts that can have no more than 16 tiles are one unit: four tiles for
@@ -597,27 +702,22 @@ Route route_of(const KvAttnLaunch &a)
     return r;
 }
 
-template <int D, int CG, int FMT, typename T, bool SHARED> hipError_t stream_go(const AttnArgs &A, hipStream_t stream)
+template <int D, int CG, int FMT, typename T> hipError_t stream_go(const AttnArgs &A, hipStream_t stream)
 {
-    kv_stream_kernel<D, CG, FMT, T, SHARED><<<A.workers, 64 * kWaves, 0, stream>>>(A);
+    if (A.state_s) kv_stream_kernel<D, CG, FMT, T, true><<<A.workers, 64 * kWaves, 0, stream>>>(A);
+    else kv_stream_kernel<D, CG, FMT, T, false><<<A.workers, 64 * kWaves, 0, stream>>>(A);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (!A.splits) return e;
-    kv_join_kernel<D, CG, T, SHARED><<<dim3(A.workers - 1, join_blocks(CG)), kJoinThreads, 0, stream>>>(A);
+    if (!A.splits || A.state_s) return e;
+    kv_join_kernel<D, CG, T><<<dim3(A.workers - 1, join_blocks(CG)), kJoinThreads, 0, stream>>>(A);
     return hipGetLastError();
-}
-
-template <int D, int CG, int FMT, typename T> hipError_t stream_shared(const AttnArgs &A, hipStream_t stream)
-{
-    return A.state_s || A.before_s ? stream_go<D, CG, FMT, T, true>(A, stream) : stream_go<D, CG, FMT, T, false>(A, stream);
 }
 
 template <int D, int CG> hipError_t stream_types(const AttnArgs &A, hipStream_t stream)
 {
     if (A.a.format == KV_INT8)
-        return A.a.x_dt == 0 ? stream_shared<D, CG, KV_INT8, float>(A, stream)
-                             : stream_shared<D, CG, KV_INT8, bf16_bits>(A, stream);
-    return A.a.x_dt == 0 ? stream_shared<D, CG, KV_FP8, float>(A, stream) : stream_shared<D, CG, KV_FP8, bf16_bits>(A, stream);
+        return A.a.x_dt == 0 ? stream_go<D, CG, KV_INT8, float>(A, stream) : stream_go<D, CG, KV_INT8, bf16_bits>(A, stream);
+    return A.a.x_dt == 0 ? stream_go<D, CG, KV_FP8, float>(A, stream) : stream_go<D, CG, KV_FP8, bf16_bits>(A, stream);
 }
 
 template <int D> hipError_t stream_groups(const AttnArgs &A, int groups, hipStream_t stream)
@@ -625,85 +725,138 @@ template <int D> hipError_t stream_groups(const AttnArgs &A, int groups, hipStre
     return groups == 1 ? stream_types<D, 1>(A, stream) : groups == 2 ? stream_types<D, 2>(A, stream) : stream_types<D, 4>(A, stream);
 }
 
-}  // namespace
-
-// The two kernels of a pass run one after the other: they share the workspace.
-static size_t pass_ws_floats(const KvAttnLaunch &a)
+hipError_t stream_dims(const AttnArgs &A, int groups, hipStream_t stream)
 {
-    const Route r = route_of(a);
-    return std::max(r.stream_floats + 4 * r.stream_cols, r.tile_floats + 4 * r.tile_cols);
+    switch (A.a.c.head_dim) {
+    case 64: return stream_groups<64>(A, groups, stream);
+    case 128: return stream_groups<128>(A, groups, stream);
+    case 192: return stream_groups<192>(A, groups, stream);
+    default: return stream_groups<256>(A, groups, stream);
+    }
 }
 
-// A pass over the sequences a.s.  `A` comes with the states of a two-pass call set.
-static hipError_t launch_pass(AttnArgs A, const KvAttnLaunch &a, hipStream_t stream)
+// Units of one tile, unless the list could then pass 32 bits.  Only sequences
+// with rows have segments: with rows * q_heads below 2^30 there are fewer
+// than 2^31, and the loop ends, at the latest where each is one unit.
+int unit_shift_of(const KvAttnLaunch &a, int cols, int64_t tiles)
 {
-    const Route r = route_of(a);
+    const double segments = ((double)a.s.rows * (a.q_heads / a.c.kv_heads) / cols +
+                             (double)std::min<int64_t>(a.s.batch, a.s.rows)) * a.c.kv_heads;
+    int shift = 0;
+    while (segments * (double)((tiles >> shift) + 1) >= 0x1p31) ++shift;
+    return shift;
+}
+
+}  // namespace
+
+// The kernels over a.s.  `A` comes zeroed, or with a pass's states set.
+static hipError_t launch_route(AttnArgs &A, const Route &r, const KvAttnLaunch &a, hipStream_t stream)
+{
     A.a = a;
     A.workers = kWorkers;
     A.group = a.q_heads / a.c.kv_heads;
     A.few = r.few, A.tile_bound = r.tile_bound, A.tile_splits = r.tile_splits;
-    A.unit_shift = 0, A.splits = false;
     A.part_o = static_cast<float *>(a.workspace);
     if (r.tile) {
         A.part_s = reinterpret_cast<float4 *>(A.part_o + r.tile_floats);
         const hipError_t e = launch_kv_prefill(A, stream);
         if (e != hipSuccess || !r.stream) return e;
     }
-    // Units of one tile, unless the list could then pass 32 bits.  Only sequences
-    // with rows have segments: with rows * q_heads below 2^30 there are fewer
-    // than 2^31, and the loop ends, at the latest where each is one unit.
-    const double segments =
-        ((double)a.s.rows * A.group / (16 * r.ct) + (double)std::min<int64_t>(a.s.batch, a.s.rows)) * a.c.kv_heads;
-    while (segments * (double)((r.tiles >> A.unit_shift) + 1) >= 0x1p31) ++A.unit_shift;
-    if (r.whole) A.unit_shift = kWholeShift;
+    A.unit_shift = r.whole ? kWholeShift : unit_shift_of(a, 16 * r.ct, r.tiles);
     A.splits = r.tiles > (int64_t)1 << A.unit_shift;
+    // at least two tiles for each wave, so that short contexts do not fall into
+    // parts that cost more to join than to read
+    A.least = A.unit_shift ? 1u : 2u * kWaves;
     A.part_s = reinterpret_cast<float4 *>(A.part_o + r.stream_floats);
-    switch (a.c.head_dim) {
-    case 64: return stream_groups<64>(A, r.ct, stream);
-    case 128: return stream_groups<128>(A, r.ct, stream);
-    case 192: return stream_groups<192>(A, r.ct, stream);
-    default: return stream_groups<256>(A, r.ct, stream);
-    }
+    return stream_dims(A, r.ct, stream);
 }
 
-size_t kv_attn_ws_bytes(const KvAttnLaunch &a) { return pass_ws_floats(a) * sizeof(float); }
+static size_t route_floats(const Route &r) { return std::max(r.stream_floats + 4 * r.stream_cols, r.tile_floats + 4 * r.tile_cols); }
 
-hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream) { return launch_pass(AttnArgs{}, a, stream); }
-
-// Behind a shared prefix: the prefixes' pass takes all rows that share one as
-// one sequence's queries, which see all of its tokens, and leaves their states
-// in the workspace; the sequences' own pass takes them up where it ends.
-static KvAttnLaunch prefix_pass(const KvAttnLaunch &a, const KvSeqs &prefix)
+size_t kv_attn_ws_bytes(const KvAttnLaunch &a)
 {
-    KvAttnLaunch p = a;
-    p.s = prefix;
-    p.causal = 0, p.window = 0;
-    p.out = nullptr, p.lse = nullptr;
-    return p;
+    // the two kernels run one after the other: they share the workspace
+    return route_floats(route_of(a)) * sizeof(float);
 }
-// Floats of the states, a multiple of four.
-static size_t state_floats(const KvAttnLaunch &a) { return (size_t)a.s.rows * a.q_heads * (a.c.head_dim + 4); }
 
+hipError_t launch_kv_attention(const KvAttnLaunch &a, hipStream_t stream)
+{
+    AttnArgs A{};
+    return launch_route(A, route_of(a), a, stream);
+}
+
+// The prefixes' pass takes one of the two kernels for all prefixes, by the mean
+// of their query columns.
+struct PrefixRoute {
+    bool tile;
+    int groups;         // 16-column groups of the streaming kernel
+    int cols, workers;  // of a segment, of the list
+    size_t slots;       // columns of all slots
+};
+
+static PrefixRoute prefix_route(const KvAttnLaunch &a, const KvSeqs &prefix)
+{
+    PrefixRoute f;
+    const int64_t mean = (a.s.rows + prefix.batch - 1) / prefix.batch * (a.q_heads / a.c.kv_heads);
+    f.tile = mean > kFew;
+    f.groups = mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
+    f.cols = f.tile ? prefill_columns(a) : 16 * f.groups;
+    f.workers = f.tile ? kTileWorkers : kWorkers;
+    f.slots = (size_t)2 * f.workers * f.cols;
+    return f;
+}
+
+// Workspace: the prefixes' slots and states, the sequences' states, and what
+// their own kernels take.
 size_t kv_shared_ws_bytes(const KvAttnLaunch &a, const KvSeqs &prefix)
 {
     if (prefix.batch == 0) return kv_attn_ws_bytes(a);
-    return (state_floats(a) + std::max(pass_ws_floats(a), pass_ws_floats(prefix_pass(a, prefix)))) * sizeof(float);
+    const size_t states = (size_t)a.s.rows * a.q_heads;
+    return ((prefix_route(a, prefix).slots + 2 * states) * (a.c.head_dim + 4) + route_floats(route_of(a, true))) * sizeof(float);
 }
 
 hipError_t launch_kv_shared(const KvAttnLaunch &a, const KvSeqs &prefix, hipStream_t stream)
 {
     if (prefix.batch == 0) return launch_kv_attention(a, stream);
-    float *states = static_cast<float *>(a.workspace);
-    float4 *sums = reinterpret_cast<float4 *>(states + (size_t)a.s.rows * a.q_heads * a.c.head_dim);
-    KvAttnLaunch own = a, first = prefix_pass(a, prefix);
-    own.workspace = first.workspace = states + state_floats(a);
+    const PrefixRoute f = prefix_route(a, prefix);
+    const Route r = route_of(a, true);
+    const size_t D = (size_t)a.c.head_dim, states = (size_t)a.s.rows * a.q_heads;
+    float *at = static_cast<float *>(a.workspace);
+    auto take = [&](size_t n) { float *p = at; at += n; return p; };
+
     AttnArgs A{};
-    A.state_o = states, A.state_s = sums;
-    const hipError_t e = launch_pass(A, first, stream);
+    A.a = a;
+    A.a.s = prefix, A.a.causal = 0, A.a.window = 0, A.a.out = nullptr, A.a.lse = nullptr;
+    A.group = a.q_heads / a.c.kv_heads;
+    A.few = INT32_MAX, A.workers = f.workers, A.listed = f.tile, A.tile_splits = 1;
+    A.unit_shift = unit_shift_of(A.a, f.cols, ((prefix.max_blocks << a.c.block_shift) >> 6) + 1);
+    A.least = A.unit_shift || f.tile ? 1u : (uint32_t)kWaves;
+    A.part_o = take(f.slots * D), A.part_s = reinterpret_cast<float4 *>(take(f.slots * 4));
+    A.state_o = take(states * D), A.state_s = reinterpret_cast<float4 *>(take(states * 4));
+    hipError_t e = f.tile ? launch_kv_prefill(A, stream) : stream_dims(A, f.groups, stream);
     if (e != hipSuccess) return e;
+
     AttnArgs O{};
-    O.before_o = states, O.before_s = sums, O.before_start = prefix.row_start, O.before_batch = prefix.batch;
-    return launch_pass(O, own, stream);
+    O.state_o = take(states * D), O.state_s = reinterpret_cast<float4 *>(take(states * 4));
+    KvAttnLaunch own = a;
+    own.workspace = at;
+    if ((e = launch_route(O, r, own, stream)) != hipSuccess) return e;
+
+    SharedJoin J;
+    J.a = a;
+    J.group = A.group;
+    J.prefix = {prefix, A.few, f.cols, A.unit_shift, A.workers, A.least, A.state_o, A.part_o, A.state_s, A.part_s};
+    J.own = {a.s, r.stream ? O.few : 0, 16 * r.ct, O.unit_shift, O.workers, std::max(1u, O.least), O.state_o, O.part_o, O.state_s, O.part_s};
+    const int cols = 1024 / (int)D;
+    const unsigned grid = (unsigned)((states + cols - 1) / cols);
+    auto go = [&](auto bf16, auto f32) { (a.x_dt == 0 ? f32 : bf16)<<<grid, 256 * kSharedRuns, 0, stream>>>(J); };
+    switch (D) {
+    case 64: go(kv_shared_join_kernel<64, bf16_bits>, kv_shared_join_kernel<64, float>); break;
+    case 128: go(kv_shared_join_kernel<128, bf16_bits>, kv_shared_join_kernel<128, float>); break;
+    case 192: go(kv_shared_join_kernel<192, bf16_bits>, kv_shared_join_kernel<192, float>); break;
+    default: go(kv_shared_join_kernel<256, bf16_bits>, kv_shared_join_kernel<256, float>); break;
+    }
+    return hipGetLastError();
 }
 
 }  // namespace nqk

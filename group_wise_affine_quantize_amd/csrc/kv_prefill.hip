@@ -21,9 +21,9 @@
 // 2^(kTop + kSlack) in fp16.
 //
 // 3 prompts of 2530 to 4096 tokens, 32 heads of 128 over 8 int8 key/value
-// heads: 370 to 380 us by itself (a call in a row of calls 341 to 352), 740 TFLOP/s of the
+// heads: 375 to 385 us by itself (340 in a row of calls), 740 TFLOP/s of the
 // visible products, where a large fp16 library product reaches 1131.  A tile
-// takes about 4450 cycles at the 1.97 GHz that the card keeps up: 329 vector
+// takes about 4450 cycles at the 1.97 GHz that the card keeps up: 324 vector
 // instructions for each of the two waves of a SIMD, and 2048 cycles of MFMA
 // per SIMD, overlapped as far as the two waves' phases differ.  The LDS (256
 // bytes a cycle with the placement below) is a quarter used.
@@ -107,7 +107,9 @@ template <int M> __device__ __forceinline__ int tile_locate(const AttnArgs &A, u
     return -1;
 }
 
-// SHARED: a pass of attention behind shared prefixes (see AttnArgs).
+// SHARED: a pass of attention behind shared prefixes.  The prefixes' runs
+// over the list of work that the streaming kernel has (nq_kv_attn.h), an equal run
+// of tiles for each workgroup; workgroups of one XCD take neighbouring runs.
 template <int D, int FMT, typename T, bool SHARED>
 __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
 {
@@ -125,22 +127,52 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int sh = a.c.block_shift, bmask = (1 << sh) - 1;
 
-    // workgroups of one head follow each other with the number of heads as
-    // their distance: with eight heads an XCD keeps to one head's cache
     const uint32_t heads = (uint32_t)a.c.kv_heads;
-    const int head = (int)(blockIdx.x % heads);
-    const uint32_t rest = blockIdx.x / heads;
-    const int split = (int)(rest % (uint32_t)A.tile_splits);
-    uint32_t ctile;
-    const int b = tile_locate<M>(A, rest / (uint32_t)A.tile_splits, &ctile);
-    if (b < 0) return;
-    const StreamSeq s = stream_seq(A, b, M);
+    int head, b, split = 0;
+    uint32_t ctile, worker = 0, inside = 0, total = 0, share = 0, left = 0, unit0 = 0, units = 0;
+    StreamSeq s;
+    if (SHARED && A.listed) {
+        worker = (blockIdx.x & 7u) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+        b = stream_locate(A, M, [&](uint32_t w) { return worker * w; }, &inside, &total, &share);
+        if (b < 0) return;
+        auto uniform = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); };
+        b = (int)uniform((uint32_t)b), inside = uniform(inside), total = uniform(total), share = uniform(share);
+        left = total - worker * share < share ? total - worker * share : share;
+        s = stream_seq(A, b, M);
+    } else {
+        // workgroups of one head follow each other with the number of heads as
+        // their distance: with eight heads an XCD keeps to one head's cache
+        head = (int)(blockIdx.x % heads);
+        const uint32_t rest = blockIdx.x / heads;
+        split = (int)(rest % (uint32_t)A.tile_splits);
+        b = tile_locate<M>(A, rest / (uint32_t)A.tile_splits, &ctile);
+        if (b < 0) return;
+        s = stream_seq(A, b, M);
+    }
+    do {
+    if (SHARED && A.listed) {
+        while (inside >= s.work) {      // the next sequence with work
+            inside -= s.work;
+            if (++b >= a.s.batch) return;
+            s = stream_seq(A, b, M);
+        }
+        const uint32_t seg = inside / s.units;
+        unit0 = inside - seg * s.units;
+        units = s.units - unit0 < left ? s.units - unit0 : left;
+        head = (int)(seg / s.ct);
+        ctile = seg - (uint32_t)head * s.ct;
+    }
     const int count = s.n * A.group, col0 = (int)ctile * M, end = col0 + M < count ? col0 + M : count;
     const Column c0 = column(A, s, col0, head), c1 = column(A, s, end - 1, head);
     const int seg_lo = __builtin_amdgcn_readfirstlane(c0.lo), seg_hi = __builtin_amdgcn_readfirstlane(c1.hi);
     const int first_tile = seg_lo >> 6, tiles = seg_hi > seg_lo ? ((seg_hi + 63) >> 6) - first_tile : 0;
-    const int t_begin = first_tile + (int)((int64_t)tiles * split / A.tile_splits);
-    const int t_end = first_tile + (int)((int64_t)tiles * (split + 1) / A.tile_splits);
+    int t_begin = first_tile + (int)((int64_t)tiles * split / A.tile_splits);
+    int t_end = first_tile + (int)((int64_t)tiles * (split + 1) / A.tile_splits);
+    if (SHARED && A.listed) {
+        t_begin = (int)(unit0 << A.unit_shift);
+        t_end = unit0 + units == s.units ? tiles : (int)((unit0 + units) << A.unit_shift);
+        t_begin = t_begin < t_end ? t_begin : t_end;
+    }
 
     // the query rows are on their way while the first tile is asked for
     const int wcol = col0 + wave * 32;          // the wave's first column
@@ -402,31 +434,28 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
         l *= exp2_below(lref, top);
         lref = top;
     } else lref = ref;
-    float sum = l + xor_lane<32>(l, lane);
-    if (mine.row < 0) return;
-    if (SHARED && A.tile_splits == 1 && A.state_s) {
-        const int64_t at = (int64_t)mine.row * a.q_heads + mine.head;
-        float *po = A.state_o + at * D;
+    const float sum = l + xor_lane<32>(l, lane);
+    if (SHARED && (A.listed || A.tile_splits == 1)) {
+        if (mine.row >= 0) {
+            const bool whole = !A.listed || units == s.units;
+            const int64_t at = whole ? (int64_t)mine.row * a.q_heads + mine.head
+                                     : (2 * (int64_t)worker + (unit0 == 0 ? 1 : 0)) * M + wave * 32 + r;
+            float *po = (whole ? A.state_o : A.part_o) + at * D;
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
+            for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4 *>(po + 32 * dt + 2 * i + 4 * h) =
-                    make_float4(o[dt][i], o[dt][i + 1], o[dt][i + 2], o[dt][i + 3]);
-        if (h == 0) A.state_s[at] = make_float4(ref, sum, lref, 0.0f);
-    } else if (A.tile_splits == 1) {
-        if constexpr (SHARED) {
-            const Before before = take_before(A, mine.row, mine.head, sum, ref, lref);
-            if (before.o)
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        float v[4] = {o[dt][i], o[dt][i + 1], o[dt][i + 2], o[dt][i + 3]};
-                        add_before(before, 32 * dt + 2 * i + 4 * h, v);
-                        o[dt][i] = v[0], o[dt][i + 1] = v[1], o[dt][i + 2] = v[2], o[dt][i + 3] = v[3];
-                    }
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4 *>(po + 32 * dt + 2 * i + 4 * h) =
+                        make_float4(o[dt][i], o[dt][i + 1], o[dt][i + 2], o[dt][i + 3]);
+            if (h == 0) (whole ? A.state_s : A.part_s)[at] = make_float4(ref, sum, lref, 0.0f);
         }
+        if (!A.listed) return;
+        left -= units;
+        inside += units;
+        continue;
+    }
+    if (mine.row < 0) return;
+    if (A.tile_splits == 1) {
         const float f = out_factor(sum, ref, lref, 16 * DT, reinterpret_cast<float *>(o));
         T *out = static_cast<T *>(a.out) + ((int64_t)mine.row * a.q_heads + mine.head) * D;
 #pragma unroll
@@ -449,6 +478,7 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
                     make_float4(o[dt][i], o[dt][i + 1], o[dt][i + 2], o[dt][i + 3]);
         if (h == 0) A.part_s[at] = make_float4(ref, sum, lref, 0.0f);
     }
+    } while (SHARED && left > 0);
 }
 
 // Joins the parts of a column tile's tokens, in their order; one workgroup
@@ -486,26 +516,24 @@ template <int D, typename T, bool SHARED> __global__ __launch_bounds__(256) void
         l = fmaf(exp2_below(t.z, u), t.y, l);
         v[0] = fmaf(f, o.x, v[0]), v[1] = fmaf(f, o.y, v[1]), v[2] = fmaf(f, o.z, v[2]), v[3] = fmaf(f, o.w, v[3]);
     }
-    const int64_t row = (int64_t)q.row * a.q_heads + q.head;
-    if (SHARED && A.state_s) {
+    if constexpr (SHARED) {
+        const int64_t row = (int64_t)q.row * a.q_heads + q.head;
         store_f32x4<float>(A.state_o + row * D + d, v);
         if (d == 0) A.state_s[row] = make_float4(m, l, u, 0.0f);
         return;
     }
-    if constexpr (SHARED) {
-        const Before before = take_before(A, q.row, q.head, l, m, u);
-        if (before.o) add_before(before, d, v);
-    }
     const float f = out_factor(l, m, u, 4, v);
     for (int e = 0; e < 4; ++e) v[e] *= f;
-    store_f32x4<T>(static_cast<T *>(a.out) + row * D + d, v);
-    if (a.lse && d == 0) a.lse[row] = log_sum(l, u);
+    store_f32x4<T>(static_cast<T *>(a.out) + ((int64_t)q.row * a.q_heads + q.head) * D + d, v);
+    if (a.lse && d == 0)
+        a.lse[(int64_t)q.row * a.q_heads + q.head] = log_sum(l, u);
 }
 
 template <int D, int FMT, typename T, bool SHARED> hipError_t tile_go(const AttnArgs &A, hipStream_t stream)
 {
     const unsigned segments = A.tile_bound * (unsigned)A.a.c.kv_heads;
-    kv_tile_kernel<D, FMT, T, SHARED><<<segments * (unsigned)A.tile_splits, Shape<D>::THREADS, 0, stream>>>(A);
+    const unsigned grid = A.listed ? (unsigned)A.workers : segments * (unsigned)A.tile_splits;
+    kv_tile_kernel<D, FMT, T, SHARED><<<grid, Shape<D>::THREADS, 0, stream>>>(A);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || A.tile_splits == 1) return e;
     constexpr int cols = 1024 / D;
@@ -515,7 +543,7 @@ template <int D, int FMT, typename T, bool SHARED> hipError_t tile_go(const Attn
 
 template <int D, int FMT, typename T> hipError_t tile_shared(const AttnArgs &A, hipStream_t stream)
 {
-    return A.state_s || A.before_s ? tile_go<D, FMT, T, true>(A, stream) : tile_go<D, FMT, T, false>(A, stream);
+    return A.state_s ? tile_go<D, FMT, T, true>(A, stream) : tile_go<D, FMT, T, false>(A, stream);
 }
 
 template <int D> hipError_t tile_types(const AttnArgs &A, hipStream_t stream)

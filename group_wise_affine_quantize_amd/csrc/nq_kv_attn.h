@@ -72,6 +72,22 @@ __device__ __forceinline__ float4_t mfma(half8_t a, half8_t b, float4_t c)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// Attention behind shared prefixes is two passes and a join.  The first takes all
+// rows that share a prefix as one sequence's queries, which see all of its
+// tokens; the second is over the sequences' own tokens.  Neither gives a result:
+// a segment (see below) that one workgroup had whole leaves its O, R, L and U by
+// row and head, the parts of the others lie in their workgroups' slots.  What the
+// join has to know of a pass:
+struct Pass {
+    KvSeqs s;                   // batch 0: no sequences
+    int few;                    // sequences of more columns lie by row and head
+    int cols;                   // query columns of a segment
+    int unit_shift, workers;
+    uint32_t least;
+    const float *state_o, *part_o;      // [rows][q_heads][D], [workers * 2][cols][D]
+    const float4 *state_s, *part_s;     // [rows][q_heads], [workers * 2][cols] of R, L, U
+};
+
 struct AttnArgs {
     KvAttnLaunch a;
     float *part_o;      // [workers * 2][columns][D]
@@ -84,15 +100,12 @@ struct AttnArgs {
                         // streaming kernel's, the others the tile kernel's
     int tile_splits;    // parts that the tile kernel cuts a segment's tokens into
     unsigned tile_bound;    // tile kernel: column tiles at most, over all sequences
-    // Attention in two passes (a prefix, then the sequences' own tokens).  The
-    // first keeps each row's O, R, L and U here instead of giving a result,
-    // [rows][q_heads][D] and [rows][q_heads]; the second takes them up.
-    float *state_o;                 // or null
+    uint32_t least;         // units of the list that a workgroup takes at least
+    // a pass of attention behind shared prefixes: where whole segments leave
+    // their states (see Pass), and whether the tile kernel runs over the list
+    float *state_o;             // or null
     float4 *state_s;
-    const float *before_o;          // or null
-    const float4 *before_s;
-    const int32_t *before_start;    // the prefixes' rows (see KvSeqs::row_start)
-    int before_batch;
+    bool listed;
 };
 
 // The streaming kernel's work is a flat list of units (runs of 64-token
@@ -268,41 +281,45 @@ __device__ __forceinline__ float out_factor(float l, float m, float u, int count
 // log of the sum of weights l over 2^u: -infinity for none, NaN for a NaN.
 __device__ __forceinline__ float log_sum(float l, float u) { return l == 0.0f ? kNegInf : (u + fast_log2(l)) * kLn2; }
 
-// What the first pass left of a row and head, and the factors with which it
-// and the second pass's O go into their sum.
-struct Before {
-    const float *o;     // null: no prefix has the row
-    float mine, its;
-};
-
-// Takes the first pass's state into l and the references m and u.
-__device__ __forceinline__ Before take_before(const AttnArgs &A, int row, int head, float &l, float &m, float &u)
+// Units per worker.
+__device__ __forceinline__ uint32_t share_of(const AttnArgs &A, uint32_t total)
 {
-    Before b{nullptr, 1.0f, 0.0f};
-    if (!A.before_s) return b;
-    // the last prefix that starts at this row or before it
-    int lo = 0, hi = A.before_batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (A.before_start[mid] <= row) lo = mid;
-        else hi = mid;
-    }
-    if (A.before_start[lo] > row || A.before_start[lo + 1] <= row) return b;
-    const int64_t at = (int64_t)row * A.a.q_heads + head;
-    const float4 t = A.before_s[at];
-    const float top = fmaxf(m, t.x), utop = fmaxf(u, t.z);
-    b.o = A.before_o + at * A.a.c.head_dim;
-    b.mine = exp2_below(m, top), b.its = exp2_below(t.x, top);
-    l = fmaf(exp2_below(t.z, utop), t.y, l * exp2_below(u, utop));
-    m = top, u = utop;
-    return b;
+    return list_share(total, (uint32_t)A.workers, A.least);
 }
-// Four columns of O, from column d on, become those of both passes.
-__device__ __forceinline__ void add_before(const Before &b, int d, float *v)
+
+// Finds the sequence of unit `at(share)` of the list: its number (-1: past the
+// list's end), the unit's number inside it, the list's length and the share.
+template <typename At>
+__device__ __forceinline__ int stream_locate(const AttnArgs &A, int cols, At at, uint32_t *inside, uint32_t *total,
+                                             uint32_t *share)
 {
-    const float4 w = *reinterpret_cast<const float4 *>(b.o + d);
-    v[0] = fmaf(b.its, w.x, v[0] * b.mine), v[1] = fmaf(b.its, w.y, v[1] * b.mine);
-    v[2] = fmaf(b.its, w.z, v[2] * b.mine), v[3] = fmaf(b.its, w.w, v[3] * b.mine);
+    const int batch = A.a.s.batch, lane = (int)(threadIdx.x & 63u);
+    uint32_t work = lane < batch ? stream_seq(A, lane, cols).work : 0u;     // below 2^31
+    uint32_t upto = wave_scan32_sat(work);
+    uint32_t sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+    *total = sum;
+    for (int b = 64 + lane; b - lane < batch; b += 64)
+        *total = add_sat(*total, (uint32_t)__builtin_amdgcn_readlane(
+            (int)wave_scan32_sat(b < batch ? stream_seq(A, b, cols).work : 0u), 63));
+    *total = list_total(*total);
+    *share = share_of(A, *total);
+    const uint32_t want = at(*share);
+    if (want >= *total) return -1;
+    uint32_t base = 0;      // at most `want`
+    for (int b0 = 0; b0 < batch; b0 += 64) {
+        if (b0) {
+            work = b0 + lane < batch ? stream_seq(A, b0 + lane, cols).work : 0u;
+            upto = wave_scan32_sat(work);
+            sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+        }
+        if (add_sat(base, sum) > want) {
+            const int l = __ffsll((unsigned long long)__ballot(add_sat(base, upto) > want)) - 1;
+            *inside = want - base - (uint32_t)__builtin_amdgcn_readlane((int)(upto - work), l);
+            return b0 + l;
+        }
+        base += sum;
+    }
+    return -1;
 }
 
 // The tile kernel (kv_prefill.hip).
