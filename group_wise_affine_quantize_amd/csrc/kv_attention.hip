@@ -96,16 +96,16 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
     const int sh = a.c.block_shift, bmask = (1 << sh) - 1;
 
     uint32_t inside, total, share;
-    int b = stream_locate(A, COLS, [](uint32_t s) { return blockIdx.x * s; }, &inside, &total, &share);
+    int b = stream_locate<SHARED>(A, COLS, [](uint32_t s) { return blockIdx.x * s; }, &inside, &total, &share);
     if (b < 0) return;
     uint32_t left = total - blockIdx.x * share < share ? total - blockIdx.x * share : share;
-    StreamSeq s = stream_seq(A, b, COLS);
+    StreamSeq s = stream_seq<SHARED>(A, b, COLS);
 
     while (left > 0) {
         while (inside >= s.work) {      // the next sequence with work
             inside -= s.work;
-            if (++b >= a.s.batch) return;
-            s = stream_seq(A, b, COLS);
+            if (++b >= a.s.batch + (SHARED ? A.pre.batch : 0)) return;
+            s = stream_seq<SHARED>(A, b, COLS);
         }
         const uint32_t seg = inside / s.units, unit0 = inside - seg * s.units;
         const int head = (int)(seg / s.ct);
@@ -153,6 +153,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
         // A tile's blocks: of this lane's key rows, and of its value and score
         // tokens; -1 where no column sees the 16 tokens or no block holds them.
         const int *table = a.s.table + (int64_t)b * a.s.ldt;
+        if (SHARED) table = s.prefix ? A.pre.table + (int64_t)b * A.pre.ldt : a.s.table + (int64_t)(b - A.pre.batch) * a.s.ldt;
         auto block_of = [&](int pos) -> int {
             if (pos >= seg_hi || pos + 16 <= seg_lo) return -1;     // also keeps pos inside the table
             const int id = table[pos >> sh];
@@ -355,8 +356,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
                 const int64_t at = (int64_t)c.row * a.q_heads + c.head;
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt)
-                    *reinterpret_cast<float4_t *>(A.state_o + at * D + 16 * dt + 4 * g) = st.o[dt];
-                if (g == 0) A.state_s[at] = make_float4(st.m, l, st.u, 0.0f);
+                    *reinterpret_cast<float4_t *>((s.prefix ? A.pre_o : A.state_o) + at * D + 16 * dt + 4 * g) = st.o[dt];
+                if (g == 0) (s.prefix ? A.pre_s : A.state_s)[at] = make_float4(st.m, l, st.u, 0.0f);
             } else if (whole) {
                 const float f = out_factor(l, st.m, st.u, 4 * DT, reinterpret_cast<float *>(st.o));
                 T *out = static_cast<T *>(a.out) + ((int64_t)c.row * a.q_heads + c.head) * D;
@@ -478,18 +479,23 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnArgs A)
 //   k == 0 ? first : rest + 2 * k * cols
 // of a pass's slots, or, where there is one part, at `first` of its states.
 // parts 0: no sequence of the pass has the row.
-struct Column0 {
+struct ColumnParts {
     int parts, first, rest;
 };
 
-// For each lane's row and head (row -1: none); all lanes of the wave call it.
-// The list that the pass ran over is counted again, 64 sequences at a time.
-__device__ __forceinline__ Column0 find_parts(const Pass &p, const KvCache &cache, int group, int q_heads, int row, int head)
+// The sequence of a pass that has `row`: the row's number in it, and where its
+// segments are in the pass's list, whose length is counted on the way, 64
+// sequences at a time.
+struct Found {
+    bool has;
+    int row;
+    uint32_t base, units, ct;       // units before it, of a segment; column tiles
+};
+__device__ __forceinline__ Found find_row(const Pass &p, const KvCache &cache, int group, int row, uint32_t *total)
 {
     const int lane = (int)(threadIdx.x & 63u), batch = p.s.batch;
-    bool found = false;
-    int col = 0;
-    uint32_t total = 0, base = 0, units = 0, ct = 0;
+    Found f{false, 0, 0, 0, 0};
+    *total = 0;
     for (int b0 = 0; b0 < batch; b0 += 64) {
         int r0 = 0, n = 0;
         uint32_t u = 0, c = 0;
@@ -502,49 +508,45 @@ __device__ __forceinline__ Column0 find_parts(const Pass &p, const KvCache &cach
             c = n * group <= p.few ? (uint32_t)(n * group + p.cols - 1) / (uint32_t)p.cols : 0u;
         }
         const uint32_t work = c * u * (uint32_t)cache.kv_heads, upto = wave_scan32_sat(work);
-        // the wave's rows one after the other; most often there is one
-        uint64_t open = __ballot(row >= 0 && !found);
-        while (open) {
-            const int who = __builtin_amdgcn_readlane(row, __ffsll((unsigned long long)open) - 1);
-            const uint64_t has = __ballot(who >= r0 && who < r0 + n);
-            if (has) {
-                const int at = __ffsll((unsigned long long)has) - 1;
-                auto get = [&](int v) { return __builtin_amdgcn_readlane(v, at); };
-                if (row == who && !found) {
-                    found = true;
-                    base = add_sat(total, (uint32_t)get((int)(upto - work)));
-                    col = row - get(r0), units = (uint32_t)get((int)u), ct = (uint32_t)get((int)c);
-                }
-            }
-            open &= ~__ballot(row == who);
+        const uint64_t has = __ballot(row >= r0 && row < r0 + n);
+        if (has && !f.has) {
+            const int at = __ffsll((unsigned long long)has) - 1;
+            auto get = [&](uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, at); };
+            f.has = true, f.row = row - (int)get((uint32_t)r0);
+            f.base = add_sat(*total, get(upto - work)), f.units = get(u), f.ct = get(c);
         }
-        total = add_sat(total, (uint32_t)__builtin_amdgcn_readlane((int)upto, 63));
+        *total = add_sat(*total, (uint32_t)__builtin_amdgcn_readlane((int)upto, 63));
     }
-    total = list_total(total);
-    Column0 f{0, 0, 0};
-    if (!found) return f;
-    f.parts = 1, f.first = row * q_heads + head;
-    if (ct == 0) return f;
-    const uint32_t share = list_share(total, (uint32_t)p.workers, p.least);
-    const int kv_head = head / group;
-    col = col * group + (head - kv_head * group);
-    const uint32_t tile = (uint32_t)col / (uint32_t)p.cols, c = (uint32_t)col - tile * (uint32_t)p.cols;
-    const uint64_t off = (uint64_t)base + (uint64_t)((uint32_t)kv_head * ct + tile) * units;
-    if (off + units > total) {      // past the list's end: not done
-        f.parts = 0;
-        return f;
-    }
-    const uint32_t w0 = (uint32_t)off / share, w1 = (uint32_t)(off + units - 1) / share;
-    f.parts = (int)(w1 - w0) + 1;
-    f.rest = (int)(w0 * 2 * (uint32_t)p.cols + c);
-    if (f.parts > 1) f.first = f.rest + p.cols;
     return f;
+}
+
+// The parts of a row and head, in a list of `total` units.
+__device__ __forceinline__ ColumnParts parts_of(const Pass &p, const Found &f, uint32_t total, int group, int q_heads, int row, int head)
+{
+    ColumnParts c{0, 0, 0};
+    if (!f.has) return c;
+    c.parts = 1, c.first = row * q_heads + head;
+    if (f.ct == 0) return c;
+    const uint32_t share = list_share(total, (uint32_t)p.workers, p.least);
+    const int kv_head = head / group, col = f.row * group + (head - kv_head * group);
+    const uint32_t tile = (uint32_t)col / (uint32_t)p.cols, i = (uint32_t)col - tile * (uint32_t)p.cols;
+    const uint64_t off = (uint64_t)f.base + (uint64_t)((uint32_t)kv_head * f.ct + tile) * f.units;
+    if (off + f.units > total) {      // past the list's end: not done
+        c.parts = 0;
+        return c;
+    }
+    const uint32_t w0 = (uint32_t)off / share, w1 = (uint32_t)(off + f.units - 1) / share;
+    c.parts = (int)(w1 - w0) + 1;
+    c.rest = (int)(w0 * 2 * (uint32_t)p.cols + i);
+    if (c.parts > 1) c.first = c.rest + p.cols;
+    return c;
 }
 
 struct SharedJoin {
     KvAttnLaunch a;
     Pass prefix, own;
     int group;
+    bool joint;     // one list: the prefixes' and the sequences' behind them
 };
 
 // Joins the two passes' parts of each row and head: the prefix's, then the
@@ -565,11 +567,15 @@ template <int D, typename T> __global__ __launch_bounds__(256 * kSharedRuns) voi
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = (int)threadIdx.x & 63;
     const int tid = (int)threadIdx.x & 255, run = (int)threadIdx.x >> 8, c = tid / QUADS, d = (tid % QUADS) * 4;
 
-    Column0 p{0, 0, 0}, o{0, 0, 0};
+    ColumnParts p{0, 0, 0}, o{0, 0, 0};
     if (wave < COLS && at0 + wave < count) {
         const int row = (int)((at0 + wave) / a.q_heads), head = (int)(at0 + wave - (int64_t)row * a.q_heads);
-        p = find_parts(J.prefix, a.c, J.group, a.q_heads, row, head);
-        o = find_parts(J.own, a.c, J.group, a.q_heads, row, head);
+        uint32_t its, mine;
+        const Found fp = find_row(J.prefix, a.c, J.group, row, &its);
+        Found fo = find_row(J.own, a.c, J.group, row, &mine);
+        if (J.joint) fo.base = add_sat(fo.base, its), its = mine = add_sat(its, mine);
+        p = parts_of(J.prefix, fp, list_total(its), J.group, a.q_heads, row, head);
+        o = parts_of(J.own, fo, list_total(mine), J.group, a.q_heads, row, head);
         if (o.parts == 0) p.parts = 0;      // a row that no sequence has is left alone
     }
     const int parts = p.parts + o.parts;
@@ -583,7 +589,7 @@ template <int D, typename T> __global__ __launch_bounds__(256 * kSharedRuns) voi
             if (k < parts) {
                 const bool first = k < p.parts;
                 const Pass &q = first ? J.prefix : J.own;
-                const Column0 f = first ? p : o;
+                const ColumnParts f = first ? p : o;
                 const int i = first ? k : k - p.parts;
                 const int64_t slot = i == 0 ? f.first : f.rest + 2 * (int64_t)i * q.cols;
                 t = (f.parts == 1 ? q.state_s : q.part_s)[slot];
@@ -749,6 +755,13 @@ int unit_shift_of(const KvAttnLaunch &a, int cols, int64_t tiles)
 
 }  // namespace
 
+// Units that a workgroup takes at least: segments that follow each other cost one
+// 4 us each, and what a segment is cut into is joined in any case (4 sequences
+// of 4 heads behind 700 tokens: 15 us at 1, 28 at 4); but no more than about 64
+// parts (3 sequences of 4 heads over one behind 5k and 21k tokens: 44 us with 331
+// parts, 32 with 83).
+static uint32_t least_of(int64_t tiles, int unit_shift) { return (uint32_t)std::max<int64_t>(1, (tiles >> unit_shift) / 64); }
+
 // The kernels over a.s.  `A` comes zeroed, or with a pass's states set.
 static hipError_t launch_route(AttnArgs &A, const Route &r, const KvAttnLaunch &a, hipStream_t stream)
 {
@@ -767,6 +780,7 @@ static hipError_t launch_route(AttnArgs &A, const Route &r, const KvAttnLaunch &
     // at least two tiles for each wave, so that short contexts do not fall into
     // parts that cost more to join than to read
     A.least = A.unit_shift ? 1u : 2u * kWaves;
+    if (A.state_s) A.least = least_of(r.tiles, A.unit_shift);
     A.part_s = reinterpret_cast<float4 *>(A.part_o + r.stream_floats);
     return stream_dims(A, r.ct, stream);
 }
@@ -794,16 +808,30 @@ struct PrefixRoute {
     size_t slots;       // columns of all slots
 };
 
-static PrefixRoute prefix_route(const KvAttnLaunch &a, const KvSeqs &prefix)
+// `groups`: those of the sequences' own pass, if one launch does both.
+static PrefixRoute prefix_route(const KvAttnLaunch &a, const KvSeqs &prefix, int groups)
 {
     PrefixRoute f;
     const int64_t mean = (a.s.rows + prefix.batch - 1) / prefix.batch * (a.q_heads / a.c.kv_heads);
-    f.tile = mean > kFew;
-    f.groups = mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
+    f.tile = !groups && mean > kFew;
+    f.groups = groups ? groups : mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
     f.cols = f.tile ? prefill_columns(a) : 16 * f.groups;
     f.workers = f.tile ? kTileWorkers : kWorkers;
     f.slots = (size_t)2 * f.workers * f.cols;
     return f;
+}
+
+// Both passes in one launch of the streaming kernel, over columns as the
+// sequences' own pass has them: where that is streamed and there are few segments
+// in all, so that workgroups rarely have several (16 sequences of 4 heads over 2 behind
+// 700 tokens 35 -> 21 us, behind 16000 53 -> 45; with 320 and more segments
+// it is slower, 74 -> 169 at 640).
+static bool joint_route(const KvAttnLaunch &a, const KvSeqs &prefix, const Route &r)
+{
+    const int64_t group = a.q_heads / a.c.kv_heads, cols = 16 * r.ct;
+    const int64_t own = std::min<int64_t>(a.s.batch, a.s.rows), its = std::min<int64_t>(prefix.batch, a.s.rows);
+    const int64_t segments = (own + its + 2 * (a.s.rows * group / cols)) * a.c.kv_heads;
+    return r.stream && !r.tile && segments <= 192;
 }
 
 // Workspace: the prefixes' slots and states, the sequences' states, and what
@@ -811,40 +839,61 @@ static PrefixRoute prefix_route(const KvAttnLaunch &a, const KvSeqs &prefix)
 size_t kv_shared_ws_bytes(const KvAttnLaunch &a, const KvSeqs &prefix)
 {
     if (prefix.batch == 0) return kv_attn_ws_bytes(a);
+    const Route r = route_of(a, true);
+    const bool joint = joint_route(a, prefix, r);
     const size_t states = (size_t)a.s.rows * a.q_heads;
-    return ((prefix_route(a, prefix).slots + 2 * states) * (a.c.head_dim + 4) + route_floats(route_of(a, true))) * sizeof(float);
+    return ((prefix_route(a, prefix, joint ? r.ct : 0).slots + 2 * states) * (a.c.head_dim + 4) +
+            (joint ? 0 : route_floats(r))) * sizeof(float);
 }
 
 hipError_t launch_kv_shared(const KvAttnLaunch &a, const KvSeqs &prefix, hipStream_t stream)
 {
     if (prefix.batch == 0) return launch_kv_attention(a, stream);
-    const PrefixRoute f = prefix_route(a, prefix);
     const Route r = route_of(a, true);
+    const bool joint = joint_route(a, prefix, r);
+    const PrefixRoute f = prefix_route(a, prefix, joint ? r.ct : 0);
     const size_t D = (size_t)a.c.head_dim, states = (size_t)a.s.rows * a.q_heads;
+    const int64_t tiles = ((prefix.max_blocks << a.c.block_shift) >> 6) + 1;
     float *at = static_cast<float *>(a.workspace);
     auto take = [&](size_t n) { float *p = at; at += n; return p; };
 
-    AttnArgs A{};
+    AttnArgs A{};       // the prefixes' pass
     A.a = a;
     A.a.s = prefix, A.a.causal = 0, A.a.window = 0, A.a.out = nullptr, A.a.lse = nullptr;
     A.group = a.q_heads / a.c.kv_heads;
     A.few = INT32_MAX, A.workers = f.workers, A.listed = f.tile, A.tile_splits = 1;
-    A.unit_shift = unit_shift_of(A.a, f.cols, ((prefix.max_blocks << a.c.block_shift) >> 6) + 1);
-    A.least = A.unit_shift || f.tile ? 1u : (uint32_t)kWaves;
+    A.unit_shift = unit_shift_of(A.a, f.cols, tiles);
     A.part_o = take(f.slots * D), A.part_s = reinterpret_cast<float4 *>(take(f.slots * 4));
     A.state_o = take(states * D), A.state_s = reinterpret_cast<float4 *>(take(states * 4));
-    hipError_t e = f.tile ? launch_kv_prefill(A, stream) : stream_dims(A, f.groups, stream);
-    if (e != hipSuccess) return e;
-
-    AttnArgs O{};
+    AttnArgs O{};       // the sequences'
     O.state_o = take(states * D), O.state_s = reinterpret_cast<float4 *>(take(states * 4));
-    KvAttnLaunch own = a;
-    own.workspace = at;
-    if ((e = launch_route(O, r, own, stream)) != hipSuccess) return e;
+    hipError_t e;
+    if (joint) {
+        // twice the units of the longer of the two cannot pass 32 bits either
+        const int64_t longer = std::max(tiles, r.tiles);
+        KvAttnLaunch both = a;
+        both.s.rows = 2 * a.s.rows, both.s.batch = a.s.batch + prefix.batch;
+        O.a = a;
+        O.group = A.group, O.few = INT32_MAX, O.workers = kWorkers;
+        O.unit_shift = unit_shift_of(both, f.cols, longer);
+        O.least = least_of(longer, O.unit_shift);
+        O.part_o = A.part_o, O.part_s = A.part_s;
+        O.pre = prefix, O.pre_o = A.state_o, O.pre_s = A.state_s;
+        A.unit_shift = O.unit_shift, A.least = O.least;
+        e = stream_dims(O, f.groups, stream);
+    } else {
+        A.least = least_of(tiles, A.unit_shift);
+        e = f.tile ? launch_kv_prefill(A, stream) : stream_dims(A, f.groups, stream);
+        if (e != hipSuccess) return e;
+        KvAttnLaunch own = a;
+        own.workspace = at;
+        e = launch_route(O, r, own, stream);
+    }
+    if (e != hipSuccess) return e;
 
     SharedJoin J;
     J.a = a;
-    J.group = A.group;
+    J.group = A.group, J.joint = joint;
     J.prefix = {prefix, A.few, f.cols, A.unit_shift, A.workers, A.least, A.state_o, A.part_o, A.state_s, A.part_s};
     J.own = {a.s, r.stream ? O.few : 0, 16 * r.ct, O.unit_shift, O.workers, std::max(1u, O.least), O.state_o, O.part_o, O.state_s, O.part_s};
     const int cols = 1024 / (int)D;

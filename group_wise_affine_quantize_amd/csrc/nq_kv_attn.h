@@ -106,6 +106,11 @@ struct AttnArgs {
     float *state_o;             // or null
     float4 *state_s;
     bool listed;
+    // Both passes in one launch of the streaming kernel: the prefixes come first
+    // in its list, and leave their states here.
+    KvSeqs pre;                 // batch 0: none
+    float *pre_o;
+    float4 *pre_s;
 };
 
 // The streaming kernel's work is a flat list of units (runs of 64-token
@@ -120,15 +125,19 @@ struct StreamSeq {
     uint32_t ct;            // column tiles
     uint32_t units;         // per segment
     uint32_t work;          // units of all segments
+    bool prefix;            // rows see all of its tokens
 };
 
-__device__ __forceinline__ StreamSeq stream_seq(const AttnArgs &A, int b, int cols)
+// SHARED: sequence b of the prefixes and the sequences behind them.
+template <bool SHARED = false> __device__ __forceinline__ StreamSeq stream_seq(const AttnArgs &A, int b, int cols)
 {
     const KvAttnLaunch &a = A.a;
-    const KvSeq q = kv_seq(a.s, b);
     StreamSeq s;
+    s.prefix = SHARED && b < A.pre.batch;
+    const KvSeqs &of = s.prefix ? A.pre : a.s;
+    const KvSeq q = kv_seq(of, SHARED && !s.prefix ? b - A.pre.batch : b);
     s.r0 = (int)q.r0, s.n = (int)q.n, s.first = (int)q.first, s.len = (int)q.len;
-    const int cap = (int)(a.s.max_blocks << a.c.block_shift);
+    const int cap = (int)(of.max_blocks << a.c.block_shift);
     s.hi = s.len < cap ? s.len : cap;
     s.lo = 0;
     if (a.window > 0) {
@@ -137,7 +146,7 @@ __device__ __forceinline__ StreamSeq stream_seq(const AttnArgs &A, int b, int co
     }
     s.t0 = s.lo >> 6;
     s.nt = s.hi > s.lo ? ((s.hi + 63) >> 6) - s.t0 : 1;
-    s.ct = s.n * A.group <= A.few ? (uint32_t)(s.n * A.group + cols - 1) / (uint32_t)cols : 0u;
+    s.ct = s.prefix || s.n * A.group <= A.few ? (uint32_t)(s.n * A.group + cols - 1) / (uint32_t)cols : 0u;
     s.units = (uint32_t)(s.nt + (1 << A.unit_shift) - 1) >> A.unit_shift;
     s.work = s.ct * s.units * (uint32_t)a.c.kv_heads;
     return s;
@@ -161,7 +170,7 @@ __device__ __forceinline__ Column column(const AttnArgs &A, const StreamSeq &s, 
         c.row = s.r0 + i;
         c.head = kv_head * A.group + (idx - i * A.group);
         const int pos = s.first + i;
-        c.hi = a.causal && pos < s.hi ? pos + 1 : s.hi;
+        c.hi = a.causal && !s.prefix && pos < s.hi ? pos + 1 : s.hi;
         if (a.window > 0) {
             const int64_t lo = (int64_t)pos - a.window + 1;
             c.lo = lo < 0 ? 0 : (int)lo;
@@ -289,18 +298,18 @@ __device__ __forceinline__ uint32_t share_of(const AttnArgs &A, uint32_t total)
 
 // Finds the sequence of unit `at(share)` of the list: its number (-1: past the
 // list's end), the unit's number inside it, the list's length and the share.
-template <typename At>
+template <bool SHARED = false, typename At>
 __device__ __forceinline__ int stream_locate(const AttnArgs &A, int cols, At at, uint32_t *inside, uint32_t *total,
                                              uint32_t *share)
 {
-    const int batch = A.a.s.batch, lane = (int)(threadIdx.x & 63u);
-    uint32_t work = lane < batch ? stream_seq(A, lane, cols).work : 0u;     // below 2^31
+    const int batch = A.a.s.batch + (SHARED ? A.pre.batch : 0), lane = (int)(threadIdx.x & 63u);
+    uint32_t work = lane < batch ? stream_seq<SHARED>(A, lane, cols).work : 0u;     // below 2^31
     uint32_t upto = wave_scan32_sat(work);
     uint32_t sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
     *total = sum;
     for (int b = 64 + lane; b - lane < batch; b += 64)
         *total = add_sat(*total, (uint32_t)__builtin_amdgcn_readlane(
-            (int)wave_scan32_sat(b < batch ? stream_seq(A, b, cols).work : 0u), 63));
+            (int)wave_scan32_sat(b < batch ? stream_seq<SHARED>(A, b, cols).work : 0u), 63));
     *total = list_total(*total);
     *share = share_of(A, *total);
     const uint32_t want = at(*share);
@@ -308,7 +317,7 @@ __device__ __forceinline__ int stream_locate(const AttnArgs &A, int cols, At at,
     uint32_t base = 0;      // at most `want`
     for (int b0 = 0; b0 < batch; b0 += 64) {
         if (b0) {
-            work = b0 + lane < batch ? stream_seq(A, b0 + lane, cols).work : 0u;
+            work = b0 + lane < batch ? stream_seq<SHARED>(A, b0 + lane, cols).work : 0u;
             upto = wave_scan32_sat(work);
             sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
         }
