@@ -19,7 +19,10 @@
 // write them to the workspace and a second kernel adds them in order.  All
 // statistics and sums are fp32.
 //
-// What bounds it: memory, 4 moves of a row forward and 6 backward.
+// What bounds it: memory, 4 moves of a row forward and 6 backward.  8191 rows of
+// 4096 in bf16: 43 to 47 us, 5.7 to 6.2 TB/s; the gradient of 8192 rows of 2048
+// 50 us, 4.1 TB/s, of which 4 are the sums over the chunks: 30 vector instructions
+// for each element, 13 us of them, and what is exchanged over a row's waves.
 #include <algorithm>
 
 #include "nq_kv.h"
@@ -75,15 +78,28 @@ __global__ __launch_bounds__(64 * W * teams<W>()) void block_norm_kernel(BlockNo
     const P *post = static_cast<const P *>(a.post), *pre = static_cast<const P *>(a.pre);
     for (int64_t row = (int64_t)blockIdx.x * TEAMS + team; row < a.rows; row += (int64_t)gridDim.x * TEAMS) {
         const T *h = static_cast<const T *>(a.h) + row * a.ldh;
+        const T *y = static_cast<const T *>(a.y) + row * a.ldy;
+        const P *gate = static_cast<const P *>(a.gate) + (a.gate ? row / per_gate * a.ldg : 0);
+        // everything is asked for before the first sum is waited for
+        Raw<T, E> hr[V], yr[V];
+        Raw<P, E> wpost[V], wgate[V], wpre[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = col0 + i * STRIDE;
+            hr[i] = load_cols<T, E, AL>(h, c, dim);
+            if (a.y) yr[i] = load_cols<T, E, AL>(y, c, dim);
+            if (a.gate) wgate[i] = load_cols<P, E, AL>(gate, c, dim);
+            if (a.post) wpost[i] = load_cols<P, E, AL>(post, c, dim);
+            if (a.z) wpre[i] = load_cols<P, E, AL>(pre, c, dim);
+        }
         float x[V][E];
 #pragma unroll
-        for (int i = 0; i < V; ++i) unpack<T, E>(load_cols<T, E, AL>(h, col0 + i * STRIDE, dim), x[i]);
+        for (int i = 0; i < V; ++i) unpack<T, E>(hr[i], x[i]);
         if (a.y) {
-            const T *y = static_cast<const T *>(a.y) + row * a.ldy;
             float u[V][E], s = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                unpack<T, E>(load_cols<T, E, AL>(y, col0 + i * STRIDE, dim), u[i]);
+                unpack<T, E>(yr[i], u[i]);
 #pragma unroll
                 for (int e = 0; e < E; ++e) s = fmaf(u[i][e], u[i][e], s);
             }
@@ -92,26 +108,24 @@ __global__ __launch_bounds__(64 * W * teams<W>()) void block_norm_kernel(BlockNo
                 total(&s, lane, wave);
                 f *= rsqrtf(fmaf(s, inv, a.eps));
             }
-            const P *gate = static_cast<const P *>(a.gate) + (a.gate ? row / per_gate * a.ldg : 0);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int c = col0 + i * STRIDE;
                 float w[E];
 #pragma unroll
                 for (int e = 0; e < E; ++e) u[i][e] *= f;
                 if (a.post) {
-                    unpack<P, E>(load_cols<P, E, AL>(post, c, dim), w);
+                    unpack<P, E>(wpost[i], w);
 #pragma unroll
                     for (int e = 0; e < E; ++e) u[i][e] *= w[e] + a.offset;
                 }
                 if (a.gate) {
-                    unpack<P, E>(load_cols<P, E, AL>(gate, c, dim), w);
+                    unpack<P, E>(wgate[i], w);
 #pragma unroll
                     for (int e = 0; e < E; ++e) u[i][e] *= w[e];
                 }
 #pragma unroll
                 for (int e = 0; e < E; ++e) x[i][e] += u[i][e];
-                store_cols<T, E, AL>(static_cast<T *>(a.h_out) + row * dim, c, dim, pack<T, E>(x[i]));
+                store_cols<T, E, AL>(static_cast<T *>(a.h_out) + row * dim, col0 + i * STRIDE, dim, pack<T, E>(x[i]));
             }
         }
         if (a.z) {
@@ -124,12 +138,11 @@ __global__ __launch_bounds__(64 * W * teams<W>()) void block_norm_kernel(BlockNo
             const float r = rsqrtf(fmaf(s, inv, a.eps));
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int c = col0 + i * STRIDE;
                 float w[E], z[E];
-                unpack<P, E>(load_cols<P, E, AL>(pre, c, dim), w);
+                unpack<P, E>(wpre[i], w);
 #pragma unroll
                 for (int e = 0; e < E; ++e) z[e] = x[i][e] * r * (w[e] + a.offset);
-                store_cols<T, E, AL>(static_cast<T *>(a.z) + row * dim, c, dim, pack<T, E>(z));
+                store_cols<T, E, AL>(static_cast<T *>(a.z) + row * dim, col0 + i * STRIDE, dim, pack<T, E>(z));
             }
         }
     }
@@ -149,10 +162,13 @@ struct Chunks {
 
 Chunks chunks_of(int64_t rows, int64_t gates)
 {
-    constexpr int64_t kMost = 512, kLeast = 8;
+    // two workgroups per compute unit (8192 rows of 2048: 54 us with one of twice
+    // the waves); at least 4 rows each (1501 rows of 1407: 24 us, 26.5 with 8);
+    // and up to 16 rows in one, which takes less than a second launch
+    constexpr int64_t kMost = 512, kLeast = 4, kAlone = 16;
     Chunks c{};
     if (rows == 0) return c;
-    const int64_t want = std::max<int64_t>(kLeast, (rows + kMost - 1) / kMost);
+    const int64_t want = rows <= kAlone ? kAlone : std::max<int64_t>(kLeast, (rows + kMost - 1) / kMost);
     c.per_gate = rows / gates;
     if (c.per_gate < want) {
         c.gates = want / c.per_gate;
@@ -168,7 +184,7 @@ Chunks chunks_of(int64_t rows, int64_t gates)
     return c;
 }
 
-// Teams of a workgroup of the gradient: they take the rows of a chunk (or its
+// Teams of a workgroup of the gradient (eight waves, or one team): they take the rows of a chunk (or its
 // gates' runs of rows) by turns and add up their sums at the end.
 template <int W> constexpr int grad_teams() { return W >= 8 ? 1 : 8 / W; }
 
@@ -177,6 +193,10 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
                                                                                   float *part_post, float *part_gate)
 {
     constexpr int TEAMS = grad_teams<W>(), STRIDE = 64 * W * E, COLS = STRIDE * V;
+    // rows past 8192 columns leave 128 registers to each thread of their 16
+    // waves: nothing is kept there over the rows but the sums (which spill all the
+    // same; 2048 rows of 16384: 271 us, 1.5 TB/s)
+    constexpr bool LEAN = V * E == 16;
     __shared__ float sh3[TEAMS][2][W][3], sh1[TEAMS][2][W][1];
     __shared__ float sh_sum[TEAMS > 1 ? TEAMS - 1 : 1][TEAMS > 1 ? COLS : 1];
     const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6) % W;
@@ -210,6 +230,7 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = col0 + i * STRIDE;
+        if constexpr (LEAN) continue;
         wpre[i] = a.pre ? load_cols<P, E, AL>(static_cast<const P *>(a.pre), c, dim) : raw_zero<P, E>();
         wpost[i] = a.post ? load_cols<P, E, AL>(static_cast<const P *>(a.post), c, dim) : raw_zero<P, E>();
     }
@@ -218,20 +239,38 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
     auto load = [&](const void *p, int64_t ld, int64_t row, Raw<T, E> *to) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            to[i] = p && row < last ? load_cols<T, E, AL>(static_cast<const T *>(p) + row * ld, col0 + i * STRIDE, dim) : raw_zero<T, E>();
+            to[i] = p && row < last ? load_cols<T, E, AL, true>(static_cast<const T *>(p) + row * ld, col0 + i * STRIDE, dim) : raw_zero<T, E>();
     };
     int64_t row = first + team * run;
-    load(a.h_out, a.ldh, row, x), load(a.dz, a.ldz, row, t), load(a.dh_out, a.ldd, row, d0), load(a.y, a.ldy, row, y);
+    auto load_all = [&](int64_t r) {
+        load(a.h_out, a.ldh, r, x), load(a.dz, a.ldz, r, t), load(a.dh_out, a.ldd, r, d0), load(a.y, a.ldy, r, y);
+    };
+    if constexpr (!LEAN) load_all(row);
+    auto weight = [&](const void *p, const Raw<P, E> &kept, int i, float *w) {
+        if constexpr (LEAN) {
+            if (p) unpack<P, E>(load_cols<P, E, AL>(static_cast<const P *>(p), col0 + i * STRIDE, dim), w);
+            else unpack<P, E>(raw_zero<P, E>(), w);
+        } else unpack<P, E>(kept, w);
+    };
     int64_t in_run = 0;
     for (int64_t step = 0; step < steps; ++step) {
         const bool there = row < last;
+        if constexpr (LEAN) load_all(row);
+        Raw<P, E> wgate[V];
+        auto load_gate = [&](int i) {
+            wgate[i] = load_cols<P, E, AL>(static_cast<const P *>(a.gate) + gate_row * a.ldg, col0 + i * STRIDE, dim);
+        };
+        if constexpr (!LEAN)
+            if (a.gate && there)
+#pragma unroll
+                for (int i = 0; i < V; ++i) load_gate(i);
         int64_t next = row + 1;
         if (++in_run == run) in_run = 0, next = row + 1 + (TEAMS - 1) * run;
         float s[3] = {0.0f, 0.0f, 0.0f};    // of h'^2, v h', y^2
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float w[E], xf[E], tf[E], yf[E];
-            unpack<P, E>(wpre[i], w);
+            weight(a.pre, wpre[i], i, w);
             unpack<T, E>(x[i], xf), unpack<T, E>(t[i], tf), unpack<T, E>(y[i], yf);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -248,7 +287,7 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
             float w[E], xf[E], tf[E];
             unpack<T, E>(d0[i], d[i]);
             if (a.dz) {
-                unpack<P, E>(wpre[i], w);
+                weight(a.pre, wpre[i], i, w);
                 unpack<T, E>(x[i], xf), unpack<T, E>(t[i], tf);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
@@ -260,9 +299,8 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
             if (there) store_cols<T, E, AL>(static_cast<T *>(a.dh) + row * dim, col0 + i * STRIDE, dim, pack<T, E>(d[i]));
         }
         // the next row's, while this one's second half runs
-        load(a.h_out, a.ldh, next, x), load(a.dz, a.ldz, next, t), load(a.dh_out, a.ldd, next, d0);
+        if constexpr (!LEAN) load(a.h_out, a.ldh, next, x), load(a.dz, a.ldz, next, t), load(a.dh_out, a.ldd, next, d0);
         if (a.y) {
-            const P *gate = static_cast<const P *>(a.gate) + gate_row * a.ldg;
             const float ry = a.post ? rsqrtf(fmaf(s[2], inv, a.eps)) : 1.0f;
             float sw = 0.0f;
 #pragma unroll
@@ -270,9 +308,12 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
                 float g[E], p[E], yf[E];
 #pragma unroll
                 for (int e = 0; e < E; ++e) g[e] = 1.0f, p[e] = 1.0f;
-                if (a.gate && there) unpack<P, E>(load_cols<P, E, AL>(gate, col0 + i * STRIDE, dim), g);
+                if (a.gate && there) {
+                    if constexpr (LEAN) load_gate(i);
+                    unpack<P, E>(wgate[i], g);
+                }
                 if (a.post) {
-                    unpack<P, E>(wpost[i], p);
+                    weight(a.post, wpost[i], i, p);
 #pragma unroll
                     for (int e = 0; e < E; ++e) p[e] += a.offset;
                 }
@@ -312,13 +353,13 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
                 if (a.gate) gate_row += TEAMS;
             }
         }
-        load(a.y, a.ldy, next, y);
+        if constexpr (!LEAN) load(a.y, a.ldy, next, y);
         row = next;
     }
 
     // the chunk's sums, the teams' in their order
-    auto finish = [&](float (*sum)[E], float *part) {
-        if (!part) return;
+    auto finish = [&](float (*sum)[E], float *part, void *out) {
+        if (ch.chunks == 1 ? !out : !part) return;
         if constexpr (TEAMS > 1) {
             __syncthreads();
             if (team > 0)
@@ -337,11 +378,13 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
         }
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            store_cols<float, E, AL>(part + (int64_t)blockIdx.x * dim, col0 + i * STRIDE, dim, pack<float, E>(sum[i]));
+            if (ch.chunks == 1) store_cols<P, E, AL>(static_cast<P *>(out), col0 + i * STRIDE, dim, pack<P, E>(sum[i]));
+            else store_cols<float, E, AL>(part + (int64_t)blockIdx.x * dim, col0 + i * STRIDE, dim, pack<float, E>(sum[i]));
     };
-    finish(dpre, part_pre);
-    finish(dpost, part_post);
-    finish(dgate, part_gate);
+    // (one chunk alone is all there is to add; gates of its own it has written)
+    finish(dpre, part_pre, a.dpre);
+    finish(dpost, part_post, a.dpost);
+    finish(dgate, part_gate, ch.gates ? nullptr : a.dgate);
 }
 
 // out[g][c] = sum over the chunks g * cuts .. of part[chunk][c], in order within
@@ -397,15 +440,18 @@ template <typename T, typename P, int E, int W, int V, bool AL> struct Backward 
         const Chunks ch = chunks_of(a.rows, a.gates);
         const int64_t part = ch.chunks * a.dim;
         float *at = a.partials, *pre = nullptr, *post = nullptr, *gate = nullptr;
-        if (a.dpre) pre = at, at += part;
-        if (a.dpost) post = at, at += part;
-        if (a.dgate && !ch.gates) gate = at;
+        if (ch.chunks > 1) {
+            if (a.dpre) pre = at, at += part;
+            if (a.dpost) post = at, at += part;
+            if (a.dgate && !ch.gates) gate = at;
+        }
         if (ch.chunks) {
             block_norm_grad_kernel<T, P, E, W, V, AL><<<(unsigned)ch.chunks, 64 * W * grad_teams<W>(), 0, stream>>>(a, ch, pre, post, gate);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
         const bool gates = a.dgate && !ch.gates;
+        if (ch.chunks == 1) return hipSuccess;      // that workgroup wrote them
         if (!a.dpre && !a.dpost && !gates) return hipSuccess;
         const ColumnSums c{{pre, post, gate}, {a.dpre, a.dpost, gates ? a.dgate : nullptr}, {ch.chunks, ch.chunks, ch.cuts},
                            {1, 1, a.gates}, (int)a.dim};
@@ -415,18 +461,19 @@ template <typename T, typename P, int E, int W, int V, bool AL> struct Backward 
     }
 };
 
-// The smallest team that holds a row in 16 elements per thread.
-template <template <typename, typename, int, int, int, bool> class Go, typename T, typename P, bool AL, typename A>
+// The smallest team that holds a row in `held` elements per thread.
+template <template <typename, typename, int, int, int, bool> class Go, typename T, typename P, bool AL, int HELD, typename A>
 hipError_t by_width(const A &a, hipStream_t stream)
 {
-    constexpr int E = 16 / (int)sizeof(T), V = 16 / E;
+    constexpr int E = 16 / (int)sizeof(T), V = HELD / E, W0 = 64 * HELD;
     const int64_t dim = a.dim;
-    if (dim <= 64 * E) return Go<T, P, E, 1, 1, AL>::run(a, stream);
-    if (dim <= 1024) return Go<T, P, E, 1, V, AL>::run(a, stream);
-    if (dim <= 2048) return Go<T, P, E, 2, V, AL>::run(a, stream);
-    if (dim <= 4096) return Go<T, P, E, 4, V, AL>::run(a, stream);
-    if (dim <= 8192) return Go<T, P, E, 8, V, AL>::run(a, stream);
-    return Go<T, P, E, 16, V, AL>::run(a, stream);
+    if (V > 1 && dim <= 64 * E) return Go<T, P, E, 1, 1, AL>::run(a, stream);
+    if (dim <= W0) return Go<T, P, E, 1, V, AL>::run(a, stream);
+    if (dim <= 2 * W0) return Go<T, P, E, 2, V, AL>::run(a, stream);
+    if (dim <= 4 * W0) return Go<T, P, E, 4, V, AL>::run(a, stream);
+    if (dim <= 8 * W0) return Go<T, P, E, 8, V, AL>::run(a, stream);
+    if (dim <= 16 * W0) return Go<T, P, E, 16, V, AL>::run(a, stream);
+    return Go<T, P, E, 16, 16 / E, AL>::run(a, stream);
 }
 
 // Whether all rows start at multiples of 16 bytes and end with a whole piece.
@@ -442,29 +489,31 @@ bool aligned_rows(const BlockNormGradLaunch &a, int e)
            aligned(a.pre) && aligned(a.dh) && aligned(a.dy) && aligned(a.dpost) && aligned(a.dgate) && aligned(a.dpre);
 }
 
-template <template <typename, typename, int, int, int, bool> class Go, typename T, typename P, typename A>
+template <template <typename, typename, int, int, int, bool> class Go, int HELD, typename T, typename P, typename A>
 hipError_t by_alignment(const A &a, hipStream_t stream)
 {
-    return aligned_rows(a, 8) ? by_width<Go, T, P, true>(a, stream) : by_width<Go, T, P, false>(a, stream);
+    return aligned_rows(a, 8) ? by_width<Go, T, P, true, HELD>(a, stream) : by_width<Go, T, P, false, HELD>(a, stream);
 }
 
-template <template <typename, typename, int, int, int, bool> class Go, typename A> hipError_t by_types(const A &a, hipStream_t stream)
+template <template <typename, typename, int, int, int, bool> class Go, int HELD, typename A> hipError_t by_types(const A &a, hipStream_t stream)
 {
     if (a.x_dt == 0)
-        return a.p_dt == 0 ? by_alignment<Go, float, float>(a, stream) : by_alignment<Go, float, bf16_bits>(a, stream);
-    return a.p_dt == 0 ? by_alignment<Go, bf16_bits, float>(a, stream) : by_alignment<Go, bf16_bits, bf16_bits>(a, stream);
+        return a.p_dt == 0 ? by_alignment<Go, HELD, float, float>(a, stream) : by_alignment<Go, HELD, float, bf16_bits>(a, stream);
+    return a.p_dt == 0 ? by_alignment<Go, HELD, bf16_bits, float>(a, stream) : by_alignment<Go, HELD, bf16_bits, bf16_bits>(a, stream);
 }
 
 }  // namespace
 
-hipError_t launch_block_norm(const BlockNormLaunch &a, hipStream_t stream) { return by_types<Forward>(a, stream); }
+hipError_t launch_block_norm(const BlockNormLaunch &a, hipStream_t stream) { return by_types<Forward, 16>(a, stream); }
 
-// A row of fp32 sums for each chunk and each of three parameters.
+// A row of fp32 sums for each chunk and each of three parameters; one chunk alone
+// needs none.
 size_t block_norm_grad_ws_bytes(int64_t rows, int64_t dim, int64_t gates)
 {
-    return (size_t)(3 * chunks_of(rows, gates).chunks * dim) * sizeof(float);
+    const int64_t chunks = chunks_of(rows, gates).chunks;
+    return chunks == 1 ? 0 : (size_t)(3 * chunks * dim) * sizeof(float);
 }
 
-hipError_t launch_block_norm_grad(const BlockNormGradLaunch &a, hipStream_t stream) { return by_types<Backward>(a, stream); }
+hipError_t launch_block_norm_grad(const BlockNormGradLaunch &a, hipStream_t stream) { return by_types<Backward, 8>(a, stream); }
 
 }  // namespace nqk

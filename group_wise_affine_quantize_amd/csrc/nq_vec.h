@@ -2,8 +2,8 @@
 // their size has.  AL: runs start at multiples of 16 bytes (or of their size);
 // without it they only have to be aligned to their elements, which the memory
 // takes as one access all the same (unaligned access is this target's mode), at
-// the price of a second line now and then: rows of 1407 fp32 numbers 12.0 us
-// instead of 13.8 with an access for each element (a gradient's 52 to 26).
+// the price of a second line now and then: 1501 rows of 1407 fp32 numbers 11.4 us
+// instead of 13.8 with an access for each element.
 #pragma once
 
 #include <type_traits>
@@ -24,7 +24,10 @@ template <typename T, int E> struct Raw {
     uint32_t w[words];
 };
 
-template <typename T, int E, bool AL = true> __device__ __forceinline__ Raw<T, E> load_raw(const T *p)
+// ONCE: an access of 16 bytes that is not kept in the caches (where runs are
+// aligned: others share lines with their neighbours, 25 -> 30 us for a gradient
+// of 1501 rows of 1407).
+template <typename T, int E, bool AL = true, bool ONCE = false> __device__ __forceinline__ Raw<T, E> load_raw(const T *p)
 {
     using W4 = std::conditional_t<AL, words4, loose4>;
     using W2 = std::conditional_t<AL, words2, loose2>;
@@ -33,7 +36,9 @@ template <typename T, int E, bool AL = true> __device__ __forceinline__ Raw<T, E
     if constexpr (Raw<T, E>::bytes % 16 == 0) {
 #pragma unroll
         for (int i = 0; i < Raw<T, E>::words / 4; ++i) {
-            const words4 v = reinterpret_cast<const W4 *>(p)[i];
+            words4 v;
+            if constexpr (ONCE && AL) v = __builtin_nontemporal_load(reinterpret_cast<const W4 *>(p) + i);
+            else v = reinterpret_cast<const W4 *>(p)[i];
             r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
         }
     } else if constexpr (Raw<T, E>::bytes == 8) {
@@ -44,15 +49,18 @@ template <typename T, int E, bool AL = true> __device__ __forceinline__ Raw<T, E
     return r;
 }
 
-template <typename T, int E, bool AL = true> __device__ __forceinline__ void store_raw(T *p, const Raw<T, E> &r)
+template <typename T, int E, bool AL = true, bool ONCE = false> __device__ __forceinline__ void store_raw(T *p, const Raw<T, E> &r)
 {
     using W4 = std::conditional_t<AL, words4, loose4>;
     using W2 = std::conditional_t<AL, words2, loose2>;
     using W1 = std::conditional_t<AL, uint32_t, loose1>;
     if constexpr (Raw<T, E>::bytes % 16 == 0) {
 #pragma unroll
-        for (int i = 0; i < Raw<T, E>::words / 4; ++i)
-            reinterpret_cast<W4 *>(p)[i] = words4{r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]};
+        for (int i = 0; i < Raw<T, E>::words / 4; ++i) {
+            const W4 v = words4{r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]};
+            if constexpr (ONCE && AL) __builtin_nontemporal_store(v, reinterpret_cast<W4 *>(p) + i);
+            else reinterpret_cast<W4 *>(p)[i] = v;
+        }
     } else if constexpr (Raw<T, E>::bytes == 8) *reinterpret_cast<W2 *>(p) = words2{r.w[0], r.w[1]};
     else if constexpr (Raw<T, E>::bytes == 4) *reinterpret_cast<W1 *>(p) = r.w[0];
     else *reinterpret_cast<uint16_t *>(p) = (uint16_t)r.w[0];
@@ -111,9 +119,9 @@ template <typename T, int E, bool AL = true> __device__ __forceinline__ void sto
 
 // Columns c .. c + E - 1 of a row of `dim`; what lies behind the row reads as
 // zeros and is not written.  With AL, dim is a multiple of E.
-template <typename T, int E, bool AL> __device__ __forceinline__ Raw<T, E> load_cols(const T *row, int64_t c, int64_t dim)
+template <typename T, int E, bool AL, bool ONCE = false> __device__ __forceinline__ Raw<T, E> load_cols(const T *row, int64_t c, int64_t dim)
 {
-    if (c + E <= dim) return load_raw<T, E, AL>(row + c);
+    if (c + E <= dim) return load_raw<T, E, AL, ONCE>(row + c);
     Raw<T, E> r = raw_zero<T, E>();
     if constexpr (!AL && E > 1) {
 #pragma unroll
@@ -125,9 +133,10 @@ template <typename T, int E, bool AL> __device__ __forceinline__ Raw<T, E> load_
     }
     return r;
 }
-template <typename T, int E, bool AL> __device__ __forceinline__ void store_cols(T *row, int64_t c, int64_t dim, const Raw<T, E> &r)
+template <typename T, int E, bool AL, bool ONCE = false>
+__device__ __forceinline__ void store_cols(T *row, int64_t c, int64_t dim, const Raw<T, E> &r)
 {
-    if (c + E <= dim) store_raw<T, E, AL>(row + c, r);
+    if (c + E <= dim) store_raw<T, E, AL, ONCE>(row + c, r);
     else if constexpr (!AL && E > 1) {
 #pragma unroll
         for (int e = 0; e < E; ++e)

@@ -82,14 +82,14 @@ def test_norm_grad_outputs(lib):
     for bad in (dict(ldd=63), dict(ldz=63)):
         assert norm_grad(lib, **bad) == SHAPE, bad
     for bad in (dict(dh=AT["h"]), dict(dh=AT["dh_out"]), dict(dy=AT["y"]), dict(dy=AT["dz"]), dict(dh=AT["dy"]),
-                dict(dpost=AT["post"]), dict(dgate=AT["dpre"]), dict(dpre=AT["pre"]), dict(ws=AT["h"]), dict(ws=AT["dh"])):
+                dict(dpost=AT["post"]), dict(dgate=AT["dpre"]), dict(dpre=AT["pre"]), dict(rows=80, ws=AT["h"]), dict(rows=80, ws=AT["dh"])):
         assert norm_grad(lib, **bad) == ALIAS, bad
     for name in ("dh", "dy", "dpost", "dgate", "dpre"):
         assert norm_grad(lib, **{name: AT[name] + 1}) == ALIGN, name
-    need = B.nq_block_norm_grad_workspace_bytes(8, 64, 4)
+    need = B.nq_block_norm_grad_workspace_bytes(80, 64, 4)
     assert need > 0
-    assert norm_grad(lib, ws=0) == WORKSPACE and norm_grad(lib, ws_bytes=need - 1) == WORKSPACE
-    assert norm_grad(lib, ws=AT["ws"] + 8) == ALIGN
+    assert norm_grad(lib, rows=80, ws=0) == WORKSPACE and norm_grad(lib, rows=80, ws_bytes=need - 1) == WORKSPACE
+    assert norm_grad(lib, rows=80, ws=AT["ws"] + 8) == ALIGN
     assert B.nq_block_norm_grad_workspace_bytes(0, 64) == 0 and B.nq_block_norm_grad_workspace_bytes(8, 0) == 0
 
 

@@ -193,7 +193,7 @@ def test_norm_forms():
     assert bits_equal(bare[0], grads[0]) and bits_equal(bare[1], grads[1]) and bare[2:] == (None, None, None)
 
 
-@pytest.mark.parametrize("rows,gates", [(700, 0), (700, "channel"), (700, 7), (700, 350), (9000, 3), (9000, 1125), (2048, 2048),
+@pytest.mark.parametrize("rows,gates", [(16, 0), (16, 8), (8, "channel"), (700, 0), (700, "channel"), (700, 7), (700, 350), (9000, 3), (9000, 1125), (2048, 2048),
                                         (17, "channel")])
 def test_norm_parameter_gradients_over_many_rows(rows, gates):
     """Chunks that are parts of a gate's rows, one gate's, or several gates'."""
@@ -525,14 +525,14 @@ def test_other_streams_and_devices():
 
 
 def test_refusals_of_the_binding():
-    h, p = normal(1, (4, 64), "f32"), normal(2, (64,), "f32")
+    h, p, many = normal(1, (4, 64), "f32"), normal(2, (64,), "f32"), normal(1, (40, 64), "f32")
     bad = [lambda: B.nq_block_norm(h, h[:3], pre=p), lambda: B.nq_block_norm(h, h.bfloat16(), pre=p),
            lambda: B.nq_block_norm(h, h, post=p, pre=p.bfloat16()), lambda: B.nq_block_norm(h, h, gate=normal(3, (3, 64), "f32")),
            lambda: B.nq_block_norm(h), lambda: B.nq_block_norm(h, post=p, pre=p), lambda: B.nq_block_norm(h, pre=p, eps=0.0),
            lambda: B.nq_block_norm(h.t(), pre=normal(2, (4,), "f32")), lambda: B.nq_block_norm(h.cpu(), pre=p),
            lambda: B.nq_block_norm(h, h, pre=p, z=h), lambda: B.nq_block_norm(h.half(), pre=p.half()),
            lambda: B.nq_block_norm_grad(h, pre=p), lambda: B.nq_block_norm_grad(h, dz=h, dh=h),
-           lambda: B.nq_block_norm_grad(h, h, h, post=p, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           lambda: B.nq_block_norm_grad(many, many, many, post=p, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
            lambda: B.nq_rope(B.Rope(128), h.view(4, 1, 64), torch.zeros(4, dtype=torch.int32, device="cuda")),
            lambda: B.nq_rope(B.Rope(64), h.view(4, 1, 64), torch.zeros(4, dtype=torch.int64, device="cuda")),
            lambda: B.nq_rope(B.Rope(64, sections=[16, 16]), h.view(4, 1, 64), torch.zeros(4, dtype=torch.int32, device="cuda")),
