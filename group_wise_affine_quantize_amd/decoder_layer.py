@@ -3,11 +3,13 @@
 
     python -m group_wise_affine_quantize_amd.decoder_layer
 
-Every product, the cache, the attention and the routing are libnq calls;
-norms, the position rotation and the activation between the experts' products
-are plain torch.  The demonstration fills the cache with a few prompts of
-uneven lengths, then serves tokens step by step, as a server would: lengths
-grow on the device, and the same tensors describe every step.
+All of it but the activation between the experts' products are libnq calls:
+norms with their residual sums, products, rotary positions, the cache, the
+attention, the routing, and tokens sorted by expert and back.  The
+demonstration fills the cache with a system prompt and a few prompts of uneven
+lengths behind it, then serves tokens step by step, as a server would: lengths
+grow on the device, the same tensors describe every step, and the system
+prompt's keys and values are stored and read once for all sequences.
 """
 import torch
 
@@ -24,6 +26,9 @@ class DecoderLayer:
                  seed=0, device="cuda"):
         self.hidden, self.heads, self.kv_heads, self.head_dim = hidden, heads, kv_heads, head_dim
         self.router = B.MoERouter(experts, top_k, score="softmax", renormalise=True)
+        self.rope = B.Rope(head_dim, theta=10000.0, device=device)
+        self.scale_in = torch.ones(hidden, dtype=torch.bfloat16, device=device)     # the two norms' weights
+        self.scale_mid = torch.ones(hidden, dtype=torch.bfloat16, device=device)
         g = torch.Generator(device=device)
         g.manual_seed(seed)
 
@@ -40,6 +45,7 @@ class DecoderLayer:
     def new_cache(self, blocks, block_tokens=64, format="int8"):
         return B.KVCache(blocks, self.kv_heads, block_tokens, self.head_dim, format)
 
+    # What the calls for norms and positions compute, in plain torch.
     @staticmethod
     def _norm(x):
         f = x.float()
@@ -52,53 +58,67 @@ class DecoderLayer:
         a, b = x.float().split(half, -1)
         return torch.cat([a * angle.cos() - b * angle.sin(), b * angle.cos() + a * angle.sin()], -1).to(x.dtype)
 
-    def forward(self, x, positions, cache, seqs):
-        """x [rows, hidden] bf16, positions [rows] (of each row in its
-        sequence); seqs' lengths already count these rows.  Returns the
-        layer's output and the experts chosen."""
+    def forward(self, x, positions, cache, seqs, prefix=None):
+        """x [rows, hidden] bf16, positions [rows] (of each row in its context);
+        seqs' lengths already count these rows.  prefix: KVSequences of the
+        prefixes that rows share, if any (their tokens come first in positions, and
+        are not counted in seqs).  Returns the layer's output and the experts chosen."""
         rows, h, kv, d = x.shape[0], self.heads, self.kv_heads, self.head_dim
-        fused = B.nq_qmm(self._norm(x), *self.qkv, self.GROUP, self.BITS).view(rows, h + 2 * kv, d)
-        fused[:, : h + kv] = self._rotate(fused[:, : h + kv], positions)
-        q, k, v = fused.split([h, kv, kv], dim=1)       # column ranges: no copies
+        _, z = B.nq_block_norm(x, pre=self.scale_in)
+        fused = B.nq_qmm(z, *self.qkv, self.GROUP, self.BITS).view(rows, h + 2 * kv, d)
+        turned = fused[:, : h + kv]                     # column ranges: no copies
+        B.nq_rope(self.rope, turned, positions.to(torch.int32), out=turned)
+        q, k, v = fused.split([h, kv, kv], dim=1)
         B.nq_kv_append(cache, seqs, k, v)
-        y = B.nq_kv_attention(cache, seqs, q)
-        x = x + B.nq_qmm(y.view(rows, h * d), *self.out, self.GROUP, self.BITS)
+        if prefix is None:
+            y = B.nq_kv_attention(cache, seqs, q)
+        else:
+            y = B.nq_kv_attention_shared(cache, prefix, seqs, q)
+        y = B.nq_qmm(y.view(rows, h * d), *self.out, self.GROUP, self.BITS)
+        x, z = B.nq_block_norm(x, y, pre=self.scale_mid)
 
-        z = self._norm(x)
         logits = B.nq_qmm(z, *self.gate, self.GROUP, self.ROUTER_BITS)
         ids, weights = B.nq_moe_route(self.router, logits)
-        chosen, top_k = ids.view(-1), ids.shape[1]
-        token = torch.arange(rows, device=x.device, dtype=torch.int32).repeat_interleave(top_k)
-        up = B.nq_gather_qmm_lhs(z.view(rows, 1, -1), *self.up, self.GROUP, self.BITS, token, chosen)
+        order = B.nq_moe_sort(ids, self.router.experts)
+        up = B.nq_gather_qmm_lhs(z.view(rows, 1, -1), *self.up, self.GROUP, self.BITS, order.row_token, order.row_expert)
         a, b = up.chunk(2, -1)
         mid = (torch.nn.functional.silu(a.float()) * b.float()).to(x.dtype).contiguous()
-        down = B.nq_gather_qmm(mid, *self.down, self.GROUP, self.BITS, chosen).view(rows, top_k, -1)
-        return x + (down.float() * weights[..., None]).sum(1).to(x.dtype), ids
+        down = B.nq_gather_qmm(mid, *self.down, self.GROUP, self.BITS, order.row_expert)
+        return B.nq_moe_combine(order, down.view(len(down), -1), weights, residual=x), ids
 
 
 def main():
     import time
     layer = DecoderLayer()
-    prompts, steps, block = [700, 33, 1, 410], 32, 64
-    batch, wide = len(prompts), -(-(max(prompts) + steps) // block)
-    cache = layer.new_cache(batch * wide, block)
-    table = torch.randperm(batch * wide, device="cuda").to(torch.int32).view(batch, wide)
+    system, prompts, steps, block = 500, [700, 33, 1, 410], 32, 64
+    batch, wide, shared = len(prompts), -(-(max(prompts) + steps) // block), -(-system // block)
+    cache = layer.new_cache(batch * wide + shared, block)
+    blocks = torch.randperm(batch * wide + shared, device="cuda").to(torch.int32)
+    table, system_table = blocks[shared:].view(batch, wide), blocks[:shared].view(1, shared)
     lengths = torch.tensor(prompts, dtype=torch.int32).cuda()
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32).cuda()
 
+    # the system prompt, once
+    x = torch.randn(system, layer.hidden, device="cuda").to(torch.bfloat16)
+    layer.forward(x, torch.arange(system, device="cuda"), cache,
+                  B.KVSequences(i32([0, system]), i32([system]), system_table, system))
+    # the prompts behind it
     rows = sum(prompts)
-    start = torch.tensor([0] + prompts, dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
-    positions = torch.cat([torch.arange(n) for n in prompts]).cuda()
+    start = i32([0] + prompts).cumsum(0).to(torch.int32)
+    positions = torch.cat([torch.arange(n) for n in prompts]).cuda() + system
     x = torch.randn(rows, layer.hidden, device="cuda").to(torch.bfloat16)
-    y, _ = layer.forward(x, positions, cache, B.KVSequences(start, lengths, table, rows))
-    print(f"{batch} prompts of {prompts} tokens: output {tuple(y.shape)}")
+    prefix = B.KVSequences(i32([0, rows]), i32([system]), system_table, rows)
+    y, _ = layer.forward(x, positions, cache, B.KVSequences(start, lengths, table, rows), prefix)
+    print(f"{batch} prompts of {prompts} tokens behind {system}: output {tuple(y.shape)}")
 
     seqs = B.KVSequences(torch.arange(batch + 1, dtype=torch.int32, device="cuda"), lengths, table, batch)
+    prefix = B.KVSequences(i32([0, batch]), i32([system]), system_table, batch)
     x = y[(start[1:] - 1).long()]       # each sequence's last row
     torch.cuda.synchronize()
     began = time.perf_counter()
     for _ in range(steps):
         lengths += 1
-        x, ids = layer.forward(x, lengths - 1, cache, seqs)
+        x, ids = layer.forward(x, lengths + (system - 1), cache, seqs, prefix)
         x = DecoderLayer._norm(x)       # in the place of the layers and the sampling between
     torch.cuda.synchronize()
     each = (time.perf_counter() - began) / steps
