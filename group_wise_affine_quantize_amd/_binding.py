@@ -1364,8 +1364,8 @@ def _turn(name, rope, x, positions, out, stream, names):
 
 def nq_rope(rope, x, positions, out=None, stream=None):
     """x [rows, heads, head_dim] (f32 or bf16, any row stride, e.g. columns of a
-    fused projection) turned by positions, int32 [axes, rows] (or [rows] with one
-    axis) -> out, dense unless given; out=x turns in place."""
+    fused projection) turned by positions, int32 [axes, rows] (an expanded
+    [rows] too, or [rows] itself with one axis) -> out, dense unless given; out=x turns in place."""
     return _turn("nq_rope", rope, x, positions, out, stream, ("x", "out"))
 
 

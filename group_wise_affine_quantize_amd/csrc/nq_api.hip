@@ -1722,8 +1722,8 @@ static nq_status rope_impl(const char *op, bool back, const nq_rope_plan *plan, 
     const int64_t width = (int64_t)heads * head_dim, xb = dtype_bytes(x_dt);
     if (rows < 0 || rows >= kMaxDim || (rows > 0 && rows > kMaxElems / width))
         return fail(NQ_ERR_SHAPE, "%s: rows=%lld is negative or too large", op, (long long)rows);
-    if (ldp < rows && plan->axes > 1)
-        return fail(NQ_ERR_SHAPE, "%s: axis stride %lld of positions is below rows=%lld", op, (long long)ldp, (long long)rows);
+    if (ldp < 0 || (ldp > 0 && ldp < rows && plan->axes > 1))
+        return fail(NQ_ERR_SHAPE, "%s: axis stride %lld of positions is neither 0 nor at least rows=%lld", op, (long long)ldp, (long long)rows);
     if (ldp > kMaxElems) return fail(NQ_ERR_SHAPE, "%s: axis stride %lld of positions is too large", op, (long long)ldp);
     if (rows == 0) return NQ_OK;
     if (!plan->freq || !positions) return fail(NQ_ERR_NULL, "%s: freq and positions must be non-null", op);

@@ -598,7 +598,8 @@ nq_status nq_moe_route_grad(const nq_moe_router *router, const void *logits, nq_
  * experts, so that each expert's rows are neighbours.  Pair (t, j) has the number
  * t * top_k + j; among pairs of one expert the lower number comes first.  ids
  * [tokens, top_k] as nq_moe_route gives them, or any: an id >= experts is
- * dropped (an expert of another device, say), and dropped pairs come last.
+ * dropped, and dropped pairs come last (a device that has the experts from some
+ * id on subtracts that id, and the unsigned numbers of the others are all too large).
  * Outputs:
  *   starts [experts + 1] int32: expert e has rows starts[e] .. starts[e + 1] - 1;
  *     starts[experts] rows are not dropped;
@@ -606,7 +607,8 @@ nq_status nq_moe_route_grad(const nq_moe_router *router, const void *logits, nq_
  *   row_token, row_expert [tokens * top_k] uint32: each row's token and its id as
  *     it was in ids -- what nq_gather_qmm_lhs takes as lhs_idx and rhs_idx.
  * experts is 1 .. 1024, top_k 1 .. 32, tokens * top_k below 2^31.  tokens == 0
- * writes starts (zeros).  All arrays are 4-byte aligned. */
+ * writes starts (zeros).  All arrays are 4-byte aligned, the workspace (scratch of
+ * one call at a time) 16-byte aligned. */
 size_t nq_moe_sort_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts);
 nq_status nq_moe_sort(const uint32_t *ids, int64_t tokens, int32_t top_k, int32_t experts, int32_t *starts,
                       int32_t *place, uint32_t *row_token, uint32_t *row_expert, void *workspace,
@@ -685,7 +687,7 @@ nq_status nq_block_norm(const nq_block_norm_shape *shape, const void *h, int64_t
  * and dz needs pre.  Parameter gradients are sums over rows in fp32 in a fixed order.
  * rows == 0 writes zeros to the parameters' gradients.  workspace: 16-byte aligned, at
  * least nq_block_norm_grad_workspace_bytes (room for partial sums of all three
- * parameters). */
+ * parameters), scratch of one call at a time. */
 size_t nq_block_norm_grad_workspace_bytes(const nq_block_norm_shape *shape);
 nq_status nq_block_norm_grad(const nq_block_norm_shape *shape, const void *h_out, int64_t ldh, const void *y,
                              int64_t ldy, const void *dh_out, int64_t ldd, const void *dz, int64_t ldz,
@@ -713,7 +715,8 @@ typedef struct {
  * row] (taken in float64), pair (a, b) becomes scale * (a cos t - b sin t) and
  * scale * (b cos t + a sin t); columns from rotary_dim on are copied.  x and out
  * [rows, heads, head_dim] (x_dt) with row strides ldx and ldo in elements;
- * positions [axes, rows] int32 with axis stride ldp, any values.  heads is 1 ..
+ * positions [axes, rows] int32 with axis stride ldp (0: the same positions on
+ * all axes, as text has among images), any values.  heads is 1 ..
  * 65535, head_dim rotary_dim .. 1024.  An axis outside 0 .. axes - 1 turns by
  * nothing.  out may be x itself (with ldo = ldx): heads are then turned in
  * place, e.g. the queries and keys among a fused projection's columns.  Arrays

@@ -108,7 +108,7 @@ def test_rope_arguments(lib, grad):
     assert rope(lib, plan=False, grad=grad) == NULL
     for bad in (dict(layout=0), dict(layout=3), dict(rotary_dim=0), dict(rotary_dim=63), dict(rotary_dim=130), dict(rotary_dim=-2),
                 dict(head_dim=1025, ldx=1 << 20, ldo=1 << 20), dict(axes=0), dict(axes=17), dict(scale=0.0), dict(scale=NAN),
-                dict(heads=0), dict(heads=65536), dict(rows=-1), dict(rows=1 << 31), dict(ldp=7), dict(ldx=639), dict(ldo=639),
+                dict(heads=0), dict(heads=65536), dict(rows=-1), dict(rows=1 << 31), dict(ldp=7), dict(ldp=-1), dict(ldx=639), dict(ldo=639),
                 dict(ldp=1 << 62)):
         assert rope(lib, grad=grad, **bad) == SHAPE, bad
         assert (b"nq_rope_grad" if grad else b"nq_rope:") in lib.nq_last_error()

@@ -66,6 +66,8 @@ CASES = [
     ([90], [2], 1, [3, 20, 7], [30, 20, 7], 6, 2, 256, 32, "int8", "bf16", {"causal": False}),
     ([90], [2], 1, [33, 20, 7], [33, 20, 7], 6, 1, 256, 128, "fp8", "f32", {"causal": False, "scale": 0.2}),
     ([0, 0], [1, 1], 1, [1, 2, 1], [5, 5, 5], 2, 1, 64, 16, "int8", "bf16", {}),
+    ([8000], [2], 0, [1, 1], [40, 7000], 3, 1, 64, 64, "int8", "bf16", {}),                         # over 64 parts of both
+    ([8100], [9], 0, [2] * 9, [(31 * i) % 40 + 2 for i in range(9)], 4, 1, 64, 128, "fp8", "f32", {}),   # the same, of tiles
 ]
 
 

@@ -326,6 +326,13 @@ def test_rope_defaults_and_sections():
     assert B.nq_rope(B.Rope(64), x[:0], pos[:0]).shape == (0, 2, 64)
 
 
+def test_rope_of_the_same_positions_on_all_axes():
+    x, pos = normal(4, (9, 3, 64), "bf16"), torch.arange(9, dtype=torch.int32, device="cuda") * 77
+    rope = B.Rope(64, sections=[16, 8, 8])
+    assert bits_equal(B.nq_rope(rope, x, pos.expand(3, 9)), B.nq_rope(rope, x, torch.stack([pos] * 3)))
+    assert bits_equal(B.nq_rope(rope, x, pos.expand(3, 9)), B.nq_rope(B.Rope(64), x, pos))
+
+
 def test_rope_far_positions_and_odd_axes():
     """The angle is right to 64 bits at both ends of int32; a pair without an axis is not turned."""
     pos = torch.tensor([[2 ** 31 - 1, -2 ** 31, 2 ** 31 - 2, 0]], dtype=torch.int32, device="cuda")
@@ -440,6 +447,42 @@ def test_moving_past_foreign_places():
     within(y, L.moe_combine(f64(ys), there, 12, f64(w)), 4 * U * L.moe_combine(np.abs(f64(ys)), there, 12, np.abs(f64(w))))
     dys, dw = B.nq_moe_combine_grad(order, x, ys, w, dys=torch.full((12, 40), 7.0, device="cuda"))
     assert (dys[[1, 2, 9, 10]] == 7).all() and (dw[torch.from_numpy(~valid).cuda()] == 0).all()
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+def test_rows_past_32_bits():
+    """More than 2^31 elements, and more than 2^32 bytes; what lies behind the offsets equals the same rows alone."""
+    tokens, k, hidden = 70_000, 4, 8192
+    order = B.nq_moe_sort(on_gpu(ids_of(1, tokens, k, 64)), 64)
+    x = torch.empty((tokens, hidden), dtype=torch.bfloat16, device="cuda").normal_()
+    xs = B.nq_moe_dispatch(order, x)
+    assert xs.numel() > 2 ** 31
+    for at in (slice(0, 1000), slice(130_000, 131_000), slice(-1000, None)):
+        assert torch.equal(xs[at], x[order.row_token[at].long()])
+    w = torch.rand((tokens, k), device="cuda")
+    few = torch.randperm(tokens, device="cuda")[:300]
+    rows = xs[order.place[few].view(-1).long()].float().view(300, k, hidden)
+    want = (rows * w[few, :, None]).sum(1)
+    assert (B.nq_moe_combine(order, xs, w)[few].float() - want).abs().max() <= 2.0 ** -7 * want.abs().max()
+    dys, dw = B.nq_moe_combine_grad(order, x, xs, w)
+    assert torch.equal(dys[order.place[few].long()], (w[few, :, None] * x[few, None].float()).to(torch.bfloat16))
+    want = (rows * x[few, None].float()).sum(-1)
+    assert (dw[few] - want).abs().max() <= 1e-5 * want.abs().max()
+    del xs, dys, rows
+    # norms and rotations do not look at other rows: the last ones of many are those of a few
+    h = torch.empty((140_000, 16384), dtype=torch.bfloat16, device="cuda").normal_()
+    p = torch.ones(16384, device="cuda")
+    h_out, z = B.nq_block_norm(h, h, post=p, pre=p)
+    last = B.nq_block_norm(h[-5:], h[-5:], post=p, pre=p)
+    assert bits_equal(h_out[-5:], last[0]) and bits_equal(z[-5:], last[1])
+    del h_out, z
+    dh, dy, *_ = B.nq_block_norm_grad(h, h, h, h, post=p, pre=p)
+    last = B.nq_block_norm_grad(h[-5:], h[-5:], h[-5:], h[-5:], post=p, pre=p)
+    assert bits_equal(dh[-5:], last[0]) and bits_equal(dy[-5:], last[1])
+    del dh, dy
+    rope, pos = B.Rope(128), torch.arange(280_000, dtype=torch.int32, device="cuda")
+    out = B.nq_rope(rope, h.view(280_000, 64, 128), pos)
+    assert bits_equal(out[-5:], B.nq_rope(rope, h.view(280_000, 64, 128)[-5:], pos[-5:]))
 
 
 # ---------------------------------------------------------------- streams, graphs, refusals
