@@ -858,11 +858,11 @@ def nq_kv_attention_shared(cache, prefix, seqs, q, scale=None, causal=True, out=
     else:
         _contig("workspace", workspace)
         ws_bytes = workspace.numel() * workspace.element_size()
-    _one_device(stream, cache.k_codes, prefix.lengths, seqs.lengths, q, out, lse, workspace)
+    on = _launch_on(stream, cache.k_codes, prefix.lengths, seqs.lengths, q, out, lse, workspace)
     status = lib.nq_kv_attention_shared(cache._ref, prefix._ref, seqs._ref, q.data_ptr(), dt, ldq, heads,
                                         cache.head_dim ** -0.5 if scale is None else scale, int(bool(causal)),
                                         out.data_ptr(), _address(lse), _address(workspace), ws_bytes,
-                                        _raw_stream(stream))
+                                        on)
     if status:
         _check(status)
     return out
@@ -980,13 +980,19 @@ def _type(t):
     return _dt(t) if dt is None else dt     # _dt refuses
 
 
-def _one_device(stream, *tensors):
-    """All tensors (None left out) are on the GPU of the call's stream."""
-    at = _torch().cuda.current_device() if stream is None else stream.device.index
+def _launch_on(stream, *tensors):
+    """The handle of the call's stream; all tensors (None left out) are on its GPU."""
+    if stream is not None:
+        at, handle = stream.device.index, stream.cuda_stream
+    else:
+        c = _torch()._C
+        at = c._cuda_getDevice()
+        handle = c._cuda_getCurrentRawStream(at)
     for t in tensors:
         if t is not None and t.get_device() != at:
             raise ValueError(f"a tensor on {t.device} in a call on cuda:{at}; make that device the current one "
                              "or pass a stream of it")
+    return handle
 
 
 def _given(name, t, shape, dtype):
@@ -1079,10 +1085,10 @@ def nq_moe_sort(ids, experts, order=None, workspace=None, stream=None):
     else:
         _contig("workspace", workspace)
         ws_bytes = workspace.numel() * workspace.element_size()
-    _one_device(stream, ids, order.place, workspace)
+    on = _launch_on(stream, ids, order.place, workspace)
     status = lib.nq_moe_sort(ids.data_ptr(), tokens, top_k, experts, order.starts.data_ptr(), order.place.data_ptr(),
                              order.row_token.data_ptr(), order.row_expert.data_ptr(),
-                             None if workspace is None else workspace.data_ptr(), ws_bytes, _raw_stream(stream))
+                             None if workspace is None else workspace.data_ptr(), ws_bytes, on)
     if status:
         _check(status)
     return order
@@ -1099,8 +1105,8 @@ def nq_moe_dispatch(order, x, xs=None, stream=None):
         raise ValueError(f"x must have {order.tokens} rows")
     shape = (tokens * order.top_k, hidden)
     xs = _fresh(stream, x, shape) if xs is None else _given("xs", xs, shape, x.dtype)
-    _one_device(stream, order.place, x, xs)
-    status = lib.nq_moe_dispatch(order._ref, x.data_ptr(), _type(x), ldx, hidden, xs.data_ptr(), _raw_stream(stream))
+    on = _launch_on(stream, order.place, x, xs)
+    status = lib.nq_moe_dispatch(order._ref, x.data_ptr(), _type(x), ldx, hidden, xs.data_ptr(), on)
     if status:
         _check(status)
     return xs
@@ -1120,8 +1126,8 @@ def nq_moe_dispatch_grad(order, dxs, dx=None, stream=None):
     hidden = _expert_rows("dxs", order, dxs)
     shape = (order.tokens, hidden)
     dx = _fresh(stream, dxs, shape) if dx is None else _given("dx", dx, shape, dxs.dtype)
-    _one_device(stream, order.place, dxs, dx)
-    status = lib.nq_moe_dispatch_grad(order._ref, dxs.data_ptr(), _type(dxs), hidden, dx.data_ptr(), _raw_stream(stream))
+    on = _launch_on(stream, order.place, dxs, dx)
+    status = lib.nq_moe_dispatch_grad(order._ref, dxs.data_ptr(), _type(dxs), hidden, dx.data_ptr(), on)
     if status:
         _check(status)
     return dx
@@ -1142,10 +1148,10 @@ def nq_moe_combine(order, ys, weights=None, residual=None, y=None, stream=None):
     shape = (order.tokens, hidden)
     ldr = 0 if residual is None else _matrix("residual", residual, *shape, ys.dtype)
     y = _fresh(stream, ys, shape) if y is None else _given("y", y, shape, ys.dtype)
-    _one_device(stream, order.place, ys, weights, residual, y)
+    on = _launch_on(stream, order.place, ys, weights, residual, y)
     status = lib.nq_moe_combine(order._ref, ys.data_ptr(), _type(ys), hidden, _pair_weights(order, weights),
                                 None if residual is None else residual.data_ptr(), ldr, y.data_ptr(),
-                                _raw_stream(stream))
+                                on)
     if status:
         _check(status)
     return y
@@ -1171,11 +1177,11 @@ def nq_moe_combine_grad(order, dy, ys=None, weights=None, dys=None, dweights=Non
         shape = (tokens, order.top_k)
         dweights = _fresh(stream, dy, shape, torch.float32) if dweights is None else \
             _given("dweights", dweights, shape, torch.float32)
-    _one_device(stream, order.place, dy, ys, weights, dys, dweights)
+    on = _launch_on(stream, order.place, dy, ys, weights, dys, dweights)
     status = lib.nq_moe_combine_grad(order._ref, dy.data_ptr(), _type(dy), ldd, hidden,
                                      None if ys is None else ys.data_ptr(), _pair_weights(order, weights),
                                      dys.data_ptr(), None if dweights is None else dweights.data_ptr(),
-                                     _raw_stream(stream))
+                                     on)
     if status:
         _check(status)
     return dys, dweights
@@ -1234,10 +1240,10 @@ def nq_block_norm(h, y=None, post=None, gate=None, pre=None, scale=1.0, offset=0
         z = _fresh(stream, h, (rows, dim)) if z is None else _given("z", z, (rows, dim), h.dtype)
     elif z is not None:
         raise ValueError("z needs pre")
-    _one_device(stream, h, y, post, gate, pre, h_out, z)
+    on = _launch_on(stream, h, y, post, gate, pre, h_out, z)
     status = lib.nq_block_norm(ctypes.byref(shape), h.data_ptr(), ldh, _address(y), ldy, _type(h), _address(post),
                                _address(gate), ldg, _address(pre), p_dt, _address(h_out), _address(z),
-                               _raw_stream(stream))
+                               on)
     if status:
         _check(status)
     return (h if y is None else h_out), z
@@ -1279,11 +1285,11 @@ def nq_block_norm_grad(h_out, y=None, dh_out=None, dz=None, post=None, gate=None
     else:
         _contig("workspace", workspace)
         ws_bytes = workspace.numel() * workspace.element_size()
-    _one_device(stream, h_out, y, dh_out, dz, post, gate, pre, dh, dy, workspace)
+    on = _launch_on(stream, h_out, y, dh_out, dz, post, gate, pre, dh, dy, workspace)
     status = lib.nq_block_norm_grad(ctypes.byref(shape), h_out.data_ptr(), ldh, _address(y), ldy, _address(dh_out),
                                     ldd, _address(dz), ldz, _type(h_out), _address(post), _address(gate), ldg,
                                     _address(pre), p_dt, dh.data_ptr(), _address(dy), _address(dpost), _address(dgate),
-                                    _address(dpre), _address(workspace), ws_bytes, _raw_stream(stream))
+                                    _address(dpre), _address(workspace), ws_bytes, on)
     if status:
         _check(status)
     return dh, dy, dpost, dgate, dpre
@@ -1354,9 +1360,9 @@ def _turn(name, rope, x, positions, out, stream, names):
         if out.dtype != x.dtype:
             raise TypeError(f"{names[1]} must have {names[0]}'s dtype")
         ldo = _row_stride(names[1], out, rows, heads, dim)
-    _one_device(stream, rope.freq, x, positions, out)
+    on = _launch_on(stream, rope.freq, x, positions, out)
     status = getattr(lib, name)(rope._ref, x.data_ptr(), _type(x), rows, ldx, heads, dim, positions.data_ptr(), ldp,
-                                out.data_ptr(), ldo, _raw_stream(stream))
+                                out.data_ptr(), ldo, on)
     if status:
         _check(status)
     return out
