@@ -43,11 +43,16 @@ __device__ __forceinline__ float2 cos_sin(double t)
     return make_float2(turn == 1 || turn == 2 ? -a : a, turn >= 2 ? -b : b);
 }
 
-// A piece of a head: E columns of both halves, E neighbouring columns that
-// are whole pairs, or E columns that are only copied.
-template <typename T, int E> struct Piece {
-    Raw<T, E> a, b;     // b: of the second half, or a pair's second element
+// How a thread comes by the two elements of a pair.
+enum {
+    kNeighbours,    // the layout of pairs: both lie in its piece of E columns
+    kSwap,          // halves: its piece is of one half, a lane of its wave has the other
+    kBoth,          // halves: it takes a piece of each
 };
+// Writing whole heads in neighbouring lanes is what kSwap is for: the memory
+// moved twice the bytes of kBoth's stores, of which each covers half of every
+// head (8192 rows of 40 heads of 128 in bf16, 168 MB: 57 us, WRITE_SIZE 168 MB for
+// 84).  kBoth is left for single elements and for heads of more than 64 pieces.
 
 // Where a thread is among the pieces of a workgroup's rows: `lanes` threads
 // take the pieces of one head, and heads follow each other over the rows.
@@ -61,63 +66,109 @@ struct Walk {
 
 // A workgroup takes `rows_each` rows.  Its first loads are on their way while
 // the angles are computed, kAhead of them to a thread.
-template <typename T, int E, bool PAIRS, bool AL>
+template <typename T, int E, int HOW, bool AL>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeLaunch a, int64_t row0, int rows_each)
 {
-    constexpr int kAhead = 4, P = E == 1 ? 1 : PAIRS ? E / 2 : E;   // pairs of a piece
-    __shared__ float2 turn[kTurns];
-    const int half = a.rotary >> 1, tid = (int)threadIdx.x;
+    constexpr int kAhead = 4;
+    constexpr int P = HOW != kNeighbours ? E : E == 1 ? 1 : E / 2;      // pairs that a piece has a part in
+    constexpr bool TWO = HOW == kBoth || E == 1;                        // two accesses to a piece
+    __shared__ __align__(16) float2 turn[kTurns];
+    const int half = a.rotary >> 1, tid = (int)threadIdx.x, lane = tid & 63;
     const int64_t first = row0 + (int64_t)blockIdx.x * rows_each;
     const int rows = a.rows - first < rows_each ? (int)(a.rows - first) : rows_each;
     const T *x = static_cast<const T *>(a.x) + first * a.ldx;
     T *out = static_cast<T *>(a.out) + first * a.ldo;
     // pieces of a head: those that turn, then those that are copied
-    const int turning = half / P, per = turning + (a.x == a.out ? 0 : (a.head_dim - a.rotary) / E);
-    const int lanes = per < kThreads ? per : kThreads, side = kThreads / lanes, mine = tid / lanes;
-    Walk w{0, mine, tid - mine * lanes};
+    const int half_pieces = half / P, turning = HOW == kSwap ? 2 * half_pieces : half_pieces;
+    const int per = turning + (a.x == a.out ? 0 : (a.head_dim - a.rotary) / E);
+    // heads that are taken at once; with kSwap no head lies in two waves
+    const int lanes = per < kThreads ? per : kThreads, in_wave = 64 / lanes;
+    const int side = HOW == kSwap ? kThreads / 64 * in_wave : kThreads / lanes;
+    const int at0 = HOW == kSwap ? lane : tid, h0 = at0 / lanes;
+    const bool idle = HOW == kSwap ? h0 >= in_wave : h0 >= side;
+    const int start = at0 - h0 * lanes;
+    Walk w{0, HOW == kSwap ? (tid >> 6) * in_wave + h0 : h0, start};
     w.carry(a.heads);
-    if (mine >= side) w.row = rows;     // no place for another head
-    const int start = w.j;
+    if (idle) w.row = rows;
     auto advance = [&](Walk &v) {
         v.j += lanes;
         if (v.j >= per) v.j = start, v.head += side, v.carry(a.heads);
     };
-    auto load = [&](const Walk &v, Piece<T, E> &p) {
-        if (v.row >= rows) return;
-        const T *at = x + v.row * a.ldx + (int64_t)v.head * a.head_dim;
-        if (v.j >= turning) p.a = load_raw<T, E, AL>(at + a.rotary + (v.j - turning) * E);
-        else if (PAIRS && E > 1) p.a = load_raw<T, E, AL>(at + v.j * E);
-        else if (PAIRS) p.a = load_raw<T, E, AL>(at + 2 * v.j), p.b = load_raw<T, E, AL>(at + 2 * v.j + 1);
-        else p.a = load_raw<T, E, AL>(at + v.j * E), p.b = load_raw<T, E, AL>(at + half + v.j * E);
+    // the columns of a piece (and of its second access)
+    auto column = [&](int j) {
+        if (j >= turning) return a.rotary + (j - turning) * E;
+        return HOW == kNeighbours && E == 1 ? 2 * j : j * E;
     };
-    auto finish = [&](const Walk &v, const Piece<T, E> &p) {
+    const int second = HOW == kNeighbours ? 1 : half;
+    struct Piece {
+        Raw<T, E> a, b;
+    };
+    auto load = [&](const Walk &v, Piece &p) {
         if (v.row >= rows) return;
-        T *at = out + v.row * a.ldo + (int64_t)v.head * a.head_dim;
-        const float2 *t = turn + v.row * half + v.j * P;
-        if (v.j >= turning) store_raw<T, E, AL>(at + a.rotary + (v.j - turning) * E, p.a);
-        else if constexpr (PAIRS && E > 1) {
-            float u[E], r[E];
-            unpack<T, E>(p.a, u);
+        const T *at = x + v.row * a.ldx + (int64_t)v.head * a.head_dim + column(v.j);
+        p.a = load_raw<T, E, AL>(at);
+        if (TWO && v.j < turning) p.b = load_raw<T, E, AL>(at + second);
+    };
+    // The turns of a piece lie apart by the number of pieces, two of them in 16
+    // bytes, so that neighbouring lanes read neighbouring 16 bytes.
+    auto turn_at = [&](int row, int piece, int i) -> float2 * {
+        if constexpr (P == 1) return turn + row * half + piece;
+        else return turn + row * half + 2 * ((i >> 1) * half_pieces + piece) + (i & 1);
+    };
+    const bool power = (half_pieces & (half_pieces - 1)) == 0 && lanes % (2 * half_pieces) == 0;
+    auto finish = [&](const Walk &v, const Piece &p) {
+        Raw<T, E> other = p.a;
+        const bool upper = HOW == kSwap && v.j >= half_pieces;
+        if constexpr (HOW == kSwap) {
+            // for all lanes: a head's lanes are all here or all past the rows
+            const int from = v.j < turning ? (upper ? lane - half_pieces : lane + half_pieces) : lane;
 #pragma unroll
-            for (int e = 0; e < P; ++e) {
-                r[2 * e] = fmaf(u[2 * e], t[e].x, -(u[2 * e + 1] * t[e].y));
-                r[2 * e + 1] = fmaf(u[2 * e + 1], t[e].x, u[2 * e] * t[e].y);
+            for (int i = 0; i < Raw<T, E>::words; ++i) {
+                const float mine = __uint_as_float(p.a.w[i]);
+                other.w[i] = __float_as_uint(power && half_pieces == 8    ? xor_lane<8>(mine, lane)
+                                             : power && half_pieces == 16 ? xor_lane<16>(mine, lane)
+                                             : power && half_pieces == 4  ? xor_lane<4>(mine, lane)
+                                                                          : __shfl(mine, from));
             }
-            store_run<T, E, AL>(at + v.j * E, r);
-        } else {
-            float u[E], z[E], r[E], q[E];
-            unpack<T, E>(p.a, u), unpack<T, E>(p.b, z);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                r[e] = fmaf(u[e], t[e].x, -(z[e] * t[e].y));
-                q[e] = fmaf(z[e], t[e].x, u[e] * t[e].y);
-            }
-            store_run<T, E, AL>(at + (PAIRS ? 2 * v.j : v.j * E), r);
-            store_run<T, E, AL>(at + (PAIRS ? 2 * v.j + 1 : half + v.j * E), q);
         }
+        if (v.row >= rows) return;
+        T *at = out + v.row * a.ldo + (int64_t)v.head * a.head_dim + column(v.j);
+        if (v.j >= turning) {
+            store_raw<T, E, AL>(at, p.a);
+            return;
+        }
+        const int piece = upper ? v.j - half_pieces : v.j;
+        float u[E], z[E], r[E], q[E];
+        unpack<T, E>(p.a, u);
+        if constexpr (HOW == kNeighbours && E > 1) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float2 t = *turn_at(v.row, piece, i);
+                r[2 * i] = fmaf(u[2 * i], t.x, -(u[2 * i + 1] * t.y));
+                r[2 * i + 1] = fmaf(u[2 * i + 1], t.x, u[2 * i] * t.y);
+            }
+        } else if constexpr (HOW == kSwap) {
+            unpack<T, E>(other, z);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float2 t = *turn_at(v.row, piece, i);
+                const float s = z[i] * t.y;
+                r[i] = fmaf(u[i], t.x, upper ? s : -s);
+            }
+        } else {
+            unpack<T, E>(p.b, z);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float2 t = *turn_at(v.row, piece, i);
+                r[i] = fmaf(u[i], t.x, -(z[i] * t.y));
+                q[i] = fmaf(z[i], t.x, u[i] * t.y);
+            }
+            store_run<T, E, AL>(at + second, q);
+        }
+        store_run<T, E, AL>(at, r);
     };
     Walk ahead[kAhead];
-    Piece<T, E> p[kAhead];
+    Piece p[kAhead];
     auto fetch = [&]() {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) ahead[i] = w, load(w, p[i]), advance(w);
@@ -127,10 +178,11 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeLaunch a, int64_t ro
         const int r = i / half, k = i - r * half, ax = a.axis ? a.axis[k] : 0;
         const double pos = (unsigned)ax < (unsigned)a.axes ? (double)a.positions[(int64_t)ax * a.ldp + first + r] : 0.0;
         const float2 t = cos_sin(pos * a.freq[k]);
-        turn[i] = make_float2(t.x * a.cos_scale, t.y * a.sin_scale);
+        *turn_at(r, k / P, k % P) = make_float2(t.x * a.cos_scale, t.y * a.sin_scale);
     }
     lds_barrier();
-    while (ahead[0].row < rows) {
+    // a wave stays until its last lane is done (it swaps with the others)
+    while (__any(ahead[0].row < rows)) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) finish(ahead[i], p[i]);
         fetch();
@@ -139,7 +191,9 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeLaunch a, int64_t ro
 
 template <typename T, int E> hipError_t rope_go(const RopeLaunch &a, bool aligned, hipStream_t stream)
 {
-    const int half = a.rotary / 2, per = a.pairs && E > 1 ? a.head_dim / E : half / E + (a.head_dim - a.rotary) / E;
+    const int half = a.rotary / 2, whole = a.head_dim / E;
+    const int how = a.pairs ? kNeighbours : E > 1 && whole <= 64 ? kSwap : kBoth;
+    const int per = how == kBoth || E == 1 ? half / E + (a.head_dim - a.rotary) / E : whole;
     // rows of a workgroup: about four pieces to a thread, but no fewer than 512 workgroups
     int64_t each = std::max<int64_t>(1, std::min<int64_t>(4 * kThreads / ((int64_t)a.heads * per), kTurns / half));
     each = std::max<int64_t>(1, std::min<int64_t>(each, a.rows / 512));
@@ -147,8 +201,9 @@ template <typename T, int E> hipError_t rope_go(const RopeLaunch &a, bool aligne
     for (int64_t row0 = 0; row0 < a.rows; row0 += most) {
         const unsigned groups = (unsigned)((std::min<int64_t>(most, a.rows - row0) + each - 1) / each);
         auto go = [&](auto kernel) { kernel<<<groups, kThreads, 0, stream>>>(a, row0, (int)each); };
-        if (a.pairs) aligned ? go(rope_kernel<T, E, true, true>) : go(rope_kernel<T, E, true, false>);
-        else aligned ? go(rope_kernel<T, E, false, true>) : go(rope_kernel<T, E, false, false>);
+        if (how == kNeighbours) aligned ? go(rope_kernel<T, E, kNeighbours, true>) : go(rope_kernel<T, E, kNeighbours, false>);
+        else if (how == kBoth) aligned ? go(rope_kernel<T, E, kBoth, true>) : go(rope_kernel<T, E, kBoth, false>);
+        else if constexpr (E > 1) aligned ? go(rope_kernel<T, E, kSwap, true>) : go(rope_kernel<T, E, kSwap, false>);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
