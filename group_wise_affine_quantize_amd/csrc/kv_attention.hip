@@ -491,7 +491,8 @@ struct Found {
     int row;
     uint32_t base, units, ct;       // units before it, of a segment; column tiles
 };
-__device__ __forceinline__ Found find_row(const Pass &p, const KvCache &cache, int group, int row, uint32_t *total)
+// `first`: the lane's sequence of the first 64.
+__device__ __forceinline__ Found find_row(const Pass &p, const KvSeq &first, const KvCache &cache, int group, int row, uint32_t *total)
 {
     const int lane = (int)(threadIdx.x & 63u), batch = p.s.batch;
     Found f{false, 0, 0, 0, 0};
@@ -500,7 +501,7 @@ __device__ __forceinline__ Found find_row(const Pass &p, const KvCache &cache, i
         int r0 = 0, n = 0;
         uint32_t u = 0, c = 0;
         if (b0 + lane < batch) {
-            const KvSeq q = kv_seq(p.s, b0 + lane);
+            const KvSeq q = b0 ? kv_seq(p.s, b0 + lane) : first;
             const int64_t cap = p.s.max_blocks << cache.block_shift, len = q.len < cap ? q.len : cap;
             const int tiles = len > 0 ? (int)((len + 63) >> 6) : 1;
             r0 = (int)q.r0, n = (int)q.n;
@@ -569,10 +570,14 @@ template <int D, typename T> __global__ __launch_bounds__(256 * kSharedRuns) voi
 
     ColumnParts p{0, 0, 0}, o{0, 0, 0};
     if (wave < COLS && at0 + wave < count) {
-        const int row = (int)((at0 + wave) / a.q_heads), head = (int)(at0 + wave - (int64_t)row * a.q_heads);
+        const uint32_t at = (uint32_t)at0 + (uint32_t)wave;     // below 2^30
+        const int row = (int)(at / (uint32_t)a.q_heads), head = (int)at - row * a.q_heads;
         uint32_t its, mine;
-        const Found fp = find_row(J.prefix, a.c, J.group, row, &its);
-        Found fo = find_row(J.own, a.c, J.group, row, &mine);
+        KvSeq qp{0, 0, 0, 0}, qo{0, 0, 0, 0};
+        if (lane < J.prefix.s.batch) qp = kv_seq(J.prefix.s, lane);
+        if (lane < J.own.s.batch) qo = kv_seq(J.own.s, lane);
+        const Found fp = find_row(J.prefix, qp, a.c, J.group, row, &its);
+        Found fo = find_row(J.own, qo, a.c, J.group, row, &mine);
         if (J.joint) fo.base = add_sat(fo.base, its), its = mine = add_sat(its, mine);
         p = parts_of(J.prefix, fp, list_total(its), J.group, a.q_heads, row, head);
         o = parts_of(J.own, fo, list_total(mine), J.group, a.q_heads, row, head);
