@@ -1039,6 +1039,8 @@ class MoEOrder(_Described):
             _contig(name, t)
             if t.dtype != torch.int32 or t.numel() != n:
                 raise ValueError(f"{name} must hold {n} int32 numbers")
+            if t.device != place.device:
+                raise ValueError(f"{name} is not on place's device")
         self._bind(starts, place, row_token, row_expert, *place.shape, starts.numel() - 1)
 
     def _bind(self, starts, place, row_token, row_expert, tokens, top_k, experts):
@@ -1208,7 +1210,12 @@ def _norm_call(like, rows, dim, post, gate, pre, scale, offset, eps):
         else:
             if gate.dim() != 2 or gate.shape[1] != dim:
                 raise ValueError(f"gate must be [{dim}] or [gates, {dim}], got {tuple(gate.shape)}")
-            ldg, gates = _matrix("gate", gate, dtype=dtype), max(1, gate.shape[0])
+            gates = gate.shape[0]
+            if gates == 0:
+                if rows:
+                    raise ValueError("gate has no rows")
+                gates = 1
+            ldg = _matrix("gate", gate, dtype=dtype)
     return _BlockNormStruct(rows, dim, gates, eps, offset, scale), _type(p), ldg
 
 

@@ -549,6 +549,7 @@ __device__ __forceinline__ ColumnParts parts_of(const Pass &p, const Found &f, u
 struct SharedJoin {
     KvAttnLaunch a;
     Pass prefix, own;
+    int64_t first;  // row and head of the launch's first column
     int group;
     bool joint;     // one list: the prefixes' and the sequences' behind them
 };
@@ -567,7 +568,7 @@ template <int D, typename T> __global__ __launch_bounds__(256 * kSharedRuns) voi
     __shared__ int sh_n[COLS];
     __shared__ float4 sh_o[kSharedRuns - 1][256];
     const KvAttnLaunch &a = J.a;
-    const int64_t at0 = (int64_t)blockIdx.x * COLS, count = a.s.rows * a.q_heads;
+    const int64_t at0 = J.first + (int64_t)blockIdx.x * COLS, count = a.s.rows * a.q_heads;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = (int)threadIdx.x & 63;
     const int tid = (int)threadIdx.x & 255, run = (int)threadIdx.x >> 8, c = tid / QUADS, d = (tid % QUADS) * 4;
 
@@ -905,15 +906,21 @@ hipError_t launch_kv_shared(const KvAttnLaunch &a, const KvSeqs &prefix, hipStre
     J.prefix = {prefix, A.few, f.cols, A.unit_shift, A.workers, A.least, A.state_o, A.part_o, A.state_s, A.part_s};
     J.own = {a.s, r.stream ? O.few : 0, 16 * r.ct, O.unit_shift, O.workers, std::max(1u, O.least), O.state_o, O.part_o, O.state_s, O.part_s};
     const int cols = 1024 / (int)D;
-    const unsigned grid = (unsigned)((states + cols - 1) / cols);
-    auto go = [&](auto bf16, auto f32) { (a.x_dt == 0 ? f32 : bf16)<<<grid, 256 * kSharedRuns, 0, stream>>>(J); };
+    const int64_t most = most_workgroups(256 * kSharedRuns) * cols;     // columns of a launch
+    auto go = [&](auto bf16, auto f32) {
+        for (J.first = 0; J.first < (int64_t)states; J.first += most) {
+            const int64_t n = std::min<int64_t>(most, (int64_t)states - J.first);
+            (a.x_dt == 0 ? f32 : bf16)<<<(unsigned)((n + cols - 1) / cols), 256 * kSharedRuns, 0, stream>>>(J);
+            if ((e = hipGetLastError()) != hipSuccess) return;
+        }
+    };
     switch (D) {
     case 64: go(kv_shared_join_kernel<64, bf16_bits>, kv_shared_join_kernel<64, float>); break;
     case 128: go(kv_shared_join_kernel<128, bf16_bits>, kv_shared_join_kernel<128, float>); break;
     case 192: go(kv_shared_join_kernel<192, bf16_bits>, kv_shared_join_kernel<192, float>); break;
     default: go(kv_shared_join_kernel<256, bf16_bits>, kv_shared_join_kernel<256, float>); break;
     }
-    return hipGetLastError();
+    return e;
 }
 
 }  // namespace nqk

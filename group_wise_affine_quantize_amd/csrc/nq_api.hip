@@ -557,7 +557,7 @@ nq_status check_moe_sizes(const char *op, int64_t tokens, int32_t top_k, int32_t
 {
     if (experts < 1 || experts > 1024) return fail(NQ_ERR_SHAPE, "%s: experts=%d is not in 1 .. 1024", op, experts);
     if (top_k < 1 || top_k > 32) return fail(NQ_ERR_SHAPE, "%s: top_k=%d is not in 1 .. 32", op, top_k);
-    if (tokens < 0 || tokens * top_k >= kMaxDim || tokens >= kMaxDim)
+    if (tokens < 0 || tokens >= kMaxDim || tokens * top_k >= kMaxDim)
         return fail(NQ_ERR_SHAPE, "%s: tokens=%lld is negative, or times top_k=%d not below 2^31", op, (long long)tokens, top_k);
     return NQ_OK;
 }
@@ -601,11 +601,12 @@ nq_status check_norm_shape(const char *op, const nq_block_norm_shape *s, int x_d
     if (s->dim < 1 || s->dim > nqk::kNormMaxDim)
         return fail(NQ_ERR_SHAPE, "%s: dim=%lld is not in 1 .. %d", op, (long long)s->dim, nqk::kNormMaxDim);
     if (s->rows < 0 || s->rows >= kMaxDim) return fail(NQ_ERR_SHAPE, "%s: rows=%lld is negative or too large", op, (long long)s->rows);
-    if (s->gates < 1 || s->rows % s->gates)
-        return fail(NQ_ERR_SHAPE, "%s: gates=%lld is not positive or does not divide rows=%lld", op, (long long)s->gates,
+    if (s->gates < 1 || s->gates >= kMaxDim || s->rows % s->gates)
+        return fail(NQ_ERR_SHAPE, "%s: gates=%lld is not positive, too large, or does not divide rows=%lld", op, (long long)s->gates,
                     (long long)s->rows);
-    if (!finite(s->eps) || !(s->eps > 0.0f) || !finite(s->offset) || !finite(s->scale))
-        return fail(NQ_ERR_SHAPE, "%s: eps is not positive, or eps, offset or scale not finite", op);
+    // (the reciprocal square root takes smaller numbers for zeros)
+    if (!finite(s->eps) || !(s->eps >= 0x1p-126f) || !finite(s->offset) || !finite(s->scale))
+        return fail(NQ_ERR_SHAPE, "%s: eps is below 2^-126, or eps, offset or scale not finite", op);
     return NQ_OK;
 }
 

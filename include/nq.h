@@ -668,7 +668,7 @@ nq_status nq_moe_combine_grad(const nq_moe_order *order, const void *dy, nq_dtyp
  * gates), so gates divides rows: 1 for a gate per column, the number of
  * sequences for one per sequence, rows for one per row.  z is made of h_out
  * before its rounding to x_dt.  Squares are summed in fp32: rows past 2^63 give a
- * norm of zero.  eps is positive and finite, offset and scale finite.  Arrays need
+ * norm of zero.  eps is at least 2^-126 and finite, offset and scale finite.  Arrays need
  * only be aligned to their elements; 16-byte aligned rows are moved faster. */
 typedef struct {
     int64_t rows, dim, gates;

@@ -52,6 +52,7 @@ def norm_grad(lib, shape=True, **c):
 def test_norm_shapes_and_inputs(lib, call):
     assert call(lib, shape=False) == NULL
     for bad in (dict(dim=0), dict(dim=16385), dict(rows=-1), dict(rows=1 << 31), dict(gates=0), dict(gates=3), dict(gates=-1),
+                dict(gates=1 << 31, rows=0), dict(eps=1e-38),
                 dict(eps=0.0), dict(eps=-1.0), dict(eps=NAN), dict(eps=INF), dict(offset=INF), dict(scale=NAN),
                 dict(ldh=63), dict(ldy=10), dict(ldg=63), dict(ldh=1 << 31)):
         assert call(lib, **bad) == SHAPE, bad

@@ -23,8 +23,8 @@ def attend(p, prefix, own, q, fill=None, **how):
     return out, lse
 
 
-def check(p, prefix, own, q, out, lse, rows_of=None, scale=None, causal=True):
-    """The roundings, relative: the scores' sums (dim terms) and exponents (24 bits of log2 e * |z|, twice), value scales
+def limits(p, prefix, own, q, scale=None, causal=True):
+    """out and lse in 64 bits, and how far they may be off.  The roundings, relative: the scores' sums (dim terms) and exponents (24 bits of log2 e * |z|, twice), value scales
     of up to 2^120 in the exponent, the weights (2^-12 as fp16, 2^-22 as two of them), sums over the tokens, and three
     more where the two parts join; for fp32 the query's 22 bits.  Weights times value scales end at 2^-37 of the largest."""
     dim, wide = p.host.dim, q.dtype == torch.float32
@@ -35,14 +35,19 @@ def check(p, prefix, own, q, out, lse, rows_of=None, scale=None, causal=True):
     rest = (want["seen"][:, None, None] + 3) * 2.0 ** -24
     bound = (weight + rest) * want["spread"] + np.abs(want["out"]) * (2.0 ** -22 if wide else 2.0 ** -8) + 1e-37
     bound += (want["seen"][:, None] * want["largest"])[..., None] * 2.0 ** -37
+    lse = weight[..., 0] + rest[..., 0] + 2.0 ** -22 * np.abs(np.where(np.isneginf(want["lse"]), 0, want["lse"])) + 2.0 ** -20
+    return want, bound, lse
+
+
+def check(p, prefix, own, q, out, lse, rows_of=None, scale=None, causal=True):
+    want, bound, lim = limits(p, prefix, own, q, scale, causal)
     at = slice(None) if rows_of is None else rows_of
     err = np.abs(out.double().cpu().numpy() - want["out"])[at]
     assert np.all(np.isfinite(err)) and np.all(err <= bound[at]), float((err / bound[at]).max())
     g, w = lse.double().cpu().numpy()[at], want["lse"][at]
     none = np.isneginf(w)
     assert np.array_equal(np.isneginf(g), none)
-    lim = (weight[..., 0] + rest[..., 0])[at] + 2.0 ** -22 * np.abs(np.where(none, 0, w)) + 2.0 ** -20
-    assert np.all(np.abs(g[~none] - w[~none]) <= lim[~none])
+    assert np.all(np.abs(g[~none] - w[~none]) <= lim[at][~none])
 
 
 def starts(counts, first=0):
@@ -220,6 +225,23 @@ def test_serving_steps_replay_from_a_graph():
         s.synchronize()
         assert bits_equal(other, want)
         check(p, ([0, seqs], [1200], table[seqs:]), (starts([1] * seqs), lengths.tolist(), table[:seqs]), q, want, want_lse)
+
+
+def test_more_rows_than_one_launch_has_threads_for():
+    """2^26 rows and heads and some: at 64 threads to each in the join, their threads pass 32 bits."""
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of memory")
+    n, heads, period = (1 << 20) + 8, 64, 7
+    p, table = filled(97, "int8", 16, 64, 1, [70, 1])
+    some = rows(98, period, heads, 64, "bf16")
+    q = some[torch.arange(n, device="cuda") % period]
+    prefix, own = ([0, n], [70], table[:1]), ([0, n], [0], table[1:])
+    out, lse = attend(p, prefix, own, q, fill=7.0)
+    want, bound, lim = limits(p, ([0, period], *prefix[1:]), ([0, period], *own[1:]), some)
+    want, bound, want_lse, lim = (torch.tensor(t, device="cuda") for t in (want["out"], bound, want["lse"], lim))
+    for at in torch.arange(n, device="cuda").split(1 << 17):
+        which = at % period
+        assert ((out[at] - want[which]).abs() <= bound[which]).all() and ((lse[at] - want_lse[which]).abs() <= lim[which]).all()
 
 
 def test_empty_calls_and_refusals():

@@ -571,6 +571,7 @@ def test_refusals_of_the_binding():
     h, p, many = normal(1, (4, 64), "f32"), normal(2, (64,), "f32"), normal(1, (40, 64), "f32")
     bad = [lambda: B.nq_block_norm(h, h[:3], pre=p), lambda: B.nq_block_norm(h, h.bfloat16(), pre=p),
            lambda: B.nq_block_norm(h, h, post=p, pre=p.bfloat16()), lambda: B.nq_block_norm(h, h, gate=normal(3, (3, 64), "f32")),
+           lambda: B.nq_block_norm(h, h, gate=normal(3, (3, 64), "f32")[:0]), lambda: B.nq_block_norm(h, pre=p, eps=1e-39),
            lambda: B.nq_block_norm(h), lambda: B.nq_block_norm(h, post=p, pre=p), lambda: B.nq_block_norm(h, pre=p, eps=0.0),
            lambda: B.nq_block_norm(h.t(), pre=normal(2, (4,), "f32")), lambda: B.nq_block_norm(h.cpu(), pre=p),
            lambda: B.nq_block_norm(h, h, pre=p, z=h), lambda: B.nq_block_norm(h.half(), pre=p.half()),
