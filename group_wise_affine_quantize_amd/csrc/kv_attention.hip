@@ -555,8 +555,9 @@ struct SharedJoin {
 };
 
 // Joins the two passes' parts of each row and head: the prefix's, then the
-// sequence's own, each in the order of the tokens.  A workgroup takes 1024 / D
-// neighbouring heads and rows.  A wave to a column finds its parts and their
+// sequence's own, each in the order of the tokens, with four threads for
+// every 16 bytes of O: 64 rows of 32 heads of 128, two or more parts to each, 33.5 MB of them: 11.5
+// us; 4 rows, 6.6 us of dependent loads.  A workgroup takes 1024 / D neighbouring heads and rows.  A wave to a column finds its parts and their
 // factors, 64 at a time; then four runs of threads take turns at them.
 constexpr int kSharedRuns = 4;
 template <int D, typename T> __global__ __launch_bounds__(256 * kSharedRuns) void kv_shared_join_kernel(SharedJoin J)

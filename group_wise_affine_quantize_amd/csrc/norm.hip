@@ -20,9 +20,10 @@
 // statistics and sums are fp32.
 //
 // What bounds it: memory, 4 moves of a row forward and 6 backward.  8191 rows of
-// 4096 in bf16: 43 to 47 us, 5.7 to 6.2 TB/s; the gradient of 8192 rows of 2048
-// 50 us, 4.1 TB/s, of which 4 are the sums over the chunks: 30 vector instructions
-// for each element, 13 us of them, and what is exchanged over a row's waves.
+// 4096 in bf16: 40 to 44 us, 6.1 to 6.7 TB/s (some of the rows lie in the last
+// cache); the gradient of 8192 rows of 2048 42 to 50 us, 4.1 to 4.8 TB/s, and 4.6 for the
+// sums over the chunks: 30 vector instructions for each element, 13 us of them,
+// and what is exchanged over a row's waves.
 #include <algorithm>
 
 #include "nq_kv.h"

