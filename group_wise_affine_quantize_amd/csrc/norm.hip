@@ -195,11 +195,13 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
 {
     constexpr int TEAMS = grad_teams<W>(), STRIDE = 64 * W * E, COLS = STRIDE * V;
     // rows past 8192 columns leave 128 registers to each thread of their 16
-    // waves: nothing is kept there over the rows but the sums (which spill all the
-    // same; 2048 rows of 16384: 271 us, 1.5 TB/s)
+    // waves: nothing is kept there over the rows but dpre's sums, the others'
+    // are in LDS, each thread's columns its own (2048 rows of 16384 in bf16: 274 us with
+    // all in registers, of which 127 spilled; 146 so, with 12)
     constexpr bool LEAN = V * E == 16;
     __shared__ float sh3[TEAMS][2][W][3], sh1[TEAMS][2][W][1];
     __shared__ float sh_sum[TEAMS > 1 ? TEAMS - 1 : 1][TEAMS > 1 ? COLS : 1];
+    __shared__ float4 sh_own[LEAN ? 2 : 1][LEAN ? V * E / 4 : 1][LEAN ? 64 * W : 1];     // dpost, dgate
     const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6) % W;
     const int team = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) / W);
     TeamSum<W, 3> total3{sh3[team], 0};
@@ -222,11 +224,27 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
     const int64_t steps = ((last - first) / run + TEAMS - 1) / TEAMS * run;
     int64_t gate_row = a.gate ? (ch.gates ? first / ch.per_gate + team : first / ch.per_gate) : 0;
 
-    float dpre[V][E], dpost[V][E], dgate[V][E];
+    constexpr int HELD = LEAN ? 1 : V;      // pieces of dpost and dgate in registers
+    float dpre[V][E], dpost[HELD][E], dgate[HELD][E];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int e = 0; e < E; ++e) dpre[i][e] = dpost[i][e] = dgate[i][e] = 0.0f;
+        for (int e = 0; e < E; ++e) dpre[i][e] = dpost[i % HELD][e] = dgate[i % HELD][e] = 0.0f;
+    auto get_own = [&](int which, int i, float *v) {
+#pragma unroll
+        for (int q = 0; q < E / 4; ++q) {
+            const float4 s = sh_own[which][i * (E / 4) + q][threadIdx.x];
+            v[4 * q] = s.x, v[4 * q + 1] = s.y, v[4 * q + 2] = s.z, v[4 * q + 3] = s.w;
+        }
+    };
+    auto put_own = [&](int which, int i, const float *v) {
+#pragma unroll
+        for (int q = 0; q < E / 4; ++q)
+            sh_own[which][i * (E / 4) + q][threadIdx.x] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    };
+    if constexpr (LEAN)
+#pragma unroll
+        for (int i = 0; i < V; ++i) put_own(0, i, dpost[0]), put_own(1, i, dgate[0]);
     Raw<P, E> wpre[V], wpost[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -319,15 +337,17 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
                     for (int e = 0; e < E; ++e) p[e] += a.offset;
                 }
                 unpack<T, E>(y[i], yf);
+                if constexpr (LEAN) get_own(0, i, dpost[0]), get_own(1, i, dgate[0]);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const float yh = yf[e] * ry, sd = a.scale * d[i][e];
                     const float du = sd * g[e];
-                    dgate[i][e] = fmaf(sd, yh * p[e], dgate[i][e]);
-                    dpost[i][e] = fmaf(du, yh, dpost[i][e]);
+                    dgate[i % HELD][e] = fmaf(sd, yh * p[e], dgate[i % HELD][e]);
+                    dpost[i % HELD][e] = fmaf(du, yh, dpost[i % HELD][e]);
                     d[i][e] = du * p[e];
                     sw = fmaf(d[i][e], yf[e], sw);
                 }
+                if constexpr (LEAN) put_own(0, i, dpost[0]), put_own(1, i, dgate[0]);
             }
             float ky = 0.0f;
             if (a.post) {
@@ -345,12 +365,17 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
             if (ch.gates && in_run == 0) {
                 if (a.dgate && there)
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        store_cols<P, E, AL>(static_cast<P *>(a.dgate) + gate_row * dim, col0 + i * STRIDE, dim, pack<P, E>(dgate[i]));
+                    for (int i = 0; i < V; ++i) {
+                        if constexpr (LEAN) get_own(1, i, dgate[0]);
+                        store_cols<P, E, AL>(static_cast<P *>(a.dgate) + gate_row * dim, col0 + i * STRIDE, dim, pack<P, E>(dgate[i % HELD]));
+                    }
 #pragma unroll
-                for (int i = 0; i < V; ++i)
+                for (int i = 0; i < HELD; ++i)
 #pragma unroll
                     for (int e = 0; e < E; ++e) dgate[i][e] = 0.0f;
+                if constexpr (LEAN)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) put_own(1, i, dgate[0]);
                 if (a.gate) gate_row += TEAMS;
             }
         }
@@ -359,7 +384,7 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
     }
 
     // the chunk's sums, the teams' in their order
-    auto finish = [&](float (*sum)[E], float *part, void *out) {
+    auto finish = [&](float (*sum)[E], int own, float *part, void *out) {
         if (ch.chunks == 1 ? !out : !part) return;
         if constexpr (TEAMS > 1) {
             __syncthreads();
@@ -378,14 +403,20 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
                     for (int e = 0; e < E; ++e) sum[i][e] += sh_sum[k][col0 + i * STRIDE + e];
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (ch.chunks == 1) store_cols<P, E, AL>(static_cast<P *>(out), col0 + i * STRIDE, dim, pack<P, E>(sum[i]));
-            else store_cols<float, E, AL>(part + (int64_t)blockIdx.x * dim, col0 + i * STRIDE, dim, pack<float, E>(sum[i]));
+        for (int i = 0; i < V; ++i) {
+            float v[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = sum[LEAN && own >= 0 ? 0 : i][e];
+            if constexpr (LEAN)
+                if (own >= 0) get_own(own, i, v);
+            if (ch.chunks == 1) store_cols<P, E, AL>(static_cast<P *>(out), col0 + i * STRIDE, dim, pack<P, E>(v));
+            else store_cols<float, E, AL>(part + (int64_t)blockIdx.x * dim, col0 + i * STRIDE, dim, pack<float, E>(v));
+        }
     };
     // (one chunk alone is all there is to add; gates of its own it has written)
-    finish(dpre, part_pre, a.dpre);
-    finish(dpost, part_post, a.dpost);
-    finish(dgate, part_gate, ch.gates ? nullptr : a.dgate);
+    finish(dpre, -1, part_pre, a.dpre);
+    finish(dpost, 0, part_post, a.dpost);
+    finish(dgate, 1, part_gate, ch.gates ? nullptr : a.dgate);
 }
 
 // out[g][c] = sum over the chunks g * cuts .. of part[chunk][c], in order within
