@@ -150,6 +150,8 @@ NORMS = [
     (5, 16384, "bf16", "bf16", True, 5, True),
     (4, 16384, "f32", "f32", True, "channel", True),
     (3, 16383, "bf16", "f32", True, 3, True),
+    (40, 9001, "f32", "bf16", True, 8, True),
+    (24, 16384, "bf16", "f32", True, 2, True),
 ]
 
 
