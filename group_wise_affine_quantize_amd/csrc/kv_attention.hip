@@ -110,10 +110,21 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
             if (++b >= a.s.batch + (SHARED ? A.pre.batch : 0)) return;
             s = stream_seq<SHARED>(A, b, COLS);
         }
-        const uint32_t seg = inside / s.units, unit0 = inside - seg * s.units;
+        const uint32_t span = SHARED ? s.slots : s.units;
+        const uint32_t seg = inside / span, slot0 = inside - seg * span;
         const int head = (int)(seg / s.ct);
         const int ctile = (int)(seg - (uint32_t)head * s.ct);
-        const uint32_t units = s.units - unit0 < left ? s.units - unit0 : left;
+        const uint32_t slots = span - slot0 < left ? span - slot0 : left;
+        uint32_t unit0 = slot0, units = slots;
+        if (SHARED) {       // what lies behind the slots of no units
+            unit0 = slot0 < A.extra ? 0u : slot0 - A.extra;
+            units = slot0 + slots < A.extra ? 0u : slot0 + slots - A.extra - unit0;
+            if (units == 0) {
+                left -= slots;
+                inside += slots;
+                continue;
+            }
+        }
         const bool whole = units == s.units;
         const int tile0 = (int)(unit0 << A.unit_shift);
         const int tile1 = unit0 + units == s.units ? s.nt : (int)((unit0 + units) << A.unit_shift);
@@ -380,8 +391,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
             }
         }
         __syncthreads();
-        left -= units;
-        inside += units;
+        left -= slots;
+        inside += slots;
     }
 }
 
@@ -492,7 +503,7 @@ struct ColumnParts {
 struct Found {
     bool has;
     int row;
-    uint32_t base, units, ct;       // units before it, of a segment; column tiles
+    uint32_t base, slots, ct;       // slots before it, of a segment; column tiles
 };
 // `first`: the lane's sequence of the first 64.
 __device__ __forceinline__ Found find_row(const Pass &p, const KvSeq &first, const KvCache &cache, int group, int row, uint32_t *total)
@@ -508,7 +519,7 @@ __device__ __forceinline__ Found find_row(const Pass &p, const KvSeq &first, con
             const int64_t cap = p.s.max_blocks << cache.block_shift, len = q.len < cap ? q.len : cap;
             const int tiles = len > 0 ? (int)((len + 63) >> 6) : 1;
             r0 = (int)q.r0, n = (int)q.n;
-            u = (uint32_t)(tiles + (1 << p.unit_shift) - 1) >> p.unit_shift;
+            u = ((uint32_t)(tiles + (1 << p.unit_shift) - 1) >> p.unit_shift) + p.extra;
             c = n * group <= p.few ? (uint32_t)(n * group + p.cols - 1) / (uint32_t)p.cols : 0u;
         }
         const uint32_t work = c * u * (uint32_t)cache.kv_heads, upto = wave_scan32_sat(work);
@@ -517,14 +528,14 @@ __device__ __forceinline__ Found find_row(const Pass &p, const KvSeq &first, con
             const int at = __ffsll((unsigned long long)has) - 1;
             auto get = [&](uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, at); };
             f.has = true, f.row = row - (int)get((uint32_t)r0);
-            f.base = add_sat(*total, get(upto - work)), f.units = get(u), f.ct = get(c);
+            f.base = add_sat(*total, get(upto - work)), f.slots = get(u), f.ct = get(c);
         }
         *total = add_sat(*total, (uint32_t)__builtin_amdgcn_readlane((int)upto, 63));
     }
     return f;
 }
 
-// The parts of a row and head, in a list of `total` units.
+// The parts of a row and head, in a list of `total` slots.
 __device__ __forceinline__ ColumnParts parts_of(const Pass &p, const Found &f, uint32_t total, int group, int q_heads, int row, int head)
 {
     ColumnParts c{0, 0, 0};
@@ -534,12 +545,12 @@ __device__ __forceinline__ ColumnParts parts_of(const Pass &p, const Found &f, u
     const uint32_t share = list_share(total, (uint32_t)p.workers, p.least);
     const int kv_head = head / group, col = f.row * group + (head - kv_head * group);
     const uint32_t tile = (uint32_t)col / (uint32_t)p.cols, i = (uint32_t)col - tile * (uint32_t)p.cols;
-    const uint64_t off = (uint64_t)f.base + (uint64_t)((uint32_t)kv_head * f.ct + tile) * f.units;
-    if (off + f.units > total) {      // past the list's end: not done
+    const uint64_t off = (uint64_t)f.base + (uint64_t)((uint32_t)kv_head * f.ct + tile) * f.slots;
+    if (off + f.slots > total) {      // past the list's end: not done
         c.parts = 0;
         return c;
     }
-    const uint32_t w0 = (uint32_t)off / share, w1 = (uint32_t)(off + f.units - 1) / share;
+    const uint32_t w0 = ((uint32_t)off + p.extra) / share, w1 = (uint32_t)(off + f.slots - 1) / share;
     c.parts = (int)(w1 - w0) + 1;
     c.rest = (int)(w0 * 2 * (uint32_t)p.cols + i);
     if (c.parts > 1) c.first = c.rest + p.cols;
@@ -751,23 +762,32 @@ hipError_t stream_dims(const AttnArgs &A, int groups, hipStream_t stream)
     }
 }
 
+// What a segment costs a workgroup besides its tiles, in tiles: a pass behind
+// shared prefixes counts it in its list, so that workgroups with many short
+// segments end when the others do (16 sequences of 64 tokens and 8 heads behind four
+// prefixes of 16000 in one launch: 95 us at 0, 50 at 2, 42 at 4, 43 at 8; three
+// prefixes' tiles for 40 sequences of 3 drafts, 83, 79, 77 and 77).  The segments of
+// one prefix alone are as long as each other, and often whole numbers of shares, which
+// it would spoil (64 sequences behind 16384 tokens 65 -> 69 us).
+constexpr int kSegmentTiles = 4;
+
 // Units of one tile, unless the list could then pass 32 bits.  Only sequences
 // with rows have segments: with rows * q_heads below 2^30 there are fewer
 // than 2^31, and the loop ends, at the latest where each is one unit.
-int unit_shift_of(const KvAttnLaunch &a, int cols, int64_t tiles)
+int unit_shift_of(const KvAttnLaunch &a, int cols, int64_t tiles, int extra = 0)
 {
     const double segments = ((double)a.s.rows * (a.q_heads / a.c.kv_heads) / cols +
                              (double)std::min<int64_t>(a.s.batch, a.s.rows)) * a.c.kv_heads;
     int shift = 0;
-    while (segments * (double)((tiles >> shift) + 1) >= 0x1p31) ++shift;
+    while (segments * (double)((tiles >> shift) + 1 + (extra >> shift)) >= 0x1p31) ++shift;
     return shift;
 }
 
 }  // namespace
 
-// Units that a workgroup takes at least: segments that follow each other cost one
-// 4 us each, and what a segment is cut into is joined in any case (4 sequences
-// of 4 heads behind 700 tokens: 15 us at 1, 28 at 4); but no more than about 64
+
+// Units that a workgroup takes at least: what a segment is cut into is joined
+// in any case (4 sequences of 4 heads behind 700 tokens: 15 us at 1, 28 at 4); but no more than about 64
 // parts (3 sequences of 4 heads over one behind 5k and 21k tokens: 44 us with 331
 // parts, 32 with 83).
 static uint32_t least_of(int64_t tiles, int unit_shift) { return (uint32_t)std::max<int64_t>(1, (tiles >> unit_shift) / 64); }
@@ -785,12 +805,12 @@ static hipError_t launch_route(AttnArgs &A, const Route &r, const KvAttnLaunch &
         const hipError_t e = launch_kv_prefill(A, stream);
         if (e != hipSuccess || !r.stream) return e;
     }
-    A.unit_shift = r.whole ? kWholeShift : unit_shift_of(a, 16 * r.ct, r.tiles);
+    A.unit_shift = r.whole ? kWholeShift : unit_shift_of(a, 16 * r.ct, r.tiles, A.state_s ? kSegmentTiles : 0);
     A.splits = r.tiles > (int64_t)1 << A.unit_shift;
     // at least two tiles for each wave, so that short contexts do not fall into
     // parts that cost more to join than to read
     A.least = A.unit_shift ? 1u : 2u * kWaves;
-    if (A.state_s) A.least = least_of(r.tiles, A.unit_shift);
+    if (A.state_s) A.least = least_of(r.tiles, A.unit_shift), A.extra = kSegmentTiles >> A.unit_shift;
     A.part_s = reinterpret_cast<float4 *>(A.part_o + r.stream_floats);
     return stream_dims(A, r.ct, stream);
 }
@@ -832,16 +852,23 @@ static PrefixRoute prefix_route(const KvAttnLaunch &a, const KvSeqs &prefix, int
 }
 
 // Both passes in one launch of the streaming kernel, over columns as the
-// sequences' own pass has them: where that is streamed and there are few segments
-// in all, so that workgroups rarely have several (16 sequences of 4 heads over 2 behind
-// 700 tokens 35 -> 21 us, behind 16000 53 -> 45; with 320 and more segments
-// it is slower, 74 -> 169 at 640).
+// sequences' own pass has them: where that is streamed, where there are not very many
+// segments, and where a prefix that more columns share is not read again too
+// often.  32 heads of 128 over 8, 1500 own tokens, two launches -> one: 16 sequences
+// behind 5000 tokens 43 -> 29 us (1900 tiles read again), 64 behind 1500 62 -> 46 (2900), 48
+// behind 5000 60 -> 53 (7000), 24 behind 16000 54 -> 55 (10000), 64 behind
+// 16000 81 -> 126 (30000); of 64, 100 of 8 over 2 behind 16000 47 -> 40
+// (12000); of 256, 32 of 16 over 4 behind two of 5000 80 -> 56 (1900).  128 sequences
+// behind 32 prefixes of 1500, 1280 segments, 92 -> 84; 256 behind 64, 2560, 163 -> 168.
 static bool joint_route(const KvAttnLaunch &a, const KvSeqs &prefix, const Route &r)
 {
+    if (!r.stream || r.tile) return false;
     const int64_t group = a.q_heads / a.c.kv_heads, cols = 16 * r.ct;
     const int64_t own = std::min<int64_t>(a.s.batch, a.s.rows), its = std::min<int64_t>(prefix.batch, a.s.rows);
     const int64_t segments = (own + its + 2 * (a.s.rows * group / cols)) * a.c.kv_heads;
-    return r.stream && !r.tile && segments <= 192;
+    const int64_t reads = ((a.s.rows + its - 1) / its * group + cols - 1) / cols;       // of a prefix
+    const int64_t tiles = ((prefix.max_blocks << a.c.block_shift) >> 6) + 1;
+    return segments <= 2048 && (double)((reads - 1) * its * a.c.kv_heads) * (double)tiles * a.c.head_dim <= 0x1p20;
 }
 
 // Workspace: the prefixes' slots and states, the sequences' states, and what
@@ -872,7 +899,8 @@ hipError_t launch_kv_shared(const KvAttnLaunch &a, const KvSeqs &prefix, hipStre
     A.a.s = prefix, A.a.causal = 0, A.a.window = 0, A.a.out = nullptr, A.a.lse = nullptr;
     A.group = a.q_heads / a.c.kv_heads;
     A.few = INT32_MAX, A.workers = f.workers, A.listed = f.tile, A.tile_splits = 1;
-    A.unit_shift = unit_shift_of(A.a, f.cols, tiles);
+    A.unit_shift = unit_shift_of(A.a, f.cols, tiles, kSegmentTiles);
+    if (prefix.batch > 1) A.extra = kSegmentTiles >> A.unit_shift;
     A.part_o = take(f.slots * D), A.part_s = reinterpret_cast<float4 *>(take(f.slots * 4));
     A.state_o = take(states * D), A.state_s = reinterpret_cast<float4 *>(take(states * 4));
     AttnArgs O{};       // the sequences'
@@ -885,11 +913,11 @@ hipError_t launch_kv_shared(const KvAttnLaunch &a, const KvSeqs &prefix, hipStre
         both.s.rows = 2 * a.s.rows, both.s.batch = a.s.batch + prefix.batch;
         O.a = a;
         O.group = A.group, O.few = INT32_MAX, O.workers = kWorkers;
-        O.unit_shift = unit_shift_of(both, f.cols, longer);
+        O.unit_shift = unit_shift_of(both, f.cols, longer, kSegmentTiles), O.extra = kSegmentTiles >> O.unit_shift;
         O.least = least_of(longer, O.unit_shift);
         O.part_o = A.part_o, O.part_s = A.part_s;
         O.pre = prefix, O.pre_o = A.state_o, O.pre_s = A.state_s;
-        A.unit_shift = O.unit_shift, A.least = O.least;
+        A.unit_shift = O.unit_shift, A.least = O.least, A.extra = O.extra;
         e = stream_dims(O, f.groups, stream);
     } else {
         A.least = least_of(tiles, A.unit_shift);
@@ -904,8 +932,8 @@ hipError_t launch_kv_shared(const KvAttnLaunch &a, const KvSeqs &prefix, hipStre
     SharedJoin J;
     J.a = a;
     J.group = A.group, J.joint = joint;
-    J.prefix = {prefix, A.few, f.cols, A.unit_shift, A.workers, A.least, A.state_o, A.part_o, A.state_s, A.part_s};
-    J.own = {a.s, r.stream ? O.few : 0, 16 * r.ct, O.unit_shift, O.workers, std::max(1u, O.least), O.state_o, O.part_o, O.state_s, O.part_s};
+    J.prefix = {prefix, A.few, f.cols, A.unit_shift, A.workers, A.least, A.extra, A.state_o, A.part_o, A.state_s, A.part_s};
+    J.own = {a.s, r.stream ? O.few : 0, 16 * r.ct, O.unit_shift, O.workers, std::max(1u, O.least), O.extra, O.state_o, O.part_o, O.state_s, O.part_s};
     const int cols = 1024 / (int)D;
     const int64_t most = most_workgroups(256 * kSharedRuns) * cols;     // columns of a launch
     auto go = [&](auto bf16, auto f32) {

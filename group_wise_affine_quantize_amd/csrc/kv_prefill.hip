@@ -129,16 +129,16 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
 
     const uint32_t heads = (uint32_t)a.c.kv_heads;
     int head, b, split = 0;
-    uint32_t ctile, worker = 0, inside = 0, total = 0, share = 0, left = 0, unit0 = 0, units = 0;
+    uint32_t ctile, worker = 0, inside = 0, total = 0, share = 0, left = 0, unit0 = 0, units = 0, slots = 0;
     StreamSeq s;
+    auto uniform = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); };
     if (SHARED && A.listed) {
         worker = (blockIdx.x & 7u) * (gridDim.x >> 3) + (blockIdx.x >> 3);
-        b = stream_locate(A, M, [&](uint32_t w) { return worker * w; }, &inside, &total, &share);
+        b = stream_locate<SHARED>(A, M, [&](uint32_t w) { return worker * w; }, &inside, &total, &share);
         if (b < 0) return;
-        auto uniform = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); };
         b = (int)uniform((uint32_t)b), inside = uniform(inside), total = uniform(total), share = uniform(share);
         left = total - worker * share < share ? total - worker * share : share;
-        s = stream_seq(A, b, M);
+        s = stream_seq<SHARED>(A, b, M);
     } else {
         // workgroups of one head follow each other with the number of heads as
         // their distance: with eight heads an XCD keeps to one head's cache
@@ -151,16 +151,26 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
     }
     do {
     if (SHARED && A.listed) {
-        while (inside >= s.work) {      // the next sequence with work
-            inside -= s.work;
-            if (++b >= a.s.batch) return;
-            s = stream_seq(A, b, M);
+        uint32_t seg;
+        for (;;) {
+            while (inside >= s.work) {      // the next sequence with work
+                inside -= s.work;
+                if (++b >= a.s.batch) return;
+                s = stream_seq<SHARED>(A, b, M);
+            }
+            const uint32_t span = uniform(s.slots);
+            seg = inside / span;
+            const uint32_t slot0 = inside - seg * span;
+            slots = span - slot0 < left ? span - slot0 : left;
+            unit0 = slot0 < A.extra ? 0u : slot0 - A.extra;
+            units = slot0 + slots < A.extra ? 0u : slot0 + slots - A.extra - unit0;
+            if (units) break;
+            left -= slots, inside += slots;
+            if (left == 0) return;
         }
-        const uint32_t seg = inside / s.units;
-        unit0 = inside - seg * s.units;
-        units = s.units - unit0 < left ? s.units - unit0 : left;
-        head = (int)(seg / s.ct);
-        ctile = seg - (uint32_t)head * s.ct;
+        const uint32_t ct = uniform(s.ct);
+        head = (int)(seg / ct);
+        ctile = seg - (uint32_t)head * ct;
     }
     const int count = s.n * A.group, col0 = (int)ctile * M, end = col0 + M < count ? col0 + M : count;
     const Column c0 = column(A, s, col0, head), c1 = column(A, s, end - 1, head);
@@ -450,8 +460,8 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
             if (h == 0) (whole ? A.state_s : A.part_s)[at] = make_float4(ref, sum, lref, 0.0f);
         }
         if (!A.listed) return;
-        left -= units;
-        inside += units;
+        left -= slots;
+        inside += slots;
         continue;
     }
     if (mine.row < 0) return;

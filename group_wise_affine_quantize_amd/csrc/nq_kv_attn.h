@@ -83,7 +83,7 @@ struct Pass {
     int few;                    // sequences of more columns lie by row and head
     int cols;                   // query columns of a segment
     int unit_shift, workers;
-    uint32_t least;
+    uint32_t least, extra;
     const float *state_o, *part_o;      // [rows][q_heads][D], [workers * 2][cols][D]
     const float4 *state_s, *part_s;     // [rows][q_heads], [workers * 2][cols] of R, L, U
 };
@@ -106,6 +106,7 @@ struct AttnArgs {
     float *state_o;             // or null
     float4 *state_s;
     bool listed;
+    uint32_t extra;             // units that stand for what a segment costs besides its own
     // Both passes in one launch of the streaming kernel: the prefixes come first
     // in its list, and leave their states here.
     KvSeqs pre;                 // batch 0: none
@@ -124,7 +125,8 @@ struct StreamSeq {
     int t0, nt;             // first tile, tiles (at least one)
     uint32_t ct;            // column tiles
     uint32_t units;         // per segment
-    uint32_t work;          // units of all segments
+    uint32_t slots;         // the same, with A.extra before them
+    uint32_t work;          // slots of all segments
     bool prefix;            // rows see all of its tokens
 };
 
@@ -148,7 +150,8 @@ template <bool SHARED = false> __device__ __forceinline__ StreamSeq stream_seq(c
     s.nt = s.hi > s.lo ? ((s.hi + 63) >> 6) - s.t0 : 1;
     s.ct = s.prefix || s.n * A.group <= A.few ? (uint32_t)(s.n * A.group + cols - 1) / (uint32_t)cols : 0u;
     s.units = (uint32_t)(s.nt + (1 << A.unit_shift) - 1) >> A.unit_shift;
-    s.work = s.ct * s.units * (uint32_t)a.c.kv_heads;
+    s.slots = s.units + (SHARED ? A.extra : 0u);
+    s.work = s.ct * s.slots * (uint32_t)a.c.kv_heads;
     return s;
 }
 

@@ -73,6 +73,11 @@ CASES = [
     ([0, 0], [1, 1], 1, [1, 2, 1], [5, 5, 5], 2, 1, 64, 16, "int8", "bf16", {}),
     ([8000], [2], 0, [1, 1], [40, 7000], 3, 1, 64, 64, "int8", "bf16", {}),                         # over 64 parts of both
     ([8100], [9], 0, [2] * 9, [(31 * i) % 40 + 2 for i in range(9)], 4, 1, 64, 128, "fp8", "f32", {}),   # the same, of tiles
+    # more segments than one launch takes for both passes: prefixes by tiles, one of them and three, and streamed
+    ([2100], [200], 0, [1] * 200, [(11 * i) % 130 + 1 for i in range(200)], 32, 8, 64, 64, "int8", "bf16", {}),
+    ([900, 0, 3000], [70, 60, 90], 5, [1] * 225, [(13 * i) % 1200 + 1 for i in range(225)], 32, 8, 64, 128, "fp8", "f32", {}),
+    ([(97 * i) % 400 for i in range(40)], [6] * 40, 10, [1] * 250, [(17 * i) % 200 for i in range(250)], 16, 8, 64, 16, "int8", "f32", {}),
+    ([1300, 70, 2], [90, 1, 90], 0, [1] * 181, [(29 * i) % 900 + 1 for i in range(181)], 32, 8, 128, 32, "int8", "bf16", {}),
 ]
 
 
