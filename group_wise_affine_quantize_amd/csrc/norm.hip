@@ -28,6 +28,7 @@
 
 #include "nq_kv.h"
 #include "nq_layer.h"
+#include "nq_norm_chunks.h"
 #include "nq_tiles.h"
 #include "nq_vec.h"
 
@@ -147,42 +148,6 @@ __global__ __launch_bounds__(64 * W * teams<W>()) void block_norm_kernel(BlockNo
             }
         }
     }
-}
-
-// How the gradient's rows are dealt to workgroups.  Rows that share a gate are
-// kept together: where they are fewer than a chunk, a chunk is some whole
-// gates' rows and adds their gate gradients itself; where they are more, each
-// gate's rows are cut into `cuts` chunks.
-struct Chunks {
-    int64_t chunks;     // workgroups
-    int64_t per_gate;   // rows that share a gate
-    int64_t gates;      // gates of a chunk (0: the chunk is a part of one)
-    int64_t cuts;       // chunks of a gate
-    int64_t size;       // rows of a chunk
-};
-
-Chunks chunks_of(int64_t rows, int64_t gates)
-{
-    // two workgroups per compute unit (8192 rows of 2048: 54 us with one of twice
-    // the waves); at least 4 rows each (1501 rows of 1407: 24 us, 26.5 with 8);
-    // and up to 16 rows in one, which takes less than a second launch
-    constexpr int64_t kMost = 512, kLeast = 4, kAlone = 16;
-    Chunks c{};
-    if (rows == 0) return c;
-    const int64_t want = rows <= kAlone ? kAlone : std::max<int64_t>(kLeast, (rows + kMost - 1) / kMost);
-    c.per_gate = rows / gates;
-    if (c.per_gate < want) {
-        c.gates = want / c.per_gate;
-        c.cuts = 1;
-        c.size = c.gates * c.per_gate;
-        c.chunks = (gates + c.gates - 1) / c.gates;
-    } else {
-        c.cuts = (c.per_gate + want - 1) / want;
-        c.size = (c.per_gate + c.cuts - 1) / c.cuts;
-        c.cuts = (c.per_gate + c.size - 1) / c.size;
-        c.chunks = gates * c.cuts;
-    }
-    return c;
 }
 
 // Teams of a workgroup of the gradient (eight waves, or one team): they take the rows of a chunk (or its
@@ -383,9 +348,10 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
         row = next;
     }
 
-    // the chunk's sums, the teams' in their order
-    auto finish = [&](float (*sum)[E], int own, float *part, void *out) {
-        if (ch.chunks == 1 ? !out : !part) return;
+    // the chunk's sums, the teams' in their order: to `part`, or where that is
+    // null and the chunk is all there is to add to `out`
+    auto finish = [&](float (*sum)[E], int own, float *part, P *out) {
+        if (!part && !out) return;
         if constexpr (TEAMS > 1) {
             __syncthreads();
             if (team > 0)
@@ -409,14 +375,14 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
             for (int e = 0; e < E; ++e) v[e] = sum[LEAN && own >= 0 ? 0 : i][e];
             if constexpr (LEAN)
                 if (own >= 0) get_own(own, i, v);
-            if (ch.chunks == 1) store_cols<P, E, AL>(static_cast<P *>(out), col0 + i * STRIDE, dim, pack<P, E>(v));
-            else store_cols<float, E, AL>(part + (int64_t)blockIdx.x * dim, col0 + i * STRIDE, dim, pack<float, E>(v));
+            if (part) store_cols<float, E, AL>(part + (int64_t)blockIdx.x * dim, col0 + i * STRIDE, dim, pack<float, E>(v));
+            else store_cols<P, E, AL>(out, col0 + i * STRIDE, dim, pack<P, E>(v));
         }
     };
-    // (one chunk alone is all there is to add; gates of its own it has written)
-    finish(dpre, -1, part_pre, a.dpre);
-    finish(dpost, 0, part_post, a.dpost);
-    finish(dgate, 1, part_gate, ch.gates ? nullptr : a.dgate);
+    finish(dpre, -1, part_pre, static_cast<P *>(a.dpre));
+    finish(dpost, 0, part_post, static_cast<P *>(a.dpost));
+    // (gates of its own the chunk has written)
+    finish(dgate, 1, part_gate, ch.gates || !a.dgate ? nullptr : static_cast<P *>(a.dgate) + gate_row * dim);
 }
 
 // out[g][c] = sum over the chunks g * cuts .. of part[chunk][c], in order within
@@ -469,20 +435,21 @@ template <typename T, typename P, int E, int W, int V, bool AL> struct Forward {
 template <typename T, typename P, int E, int W, int V, bool AL> struct Backward {
     static hipError_t run(const BlockNormGradLaunch &a, hipStream_t stream)
     {
-        const Chunks ch = chunks_of(a.rows, a.gates);
+        const Chunks ch = norm_chunks(a.rows, a.gates, norm_grad_teams(a.dim));
         const int64_t part = ch.chunks * a.dim;
         float *at = a.partials, *pre = nullptr, *post = nullptr, *gate = nullptr;
+        // a gate's chunk alone writes its gradient itself
+        const bool gates = a.dgate && !ch.gates && (ch.cuts > 1 || ch.chunks == 0);
         if (ch.chunks > 1) {
             if (a.dpre) pre = at, at += part;
             if (a.dpost) post = at, at += part;
-            if (a.dgate && !ch.gates) gate = at;
+            if (gates) gate = at;
         }
         if (ch.chunks) {
             block_norm_grad_kernel<T, P, E, W, V, AL><<<(unsigned)ch.chunks, 64 * W * grad_teams<W>(), 0, stream>>>(a, ch, pre, post, gate);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
-        const bool gates = a.dgate && !ch.gates;
         if (ch.chunks == 1) return hipSuccess;      // that workgroup wrote them
         if (!a.dpre && !a.dpost && !gates) return hipSuccess;
         const ColumnSums c{{pre, post, gate}, {a.dpre, a.dpost, gates ? a.dgate : nullptr}, {ch.chunks, ch.chunks, ch.cuts},
@@ -542,7 +509,7 @@ hipError_t launch_block_norm(const BlockNormLaunch &a, hipStream_t stream) { ret
 // needs none.
 size_t block_norm_grad_ws_bytes(int64_t rows, int64_t dim, int64_t gates)
 {
-    const int64_t chunks = chunks_of(rows, gates).chunks;
+    const int64_t chunks = norm_chunks(rows, gates, norm_grad_teams(dim)).chunks;
     return chunks == 1 ? 0 : (size_t)(3 * chunks * dim) * sizeof(float);
 }
 
