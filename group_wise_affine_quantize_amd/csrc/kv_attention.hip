@@ -117,8 +117,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
         const uint32_t slots = span - slot0 < left ? span - slot0 : left;
         uint32_t unit0 = slot0, units = slots;
         if (SHARED) {       // what lies behind the slots of no units
-            unit0 = slot0 < A.extra ? 0u : slot0 - A.extra;
-            units = slot0 + slots < A.extra ? 0u : slot0 + slots - A.extra - unit0;
+            const ListUnits u = list_units(slot0, slots, A.extra);
+            unit0 = u.first, units = u.count;
             if (units == 0) {
                 left -= slots;
                 inside += slots;
@@ -363,7 +363,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void kv_stream_kerne
         }
         const Column c = column(A, s, ctile * COLS + col, head);
         if (turn == 0 && c.row >= 0) {
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0);
+            const int64_t slot = list_place(blockIdx.x, unit0 == 0);
             float l = sh_l[0][col];
             for (int w = 1; w < TL; ++w) l += sh_l[w][col];
             if (SHARED && whole) {
@@ -505,12 +505,16 @@ struct Found {
     int row;
     uint32_t base, slots, ct;       // slots before it, of a segment; column tiles
 };
+// What a pass's share of its list goes by: its slots, and the units of its longest segment.
+struct ListSize {
+    uint32_t total, longest;
+};
 // `first`: the lane's sequence of the first 64.
-__device__ __forceinline__ Found find_row(const Pass &p, const KvSeq &first, const KvCache &cache, int group, int row, uint32_t *total)
+__device__ __forceinline__ Found find_row(const Pass &p, const KvSeq &first, const KvCache &cache, int group, int row, ListSize *size)
 {
     const int lane = (int)(threadIdx.x & 63u), batch = p.s.batch;
     Found f{false, 0, 0, 0, 0};
-    *total = 0;
+    uint32_t total = 0, longest = 0;
     for (int b0 = 0; b0 < batch; b0 += 64) {
         int r0 = 0, n = 0;
         uint32_t u = 0, c = 0;
@@ -519,8 +523,10 @@ __device__ __forceinline__ Found find_row(const Pass &p, const KvSeq &first, con
             const int64_t cap = p.s.max_blocks << cache.block_shift, len = q.len < cap ? q.len : cap;
             const int tiles = len > 0 ? (int)((len + 63) >> 6) : 1;
             r0 = (int)q.r0, n = (int)q.n;
-            u = ((uint32_t)(tiles + (1 << p.unit_shift) - 1) >> p.unit_shift) + p.extra;
+            u = (uint32_t)(tiles + (1 << p.unit_shift) - 1) >> p.unit_shift;
             c = n * group <= p.few ? (uint32_t)(n * group + p.cols - 1) / (uint32_t)p.cols : 0u;
+            if (c && u > longest) longest = u;
+            u += p.extra;
         }
         const uint32_t work = c * u * (uint32_t)cache.kv_heads, upto = wave_scan32_sat(work);
         const uint64_t has = __ballot(row >= r0 && row < r0 + n);
@@ -528,32 +534,28 @@ __device__ __forceinline__ Found find_row(const Pass &p, const KvSeq &first, con
             const int at = __ffsll((unsigned long long)has) - 1;
             auto get = [&](uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, at); };
             f.has = true, f.row = row - (int)get((uint32_t)r0);
-            f.base = add_sat(*total, get(upto - work)), f.slots = get(u), f.ct = get(c);
+            f.base = add_sat(total, get(upto - work)), f.slots = get(u), f.ct = get(c);
         }
-        *total = add_sat(*total, (uint32_t)__builtin_amdgcn_readlane((int)upto, 63));
+        total = add_sat(total, (uint32_t)__builtin_amdgcn_readlane((int)upto, 63));
     }
+    *size = {total, wave_max32(longest)};
     return f;
 }
 
-// The parts of a row and head, in a list of `total` slots.
-__device__ __forceinline__ ColumnParts parts_of(const Pass &p, const Found &f, uint32_t total, int group, int q_heads, int row, int head)
+// The parts of a row and head.
+__device__ __forceinline__ ColumnParts parts_of(const Pass &p, const Found &f, ListSize size, int group, int q_heads, int row, int head)
 {
     ColumnParts c{0, 0, 0};
     if (!f.has) return c;
     c.parts = 1, c.first = row * q_heads + head;
     if (f.ct == 0) return c;
-    const uint32_t share = list_share(total, (uint32_t)p.workers, p.least);
+    const uint32_t total = list_total(size.total), share = list_share(total, (uint32_t)p.workers, list_least(size.longest));
     const int kv_head = head / group, col = f.row * group + (head - kv_head * group);
     const uint32_t tile = (uint32_t)col / (uint32_t)p.cols, i = (uint32_t)col - tile * (uint32_t)p.cols;
-    const uint64_t off = (uint64_t)f.base + (uint64_t)((uint32_t)kv_head * f.ct + tile) * f.slots;
-    if (off + f.slots > total) {      // past the list's end: not done
-        c.parts = 0;
-        return c;
-    }
-    const uint32_t w0 = ((uint32_t)off + p.extra) / share, w1 = (uint32_t)(off + f.slots - 1) / share;
-    c.parts = (int)(w1 - w0) + 1;
-    c.rest = (int)(w0 * 2 * (uint32_t)p.cols + i);
-    if (c.parts > 1) c.first = c.rest + p.cols;
+    const ListParts at = list_segment((uint64_t)f.base + (uint64_t)((uint32_t)kv_head * f.ct + tile) * f.slots, f.slots, p.extra, share, total);
+    c.parts = at.count;         // 0 past the list's end: not done
+    c.rest = (int)(list_place(at.first, false) * (uint32_t)p.cols + i);
+    if (c.parts > 1) c.first = (int)(list_place(at.first, true) * (uint32_t)p.cols + i);
     return c;
 }
 
@@ -588,15 +590,18 @@ template <int D, typename T> __global__ __launch_bounds__(256 * kSharedRuns) voi
     if (wave < COLS && at0 + wave < count) {
         const uint32_t at = (uint32_t)at0 + (uint32_t)wave;     // below 2^30
         const int row = (int)(at / (uint32_t)a.q_heads), head = (int)at - row * a.q_heads;
-        uint32_t its, mine;
+        ListSize its, mine;
         KvSeq qp{0, 0, 0, 0}, qo{0, 0, 0, 0};
         if (lane < J.prefix.s.batch) qp = kv_seq(J.prefix.s, lane);
         if (lane < J.own.s.batch) qo = kv_seq(J.own.s, lane);
         const Found fp = find_row(J.prefix, qp, a.c, J.group, row, &its);
         Found fo = find_row(J.own, qo, a.c, J.group, row, &mine);
-        if (J.joint) fo.base = add_sat(fo.base, its), its = mine = add_sat(its, mine);
-        p = parts_of(J.prefix, fp, list_total(its), J.group, a.q_heads, row, head);
-        o = parts_of(J.own, fo, list_total(mine), J.group, a.q_heads, row, head);
+        if (J.joint) {
+            fo.base = add_sat(fo.base, its.total);
+            its = mine = {add_sat(its.total, mine.total), its.longest > mine.longest ? its.longest : mine.longest};
+        }
+        p = parts_of(J.prefix, fp, its, J.group, a.q_heads, row, head);
+        o = parts_of(J.own, fo, mine, J.group, a.q_heads, row, head);
         if (o.parts == 0) p.parts = 0;      // a row that no sequence has is left alone
     }
     const int parts = p.parts + o.parts;
@@ -785,13 +790,6 @@ int unit_shift_of(const KvAttnLaunch &a, int cols, int64_t tiles, int extra = 0)
 
 }  // namespace
 
-
-// Units that a workgroup takes at least: what a segment is cut into is joined
-// in any case (4 sequences of 4 heads behind 700 tokens: 15 us at 1, 28 at 4); but no more than about 64
-// parts (3 sequences of 4 heads over one behind 5k and 21k tokens: 44 us with 331
-// parts, 32 with 83).
-static uint32_t least_of(int64_t tiles, int unit_shift) { return (uint32_t)std::max<int64_t>(1, (tiles >> unit_shift) / 64); }
-
 // The kernels over a.s.  `A` comes zeroed, or with a pass's states set.
 static hipError_t launch_route(AttnArgs &A, const Route &r, const KvAttnLaunch &a, hipStream_t stream)
 {
@@ -810,7 +808,7 @@ static hipError_t launch_route(AttnArgs &A, const Route &r, const KvAttnLaunch &
     // at least two tiles for each wave, so that short contexts do not fall into
     // parts that cost more to join than to read
     A.least = A.unit_shift ? 1u : 2u * kWaves;
-    if (A.state_s) A.least = least_of(r.tiles, A.unit_shift), A.extra = kSegmentTiles >> A.unit_shift;
+    if (A.state_s) A.extra = kSegmentTiles >> A.unit_shift;
     A.part_s = reinterpret_cast<float4 *>(A.part_o + r.stream_floats);
     return stream_dims(A, r.ct, stream);
 }
@@ -914,13 +912,11 @@ hipError_t launch_kv_shared(const KvAttnLaunch &a, const KvSeqs &prefix, hipStre
         O.a = a;
         O.group = A.group, O.few = INT32_MAX, O.workers = kWorkers;
         O.unit_shift = unit_shift_of(both, f.cols, longer, kSegmentTiles), O.extra = kSegmentTiles >> O.unit_shift;
-        O.least = least_of(longer, O.unit_shift);
         O.part_o = A.part_o, O.part_s = A.part_s;
         O.pre = prefix, O.pre_o = A.state_o, O.pre_s = A.state_s;
-        A.unit_shift = O.unit_shift, A.least = O.least, A.extra = O.extra;
+        A.unit_shift = O.unit_shift, A.extra = O.extra;
         e = stream_dims(O, f.groups, stream);
     } else {
-        A.least = least_of(tiles, A.unit_shift);
         e = f.tile ? launch_kv_prefill(A, stream) : stream_dims(A, f.groups, stream);
         if (e != hipSuccess) return e;
         KvAttnLaunch own = a;
@@ -932,8 +928,8 @@ hipError_t launch_kv_shared(const KvAttnLaunch &a, const KvSeqs &prefix, hipStre
     SharedJoin J;
     J.a = a;
     J.group = A.group, J.joint = joint;
-    J.prefix = {prefix, A.few, f.cols, A.unit_shift, A.workers, A.least, A.extra, A.state_o, A.part_o, A.state_s, A.part_s};
-    J.own = {a.s, r.stream ? O.few : 0, 16 * r.ct, O.unit_shift, O.workers, std::max(1u, O.least), O.extra, O.state_o, O.part_o, O.state_s, O.part_s};
+    J.prefix = {prefix, A.few, f.cols, A.unit_shift, A.workers, A.extra, A.state_o, A.part_o, A.state_s, A.part_s};
+    J.own = {a.s, r.stream ? O.few : 0, 16 * r.ct, O.unit_shift, O.workers, O.extra, O.state_o, O.part_o, O.state_s, O.part_s};
     const int cols = 1024 / (int)D;
     const int64_t most = most_workgroups(256 * kSharedRuns) * cols;     // columns of a launch
     auto go = [&](auto bf16, auto f32) {

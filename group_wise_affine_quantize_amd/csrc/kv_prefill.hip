@@ -162,8 +162,8 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
                 seg = inside / span;
                 const uint32_t slot0 = inside - seg * span;
                 slots = span - slot0 < left ? span - slot0 : left;
-                unit0 = slot0 < A.extra ? 0u : slot0 - A.extra;
-                units = slot0 + slots < A.extra ? 0u : slot0 + slots - A.extra - unit0;
+                const ListUnits u = list_units(slot0, slots, A.extra);
+                unit0 = u.first, units = u.count;
                 if (units) break;
                 left -= slots, inside += slots;
                 if (left == 0) return;
@@ -449,7 +449,7 @@ __global__ __launch_bounds__(Shape<D>::THREADS) void kv_tile_kernel(AttnArgs A)
             if (mine.row >= 0) {
                 const bool whole = !A.listed || units == s.units;
                 const int64_t at = whole ? (int64_t)mine.row * a.q_heads + mine.head
-                                         : (2 * (int64_t)worker + (unit0 == 0 ? 1 : 0)) * M + wave * 32 + r;
+                                         : (int64_t)list_place(worker, unit0 == 0) * M + wave * 32 + r;
                 float *po = (whole ? A.state_o : A.part_o) + at * D;
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt)

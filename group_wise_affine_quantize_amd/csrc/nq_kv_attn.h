@@ -83,7 +83,7 @@ struct Pass {
     int few;                    // sequences of more columns lie by row and head
     int cols;                   // query columns of a segment
     int unit_shift, workers;
-    uint32_t least, extra;
+    uint32_t extra;
     const float *state_o, *part_o;      // [rows][q_heads][D], [workers * 2][cols][D]
     const float4 *state_s, *part_s;     // [rows][q_heads], [workers * 2][cols] of R, L, U
 };
@@ -101,6 +101,7 @@ struct AttnArgs {
     int tile_splits;    // parts that the tile kernel cuts a segment's tokens into
     unsigned tile_bound;    // tile kernel: column tiles at most, over all sequences
     uint32_t least;         // units of the list that a workgroup takes at least
+                            // (behind shared prefixes: list_least)
     // a pass of attention behind shared prefixes: where whole segments leave
     // their states (see Pass), and whether the tile kernel runs over the list
     float *state_o;             // or null
@@ -293,12 +294,6 @@ __device__ __forceinline__ float out_factor(float l, float m, float u, int count
 // log of the sum of weights l over 2^u: -infinity for none, NaN for a NaN.
 __device__ __forceinline__ float log_sum(float l, float u) { return l == 0.0f ? kNegInf : (u + fast_log2(l)) * kLn2; }
 
-// Units per worker.
-__device__ __forceinline__ uint32_t share_of(const AttnArgs &A, uint32_t total)
-{
-    return list_share(total, (uint32_t)A.workers, A.least);
-}
-
 // Finds the sequence of unit `at(share)` of the list: its number (-1: past the
 // list's end), the unit's number inside it, the list's length and the share.
 template <bool SHARED = false, typename At>
@@ -306,21 +301,27 @@ __device__ __forceinline__ int stream_locate(const AttnArgs &A, int cols, At at,
                                              uint32_t *share)
 {
     const int batch = A.a.s.batch + (SHARED ? A.pre.batch : 0), lane = (int)(threadIdx.x & 63u);
-    uint32_t work = lane < batch ? stream_seq<SHARED>(A, lane, cols).work : 0u;     // below 2^31
+    uint32_t longest = 0;       // units of a segment, of this lane's sequences
+    auto work_of = [&](int b) {
+        if (b >= batch) return 0u;
+        const StreamSeq s = stream_seq<SHARED>(A, b, cols);
+        if (SHARED && s.ct && s.units > longest) longest = s.units;
+        return s.work;
+    };
+    uint32_t work = work_of(lane);      // below 2^31
     uint32_t upto = wave_scan32_sat(work);
     uint32_t sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
     *total = sum;
     for (int b = 64 + lane; b - lane < batch; b += 64)
-        *total = add_sat(*total, (uint32_t)__builtin_amdgcn_readlane(
-            (int)wave_scan32_sat(b < batch ? stream_seq<SHARED>(A, b, cols).work : 0u), 63));
+        *total = add_sat(*total, (uint32_t)__builtin_amdgcn_readlane((int)wave_scan32_sat(work_of(b)), 63));
     *total = list_total(*total);
-    *share = share_of(A, *total);
+    *share = list_share(*total, (uint32_t)A.workers, SHARED ? list_least(wave_max32(longest)) : A.least);
     const uint32_t want = at(*share);
     if (want >= *total) return -1;
     uint32_t base = 0;      // at most `want`
     for (int b0 = 0; b0 < batch; b0 += 64) {
         if (b0) {
-            work = b0 + lane < batch ? stream_seq<SHARED>(A, b0 + lane, cols).work : 0u;
+            work = work_of(b0 + lane);
             upto = wave_scan32_sat(work);
             sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
         }

@@ -151,6 +151,19 @@ __device__ __forceinline__ uint32_t wave_scan32_sat(uint32_t v)
     return v;
 }
 
+// The largest of the lanes' numbers, for all lanes.
+__device__ __forceinline__ uint32_t wave_max32(uint32_t v)
+{
+    auto take = [&](int o) { v = (uint32_t)o > v ? (uint32_t)o : v; };
+    take(__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true));
+    take(__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true));
+    take(__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true));
+    take(__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true));
+    take(__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));
+    take(__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
 // Finds, for a wave, which sequence holds item `item` when sequence b has
 // count(b) items, and the item's number in it; -1 when there is none.  Lanes
 // look at 64 sequences at a time.
