@@ -675,7 +675,8 @@ template <int D, typename T> __global__ __launch_bounds__(256 * kSharedRuns) voi
 // there are at most two rows per sequence (then all of them are streamed).
 // One sequence goes by the call's rows, of which it may own any number: the
 // kernel that is launched takes it whatever it owns.  More sequences than a
-// launch of the tile kernel has workgroups for are all streamed too.
+// launch of the tile kernel has workgroups for are all streamed too, and behind shared
+// prefixes batches of few rows to a sequence (list_streams_all).
 constexpr int kFew = 64;
 constexpr int kWholeShift = 4, kWholeTiles = 1 << kWholeShift;
 // The tile kernel over a list of work: one workgroup per compute unit, which
@@ -706,8 +707,7 @@ Route route_of(const KvAttnLaunch &a, bool joined = false)
     else r.stream = r.tile = true, r.few = kFew;
     const int64_t per = std::max<int64_t>(1, (a.s.rows + a.s.batch - 1) / a.s.batch) * group;
     r.ct = per <= 16 ? 1 : per <= 32 ? 2 : 4;
-    // up to 64 columns in the mean: two launches that most often find nothing are saved
-    if (joined && a.s.batch > 1 && per <= kFew) r.stream = true, r.tile = false, r.few = INT32_MAX;
+    if (joined && list_streams_all(a.s.batch, a.s.rows, group)) r.stream = true, r.tile = false, r.few = INT32_MAX;
     const int64_t M = prefill_columns(a), bound = std::min<int64_t>(cols / M + a.s.batch, cols);
     if (r.tile && bound * a.c.kv_heads > most_workgroups(512)) r.stream = true, r.tile = false, r.few = INT32_MAX;
     // Contexts that can have no more than 16 tiles are one unit: four tiles for

@@ -45,3 +45,18 @@ def test_tables_wider_than_their_contexts(prefixes, behind, lengths, new, heads,
         need = B.nq_kv_attention_shared_workspace_bytes(p.dev, *seqs, heads, q.dtype)
         got = attend(p, *wide, q, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
         assert bits_equal(out, got[0]) and bits_equal(lse, got[1])
+
+
+@pytest.mark.parametrize("chunk,singles,heads,kv,dim,block,fmt,dtype", [(300, 120, 16, 1, 64, 32, "int8", "bf16"),
+                                                                      (520, 130, 8, 1, 128, 64, "fp8", "f32")])
+@pytest.mark.parametrize("at", [0, 60])
+def test_a_long_chunk_among_single_tokens(chunk, singles, heads, kv, dim, block, fmt, dtype, at):
+    """Long and short sequences take a kernel each, wherever in the batch the long one is; some rows without a prefix."""
+    n, lengths = [1] * singles, [(7 * i) % 90 + 1 for i in range(singles)]
+    n.insert(at, chunk), lengths.insert(at, chunk + 45)
+    p, table = filled(160, fmt, block, dim, kv, lengths + [500])
+    start = starts(n)
+    q = rows(161, sum(n), heads, dim, dtype, 2.0)
+    prefix, own = ([0, start[singles - 10]], [500], table[-1:]), (start, lengths, table[:-1])
+    out, lse = attend(p, prefix, own, q, fill=7.0)
+    check(p, prefix, own, q, out, lse)

@@ -17,6 +17,7 @@ extern "C" {
 uint32_t total(uint32_t sum) { return nqk::list_total(sum); }
 uint32_t share(uint32_t t, uint32_t w, uint32_t least) { return nqk::list_share(t, w, least); }
 uint32_t least(uint32_t longest) { return nqk::list_least(longest); }
+int streams_all(int64_t batch, int64_t rows, int64_t group) { return nqk::list_streams_all(batch, rows, group); }
 uint32_t place(uint32_t worker, uint32_t first) { return nqk::list_place(worker, first != 0); }
 void units(uint32_t slot0, uint32_t slots, uint32_t extra, uint32_t *out)
 {
@@ -46,6 +47,7 @@ def lst(tmp_path_factory):
     u32, pair = ctypes.c_uint32, ctypes.POINTER(ctypes.c_uint32)
     for name, args in (("total", [u32]), ("share", [u32] * 3), ("least", [u32]), ("place", [u32] * 2)):
         getattr(lib, name).argtypes, getattr(lib, name).restype = args, u32
+    lib.streams_all.argtypes, lib.streams_all.restype = [ctypes.c_int64] * 3, ctypes.c_int
     lib.units.argtypes, lib.units.restype = [u32] * 3 + [pair], None
     lib.segment.argtypes, lib.segment.restype = [ctypes.c_uint64] + [u32] * 4 + [pair], None
     return lib
@@ -147,3 +149,11 @@ def test_shares_go_by_the_longest_segment(lst):
         share = lst.share(total, workers, lst.least(units))
         busy = -(-total // share)
         assert busy >= min(workers, total, 64 * heads) // 2
+
+
+@pytest.mark.parametrize("batch,rows,group,all_streamed", [
+    (4, 20, 4, True), (64, 256, 4, True), (40, 120, 4, True), (64, 63 + 256, 4, True), (256, 255 + 512, 4, True),
+    (257, 256 + 3500, 4, False), (121, 120 + 300, 16, False), (1000, 999 + 5000, 8, False),     # a long chunk among single tokens
+    (4, 200, 4, False), (1, 1, 4, False), (1, 4000, 4, False)])
+def test_a_long_chunk_among_single_tokens_is_not_streamed(lst, batch, rows, group, all_streamed):
+    assert bool(lst.streams_all(batch, rows, group)) == all_streamed
