@@ -60,3 +60,14 @@ def test_a_long_chunk_among_single_tokens(chunk, singles, heads, kv, dim, block,
     prefix, own = ([0, start[singles - 10]], [500], table[-1:]), (start, lengths, table[:-1])
     out, lse = attend(p, prefix, own, q, fill=7.0)
     check(p, prefix, own, q, out, lse)
+
+
+@pytest.mark.parametrize("n,length,prefix", [(150, 150, 300), (150, 2000, 1000), (40, 900, 65), (65, 10, 64)])
+@pytest.mark.parametrize("heads,kv,dim,fmt,dtype", [(8, 2, 128, "int8", "bf16"), (2, 1, 64, "fp8", "f32"), (4, 2, 256, "int8", "bf16")])
+def test_one_prompt_behind_a_prefix(n, length, prefix, heads, kv, dim, fmt, dtype):
+    """Rows see their own tokens up to themselves, cut up between workgroups where there are many, and all of the prefix."""
+    p, table = filled(170, fmt, 32, dim, kv, [length, prefix])
+    q = rows(171, n, heads, dim, dtype, 2.0, fused=1)
+    before, own = ([0, n], [prefix], table[1:]), ([0, n], [length], table[:1])
+    out, lse = attend(p, before, own, q, fill=7.0)
+    check(p, before, own, q, out, lse)
