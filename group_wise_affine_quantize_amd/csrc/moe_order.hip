@@ -18,7 +18,10 @@
 // What bounds it: sorting is latency (the ids are 4 bytes a pair); moving is
 // memory, each row once.  Experts' rows are read past the caches, which they
 // would fill in vain (8192 tokens of 8 rows of 8 KB, 30 % dropped, combined: 104
-// -> 91 us, 5.6 TB/s; 6 rows of 4 KB and their gradients 86 -> 75, 5.8 TB/s).
+// -> 91 us, 5.6 TB/s; 6 rows of 4 KB and their gradients 86 -> 75 in a row of calls,
+// 5.8 TB/s; 90 to 95 among a training step's other calls).  Rows off 16-byte
+// alignment take more registers and share lines: the same gradient at 2047 columns
+// takes 169 us for 78.
 #include <algorithm>
 
 #include "nq_kv_device.h"

@@ -108,10 +108,6 @@ template <typename T, int E> __device__ __forceinline__ Raw<T, E> pack(const flo
     return r;
 }
 
-template <typename T, int E, bool AL = true> __device__ __forceinline__ void load_run(const T *p, float *v)
-{
-    unpack<T, E>(load_raw<T, E, AL>(p), v);
-}
 template <typename T, int E, bool AL = true> __device__ __forceinline__ void store_run(T *p, const float *v)
 {
     store_raw<T, E, AL>(p, pack<T, E>(v));

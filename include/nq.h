@@ -545,7 +545,10 @@ nq_status nq_kv_attention(const nq_kv_cache *cache, const nq_kv_seqs *seqs, cons
  * what they see of their own sequence, whose lengths count its own tokens only.
  * row_start rises; rows that no prefix has see their own tokens alone.  The rest
  * is nq_kv_attention's, over the tokens of both: out, lse (of both), rows that see
- * nothing, NaN, precision, and what device arrays of any content may do. */
+ * nothing, NaN, precision, and what device arrays of any content may do.  The
+ * workspace holds the sums of both parts of each row's context in fp32, 2 * rows *
+ * q_heads * (head_dim + 4) numbers, and up to 140 MB of parts that workgroups
+ * share: 64 rows of 32 heads of 128 take 71 MB, 4096 of them 208 MB. */
 size_t nq_kv_attention_shared_workspace_bytes(const nq_kv_cache *cache, const nq_kv_seqs *prefix,
                                               const nq_kv_seqs *seqs, int32_t q_heads, nq_dtype x_dt);
 nq_status nq_kv_attention_shared(const nq_kv_cache *cache, const nq_kv_seqs *prefix, const nq_kv_seqs *seqs,
