@@ -348,10 +348,10 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
         row = next;
     }
 
-    // the chunk's sums, the teams' in their order: to `part`, or where that is
-    // null and the chunk is all there is to add to `out`
-    auto finish = [&](float (*sum)[E], int own, float *part, P *out) {
-        if (!part && !out) return;
+    // the chunk's sums, the teams' in their order: to `part`, or to `out` where they
+    // are all there is to add
+    auto finish = [&](float (*sum)[E], int own, float *part, P *out, bool all) {
+        if (all ? !out : !part) return;
         if constexpr (TEAMS > 1) {
             __syncthreads();
             if (team > 0)
@@ -375,14 +375,17 @@ __global__ __launch_bounds__(64 * W * grad_teams<W>()) void block_norm_grad_kern
             for (int e = 0; e < E; ++e) v[e] = sum[LEAN && own >= 0 ? 0 : i][e];
             if constexpr (LEAN)
                 if (own >= 0) get_own(own, i, v);
-            if (part) store_cols<float, E, AL>(part + (int64_t)blockIdx.x * dim, col0 + i * STRIDE, dim, pack<float, E>(v));
-            else store_cols<P, E, AL>(out, col0 + i * STRIDE, dim, pack<P, E>(v));
+            if (all) store_cols<P, E, AL>(out, col0 + i * STRIDE, dim, pack<P, E>(v));
+            else store_cols<float, E, AL>(part + (int64_t)blockIdx.x * dim, col0 + i * STRIDE, dim, pack<float, E>(v));
         }
     };
-    finish(dpre, -1, part_pre, static_cast<P *>(a.dpre));
-    finish(dpost, 0, part_post, static_cast<P *>(a.dpost));
-    // (gates of its own the chunk has written)
-    finish(dgate, 1, part_gate, ch.gates || !a.dgate ? nullptr : static_cast<P *>(a.dgate) + gate_row * dim);
+    const bool alone = ch.chunks == 1;
+    finish(dpre, -1, part_pre, static_cast<P *>(a.dpre), alone);
+    finish(dpost, 0, part_post, static_cast<P *>(a.dpost), alone);
+    // (gates of its own the chunk has written; one that it has all rows of is number blockIdx.x)
+    P *of_gate = ch.gates ? nullptr : static_cast<P *>(a.dgate);
+    if (TEAMS > 1 && of_gate) of_gate += (int64_t)blockIdx.x * dim;
+    finish(dgate, 1, part_gate, of_gate, alone || (TEAMS > 1 && ch.cuts == 1));
 }
 
 // out[g][c] = sum over the chunks g * cuts .. of part[chunk][c], in order within
@@ -438,8 +441,10 @@ template <typename T, typename P, int E, int W, int V, bool AL> struct Backward 
         const Chunks ch = norm_chunks(a.rows, a.gates, norm_grad_teams(a.dim));
         const int64_t part = ch.chunks * a.dim;
         float *at = a.partials, *pre = nullptr, *post = nullptr, *gate = nullptr;
-        // a gate's chunk alone writes its gradient itself
-        const bool gates = a.dgate && !ch.gates && (ch.cuts > 1 || ch.chunks == 0);
+        // the sums of a gate's parts; where workgroups have several teams, one that has all of
+        // a gate's rows writes its gradient (a single team has whole gates when they are few
+        // rows; and 16 waves would spill more: 2048 rows of 8192 in fp32 118 -> 128 us)
+        const bool gates = a.dgate && !ch.gates && (grad_teams<W>() == 1 || ch.cuts != 1);
         if (ch.chunks > 1) {
             if (a.dpre) pre = at, at += part;
             if (a.dpost) post = at, at += part;
